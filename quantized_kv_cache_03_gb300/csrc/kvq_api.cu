@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "kvq_internal.cuh"
+#include "kvq_paged.cuh"
 
 using namespace kvq;
 
@@ -683,6 +684,18 @@ kvq_status to_desc(const kvq_decode_desc &x, bool need_ptrs, Desc &d)
 }
 
 }  // namespace
+
+// The current device for the paged cache's entry points (kvq_paged_api.cu).
+kvq_status kvq::device_common(int *dev_out, int *n_sms, unsigned int **timeouts)
+{
+    DeviceInfo *dev = nullptr;
+    const kvq_status st = device_setup(&dev);
+    if (st != KVQ_OK) return st;
+    *dev_out = (int)(dev - g_dev);
+    *n_sms = dev->n_sms;
+    *timeouts = dev->timeouts;
+    return KVQ_OK;
+}
 
 extern "C" {
 

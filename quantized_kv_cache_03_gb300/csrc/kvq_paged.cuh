@@ -1,0 +1,173 @@
+// kvq_paged.cuh -- launch parameters and device helpers of the paged cache's
+// kernels (include/kvq_paged.h): the tile record, slots, and the deterministic
+// split of a ragged batch over persistent CTAs.
+#pragma once
+
+#include "kvq_internal.cuh"
+#include "kvq_paged.h"
+
+namespace kvq {
+
+// ------------------------------------------------------------ tile record --
+// 16 positions of one kv head in one run of bytes: K codes, K scales (int8 K),
+// V codes, V scales.  Code bytes in the fragment order of kvq_internal.cuh,
+// int8 codes biased by 128 (the form the byte-permute conversion wants, which
+// saves it an xor per word).  The scales of positions (2i, 2i + 1) sit side by
+// side, block after block, so lane c of an 8-position group gets the scale
+// pairs of its two positions for all four blocks in one 16-byte load.
+template <int VT, int KT>
+struct PageTile {
+    static constexpr int K = kWTile * kD * (KT == KVQ_K_F16 ? 2 : 1);
+    static constexpr int S = kWTile * kNB * 2;
+    static constexpr int V = kWTile * (VT == KVQ_V_Q4_0 ? kD / 2 : kD);
+    static constexpr int KS_OFF = K;
+    static constexpr int V_OFF = K + (KT == KVQ_K_F16 ? 0 : S);
+    static constexpr int VS_OFF = V_OFF + V;
+    static constexpr int BYTES = VS_OFF + S;
+};
+__host__ __device__ constexpr int page_tile_bytes(int v_type, int k_type)
+{
+    return kWTile * (kD * (k_type == KVQ_K_F16 ? 2 : 1) + (v_type == KVQ_V_Q4_0 ? kD / 2 : kD)) +
+           kWTile * kNB * 2 * (k_type == KVQ_K_F16 ? 1 : 2);
+}
+// Byte offset of block b's scale of position u in a scale area.
+__host__ __device__ constexpr int scale_off(int u, int b) { return 2 * (((u / 8) * 4 + (u % 8) / 2) * 8 + 2 * b + u % 2); }
+
+// A quantized row (quant_token) into place u of a tile.
+template <int VT, int KT>
+__device__ __forceinline__ void store_token_paged(const TokenRow &t, int u, int lane, uint8_t *tile)
+{
+    using T = PageTile<VT, KT>;
+    if (KT == KVQ_K_F16) {
+        *reinterpret_cast<uint32_t *>(tile + k16_tile_off(u, 4 * lane)) = t.kw;
+        *reinterpret_cast<uint32_t *>(tile + k16_tile_off(u, 4 * lane + 2)) = t.kw2;
+    } else {
+        *reinterpret_cast<uint32_t *>(tile + k_tile_off(u, 4 * lane)) = t.kw ^ 0x80808080u;
+        if ((lane & 7) == 0) *reinterpret_cast<uint16_t *>(tile + T::KS_OFF + scale_off(u, lane >> 3)) = t.ks;
+    }
+    uint8_t *vt = tile + T::V_OFF;
+    if (VT == KVQ_V_Q8_0) {
+        const uint32_t w = t.vw ^ 0x80808080u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) vt[v8_tile_off(u, 4 * lane + k)] = (uint8_t)(w >> (8 * k));
+    } else if ((lane & 7) < 4) {
+        const int j = 16 * (lane >> 3) + 4 * (lane & 3);
+        *reinterpret_cast<uint16_t *>(vt + v4_tile_off(u, j)) = (uint16_t)t.vw;
+        *reinterpret_cast<uint16_t *>(vt + v4_tile_off(u, j + 2)) = (uint16_t)(t.vw >> 16);
+    }
+    if ((lane & 7) == 0) *reinterpret_cast<uint16_t *>(tile + T::VS_OFF + scale_off(u, lane >> 3)) = t.vs;
+}
+
+struct PoolDesc {
+    uint8_t *data;
+    int n_pages;
+    int n_slots;        // n_pages * page_tokens
+    int pshift;         // log2(page_tokens)
+    int n_kv_heads;
+};
+
+// Tile of (slot, head): its first byte.  Offsets in 64 bits.
+__device__ __forceinline__ uint8_t *tile_of(const PoolDesc &p, int page, int h, int tile, int tile_bytes)
+{
+    return p.data + ((((size_t)page * p.n_kv_heads + h) << (p.pshift - 4)) + tile) * tile_bytes;
+}
+
+struct TableParams {
+    const int *lens, *n_new, *n_free;
+    int *free_pages, *block_table, *lens_out, *n_free_out, *q_start, *slots, *status;
+    int n_seqs, pshift, n_pages, stride, max_blocks, n_tokens;
+};
+
+struct PagedRowsParams {      // append and gather
+    PoolDesc pool;
+    const uint16_t *k16, *v16;
+    long long stride;         // elements between tokens
+    const int *slots;
+    int n_tokens;
+    void *k_out, *v_out;
+};
+
+// ------------------------------------------------------- paged attention --
+constexpr int kStagePos = 32;           // positions per work unit ("stage")
+constexpr int kPagedMinStages = 4;      // a CTA's least piece of the line: one stage per warp
+
+// A query-row tile of one kv head that several CTAs attend: what the combine
+// needs to merge its pieces (np = 0: none).
+struct PagedCut {
+    int b;        // sequence
+    int h_rt;     // kv head | row tile << 8
+    int c0, np;   // pieces: slot 1 of CTA c0, slot 0 of CTAs c0 + 1 .. c0 + np - 1
+};
+
+struct PagedAttnParams {
+    PoolDesc pool;
+    const uint16_t *q;
+    long long q_stride;
+    const int *q_start, *seq_lens, *block_table;
+    void *out;
+    float *lse;                         // may be null
+    PagedCut *cuts;                     // [CTAs][2]
+    float *ws_lse;                      // [CTAs][2][row tile]
+    float *ws_o;                        // [CTAs][2][row tile][kD]
+    unsigned int *timeouts;
+    int n_seqs, n_tokens, max_q, n_q_heads, table_stride, max_blocks, causal;
+    int gmax;                           // query heads of the busiest kv head
+    int min_rows, max_rows;             // sequences with min_rows <= rows <= max_rows per kv head are this launch's
+    float qk_scale_log2;
+    uint16_t grp_begin[KVQ_MAX_HEADS + 1];   // kv head h owns grp_q[grp_begin[h] .. grp_begin[h + 1])
+    uint8_t grp_q[KVQ_MAX_HEADS];
+};
+
+// New rows and visible length of sequence b, held to the arrays' bounds.
+__device__ __forceinline__ void seq_shape(const PagedAttnParams &p, int b, int &t0, int &n, int &len)
+{
+    t0 = min(max(p.q_start[b], 0), p.n_tokens);
+    n = min(min(max(p.q_start[b + 1], 0), p.n_tokens) - t0, p.max_q);
+    len = max(0, (int)min((long long)p.seq_lens[b], (long long)p.max_blocks << p.pool.pshift));
+}
+
+// Work of a sequence, in stages of kStagePos positions for every row tile of
+// every kv head (at least one each: rows that see nothing are still written);
+// 0 when its rows belong to the other kernel.
+__device__ __forceinline__ bool seq_mine(const PagedAttnParams &p, int n)
+{
+    const long long rows = (long long)n * p.gmax;
+    return n > 0 && rows >= p.min_rows && rows <= p.max_rows;
+}
+
+cudaError_t prepare_page_tables();
+cudaError_t launch_page_tables(const TableParams &p, cudaStream_t s, bool pdl);
+cudaError_t launch_paged_append(const PagedRowsParams &p, int v_type, int k_type, cudaStream_t s, bool pdl);
+cudaError_t launch_paged_gather(const PagedRowsParams &p, int v_type, int k_type, int out_type, cudaStream_t s,
+                                bool pdl);
+cudaError_t launch_paged_combine(const PagedAttnParams &p, int n_ctas, int tile_rows, int out_type, cudaStream_t s,
+                                 bool pdl);
+// Row-tile attention (kvq_paged_attn_q4.cu / _q8.cu): nt = 8-row tiles per CTA (1 or 2).
+cudaError_t prepare_paged_q4(int nt, int k_type, int out_type, int *ctas_per_sm);
+cudaError_t prepare_paged_q8(int nt, int k_type, int out_type, int *ctas_per_sm);
+cudaError_t launch_paged_q4(const PagedAttnParams &p, int nt, int k_type, int out_type, int n_ctas, cudaStream_t s,
+                            bool pdl);
+cudaError_t launch_paged_q8(const PagedAttnParams &p, int nt, int k_type, int out_type, int n_ctas, cudaStream_t s,
+                            bool pdl);
+
+// The current device's SM count and the address of the bounded waits' counter
+// (kvq_api.cu).
+kvq_status device_common(int *dev, int *n_sms, unsigned int **timeouts);
+
+template <typename P>
+static inline cudaError_t launch_pdl(void (*fn)(P), const P &p, int grid, int block, int smem, cudaStream_t s, bool pdl)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+}  // namespace kvq

@@ -1,0 +1,663 @@
+// kvq_paged_attn.cuh -- attention of a ragged batch over the paged cache: query
+// rows in tiles of 8 NT (NT = 1 or 2), mma.sync on the cache's own codes.
+//
+// Split of the work.  The batch is one line of stages (32 positions of one row
+// tile of one kv head): sequence after sequence, kv head after kv head, row
+// tile after row tile.  CTA i of the persistent grid takes the i-th equal piece
+// of that line, whatever the lengths are, so a batch is one wave without a
+// tail.  Every CTA derives its piece from q_start and seq_lens itself (a block
+// scan over the sequences), so nothing is planned on the host.  A row tile cut
+// by a piece boundary leaves partials (at most two per CTA) for the combine.
+//
+// A CTA has four warps; warp w takes stages w, w + 4, ... of the piece through
+// a private ring filled by bulk copies (a tile record is contiguous: one copy
+// per stage, two when pages hold 16 positions).  Nothing but the ring's
+// barriers synchronizes the main loop.
+//
+// Arithmetic per stage, for rows g and (NT = 2) g + 8 of the lane 4g + c:
+//   S = Q K^T   m16n8k16, A = query codes (rows 8..15 zero when NT = 1), B = K
+//               codes entered as 1152 + code; per 32-block an accumulator that
+//               starts at -1152 * (sum of the row's codes), so it ends exactly
+//               at the integer block dot; score = sum_b I_b * sq_b * sk_b.
+//   O^T += V^T P^T   m16n8k16, A = V codes (exact fp16 integers), B = p * d
+//               per block.  The accumulator layout of S (row g, positions 2c,
+//               2c + 1) is the B layout of P^T (k 2c, 2c + 1, n = g): no
+//               transpose.  KVQ_OUT_F32 splits p * d into an fp16 high and low
+//               part (two MMAs, about 22 bits), KVQ_OUT_F16 rounds it once
+//               (2^-12 relative to each term, below the output's own rounding).
+// Softmax in base 2.  A row's reference maximum is raised only when a score
+// passes it by more than kSlack = 1, and exponents are taken kShift above it:
+// p reaches 2^(kShift + 1), which with the largest V scale (516 for q8_0, 8188
+// for q4_0) still fits fp16, and keeps p * d out of fp16's subnormals, where
+// the low part would lose its bits (p = 2^-9, d = 0.02: the product's lower
+// half would have one bit left).  l carries the same factor, so it cancels.
+#pragma once
+
+#include <type_traits>
+
+#include "kvq_paged.cuh"
+
+namespace kvq {
+
+template <int NT, int VT, int KT>
+struct PagedCfg {
+    using T = PageTile<VT, KT>;
+    static constexpr int WARPS = 4, THREADS = WARPS * 32;
+    static constexpr bool F16K = KT == KVQ_K_F16;
+    static constexpr int TPS = kStagePos / kWTile;            // tiles per stage
+    static constexpr int STAGES = 2;
+    static constexpr int STAGE = TPS * T::BYTES, RING = STAGES * STAGE;
+    static constexpr int ROWS = 8 * NT;
+    static constexpr int KROW = F16K ? 2 * kD : kD;           // bytes of a query row's codes
+    static constexpr int Q_OFF = WARPS * RING;
+    static constexpr int QS_OFF = Q_OFF + ROWS * KROW;        // fp32 [ROWS][kNB]
+    static constexpr int QSUM_OFF = QS_OFF + ROWS * kNB * 4;  // fp32 [ROWS][kNB]: accumulator seeds
+    static constexpr int BAR_OFF = QSUM_OFF + ROWS * kNB * 4;
+    static constexpr int MISC_OFF = BAR_OFF + WARPS * STAGES * 8;
+    static constexpr int SMEM = MISC_OFF + 128;
+    static constexpr int OROW = kD + 4;
+    static constexpr int ML_OFF = WARPS * ROWS * OROW * 4;    // merge: slices, then m, l per warp, then 1/L, lse
+    static_assert(ML_OFF + (2 * WARPS + 2) * ROWS * 4 <= WARPS * RING, "the merge reuses the rings");
+    static_assert(T::BYTES % 128 == 0 && BAR_OFF % 8 == 0 && QS_OFF % 16 == 0, "alignment");
+};
+
+// Two signed int8 codes (bytes k0, k0 + 1 of w) as an exact fp16 pair.
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int k0)
+{
+    const __half2 h = __halves2half2(__int2half_rn((int)(int8_t)(w >> (8 * k0))), __int2half_rn((int)(int8_t)(w >> (8 * k0 + 8))));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 half2_of(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
+
+// V A-fragment registers of one 32-block for the position pair (t, t + 1):
+// reg[h2][half] = the exact codes of head dim g + 8 half of m-tile 2 bb + h2
+// (dims as pv_dim: q4_0 32bb + 16h2 + 2g + half, q8_0 32bb + 4g + 2h2 + half).
+template <int VT>
+__device__ __forceinline__ void v_codes(uint32_t w0, uint32_t w1, uint32_t (&reg)[2][2])
+{
+    auto h2 = [](uint32_t x) { return *reinterpret_cast<__half2 *>(&x); };
+    auto put = [](uint32_t &r, __half2 v) { r = *reinterpret_cast<uint32_t *>(&v); };
+    if (VT == KVQ_V_Q4_0) {   // nibbles under the exponent of 1024, minus 1032; high ones weigh 16
+        const __half2 k1032 = __half2half2(__ushort_as_half(0x6408)), k16th = __half2half2(__ushort_as_half(0x2c00)),
+                      km72 = __half2half2(__ushort_as_half(0xd480));
+        const uint32_t w8 = w0 >> 8;
+        put(reg[0][0], __hsub2(h2((w0 & 0x000F000Fu) | 0x64006400u), k1032));
+        put(reg[0][1], __hsub2(h2((w8 & 0x000F000Fu) | 0x64006400u), k1032));
+        put(reg[1][0], __hfma2(h2((w0 & 0x00F000F0u) | 0x64006400u), k16th, km72));
+        put(reg[1][1], __hfma2(h2((w8 & 0x00F000F0u) | 0x64006400u), k16th, km72));
+    } else {                  // code + 128 under the exponent of 1024, minus 1152
+        const __half2 k1152 = __half2half2(__ushort_as_half(0x6480));
+        put(reg[0][0], __hsub2(h2(__byte_perm(w0, 0x64646464u, 0x4140)), k1152));
+        put(reg[0][1], __hsub2(h2(__byte_perm(w0, 0x64646464u, 0x4342)), k1152));
+        put(reg[1][0], __hsub2(h2(__byte_perm(w1, 0x64646464u, 0x4140)), k1152));
+        put(reg[1][1], __hsub2(h2(__byte_perm(w1, 0x64646464u, 0x4342)), k1152));
+    }
+}
+template <int VT>
+__device__ __forceinline__ int v_dim(int mt, int g)   // the pair's first dim: half 0 of m-tile mt
+{
+    return VT == KVQ_V_Q4_0 ? 32 * (mt >> 1) + 16 * (mt & 1) + 2 * g : 32 * (mt >> 1) + 4 * g + 2 * (mt & 1);
+}
+
+// Where a CTA's piece of the line of stages begins: scanned by the whole block.
+struct LineStart {
+    int b;               // first sequence with work at or after the start
+    long long off;       // stages into it
+    long long total;     // stages of the line
+};
+
+// stages(n, len): the sequence's stages over all kv heads and row tiles.
+template <int THREADS, typename F>
+__device__ __forceinline__ void line_find(const PagedAttnParams &p, long long gmin, F stages, LineStart *res,
+                                          long long *tmp, long long &begin, long long &per)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int each = (p.n_seqs + THREADS - 1) / THREADS, i0 = min(p.n_seqs, tid * each), i1 = min(p.n_seqs, i0 + each);
+    long long sum = 0;
+    for (int i = i0; i < i1; ++i) {
+        int t0, n, len;
+        seq_shape(p, i, t0, n, len);
+        if (seq_mine(p, n)) sum += stages(n, len);
+    }
+    long long x = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) tmp[warp] = x;
+    __syncthreads();
+    long long base = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) base += tmp[w];
+        total += tmp[w];
+    }
+    per = max(gmin, (total + gridDim.x - 1) / gridDim.x);
+    begin = per * blockIdx.x;
+    long long at = base + x - sum;
+    if (begin >= at && begin < at + sum)
+        for (int i = i0; i < i1; ++i) {
+            int t0, n, len;
+            seq_shape(p, i, t0, n, len);
+            const long long s = seq_mine(p, n) ? stages(n, len) : 0;
+            if (begin < at + s) {
+                res->b = i;
+                res->off = begin - at;
+                break;
+            }
+            at += s;
+        }
+    if (tid == 0) res->total = total;
+    __syncthreads();
+}
+
+template <int NT, int VT, int KT, bool O16>
+__global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const __grid_constant__ PagedAttnParams p)
+{
+    using C = PagedCfg<NT, VT, KT>;
+    using T = PageTile<VT, KT>;
+    constexpr int W = C::WARPS, S = C::STAGES;
+    constexpr float kBias = 1152.0f, kSlack = 1.0f, kShift = VT == KVQ_V_Q4_0 ? 2.0f : 5.0f;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ LineStart line;
+    __shared__ long long tmp[W];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int H = p.pool.n_kv_heads, pshift = p.pool.pshift;
+    uint8_t *ring = smem + warp * C::RING;
+    const uint32_t ring_s = smem_u32(ring), bar_s = smem_u32(smem + C::BAR_OFF) + warp * S * 8;
+    int *bad_flag = reinterpret_cast<int *>(smem + C::MISC_OFF);
+    if (tid == 0) *bad_flag = 0;
+    if (lane == 0) {
+#pragma unroll
+        for (int st = 0; st < S; ++st) mbar_init(bar_s + st * 8, 1);
+        fence_mbar_init();
+    }
+    pdl_wait();
+    pdl_trigger();
+
+    auto seq_tiles = [&](int n) { return (n * p.gmax + C::ROWS - 1) / C::ROWS; };   // row tiles per kv head
+    auto seq_stages = [&](int len) { return max(1, (len + kStagePos - 1) / kStagePos); };
+    long long pos, per;
+    line_find<C::THREADS>(p, kPagedMinStages, [&](int n, int len) { return (long long)H * seq_tiles(n) * seq_stages(len); },
+                          &line, tmp, pos, per);
+    const long long end = min(pos + per, line.total);
+    PagedCut *cuts = p.cuts + (size_t)blockIdx.x * 2;
+    if (tid < 2) cuts[tid] = PagedCut{0, 0, 0, 0};
+    __syncthreads();
+    if (pos >= end) return;
+
+    int b = line.b - 1, t0 = 0, n = 0, L = 0, n_st = 0, n_rt = 0, h = 0, rt = 0, s0 = 0;
+    bool fresh = true;
+    int done = 0;   // stages this warp has taken since the kernel began: ring slot and phase
+    for (bool first = true; pos < end; first = false) {
+        if (fresh) {   // next sequence of this launch
+            do {
+                ++b;
+                seq_shape(p, b, t0, n, L);
+            } while (!seq_mine(p, n));
+            n_st = seq_stages(L);
+            n_rt = seq_tiles(n);
+            h = rt = s0 = 0;
+            if (first) {
+                const long long u = line.off / n_st;
+                s0 = (int)(line.off - u * n_st);
+                rt = (int)(u % n_rt);
+                h = (int)(u / n_rt);
+            }
+            fresh = false;
+        }
+        const int s1 = (int)min((long long)n_st, s0 + (end - pos));
+        const int gb = p.grp_begin[h], gsz = p.grp_begin[h + 1] - gb;
+        const int row0 = rt * C::ROWS, R = min(C::ROWS, n * gsz - row0);   // row r: token (row0 + r) / gsz of the sequence
+        const bool whole = s0 == 0 && s1 == n_st;
+        const int slot = s0 == 0 ? 1 : 0;
+        if (R > 0) {
+            if (!whole && tid == 0) {
+                const long long x0 = pos - s0, c0 = x0 / per;   // CTA that begins the row tile
+                cuts[slot] = PagedCut{b, h | rt << 8, (int)c0, (int)((x0 + n_st - 1) / per - c0 + 1)};
+            }
+            // positions the tile's last and first rows see end at lim_hi, lim_lo
+            const int lim_hi = p.causal ? L - n + (row0 + R - 1) / gsz : L - 1;
+            const int lim_lo = p.causal ? L - n + row0 / gsz : L - 1;
+            const int sv = min(s1, (lim_hi + kStagePos) / kStagePos);       // stages past sv show nothing (lim_hi >= -kStagePos)
+            const int nj = lim_hi < 0 ? 0 : max(0, (sv - s0 - warp + W - 1) / W);   // this warp's stages
+
+            // ---- page ids, 32 stages ahead per load ----
+            const int *bt = p.block_table + (size_t)b * p.table_stride;
+            int pg0 = -1, pg1 = -1, okm = 0, issued = 0;
+            auto fetch = [&](int j) {   // lane l: stage j + l
+                const int x = (s0 + warp + W * (j + lane)) * kStagePos;
+                pg0 = pg1 = -1;
+                if (j + lane < nj) {
+                    pg0 = bt[x >> pshift];
+                    if (pshift == 4 && x + 16 < L) pg1 = bt[(x >> 4) + 1];
+                }
+            };
+            auto issue = [&]() {
+                if ((issued & 31) == 0) fetch(issued);
+                const int sl = (done + issued) % S;   // `done` counts finished pieces' stages only
+                const int a0 = __shfl_sync(0xffffffffu, pg0, issued & 31);
+                const int x = (s0 + warp + W * issued) * kStagePos;
+                const int tile = (x & ((1 << pshift) - 1)) >> 4;
+                const bool v0 = a0 >= 0 && a0 < p.pool.n_pages;
+                const uint32_t dst = ring_s + sl * C::STAGE, bw = bar_s + sl * 8;
+                int ok;
+                if (pshift == 4) {
+                    const int a1 = __shfl_sync(0xffffffffu, pg1, issued & 31);
+                    const bool v1 = a1 >= 0 && a1 < p.pool.n_pages;
+                    ok = (v0 ? 1 : 0) | (v1 ? 2 : 0);
+                    mbar_arrive_expect_tx_w(bw, ((v0 ? 1 : 0) + (v1 ? 1 : 0)) * T::BYTES);
+                    if (v0) bulk_g2s_w(dst, tile_of(p.pool, a0, h, 0, T::BYTES), T::BYTES, bw);
+                    if (v1) bulk_g2s_w(dst + T::BYTES, tile_of(p.pool, a1, h, 0, T::BYTES), T::BYTES, bw);
+                } else {
+                    ok = v0 ? 3 : 0;
+                    mbar_arrive_expect_tx_w(bw, v0 ? C::STAGE : 0);
+                    if (v0) bulk_g2s_w(dst, tile_of(p.pool, a0, h, tile, T::BYTES), C::STAGE, bw);
+                }
+                okm = (okm & ~(3 << (2 * sl))) | ok << (2 * sl);
+                ++issued;
+            };
+            // a warp that lost a copy issues nothing more (its results are poisoned)
+            const int nj_live = *bad_flag ? 0 : nj;
+#pragma unroll
+            for (int k = 0; k < S; ++k)
+                if (issued < nj_live) issue();
+
+            // ---- query rows -> fragments ----
+            uint32_t qa[8][2 * NT];            // [k16 step][row g: k 2c.., k 2c + 8..; row g + 8 likewise]
+            float seed[kNB][NT], sq[kNB][NT];  // int8 K: accumulator seeds and row scales per block
+            {
+                uint32_t *qw = reinterpret_cast<uint32_t *>(smem + C::Q_OFF);
+                float *qs = reinterpret_cast<float *>(smem + C::QS_OFF), *qsum = reinterpret_cast<float *>(smem + C::QSUM_OFF);
+#pragma unroll
+                for (int k = 0; k < C::ROWS / W; ++k) {
+                    const int r = warp + W * k;
+                    uint2 raw = make_uint2(0u, 0u);
+                    if (r < R) {
+                        const size_t t = t0 + (row0 + r) / gsz;
+                        raw = *reinterpret_cast<const uint2 *>(p.q + t * p.q_stride + (size_t)p.grp_q[gb + (row0 + r) % gsz] * kD + 4 * lane);
+                    }
+                    if (C::F16K) {
+                        *reinterpret_cast<uint2 *>(qw + r * (kD / 2) + 2 * lane) = raw;
+                        continue;
+                    }
+                    const float2 lo = half2_of(raw.x), hi = half2_of(raw.y);
+                    const float xv[4] = {lo.x, lo.y, hi.x, hi.y};
+                    uint16_t s16;
+                    const uint32_t word = quant_row_i8(xv, s16);
+                    int sum = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sum += (int)(int8_t)(word >> (8 * e));
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                    qw[r * (kD / 4) + lane] = word;
+                    if ((lane & 7) == 0) {
+                        qs[r * kNB + (lane >> 3)] = __half2float(__ushort_as_half(s16)) * p.qk_scale_log2;
+                        qsum[r * kNB + (lane >> 3)] = -kBias * (float)sum;
+                    }
+                }
+                __syncthreads();
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int r = g + 8 * nt;
+                    if (C::F16K) {
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks) {
+                            qa[ks][2 * nt] = qw[r * (kD / 2) + 8 * ks + c];
+                            qa[ks][2 * nt + 1] = qw[r * (kD / 2) + 8 * ks + c + 4];
+                        }
+                    } else {
+#pragma unroll
+                        for (int bb = 0; bb < kNB; ++bb) {
+#pragma unroll
+                            for (int kk = 0; kk < 2; ++kk) {
+                                const uint32_t w = qw[r * (kD / 4) + 8 * bb + 2 * c + kk];
+                                qa[2 * bb + kk][2 * nt] = code_pair(w, 0);
+                                qa[2 * bb + kk][2 * nt + 1] = code_pair(w, 2);
+                            }
+                            seed[bb][nt] = qsum[r * kNB + bb];
+                            sq[bb][nt] = qs[r * kNB + bb];
+                        }
+                    }
+                }
+            }
+            float m[NT], l[NT], mu[NT];
+            int lim[NT];
+            float acc[8][NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int r = g + 8 * nt;
+                lim[nt] = r < R ? (p.causal ? L - n + (row0 + r) / gsz : L - 1) : -1;
+                m[nt] = -INFINITY;
+                mu[nt] = l[nt] = 0.f;
+#pragma unroll
+                for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) acc[mt][nt][k] = 0.f;
+            }
+
+            bool lost = false;
+#pragma unroll 1
+            for (int j = 0; j < nj_live; ++j) {
+                const int sl = (done + j) % S;
+                if (!__all_sync(0xffffffffu, mbar_wait(bar_s + sl * 8, ((done + j) / S) & 1))) {
+                    lost = true;
+                    break;
+                }
+                const uint8_t *stg = ring + sl * C::STAGE;
+                const int x = (s0 + warp + W * j) * kStagePos, ok = (okm >> (2 * sl)) & 3;
+                auto stage = [&](auto full_tag) {
+                    constexpr bool FULL = decltype(full_tag)::value;
+                    float2 s[NT][4];   // [8-position group]: positions 8i + 2c, + 1 of row g + 8 nt
+#pragma unroll
+                    for (int t = 0; t < C::TPS; ++t) {
+                        const uint8_t *tk = stg + t * T::BYTES;
+                        if constexpr (C::F16K) {
+                            float d[2][4] = {};
+#pragma unroll
+                            for (int ks = 0; ks < 8; ++ks) {
+                                const uint4 k4 = *reinterpret_cast<const uint4 *>(tk + ks * 512 + lane * 16);
+                                const uint32_t a[4] = {qa[ks][0], NT == 2 ? qa[ks][2 * NT - 2] : 0u, qa[ks][1], NT == 2 ? qa[ks][2 * NT - 1] : 0u};
+                                mma_f16_16816(d[0], a, k4.x, k4.z);
+                                mma_f16_16816(d[1], a, k4.y, k4.w);
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    s[nt][2 * t + i] = mul2(make_float2(d[i][2 * nt], d[i][2 * nt + 1]), make_float2(p.qk_scale_log2, p.qk_scale_log2));
+                        } else {
+                            uint4 kk[2][2], sk[2];
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                                for (int hb = 0; hb < 2; ++hb) kk[i][hb] = *reinterpret_cast<const uint4 *>(tk + (2 * i + hb) * 512 + lane * 16);
+                                sk[i] = *reinterpret_cast<const uint4 *>(tk + T::KS_OFF + (4 * i + c) * 16);
+                            }
+#pragma unroll
+                            for (int bb = 0; bb < kNB; ++bb) {
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const uint4 &kw = kk[i][bb >> 1];
+                                    const uint32_t w0 = (bb & 1) ? kw.z : kw.x, w1 = (bb & 1) ? kw.w : kw.y;
+                                    const uint32_t a0[4] = {qa[2 * bb][0], NT == 2 ? qa[2 * bb][2 * NT - 2] : 0u, qa[2 * bb][1], NT == 2 ? qa[2 * bb][2 * NT - 1] : 0u};
+                                    const uint32_t a1[4] = {qa[2 * bb + 1][0], NT == 2 ? qa[2 * bb + 1][2 * NT - 2] : 0u, qa[2 * bb + 1][1], NT == 2 ? qa[2 * bb + 1][2 * NT - 1] : 0u};
+                                    const uint32_t sd0 = __float_as_uint(seed[bb][0]), sd1 = __float_as_uint(NT == 2 ? seed[bb][NT - 1] : 0.f);
+                                    float d[4];
+                                    mma_f16_16816_c4(d, a0, __byte_perm(w0, 0x64646464u, 0x4140), __byte_perm(w0, 0x64646464u, 0x4342), make_uint4(sd0, sd0, sd1, sd1));
+                                    mma_f16_16816(d, a1, __byte_perm(w1, 0x64646464u, 0x4140), __byte_perm(w1, 0x64646464u, 0x4342));
+                                    const uint32_t sw = bb == 0 ? sk[i].x : bb == 1 ? sk[i].y : bb == 2 ? sk[i].z : sk[i].w;
+                                    const float2 s2 = half2_of(sw);
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt) {
+                                        const float2 v = mul2(make_float2(d[2 * nt], d[2 * nt + 1]), make_float2(sq[bb][nt], sq[bb][nt]));
+                                        s[nt][2 * t + i] = bb == 0 ? mul2(v, s2) : fma2(v, s2, s[nt][2 * t + i]);
+                                    }
+                                }
+                            }
+                        }
+                    }
+                    if (!FULL) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int q0 = x + 8 * i + 2 * c;
+                            const bool live = (ok >> (i >> 1)) & 1;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                s[nt][i].x = live && q0 <= lim[nt] ? s[nt][i].x : -INFINITY;
+                                s[nt][i].y = live && q0 + 1 <= lim[nt] ? s[nt][i].y : -INFINITY;
+                            }
+                        }
+                    }
+                    // ---- softmax: a row's scores sit in the four lanes of one g ----
+                    float mx[NT];
+                    bool need = false;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mx[nt] = fmaxf(fmaxf(fmaxf(s[nt][0].x, s[nt][0].y), fmaxf(s[nt][1].x, s[nt][1].y)),
+                                       fmaxf(fmaxf(s[nt][2].x, s[nt][2].y), fmaxf(s[nt][3].x, s[nt][3].y)));
+                        need |= mx[nt] > m[nt] + (kShift + kSlack);
+                    }
+                    if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float v = fmaxf(mx[nt], __shfl_xor_sync(0xffffffffu, mx[nt], 1));
+                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                            v = fmaxf(m[nt], v - kShift);   // m: the exponents' zero
+                            const float al = v == -INFINITY ? 1.f : fast_exp2(m[nt] - v);
+                            l[nt] *= al;
+                            m[nt] = v;
+                            mu[nt] = v == -INFINITY ? 0.f : v;
+                            // the accumulator's columns are rows 2c, 2c + 1: their factors sit in lanes 8c, 8c + 4
+                            const float2 a2 = make_float2(__shfl_sync(0xffffffffu, al, 8 * c), __shfl_sync(0xffffffffu, al, 8 * c + 4));
+#pragma unroll
+                            for (int mt = 0; mt < 8; ++mt) {
+                                const float2 lo = mul2(make_float2(acc[mt][nt][0], acc[mt][nt][1]), a2);
+                                const float2 hi = mul2(make_float2(acc[mt][nt][2], acc[mt][nt][3]), a2);
+                                acc[mt][nt][0] = lo.x; acc[mt][nt][1] = lo.y;
+                                acc[mt][nt][2] = hi.x; acc[mt][nt][3] = hi.y;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 e = sub2(s[nt][i], make_float2(mu[nt], mu[nt]));
+                            s[nt][i] = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+                            sum = add2(sum, s[nt][i]);
+                        }
+                        l[nt] += sum.x + sum.y;
+                    }
+                    // ---- O^T += V^T P^T ----
+#pragma unroll
+                    for (int t = 0; t < C::TPS; ++t) {
+                        const uint8_t *tv = stg + t * T::BYTES + T::V_OFF, *ts = stg + t * T::BYTES + T::VS_OFF;
+                        constexpr int NVL = VT == KVQ_V_Q4_0 ? 1 : 2;
+                        uint4 vv[2][NVL], sv4[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                            for (int hb = 0; hb < NVL; ++hb) vv[i][hb] = *reinterpret_cast<const uint4 *>(tv + (NVL * i + hb) * 512 + lane * 16);
+                            sv4[i] = *reinterpret_cast<const uint4 *>(ts + (4 * i + c) * 16);
+                            if (!FULL) {   // scales of invisible positions may hold anything: p is 0 there, make d so too
+                                const int q0 = x + 16 * t + 8 * i + 2 * c;
+                                const bool live = (ok >> t) & 1;
+                                const uint32_t keep = (live && q0 <= lim_hi ? 0xffffu : 0u) | (live && q0 + 1 <= lim_hi ? 0xffff0000u : 0u);
+                                sv4[i].x &= keep; sv4[i].y &= keep; sv4[i].z &= keep; sv4[i].w &= keep;
+                            }
+                        }
+#pragma unroll
+                        for (int bb = 0; bb < kNB; ++bb) {
+                            uint32_t a[2][4];
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                uint32_t r[2][2];
+                                if (VT == KVQ_V_Q4_0) {
+                                    const uint4 &v = vv[i][0];
+                                    v_codes<VT>(bb == 0 ? v.x : bb == 1 ? v.y : bb == 2 ? v.z : v.w, 0u, r);
+                                } else {
+                                    const uint4 &v = vv[i][NVL == 1 ? 0 : (bb >> 1)];
+                                    v_codes<VT>((bb & 1) ? v.z : v.x, (bb & 1) ? v.w : v.y, r);
+                                }
+                                a[0][2 * i] = r[0][0];
+                                a[0][2 * i + 1] = r[0][1];
+                                a[1][2 * i] = r[1][0];
+                                a[1][2 * i + 1] = r[1][1];
+                            }
+                            float2 d2[2];
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) d2[i] = half2_of(bb == 0 ? sv4[i].x : bb == 1 ? sv4[i].y : bb == 2 ? sv4[i].z : sv4[i].w);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                uint32_t hi[2], lo[2];
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const float2 xv = mul2(s[nt][2 * t + i], d2[i]);
+                                    hi[i] = pack_half2(xv.x, xv.y);
+                                    if (!O16) {   // x - hi is exact in fp32
+                                        const float2 y = sub2(xv, half2_of(hi[i]));
+                                        lo[i] = pack_half2(y.x, y.y);
+                                    }
+                                }
+#pragma unroll
+                                for (int h2 = 0; h2 < 2; ++h2) {
+                                    mma_f16_16816(acc[2 * bb + h2][nt], a[h2], hi[0], hi[1]);
+                                    if (!O16) mma_f16_16816(acc[2 * bb + h2][nt], a[h2], lo[0], lo[1]);
+                                }
+                            }
+                        }
+                    }
+                };
+                if (ok == 3 && x + kStagePos - 1 <= lim_lo)
+                    stage(std::integral_constant<bool, true>());
+                else
+                    stage(std::integral_constant<bool, false>());
+                __syncwarp();   // every lane has read the slot
+                if (issued < nj_live) {
+                    fence_proxy_async_smem();
+                    issue();
+                }
+            }
+            if (lost) {   // wait (bounded) for the copies in flight, then poison the piece
+                for (int k = 0; k < issued; ++k) mbar_wait(bar_s + ((done + k) % S) * 8, ((done + k) / S) & 1);
+                if (lane == 0) {
+                    atomicOr(bad_flag, 1);
+                    atomicAdd(p.timeouts, 1u);
+                }
+            }
+            done += nj_live;
+
+            // ---- merge the warps in a fixed order and write ----
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 1);
+                l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 2);
+            }
+            __syncthreads();   // every warp is done with its ring
+            float *sm_o = reinterpret_cast<float *>(smem), *sm_m = reinterpret_cast<float *>(smem + C::ML_OFF);
+            float *sm_l = sm_m + W * C::ROWS, *sm_inv = sm_l + W * C::ROWS, *sm_lse = sm_inv + C::ROWS;
+            if (c == 0)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    sm_m[warp * C::ROWS + g + 8 * nt] = m[nt];
+                    sm_l[warp * C::ROWS + g + 8 * nt] = l[nt];
+                }
+            __syncthreads();
+            if (tid < R) {
+                float M = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < W; ++w) M = fmaxf(M, sm_m[w * C::ROWS + tid]);
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const float mw = sm_m[w * C::ROWS + tid];
+                    if (mw != -INFINITY) sum += sm_l[w * C::ROWS + tid] * fast_exp2(mw - M);
+                }
+                float lg;
+                asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(sum));
+                const bool any = !(sum <= 0.f);
+                sm_inv[tid] = any ? __fdividef(1.f, sum) : 0.f;
+                sm_lse[tid] = any ? (M + lg) * 0.69314718055994531f : -INFINITY;
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 8 * nt + 2 * c + e;   // the accumulator's column
+                    float M = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < W; ++w) M = fmaxf(M, sm_m[w * C::ROWS + r]);
+                    const float mw = sm_m[warp * C::ROWS + r], f = mw == -INFINITY ? 0.f : fast_exp2(mw - M);
+#pragma unroll
+                    for (int mt = 0; mt < 8; ++mt)
+                        *reinterpret_cast<float2 *>(&sm_o[(warp * C::ROWS + r) * C::OROW + v_dim<VT>(mt, g)]) =
+                            make_float2(acc[mt][nt][e] * f, acc[mt][nt][2 + e] * f);
+                }
+            __syncthreads();
+            const bool poisoned = *bad_flag != 0;
+            for (int i4 = tid; i4 < R * (kD / 4); i4 += C::THREADS) {
+                const int r = i4 / (kD / 4), d = (i4 % (kD / 4)) * 4;
+                float4 o = *reinterpret_cast<const float4 *>(&sm_o[r * C::OROW + d]);
+#pragma unroll
+                for (int w = 1; w < W; ++w) {
+                    const float4 q = *reinterpret_cast<const float4 *>(&sm_o[(w * C::ROWS + r) * C::OROW + d]);
+                    o.x += q.x; o.y += q.y; o.z += q.z; o.w += q.w;
+                }
+                const float inv = sm_inv[r];
+                float ls = sm_lse[r];
+                o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
+                if (poisoned) o.x = o.y = o.z = o.w = ls = __int_as_float(0x7fc00000);
+                if (whole) {
+                    const size_t row = (size_t)(t0 + (row0 + r) / gsz) * p.n_q_heads + p.grp_q[gb + (row0 + r) % gsz];
+                    if (O16)
+                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + row * kD + d) = make_uint2(pack_half2(o.x, o.y), pack_half2(o.z, o.w));
+                    else
+                        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * kD + d) = o;
+                    if (d == 0 && p.lse) p.lse[row] = ls;
+                } else {
+                    const size_t at = ((size_t)blockIdx.x * 2 + slot) * C::ROWS + r;
+                    *reinterpret_cast<float4 *>(p.ws_o + at * kD + d) = o;
+                    if (d == 0) p.ws_lse[at] = ls;
+                }
+            }
+            fence_proxy_async_smem();   // these accesses before the copies of the next piece
+            __syncthreads();            // the rings are free again
+        }
+        pos += s1 - s0;
+        s0 = 0;
+        if (++rt == n_rt) {
+            rt = 0;
+            if (++h == H) fresh = true;
+        }
+    }
+}
+
+template <int NT, int VT, int KT, bool O16>
+cudaError_t prepare_paged_t(int *ctas)
+{
+    using C = PagedCfg<NT, VT, KT>;
+    const void *fn = (const void *)paged_attn_kernel<NT, VT, KT, O16>;
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, fn, C::THREADS, C::SMEM);
+}
+
+template <int NT, int VT, int KT, bool O16>
+cudaError_t launch_paged_t(const PagedAttnParams &p, int n_ctas, cudaStream_t s, bool pdl)
+{
+    using C = PagedCfg<NT, VT, KT>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n_ctas);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_attn_kernel<NT, VT, KT, O16>, p);
+}
+
+#define KVQ_PAGED_PICK(FN, VT, nt, k_type, out_type, ...)                                                              \
+    ((k_type) == KVQ_K_F16                                                                                             \
+         ? ((nt) == 1 ? ((out_type) == KVQ_OUT_F16 ? FN<1, VT, KVQ_K_F16, true>(__VA_ARGS__) : FN<1, VT, KVQ_K_F16, false>(__VA_ARGS__))  \
+                      : ((out_type) == KVQ_OUT_F16 ? FN<2, VT, KVQ_K_F16, true>(__VA_ARGS__) : FN<2, VT, KVQ_K_F16, false>(__VA_ARGS__))) \
+         : ((nt) == 1 ? ((out_type) == KVQ_OUT_F16 ? FN<1, VT, KVQ_K_I8, true>(__VA_ARGS__) : FN<1, VT, KVQ_K_I8, false>(__VA_ARGS__))    \
+                      : ((out_type) == KVQ_OUT_F16 ? FN<2, VT, KVQ_K_I8, true>(__VA_ARGS__) : FN<2, VT, KVQ_K_I8, false>(__VA_ARGS__))))
+
+#define KVQ_DEFINE_PAGED_ENTRY(SUFFIX, VT)                                                                           \
+    cudaError_t prepare_paged_##SUFFIX(int nt, int k_type, int out_type, int *ctas)                                  \
+    {                                                                                                                \
+        return KVQ_PAGED_PICK(prepare_paged_t, VT, nt, k_type, out_type, ctas);                                      \
+    }                                                                                                                \
+    cudaError_t launch_paged_##SUFFIX(const PagedAttnParams &p, int nt, int k_type, int out_type, int n_ctas,        \
+                                      cudaStream_t s, bool pdl)                                                      \
+    {                                                                                                                \
+        return KVQ_PAGED_PICK(launch_paged_t, VT, nt, k_type, out_type, p, n_ctas, s, pdl);                          \
+    }
+
+}  // namespace kvq

@@ -1,0 +1,435 @@
+// kvq_paged_small.cu -- page tables, append, gather and the piece combine of
+// the paged cache.
+#include "kvq_paged.cuh"
+
+namespace kvq {
+
+// ---------------------------------------------------------------------------
+// Page tables.  Three prefix sums over the sequences (rows, pages given back,
+// pages needed) say everything: row t of the batch belongs to the sequence
+// whose row range holds it, new page f to the sequence whose range of needed
+// pages holds it, and entry v of the stack past the free pages to the released
+// sequence whose range holds it.  Every CTA of one cluster computes the sums
+// for itself (n_seqs loads, three block scans: cheaper than passing them
+// around), the cluster synchronizes once, so that lens and n_free may be
+// updated in place, and the outputs are dealt out flat over its threads with
+// a binary search each.  Latency-bound: its bytes are a few hundred KB.
+// ---------------------------------------------------------------------------
+constexpr int kTabThreads = 512;
+
+__device__ __forceinline__ long long block_scan(long long v, long long *tmp, long long &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    __syncthreads();   // tmp may still be read by the previous scan
+    if (lane == 31) tmp[warp] = x;
+    __syncthreads();
+    long long base = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kTabThreads / 32; ++w) {
+        if (w < warp) base += tmp[w];
+        total += tmp[w];
+    }
+    return base + x - v;   // exclusive
+}
+
+// Last i in [0, n) with a[i] <= x (a non-decreasing, a[0] <= x).
+__device__ __forceinline__ int last_at_most(const int *a, int n, int x)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TableParams p)
+{
+    extern __shared__ int tab[];
+    __shared__ long long tmp[kTabThreads / 32];
+    __shared__ int popped_s;
+    const int n = p.n_seqs, tid = threadIdx.x, P = 1 << p.pshift;
+    int *qs = tab, *need0 = qs + n + 1, *back0 = need0 + n + 1, *len_s = back0 + n + 1;
+    uint32_t rank, ranks;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+    const long long lmax = (long long)p.max_blocks << p.pshift;
+    pdl_wait();
+    pdl_trigger();
+    const int n_free = min(max(*p.n_free, 0), p.n_pages);
+    if (tid == 0) popped_s = 0x7fffffff;
+    // rows and pages given back
+    const int per = (n + kTabThreads - 1) / kTabThreads, i0 = min(n, tid * per), i1 = min(n, i0 + per);
+    long long rows = 0, back = 0;
+    for (int i = i0; i < i1; ++i) {
+        const int len = (int)min(max((long long)p.lens[i], 0ll), lmax), add = p.n_new[i];
+        len_s[i] = len;
+        rows += max(add, 0);
+        if (add < 0) back += (len + P - 1) >> p.pshift;
+    }
+    long long rows_all, back_all, need_all;
+    const long long rows0 = block_scan(rows, tmp, rows_all), backs0 = block_scan(back, tmp, back_all);
+    // pages needed by the sequences that fit their row of the table and the batch
+    auto fits = [&](int len, int add, long long end) { return (long long)len + add <= lmax && end <= p.n_tokens; };
+    auto pages = [&](int len, int add) { return (int)((((long long)len + add + P - 1) >> p.pshift) - ((len + P - 1) >> p.pshift)); };
+    long long need = 0, r = rows0, bk = backs0;
+    for (int i = i0; i < i1; ++i) {
+        const int len = len_s[i], add = p.n_new[i];
+        qs[i] = (int)min(r, 0x7fffffffll);
+        back0[i] = (int)min(bk, 0x7fffffffll);
+        r += max(add, 0);
+        if (add < 0) bk += (len + P - 1) >> p.pshift;
+        if (add > 0 && fits(len, add, r)) need += pages(len, add);
+    }
+    const long long needs0 = block_scan(need, tmp, need_all);
+    const int avail = (int)min((long long)n_free + back_all, (long long)p.n_pages);
+    // the grant: pages in order, and nothing after the first that does not fit
+    long long nd = needs0;
+    r = rows0;
+    for (int i = i0; i < i1; ++i) {
+        const int len = len_s[i], add = p.n_new[i];
+        r += max(add, 0);
+        need0[i] = (int)min(nd, 0x7fffffffll);
+        if (add > 0 && fits(len, add, r)) {
+            const int k = pages(len, add);
+            if (k > 0 && nd + k > avail) atomicMin(&popped_s, (int)min(nd, 0x7fffffffll));
+            nd += k;
+        }
+    }
+    if (tid == 0) {
+        qs[n] = (int)min(rows_all, 0x7fffffffll);
+        need0[n] = (int)min(need_all, 0x7fffffffll);
+        back0[n] = (int)min(back_all, 0x7fffffffll);
+    }
+    // every CTA has read lens and n_free; the sums are in place
+    asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+    const int popped = min(popped_s, need0[n]), n_free_out = avail - popped;
+    // entry v < avail of the stack with the returned pages on top
+    auto stack = [&](int v) {
+        if (v < n_free) return p.free_pages[v];
+        const int x = v - n_free, b = last_at_most(back0, n, x);
+        return p.block_table[(size_t)b * p.stride + (x - back0[b])];
+    };
+    auto granted = [&](int b, int add) {   // of a sequence with add > 0
+        const int len = len_s[b];
+        if (!fits(len, add, qs[b + 1])) return 2;
+        const int k = pages(len, add);
+        return k > 0 && (long long)need0[b] + k > popped ? 1 : 0;
+    };
+    const int at = rank * kTabThreads + tid, all = ranks * kTabThreads;
+    for (int b = at; b < n; b += all) {
+        const int add = p.n_new[b], st = add > 0 ? granted(b, add) : 0;
+        p.status[b] = st;
+        p.lens_out[b] = add < 0 ? 0 : st == 0 ? len_s[b] + add : len_s[b];
+    }
+    for (int b = at; b <= n; b += all) p.q_start[b] = qs[b];
+    if (at == 0) *p.n_free_out = n_free_out;
+    for (int f = at; f < popped; f += all) {   // new pages, in order
+        const int b = last_at_most(need0, n, f);
+        const int j = ((len_s[b] + P - 1) >> p.pshift) + f - need0[b];
+        p.block_table[(size_t)b * p.stride + j] = stack(avail - 1 - f);
+    }
+    for (int v = n_free + at; v < n_free_out; v += all) p.free_pages[v] = stack(v);   // what stays of the returned pages
+    // slots, four rows a thread: one search, then forward
+    const int owned = min(qs[n], p.n_tokens);
+    for (int t = 4 * at; t < p.n_tokens; t += 4 * all) {
+        int s4[4] = {-1, -1, -1, -1};
+        if (t < owned) {
+            int b = last_at_most(qs, n, t), st = granted(b, p.n_new[b]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (t + k >= owned) break;
+                if (t + k >= qs[b + 1]) {
+                    do ++b;
+                    while (t + k >= qs[b + 1]);
+                    st = granted(b, p.n_new[b]);
+                }
+                if (st) continue;
+                const int len = len_s[b], pos = len + (t + k - qs[b]), j = pos >> p.pshift, have = (len + P - 1) >> p.pshift;
+                const int page = j < have ? p.block_table[(size_t)b * p.stride + j] : stack(avail - 1 - (need0[b] + j - have));
+                if (page >= 0 && page < p.n_pages) s4[k] = (page << p.pshift) + (pos & (P - 1));
+            }
+        }
+        if (t + 4 <= p.n_tokens && (reinterpret_cast<uintptr_t>(p.slots) & 15) == 0)
+            *reinterpret_cast<int4 *>(p.slots + t) = make_int4(s4[0], s4[1], s4[2], s4[3]);
+        else
+            for (int k = 0; k < 4 && t + k < p.n_tokens; ++k) p.slots[t + k] = s4[k];
+    }
+}
+
+cudaError_t prepare_page_tables()
+{
+    constexpr int most = (4 * KVQ_MAX_PAGED_SEQS + 3) * (int)sizeof(int);
+    static_assert(most <= 100 * 1024, "the sums of every sequence fit in shared memory");
+    return cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+
+cudaError_t launch_page_tables(const TableParams &p, cudaStream_t s, bool pdl)
+{
+    cudaLaunchConfig_t cfg = {};
+    const int ctas = 8;   // the portable cluster size
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kTabThreads);
+    cfg.dynamicSmemBytes = (4 * (size_t)p.n_seqs + 3) * sizeof(int);
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = ctas;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, page_tables_kernel, p);
+}
+
+// ---------------------------------------------------------------------------
+// Append: one warp per (token, kv head) row, as append_kernel; the slot names
+// the tile.
+// ---------------------------------------------------------------------------
+template <int VT, int KT>
+__global__ void __launch_bounds__(128) paged_append_kernel(const PagedRowsParams p)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long row = (long long)blockIdx.x * 4 + warp;
+    const int H = p.pool.n_kv_heads;
+    const int tok = (int)(row / H), h = (int)(row - (long long)tok * H);
+    if (tok >= p.n_tokens) return;
+    const int slot = p.slots[tok];
+    if (slot < 0 || slot >= p.pool.n_slots) return;
+    const size_t src = (size_t)tok * p.stride + (size_t)h * kD;
+    const TokenRow t = quant_token<VT, KT>(p.k16 + src, p.v16 + src, lane);
+    const int place = slot & ((1 << p.pool.pshift) - 1);
+    store_token_paged<VT, KT>(t, place & 15, lane,
+                              tile_of(p.pool, slot >> p.pool.pshift, h, place >> 4, PageTile<VT, KT>::BYTES));
+}
+
+cudaError_t launch_paged_append(const PagedRowsParams &p, int v_type, int k_type, cudaStream_t s, bool pdl)
+{
+    const int grid = (int)(((long long)p.n_tokens * p.pool.n_kv_heads + 3) / 4);
+    void (*fn)(PagedRowsParams) =
+        k_type == KVQ_K_F16 ? (v_type == KVQ_V_Q4_0 ? paged_append_kernel<KVQ_V_Q4_0, KVQ_K_F16> : paged_append_kernel<KVQ_V_Q8_0, KVQ_K_F16>)
+                            : (v_type == KVQ_V_Q4_0 ? paged_append_kernel<KVQ_V_Q4_0, KVQ_K_I8> : paged_append_kernel<KVQ_V_Q8_0, KVQ_K_I8>);
+    return launch_pdl(fn, p, grid, 128, 0, s, pdl);
+}
+
+// ---------------------------------------------------------------------------
+// Gather: one warp per (token, kv head) row, four values a lane.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float half_at(const uint8_t *p)
+{
+    return __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t *>(p)));
+}
+
+template <bool O16>
+__device__ __forceinline__ void put4(void *base, size_t elem, const float (&x)[4])
+{
+    if (O16)
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(base) + elem) = make_uint2(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]));
+    else
+        *reinterpret_cast<float4 *>(static_cast<float *>(base) + elem) = make_float4(x[0], x[1], x[2], x[3]);
+}
+
+template <int VT, int KT, bool O16>
+__global__ void __launch_bounds__(128) paged_gather_kernel(const PagedRowsParams p)
+{
+    using T = PageTile<VT, KT>;
+    pdl_wait();
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long row = (long long)blockIdx.x * 4 + warp;
+    const int H = p.pool.n_kv_heads;
+    const int tok = (int)(row / H), h = (int)(row - (long long)tok * H);
+    if (tok >= p.n_tokens) return;
+    const int slot = p.slots[tok];
+    if (slot < 0 || slot >= p.pool.n_slots) return;
+    const int place = slot & ((1 << p.pool.pshift) - 1), u = place & 15, b = lane >> 3;
+    const uint8_t *tile = tile_of(p.pool, slot >> p.pool.pshift, h, place >> 4, T::BYTES);
+    float x[4];
+    const size_t dst = (size_t)row * kD + 4 * lane;
+    if (KT == KVQ_K_F16) {
+        const float2 lo = __half22float2(*reinterpret_cast<const __half2 *>(tile + k16_tile_off(u, 4 * lane)));
+        const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(tile + k16_tile_off(u, 4 * lane + 2)));
+        x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
+    } else {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(tile + k_tile_off(u, 4 * lane));
+        const float s = half_at(tile + T::KS_OFF + scale_off(u, b));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = (float)((int)(w >> (8 * k) & 0xff) - 128) * s;
+    }
+    put4<O16>(p.k_out, dst, x);
+    const float d = half_at(tile + T::VS_OFF + scale_off(u, b));
+    const uint8_t *vt = tile + T::V_OFF;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (VT == KVQ_V_Q8_0) {
+            x[k] = (float)((int)vt[v8_tile_off(u, 4 * lane + k)] - 128) * d;
+        } else {   // element e of block b: byte e % 16, low nibble below 16
+            const int e = (4 * lane + k) & 31;
+            const int byte = vt[v4_tile_off(u, 16 * b + (e & 15))];
+            x[k] = (float)(((e < 16) ? byte & 15 : byte >> 4) - 8) * d;
+        }
+    }
+    put4<O16>(p.v_out, dst, x);
+}
+
+template <bool O16>
+static cudaError_t gather_t(const PagedRowsParams &p, int v_type, int k_type, cudaStream_t s, bool pdl)
+{
+    const int grid = (int)(((long long)p.n_tokens * p.pool.n_kv_heads + 3) / 4);
+    void (*fn)(PagedRowsParams) =
+        k_type == KVQ_K_F16 ? (v_type == KVQ_V_Q4_0 ? paged_gather_kernel<KVQ_V_Q4_0, KVQ_K_F16, O16> : paged_gather_kernel<KVQ_V_Q8_0, KVQ_K_F16, O16>)
+                            : (v_type == KVQ_V_Q4_0 ? paged_gather_kernel<KVQ_V_Q4_0, KVQ_K_I8, O16> : paged_gather_kernel<KVQ_V_Q8_0, KVQ_K_I8, O16>);
+    return launch_pdl(fn, p, grid, 128, 0, s, pdl);
+}
+
+cudaError_t launch_paged_gather(const PagedRowsParams &p, int v_type, int k_type, int out_type, cudaStream_t s, bool pdl)
+{
+    return out_type == KVQ_OUT_F16 ? gather_t<true>(p, v_type, k_type, s, pdl) : gather_t<false>(p, v_type, k_type, s, pdl);
+}
+
+// ---------------------------------------------------------------------------
+// Combine: the pieces of a row tile that several CTAs of the attention launch
+// attended.  Block i shares the merge of the cut tile its CTA's slot 1 began
+// and of the one its slot 0 went on with, so a tile cut into np pieces is
+// merged by np blocks.  Few pieces: a warp per row, the pieces one after
+// another.  Many: a block per row, the pieces dealt to the warps, merged in
+// warp order.  Both orders are fixed by the lengths alone.
+// ---------------------------------------------------------------------------
+constexpr int kPcWarps = 8;
+constexpr int kPcFew = 8;   // pieces up to which a warp takes a row alone
+
+struct Merged {
+    float m, w;
+    float4 o;
+};
+
+// Pieces first, first + step, ... of a row: running maximum, weight and sum.
+__device__ __forceinline__ Merged merge_pieces(const PagedAttnParams &p, const PagedCut &c, int rows, int r, int first,
+                                               int step, int lane)
+{
+    Merged a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    bool poisoned = false;
+    for (int k0 = first; k0 < c.np; k0 += 4 * step) {
+        float lv[4];
+        float4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int j = k0 + k * step;
+            lv[k] = -INFINITY;
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (j < c.np) {
+                const size_t at = ((size_t)(c.c0 + j) * 2 + (j == 0 ? 1 : 0)) * rows + r;
+                lv[k] = p.ws_lse[at];
+                v[k] = reinterpret_cast<const float4 *>(p.ws_o + at * kD)[lane];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            poisoned |= lv[k] != lv[k];
+            if (!(lv[k] > -INFINITY)) continue;
+            const float mx = fmaxf(a.m, lv[k]);
+            const float f = (a.m == -INFINITY) ? 0.f : expf(a.m - mx), w = expf(lv[k] - mx);
+            a.w = fmaf(a.w, f, w);
+            a.o.x = fmaf(w, v[k].x, a.o.x * f);
+            a.o.y = fmaf(w, v[k].y, a.o.y * f);
+            a.o.z = fmaf(w, v[k].z, a.o.z * f);
+            a.o.w = fmaf(w, v[k].w, a.o.w * f);
+            a.m = mx;
+        }
+    }
+    if (poisoned) {   // a piece whose CTA lost a copy: the row is NaN
+        a.m = INFINITY;
+        a.w = __int_as_float(0x7fc00000);
+    }
+    return a;
+}
+
+template <bool O16>
+__device__ __forceinline__ void put_merged(const PagedAttnParams &p, size_t row, const Merged &a, int lane)
+{
+    const bool any = !(a.w <= 0.f);
+    const float inv = any ? 1.f / a.w : 0.f;
+    const float x[4] = {a.o.x * inv, a.o.y * inv, a.o.z * inv, a.o.w * inv};
+    put4<O16>(p.out, row * kD + 4 * lane, x);
+    if (lane == 0 && p.lse) p.lse[row] = any ? a.m + logf(a.w) : -INFINITY;
+}
+
+template <bool O16>
+__global__ void __launch_bounds__(kPcWarps * 32) paged_combine_kernel(const __grid_constant__ PagedAttnParams p, int rows)
+{
+    __shared__ Merged part[kPcWarps][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_trigger();
+    for (int slot = 0; slot < 2; ++slot) {
+        const PagedCut c = p.cuts[(size_t)blockIdx.x * 2 + slot];
+        if (c.np < 2) continue;   // block-uniform
+        const int h = c.h_rt & 255, rt = c.h_rt >> 8, share = (int)blockIdx.x - c.c0;
+        int t0, n, len;
+        seq_shape(p, c.b, t0, n, len);
+        const int gb = p.grp_begin[h], gsz = p.grp_begin[h + 1] - gb;
+        const int row0 = rt * rows, R = min(rows, n * gsz - row0);
+        auto out_row = [&](int r) {
+            return (size_t)(t0 + (row0 + r) / gsz) * p.n_q_heads + p.grp_q[gb + (row0 + r) % gsz];
+        };
+        if (c.np <= kPcFew) {
+            for (int r = share * kPcWarps + warp; r < R; r += c.np * kPcWarps)
+                put_merged<O16>(p, out_row(r), merge_pieces(p, c, rows, r, 0, 1, lane), lane);
+        } else {
+            for (int r = share; r < R; r += c.np) {
+                part[warp][lane] = merge_pieces(p, c, rows, r, warp, kPcWarps, lane);
+                __syncthreads();
+                if (warp == 0) {
+                    Merged t = part[0][lane];
+                    float M = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < kPcWarps; ++w) M = fmaxf(M, part[w][lane].m);
+                    t.m = M;
+                    t.w = 0.f;
+                    t.o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int w = 0; w < kPcWarps; ++w) {
+                        const Merged q = part[w][lane];
+                        if (q.m == -INFINITY) continue;
+                        const float f = expf(q.m - M);
+                        t.w = fmaf(q.w, f, t.w);
+                        t.o.x = fmaf(q.o.x, f, t.o.x);
+                        t.o.y = fmaf(q.o.y, f, t.o.y);
+                        t.o.z = fmaf(q.o.z, f, t.o.z);
+                        t.o.w = fmaf(q.o.w, f, t.o.w);
+                    }
+                    put_merged<O16>(p, out_row(r), t, lane);
+                }
+                __syncthreads();
+            }
+        }
+    }
+}
+
+cudaError_t launch_paged_combine(const PagedAttnParams &p, int n_ctas, int tile_rows, int out_type, cudaStream_t s, bool pdl)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n_ctas);
+    cfg.blockDim = dim3(kPcWarps * 32);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (out_type == KVQ_OUT_F16) return cudaLaunchKernelEx(&cfg, paged_combine_kernel<true>, p, tile_rows);
+    return cudaLaunchKernelEx(&cfg, paged_combine_kernel<false>, p, tile_rows);
+}
+
+}  // namespace kvq

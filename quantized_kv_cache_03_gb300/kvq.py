@@ -1,4 +1,5 @@
-"""ctypes binding of libkvq.so (include/kvq.h): argument marshalling only.
+"""ctypes binding of libkvq.so (include/kvq.h, and include/kvq_paged.h for the
+paged cache): argument marshalling only.
 
 Every step of the decode path runs in the library's CUDA kernels; torch only
 provides device memory and the stream handle.  Importing this module does not
@@ -10,7 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from ctypes import POINTER, c_float, c_int32, c_size_t, c_void_p
+from ctypes import POINTER, c_float, c_int32, c_int64, c_size_t, c_void_p
 
 import torch
 
@@ -37,6 +38,12 @@ EXPORTED = ("kvq_append", "kvq_decode_attn", "kvq_decode_workspace_size", "kvq_d
             "kvq_decode_multi_workspace_size", "kvq_decode_attn_noalloc", "kvq_wait_timeouts",
             "kvq_reset_wait_timeouts", "kvq_status_string", "kvq_debug_qk", "kvq_debug_lose_stage",
             "kvq_debug_plan", "kvq_layout_model_default", "kvq_layout_cost", "kvq_choose_layout")
+EXPORTED_PAGED = ("kvq_page_bytes", "kvq_page_tables", "kvq_paged_append", "kvq_paged_gather", "kvq_paged_attn",
+                  "kvq_paged_attn_workspace_size")
+OUT_F32 = 0    # type of computed values
+OUT_F16 = 1
+MAX_PAGED_SEQS = 4096
+PAGE_RELEASE = -1
 MAX_CALLS = 16
 MAX_T_Q = 4096
 MAX_T_Q_APPEND = 8
@@ -69,6 +76,19 @@ class KvqLayoutModel(ctypes.Structure):
 class KvqPlanLaunch(ctypes.Structure):
     _fields_ = [("kernel", c_int32), ("n_tiles8", c_int32), ("warps", c_int32), ("chunk", c_int32),
                 ("chunk0", c_int32), ("n_ctas", c_int32), ("n_rows", c_int32)]
+
+
+class KvqPages(ctypes.Structure):
+    _fields_ = [("n_pages", c_int32), ("page_tokens", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32),
+                ("k_type", c_int32), ("v_type", c_int32), ("data", c_void_p)]
+
+
+class KvqPagedDesc(ctypes.Structure):
+    _fields_ = [("pages", POINTER(KvqPages)), ("q16", c_void_p), ("q_stride", c_int64), ("n_q_heads", c_int32),
+                ("n_tokens", c_int32), ("n_seqs", c_int32), ("max_q", c_int32), ("q_start", c_void_p),
+                ("seq_lens", c_void_p), ("block_table", c_void_p), ("table_stride", c_int32),
+                ("max_blocks", c_int32), ("causal", c_int32), ("head_map", POINTER(c_int32)), ("sm_scale", c_float),
+                ("out_type", c_int32), ("out", c_void_p), ("lse", c_void_p)]
 
 
 class KvqError(RuntimeError):
@@ -130,6 +150,22 @@ def load():
             lib.kvq_debug_plan.argtypes = [c_int32, POINTER(KvqDecodeDesc), c_int32, POINTER(c_int32),
                                            POINTER(KvqPlanLaunch), c_int32, POINTER(c_int32), POINTER(c_size_t),
                                            POINTER(c_int32)]
+            lib.kvq_page_bytes.restype = c_int32
+            lib.kvq_page_bytes.argtypes = [POINTER(KvqPages), POINTER(c_size_t)]
+            lib.kvq_page_tables.restype = c_int32
+            lib.kvq_page_tables.argtypes = [c_int32, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
+                                            c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
+                                            c_int32, c_void_p, c_void_p]
+            lib.kvq_paged_append.restype = c_int32
+            lib.kvq_paged_append.argtypes = [POINTER(KvqPages), c_void_p, c_void_p, c_int64, c_void_p, c_int32,
+                                             c_void_p]
+            lib.kvq_paged_gather.restype = c_int32
+            lib.kvq_paged_gather.argtypes = [POINTER(KvqPages), c_void_p, c_int32, c_int32, c_void_p, c_void_p,
+                                             c_void_p]
+            lib.kvq_paged_attn.restype = c_int32
+            lib.kvq_paged_attn.argtypes = [POINTER(KvqPagedDesc), c_void_p, c_size_t, c_void_p]
+            lib.kvq_paged_attn_workspace_size.restype = c_int32
+            lib.kvq_paged_attn_workspace_size.argtypes = [POINTER(KvqPagedDesc), POINTER(c_size_t)]
             _lib = lib
     return _lib
 
@@ -483,3 +519,218 @@ def kvq_debug_plan(calls, n_sms: int, ctas_per_sm=(1, 2, 2, 2), max_out: int = 6
     launches = [dict(kernel=PLAN_KERNELS[r.kernel], n_tiles8=r.n_tiles8, warps=r.warps, chunk=r.chunk,
                      chunk0=r.chunk0, n_ctas=r.n_ctas, n_rows=r.n_rows) for r in out[:min(n_out.value, max_out)]]
     return launches, int(ws.value)
+
+
+# ------------------------------------------------------- the paged cache --
+# (include/kvq_paged.h).  Each operator comes as a prepared call (a class whose
+# arguments are checked and marshalled once; calling it only passes the stream,
+# and device contents are read when the kernels run) and as a function that
+# makes one and calls it.
+
+def _check(t, name, dtype, device, shape=None, contiguous=True):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise ValueError("%s must be a %s tensor" % (name, dtype))
+    if t.device != device:
+        raise ValueError("%s is on %s, the call's tensors are on %s" % (name, t.device, device))
+    if shape is not None and (t.dim() != len(shape) or any(b is not None and a != b for a, b in zip(t.shape, shape))):
+        raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape), tuple(shape)))
+    if contiguous and not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _rows_stride(t, name, heads, device):
+    """Token stride of an fp16 [tokens][heads][128] tensor whose rows are whole."""
+    _check(t, name, torch.float16, device, (None, heads, HEAD_DIM), contiguous=False)
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != HEAD_DIM):
+        raise ValueError("%s: the heads of a token must be contiguous" % name)
+    return t.stride(0) if t.shape[0] > 1 else heads * HEAD_DIM
+
+
+class _PreparedCall:
+    """A library call with its arguments marshalled; stream: None = torch's
+    current stream of the tensors' device, which must be the current device."""
+    name = ""
+
+    def _bind(self, device, *args):
+        self.device = device
+        self._fn = getattr(load(), self.name)
+        self._args = args
+
+    def __call__(self, stream=None):
+        if self.device.type == "cuda" and self.device.index != torch.cuda.current_device():
+            raise ValueError("%s: the tensors are on %s, the current device is cuda:%d"
+                             % (self.name, self.device, torch.cuda.current_device()))
+        st = self._fn(*self._args, _stream(stream))
+        if st:
+            raise KvqError(st, self.name)
+
+
+class PagePool:
+    """A pool of pages (include/kvq_paged.h): `data`, a uint8 device tensor of
+    n_pages pages, given or allocated."""
+
+    def __init__(self, n_pages: int, page_tokens: int, n_kv_heads: int, v_type: int, k_type: int = K_I8,
+                 head_dim: int = HEAD_DIM, device=None, data: torch.Tensor | None = None):
+        self.desc = KvqPages(n_pages, page_tokens, n_kv_heads, head_dim, k_type, v_type, None)
+        self.n_pages, self.page_tokens, self.n_kv_heads = n_pages, page_tokens, n_kv_heads
+        self.k_type, self.v_type = k_type, v_type
+        self.page_bytes = page_bytes(self.desc)
+        n = n_pages * self.page_bytes
+        if data is None:
+            device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+            data = torch.empty(n, dtype=torch.uint8, device=device)
+        _check(data, "data", torch.uint8, data.device)
+        if data.numel() != n:
+            raise ValueError("data has %d bytes, the pool %d" % (data.numel(), n))
+        self.data, self.device = data, data.device
+        self.desc.data = data.data_ptr()
+
+
+def page_bytes(desc: KvqPages) -> int:
+    """kvq_page_bytes of include/kvq_paged.h."""
+    n = c_size_t(0)
+    st = load().kvq_page_bytes(ctypes.byref(desc), ctypes.byref(n))
+    if st:
+        raise KvqError(st, "kvq_page_bytes")
+    return int(n.value)
+
+
+def _table(t, n_seqs, device):
+    """(stride, columns) of an int32 block table whose rows are whole."""
+    _check(t, "block_table", torch.int32, device, (n_seqs, None), contiguous=False)
+    if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("block_table: the entries of a row must be contiguous")
+    return (t.stride(0) if n_seqs > 1 else t.shape[1]), t.shape[1]
+
+
+class PageTablesCall(_PreparedCall):
+    """kvq_page_tables of include/kvq_paged.h, prepared.  lens, n_new, lens_out,
+    status: int32 [n_seqs]; free_pages int32 [n_pages]; n_free, n_free_out int32
+    [1]; block_table int32 [n_seqs][max_blocks] (rows may be strided); q_start
+    int32 [n_seqs + 1]; slots int32 [n_tokens].  lens_out may be lens and
+    n_free_out may be n_free."""
+    name = "kvq_page_tables"
+
+    def __init__(self, page_tokens: int, n_pages: int, lens, n_new, free_pages, n_free, block_table, lens_out,
+                 n_free_out, q_start, slots, status):
+        n, dev = lens.shape[0], lens.device
+        for t, what, size in ((lens, "lens", n), (n_new, "n_new", n), (free_pages, "free_pages", n_pages),
+                              (n_free, "n_free", 1), (lens_out, "lens_out", n), (n_free_out, "n_free_out", 1),
+                              (q_start, "q_start", n + 1), (slots, "slots", None), (status, "status", n)):
+            _check(t, what, torch.int32, dev, (size,))
+        stride, cols = _table(block_table, n, dev)
+        self._keep = (lens, n_new, free_pages, n_free, block_table, lens_out, n_free_out, q_start, slots, status)
+        self._bind(dev, n, page_tokens, n_pages, _ptr(lens), _ptr(n_new), _ptr(free_pages), _ptr(n_free),
+                   _ptr(block_table), stride, cols, _ptr(lens_out), _ptr(n_free_out), _ptr(q_start), _ptr(slots),
+                   slots.shape[0], _ptr(status))
+
+
+def kvq_page_tables(page_tokens: int, n_pages: int, lens, n_new, free_pages, n_free, block_table, lens_out, n_free_out,
+                    q_start, slots, status, stream=None) -> None:
+    """kvq_page_tables of include/kvq_paged.h (arguments as PageTablesCall)."""
+    PageTablesCall(page_tokens, n_pages, lens, n_new, free_pages, n_free, block_table, lens_out, n_free_out, q_start,
+                   slots, status)(stream)
+
+
+class PagedAppendCall(_PreparedCall):
+    """kvq_paged_append of include/kvq_paged.h, prepared.  k16, v16: fp16
+    [tokens][kv heads][128] with the same token stride (views into a fused
+    projection's output will do); slots int32 [tokens]."""
+    name = "kvq_paged_append"
+
+    def __init__(self, pool: PagePool, k16, v16, slots):
+        n = slots.shape[0]
+        _check(slots, "slots", torch.int32, pool.device, (n,))
+        stride = _rows_stride(k16, "k16", pool.n_kv_heads, pool.device)
+        if _rows_stride(v16, "v16", pool.n_kv_heads, pool.device) != stride or k16.shape[0] != n or v16.shape[0] != n:
+            raise ValueError("k16, v16 and slots must have one row per token and k16, v16 the same token stride")
+        self._keep = (pool, k16, v16, slots)
+        self._bind(pool.device, ctypes.byref(pool.desc), _ptr(k16), _ptr(v16), stride, _ptr(slots), n)
+
+
+def kvq_paged_append(pool: PagePool, k16, v16, slots, stream=None) -> None:
+    """kvq_paged_append of include/kvq_paged.h (arguments as PagedAppendCall)."""
+    PagedAppendCall(pool, k16, v16, slots)(stream)
+
+
+def _out_type(t, name):
+    if t.dtype not in (torch.float32, torch.float16):
+        raise ValueError("%s must be float32 or float16" % name)
+    return OUT_F16 if t.dtype == torch.float16 else OUT_F32
+
+
+class PagedGatherCall(_PreparedCall):
+    """kvq_paged_gather of include/kvq_paged.h, prepared.  slots int32 [tokens];
+    k_out, v_out fp32 or fp16 [tokens][kv heads][128]."""
+    name = "kvq_paged_gather"
+
+    def __init__(self, pool: PagePool, slots, k_out, v_out):
+        n = slots.shape[0]
+        _check(slots, "slots", torch.int32, pool.device, (n,))
+        ot = _out_type(k_out, "k_out")
+        for t, what in ((k_out, "k_out"), (v_out, "v_out")):
+            _check(t, what, k_out.dtype, pool.device, (n, pool.n_kv_heads, HEAD_DIM))
+        self._keep = (pool, slots, k_out, v_out)
+        self._bind(pool.device, ctypes.byref(pool.desc), _ptr(slots), n, ot, _ptr(k_out), _ptr(v_out))
+
+
+def kvq_paged_gather(pool: PagePool, slots, k_out, v_out, stream=None) -> None:
+    """kvq_paged_gather of include/kvq_paged.h (arguments as PagedGatherCall)."""
+    PagedGatherCall(pool, slots, k_out, v_out)(stream)
+
+
+class PagedAttnCall(_PreparedCall):
+    """kvq_paged_attn of include/kvq_paged.h, prepared.  q16: fp16
+    [tokens][q heads][128] (tokens may be strided); q_start int32 [n_seqs + 1];
+    max_q: the most rows one sequence has; seq_lens int32 [n_seqs]; block_table
+    int32 [n_seqs][max_blocks] (rows may be strided); out fp32 or fp16
+    [tokens][q heads][128]; lse fp32 [tokens][q heads] or None; workspace: a
+    uint8 device tensor of workspace_size() bytes (None: one is allocated with
+    the call and kept with it; calls that may overlap need one each)."""
+    name = "kvq_paged_attn"
+
+    def __init__(self, pool: PagePool, q16, q_start, max_q: int, seq_lens, block_table, causal: bool, sm_scale: float,
+                 out, lse=None, head_map=None, workspace=None):
+        n, dev = seq_lens.shape[0], pool.device
+        heads = q16.shape[1] if q16.dim() == 3 else 0
+        stride = _rows_stride(q16, "q16", heads, dev)
+        tokens = q16.shape[0]
+        _check(seq_lens, "seq_lens", torch.int32, dev, (n,))
+        _check(q_start, "q_start", torch.int32, dev, (n + 1,))
+        ts, cols = _table(block_table, n, dev)
+        ot = _out_type(out, "out")
+        _check(out, "out", out.dtype, dev, (tokens, heads, HEAD_DIM))
+        if lse is not None:
+            _check(lse, "lse", torch.float32, dev, (tokens, heads))
+        if head_map is not None and len(head_map) != heads:
+            raise ValueError("head_map must list a kv head for each query head")
+        hm = None if head_map is None else _i32(head_map)
+        self.desc = KvqPagedDesc(ctypes.pointer(pool.desc), q16.data_ptr(), stride, heads, tokens, n, int(max_q),
+                                 q_start.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), ts, cols,
+                                 int(causal), None if hm is None else ctypes.cast(hm, POINTER(c_int32)),
+                                 float(sm_scale), ot, out.data_ptr(), None if lse is None else lse.data_ptr())
+        if workspace is None:
+            size = self.workspace_size()
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+        else:
+            _check(workspace, "workspace", torch.uint8, dev)
+        self._keep = (pool, q16, q_start, seq_lens, block_table, out, lse, hm, workspace)
+        self._bind(dev, ctypes.byref(self.desc), _ptr(workspace), 0 if workspace is None else workspace.numel())
+
+    def workspace_size(self) -> int:
+        size = c_size_t(0)
+        st = load().kvq_paged_attn_workspace_size(ctypes.byref(self.desc), ctypes.byref(size))
+        if st:
+            raise KvqError(st, "kvq_paged_attn_workspace_size")
+        return int(size.value)
+
+
+def kvq_paged_attn(pool: PagePool, q16, q_start, max_q: int, seq_lens, block_table, causal: bool, sm_scale: float, out,
+                   lse=None, head_map=None, workspace=None, stream=None) -> None:
+    """kvq_paged_attn of include/kvq_paged.h (arguments as PagedAttnCall)."""
+    call = PagedAttnCall(pool, q16, q_start, max_q, seq_lens, block_table, causal, sm_scale, out, lse, head_map,
+                         workspace)
+    call(stream)
+    if workspace is None and call._keep[-1] is not None and stream is not None:
+        # the workspace made here goes back to torch now: not before `stream` is done with it
+        call._keep[-1].record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
