@@ -16,7 +16,7 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkvq.so")
 SOURCES = ["kvq_api.cu", "kvq_small.cu", "kvq_attn_q4.cu", "kvq_attn_q8.cu", "kvq_prefill_q4.cu",
            "kvq_prefill_q8.cu", "kvq_paged_api.cu", "kvq_paged_small.cu", "kvq_paged_attn_q4.cu",
-           "kvq_paged_attn_q8.cu"]
+           "kvq_paged_attn_q8.cu", "kvq_paged_chunk_q4.cu", "kvq_paged_chunk_q8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

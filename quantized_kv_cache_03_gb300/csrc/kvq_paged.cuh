@@ -89,6 +89,8 @@ struct PagedRowsParams {      // append and gather
 
 // ------------------------------------------------------- paged attention --
 constexpr int kStagePos = 32;           // positions per work unit ("stage")
+constexpr int kChunkPositions = 128;    // the chunk kernel: positions per tile,
+constexpr int kChunkMinTiles = 3;       // and the least piece in tiles
 constexpr int kPagedMinStages = 4;      // a CTA's least piece of the line: one stage per warp
 
 // A query-row tile of one kv head that several CTAs attend: what the combine
@@ -112,6 +114,7 @@ struct PagedAttnParams {
     unsigned int *timeouts;
     int n_seqs, n_tokens, max_q, n_q_heads, table_stride, max_blocks, causal;
     int gmax;                           // query heads of the busiest kv head
+    int uniform;                        // every kv head has gmax query heads
     int min_rows, max_rows;             // sequences with min_rows <= rows <= max_rows per kv head are this launch's
     float qk_scale_log2;
     uint16_t grp_begin[KVQ_MAX_HEADS + 1];   // kv head h owns grp_q[grp_begin[h] .. grp_begin[h + 1])
@@ -149,6 +152,13 @@ cudaError_t launch_paged_q4(const PagedAttnParams &p, int nt, int k_type, int ou
                             bool pdl);
 cudaError_t launch_paged_q8(const PagedAttnParams &p, int nt, int k_type, int out_type, int n_ctas, cudaStream_t s,
                             bool pdl);
+
+// Chunk attention on tcgen05 (kvq_paged_chunk_q4.cu / _q8.cu), int8 K.
+constexpr int kChunkRows = 128;
+cudaError_t prepare_chunk_q4();
+cudaError_t prepare_chunk_q8();
+cudaError_t launch_chunk_q4(const PagedAttnParams &p, int out_type, int n_ctas, cudaStream_t s, bool pdl);
+cudaError_t launch_chunk_q8(const PagedAttnParams &p, int out_type, int n_ctas, cudaStream_t s, bool pdl);
 
 // The current device's SM count and the address of the bounded waits' counter
 // (kvq_api.cu).

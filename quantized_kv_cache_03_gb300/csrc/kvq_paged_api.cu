@@ -46,6 +46,8 @@ kvq_status paged_setup(PagedDevice **out, int *n_sms, unsigned int **timeouts)
                     if (e == cudaSuccess) e = prepare_paged_q4(nt, kt, ot, &d.ctas[kt][KVQ_V_Q4_0][nt][ot]);
                     if (e == cudaSuccess) e = prepare_paged_q8(nt, kt, ot, &d.ctas[kt][KVQ_V_Q8_0][nt][ot]);
                 }
+        if (e == cudaSuccess) e = prepare_chunk_q4();
+        if (e == cudaSuccess) e = prepare_chunk_q8();
         if (e != cudaSuccess) {
             cudaGetLastError();
             return KVQ_ERR_CUDA;
@@ -102,14 +104,32 @@ bool table_ok(int stride, int max_blocks, int page_tokens)
 }
 
 // ---- attention ----
+// One launch and its combine: CTAs, the row tile, and where its pieces lie in the workspace.
+struct Part {
+    int n_ctas = 0, rows = 0;
+    size_t cut_off = 0, lse_off = 0, o_off = 0;
+};
+
 struct AttnPlan {
-    int nt;          // 8-row tiles per CTA of the row-tile kernel
-    int gmax;        // query heads of the busiest kv head
-    int n_ctas;
-    size_t lse_off, o_off, bytes;
+    int nt;              // 8-row tiles per CTA of the row-tile kernel
+    int gmax;            // query heads of the busiest kv head
+    int uniform;
+    int chunk_rows;      // sequences with at least this many rows per kv head go to the chunk kernel
+    Part tile, chunk;    // the two launches (n_ctas 0: not made)
+    size_t bytes;
     uint16_t grp_begin[KVQ_MAX_HEADS + 1];
     uint8_t grp_q[KVQ_MAX_HEADS];
 };
+
+// Rows per kv head from which a sequence goes to the chunk kernel (int8 K);
+// KVQ_TC_ROWS and KVQ_PREFILL steer it as they steer kvq_decode_attn's.
+constexpr int kChunkMinRows = KVQ_MAX_ROWS + 1;
+int chunk_min_rows(const kvq_pages *g)
+{
+    const char *off = std::getenv("KVQ_PREFILL"), *e = std::getenv("KVQ_TC_ROWS");
+    if (g->k_type != KVQ_K_I8 || (off && off[0] == '0')) return INT_MAX;
+    return e && std::atoi(e) > 0 ? std::atoi(e) : kChunkMinRows;
+}
 
 kvq_status check_attn(const kvq_paged_desc *a, AttnPlan &pl)
 {
@@ -138,26 +158,48 @@ kvq_status check_attn(const kvq_paged_desc *a, AttnPlan &pl)
             if (kv[h] == k) pl.grp_q[n++] = (uint8_t)h;
     }
     pl.grp_begin[H] = (uint16_t)n;
+    pl.uniform = 1;
+    for (int k = 0; k < H; ++k) pl.uniform = pl.uniform && cnt[k] == pl.gmax;
     if (a->n_tokens > 0 && a->n_seqs > 0 && (a->max_q < 1 || a->max_q > a->n_tokens)) return KVQ_ERR_INVALID_ARG;
     return KVQ_OK;
 }
 
 bool idle(const kvq_paged_desc *a) { return a->n_tokens == 0 || a->n_seqs == 0; }
 
+// No more CTAs than the longest possible batch has pieces of `least` units of
+// `unit` positions.
+void size_part(const kvq_paged_desc *a, const AttnPlan &pl, Part &pt, int ctas, int rows, int unit, int least, size_t &at)
+{
+    const long long tiles = ((long long)a->max_q * pl.gmax + rows - 1) / rows;
+    const long long len = ((long long)a->max_blocks * a->pages->page_tokens + unit - 1) / unit;
+    const double most = (double)a->n_seqs * a->pages->n_kv_heads * tiles * (len > 1 ? len : 1) / least + 1.0;
+    pt.n_ctas = most < ctas ? (int)most : ctas;
+    pt.rows = rows;
+    const size_t slots = (size_t)pt.n_ctas * 2;
+    auto take = [&](size_t n) {
+        const size_t off = at;
+        at += (n + 255) / 256 * 256;
+        return off;
+    };
+    pt.cut_off = take(slots * sizeof(PagedCut));
+    pt.lse_off = take(slots * rows * sizeof(float));
+    pt.o_off = take(slots * rows * kD * sizeof(float));
+}
+
 void plan_attn(const kvq_paged_desc *a, const PagedDevice *dev, int n_sms, AttnPlan &pl)
 {
     const kvq_pages *g = a->pages;
-    pl.nt = (long long)a->max_q * pl.gmax <= 8 ? 1 : 2;
-    pl.n_ctas = n_sms * (dev->ctas[g->k_type][g->v_type][pl.nt][a->out_type] > 0 ? dev->ctas[g->k_type][g->v_type][pl.nt][a->out_type] : 1);
-    // no more CTAs than the longest possible batch has pieces
-    const long long tiles = ((long long)a->max_q * pl.gmax + 8 * pl.nt - 1) / (8 * pl.nt);
-    const long long st = ((long long)a->max_blocks * g->page_tokens + kStagePos - 1) / kStagePos;
-    const double most = (double)a->n_seqs * g->n_kv_heads * tiles * (st > 1 ? st : 1) / kPagedMinStages + 1.0;
-    if (most < pl.n_ctas) pl.n_ctas = (int)most;
-    const size_t slots = (size_t)pl.n_ctas * 2, rows = 8 * pl.nt;
-    pl.lse_off = (slots * sizeof(PagedCut) + 255) / 256 * 256;
-    pl.o_off = (pl.lse_off + slots * rows * sizeof(float) + 255) / 256 * 256;
-    pl.bytes = pl.o_off + slots * rows * kD * sizeof(float);
+    const long long rows = (long long)a->max_q * pl.gmax;   // most rows of a sequence per kv head
+    pl.chunk_rows = chunk_min_rows(g);
+    pl.bytes = 0;
+    pl.tile = pl.chunk = Part();
+    if (pl.chunk_rows > 1) {
+        const long long most = rows < pl.chunk_rows ? rows : pl.chunk_rows - 1;
+        pl.nt = most <= 8 ? 1 : 2;
+        const int per_sm = dev->ctas[g->k_type][g->v_type][pl.nt][a->out_type];
+        size_part(a, pl, pl.tile, n_sms * (per_sm > 0 ? per_sm : 1), 8 * pl.nt, kStagePos, kPagedMinStages, pl.bytes);
+    }
+    if (rows >= pl.chunk_rows) size_part(a, pl, pl.chunk, n_sms, kChunkRows, kChunkPositions, kChunkMinTiles, pl.bytes);
 }
 
 }  // namespace
@@ -291,10 +333,6 @@ kvq_status kvq_paged_attn(const kvq_paged_desc *a, void *workspace, size_t works
     p.block_table = a->block_table;
     p.out = a->out;
     p.lse = a->lse;
-    char *w = static_cast<char *>(workspace);
-    p.cuts = reinterpret_cast<PagedCut *>(w);
-    p.ws_lse = reinterpret_cast<float *>(w + pl.lse_off);
-    p.ws_o = reinterpret_cast<float *>(w + pl.o_off);
     p.timeouts = timeouts;
     p.n_seqs = a->n_seqs;
     p.n_tokens = a->n_tokens;
@@ -304,17 +342,36 @@ kvq_status kvq_paged_attn(const kvq_paged_desc *a, void *workspace, size_t works
     p.max_blocks = a->max_blocks;
     p.causal = a->causal ? 1 : 0;
     p.gmax = pl.gmax;
-    p.min_rows = 1;
-    p.max_rows = INT_MAX;
+    p.uniform = pl.uniform;
     p.qk_scale_log2 = a->sm_scale * 1.4426950408889634f;
     std::memcpy(p.grp_begin, pl.grp_begin, sizeof(p.grp_begin));
     std::memcpy(p.grp_q, pl.grp_q, sizeof(p.grp_q));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool pdl = pdl_on();
     const kvq_pages *g = a->pages;
-    cudaError_t e = g->v_type == KVQ_V_Q4_0 ? launch_paged_q4(p, pl.nt, g->k_type, a->out_type, pl.n_ctas, s, pdl)
-                                            : launch_paged_q8(p, pl.nt, g->k_type, a->out_type, pl.n_ctas, s, pdl);
-    if (e == cudaSuccess && pl.n_ctas > 1) e = launch_paged_combine(p, pl.n_ctas, 8 * pl.nt, a->out_type, s, pdl);
+    const bool q4 = g->v_type == KVQ_V_Q4_0;
+    auto pieces = [&](const Part &pt) {
+        char *w = static_cast<char *>(workspace);
+        p.cuts = reinterpret_cast<PagedCut *>(w + pt.cut_off);
+        p.ws_lse = reinterpret_cast<float *>(w + pt.lse_off);
+        p.ws_o = reinterpret_cast<float *>(w + pt.o_off);
+    };
+    cudaError_t e = cudaSuccess;
+    if (pl.tile.n_ctas > 0) {
+        pieces(pl.tile);
+        p.min_rows = 1;
+        p.max_rows = pl.chunk_rows - 1;
+        e = q4 ? launch_paged_q4(p, pl.nt, g->k_type, a->out_type, pl.tile.n_ctas, s, pdl)
+               : launch_paged_q8(p, pl.nt, g->k_type, a->out_type, pl.tile.n_ctas, s, pdl);
+        if (e == cudaSuccess && pl.tile.n_ctas > 1) e = launch_paged_combine(p, pl.tile.n_ctas, pl.tile.rows, a->out_type, s, pdl);
+    }
+    if (e == cudaSuccess && pl.chunk.n_ctas > 0) {
+        pieces(pl.chunk);
+        p.min_rows = pl.chunk_rows;
+        p.max_rows = INT_MAX;
+        e = q4 ? launch_chunk_q4(p, a->out_type, pl.chunk.n_ctas, s, pdl) : launch_chunk_q8(p, a->out_type, pl.chunk.n_ctas, s, pdl);
+        if (e == cudaSuccess && pl.chunk.n_ctas > 1) e = launch_paged_combine(p, pl.chunk.n_ctas, pl.chunk.rows, a->out_type, s, pdl);
+    }
     return done(e);
 }
 

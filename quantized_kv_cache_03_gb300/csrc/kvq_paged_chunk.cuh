@@ -1,0 +1,804 @@
+// kvq_paged_chunk.cuh -- attention of long query chunks over the paged cache
+// (int8 K) on the 5th-generation tensor cores (tcgen05, accumulators in TMEM).
+//
+// The line of work and its split over persistent CTAs are those of
+// kvq_paged_attn.cuh, in KV tiles of 128 positions of one 128-row tile of one kv
+// head; under the causal mask a row tile counts the tiles its last row sees.
+// One CTA per SM, 24 warps:
+//   0-7   softmax, two groups of four warps, a thread one query row (its TMEM
+//         lane): group g takes every other tile.  It quantizes half of the query
+//         row into TMEM; of a tile it takes the row's maximum (first pass over
+//         S), then p = 2^(s - m) in 32-position chunks, which overwrite S.  The
+//         row's zero point m is handed from tile to tile through shared memory.
+//         At the end of a piece each group writes half of O out.
+//   8-11  K converters: k/2 = code * (scale/2) as an fp16 high and low part.
+//   12-19 V converters: v/2 likewise, turned to [dim][position].
+//   20    QK, 21 P.V: one thread each issues and waits.
+//   22    the bulk copies of 64-position half tiles, three ahead.
+//   23    walks the CTA's pieces of the line and hands them out as records.
+// Tensor memory: S of two tiles (128 columns each), O, the query's high and low
+// parts.  Shared memory: K and V operands of two half tiles.
+// QK: S = Qh Kh + Ql Kh + Qh Kl, Q and K being code * scale to 22 bits: within
+// 2^-22 |q||k| of the exact sum of scaled integer block dots.  (The block dots
+// themselves as four accumulators cost the softmax eight fp32 operations and a
+// shared load per pair of scores and four times the tensor memory; that form
+// measured 813 us on the 512-token chunk over 32768 positions.)
+// P.V: KVQ_OUT_F16: P rounded to fp16 once (2^-11 at most of each weight, half
+// of what the output's rounding adds up to), P.V_hi + P.V_lo; KVQ_OUT_F32: P in
+// two fp16 parts, P_hi.V_hi + P_lo.V_hi + P_hi.V_lo (about 22 bits).
+// m is raised only when a score would take P past 2^14, so after the first tile
+// O is hardly ever rescaled; fp32 sums do not mind the range.
+// Every wait is bounded: a wait that gives up marks the CTA, whose rows of this
+// and later pieces come out as NaN; the roles drain what they issued and leave.
+#pragma once
+
+#include "kvq_paged.cuh"
+#include "kvq_paged_line.cuh"
+#include "kvq_prefill.cuh"
+
+namespace kvq {
+
+constexpr int kCM = kChunkRows;           // query rows per CTA: 128
+constexpr int kCN = kChunkPositions;      // positions per KV tile: 128
+constexpr int kCHalf = kCN / 2;           // positions per copied and converted half tile
+constexpr int kCSub = kCHalf / kWTile;    // cache tiles per half
+constexpr int kCChunk = 32;               // positions per softmax chunk
+constexpr int kCKConv0 = 8, kCVConv0 = 12, kCQk = 20, kCPv = 21, kCCopy = 22, kCWalk = 23;
+constexpr int kChunkWarps = 24, kChunkThreads = kChunkWarps * 32;
+// Registers per thread: the launch gives every thread kCRegs (768 threads); the
+// warpgroups then trade: 256 * 104 + 384 * 64 + 128 * 80 = 768 * 80.
+constexpr int kCRegs = 80, kCRegsSoft = 104, kCRegsConv = 64, kCRegsRest = 80;
+static_assert(256 * kCRegsSoft + 384 * kCRegsConv + 128 * kCRegsRest <= kChunkThreads * kCRegs, "register shares");
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+constexpr int kCPieces = 4;              // piece records in flight
+constexpr float kCShift = 8.0f, kCSlack = 6.0f;
+constexpr uint16_t kHalfBits = 0x3800;    // 1/2: 127 * 516 (the largest code * scale) stays inside fp16
+
+template <int VT>
+struct ChunkCfg {
+    using T = PageTile<VT, KVQ_K_I8>;
+    // raw half tiles in flight: K is converted two to four halves ahead of V, so
+    // a half stays until V has taken it (three: 582 us on the chunk named above;
+    // separate K and V rings of part copies: 887 us, bound by the copies' issue)
+    static constexpr int RS = VT == KVQ_V_Q4_0 ? 5 : 4, RAW = kCSub * T::BYTES;
+    // K operand: 8-position row groups of 16 core matrices (8 positions x 8
+    // dims), 160 bytes apart so that converter stores spread over the banks
+    static constexpr int K_LBO = 160, K_SBO = 16 * K_LBO, KBUF = (kCHalf / 8) * K_SBO;
+    // V operand [dim][position]: 8-dim row groups padded by 16 bytes, likewise
+    static constexpr int V_SBO = (kCHalf / 8) * 128 + 16, VBUF = (kD / 8) * V_SBO;
+    static constexpr int KH_OFF = 0, KL_OFF = KH_OFF + 2 * KBUF, VH_OFF = KL_OFF + 2 * KBUF, VL_OFF = VH_OFF + 2 * VBUF,
+                         RAW_OFF = VL_OFF + 2 * VBUF;
+    static constexpr int XM_OFF = RAW_OFF + RS * RAW;               // fp32 [group][128]: a tile's m
+    static constexpr int XE_OFF = XM_OFF + 2 * kCM * 4;             // float2 [group][128]: m, l at the end of a piece
+    static constexpr int REC_OFF = XE_OFF + 2 * kCM * 8;            // int [RS]: sub-tiles with a page
+    static constexpr int OREC_OFF = REC_OFF + 32;                   // int [4 tiles][half]: the same, for the softmax
+    static constexpr int PIECE_OFF = OREC_OFF + 32;                 // ChunkWalk [kCPieces], 64 bytes each
+    static constexpr int BAR_OFF = PIECE_OFF + kCPieces * 64;
+    // barriers; [i] by half, [g] by group (tile parity), [q] by lane quarter
+    static constexpr int B_RAW = 0, B_KF = B_RAW + RS, B_VF = B_KF + 2, B_PVD = B_VF + 2, B_FIN = B_PVD + 2,
+                         B_PIECE = B_FIN + 2,                                               // one arrival so far, and
+                         B_M = B_PIECE + kCPieces, B_END = B_M + 8,                         // [g][q]
+                         B_SFULL = B_END + 8,                                               // two: the QK thread and its commit
+                         B_PREADY = B_SFULL + 2, B_KR = B_PREADY + 4,                       // four warps: [g][i], [i]
+                         B_VR = B_KR + 2, B_QR = B_VR + 2,                                  // eight warps
+                         B_RAWF = B_QR + 1,                                                 // twelve warps
+                         B_PFREE = B_RAWF + RS, NBAR = B_PFREE + kCPieces;                  // all 23 roles
+    static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;             // TMEM base, bad flag
+    static constexpr int SMEM = MISC_OFF + 16;
+    static_assert(RAW % 128 == 0 && RAW_OFF % 128 == 0 && BAR_OFF % 8 == 0, "alignment");
+    static_assert(RAW_OFF < (1 << 18) && SMEM + 1024 <= 232448, "descriptor range, shared memory");
+};
+
+// 32 consecutive columns of this thread's TMEM lane; the wait passes the
+// registers through, so that nothing reading them is moved ahead of it.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+                 "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+                   "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+                   "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32])
+{
+#define KVQ_R8(x, o) "+r"(x[o]), "+r"(x[o + 1]), "+r"(x[o + 2]), "+r"(x[o + 3]), "+r"(x[o + 4]), "+r"(x[o + 5]), "+r"(x[o + 6]), "+r"(x[o + 7])
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : KVQ_R8(r, 0), KVQ_R8(r, 8)::"memory");
+    asm volatile("" : KVQ_R8(r, 16), KVQ_R8(r, 24)::"memory");
+#undef KVQ_R8
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}" : "=r"(p));
+    return p != 0;
+}
+// D (+)= A.B as umma_f16_ta_w, and its commit, by the one thread that runs this.
+__device__ __forceinline__ void umma_ta_1(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+                 ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+                 : "memory");
+}
+__device__ __forceinline__ void umma_commit_1(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Eight codes + 128 (two words) times the scale s2 (both halves): fp16 high
+// parts, and what they miss.
+__device__ __forceinline__ void u8x8_hilo(uint32_t w0, uint32_t w1, __half2 s2, uint4 &hi, uint4 &lo)
+{
+    const __half2 k1152 = __half2half2(__ushort_as_half(0x6480));
+    uint32_t r[4] = {__byte_perm(w0, 0x64646464u, 0x4140), __byte_perm(w0, 0x64646464u, 0x4342),
+                     __byte_perm(w1, 0x64646464u, 0x4140), __byte_perm(w1, 0x64646464u, 0x4342)}, l[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const __half2 c = __hsub2(*reinterpret_cast<__half2 *>(&r[k]), k1152);
+        v_hilo(*reinterpret_cast<const uint32_t *>(&c), s2, r[k], l[k]);
+    }
+    hi = make_uint4(r[0], r[1], r[2], r[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// A piece of the line, as the roles read it from shared memory.
+struct ChunkWalk {
+    int tiles;               // KV tiles with a visible position among those of the piece; negative: no more pieces
+    int s0;                  // first KV tile
+    int b, h, t0, n, L;      // sequence, kv head, first row and rows of the batch, length
+    int gb, gsz, row0, R;    // query heads of the kv head, first row and rows of the tile
+    int lim_hi;              // last position the tile's last row sees
+    int slot;                // where the result goes: -1 out, else the CTA's slot of partials
+};
+// KV tiles a row tile counts for: those its last row sees (all, when the kv
+// heads have query groups of different sizes), at least one.
+__device__ __forceinline__ int chunk_tiles(const PagedAttnParams &p, int n, int L, int rt)
+{
+    const int last = min(n - 1, (int)(((long long)rt * kCM + kCM - 1) / p.gmax));
+    const int vis = p.causal && p.uniform ? min(L, L - n + 1 + last) : L;
+    return max(1, (vis + kCN - 1) / kCN);
+}
+__device__ __forceinline__ long long chunk_head_tiles(const PagedAttnParams &p, int n, int L)
+{
+    const int n_rt = (int)(((long long)n * p.gmax + kCM - 1) / kCM);
+    long long s = 0;
+    for (int rt = 0; rt < n_rt; ++rt) s += chunk_tiles(p, n, L, rt);
+    return s;
+}
+
+// Calls body(piece) for every piece of [pos, end) until it returns false;
+// cuts: this CTA's entries.
+template <typename F>
+__device__ __forceinline__ void chunk_pieces(const PagedAttnParams &p, const LineStart &line, long long pos, long long end, long long per,
+                                             PagedCut *cuts, F body)
+{
+    ChunkWalk w;
+    w.b = line.b - 1;
+    int rt = 0, n_rt = 0;
+    bool fresh = true, first = true;
+    const int H = p.pool.n_kv_heads;
+    while (pos < end) {
+        if (fresh) {
+            do {
+                ++w.b;
+                seq_shape(p, w.b, w.t0, w.n, w.L);
+            } while (!seq_mine(p, w.n));
+            n_rt = (int)(((long long)w.n * p.gmax + kCM - 1) / kCM);
+            w.h = rt = w.s0 = 0;
+            if (first) {
+                const long long per_head = chunk_head_tiles(p, w.n, w.L);
+                w.h = (int)(line.off / per_head);
+                long long x = line.off - w.h * per_head;
+                for (;; ++rt) {
+                    const int k = chunk_tiles(p, w.n, w.L, rt);
+                    if (x < k) break;
+                    x -= k;
+                }
+                w.s0 = (int)x;
+                first = false;
+            }
+            fresh = false;
+        }
+        const int n_tl = chunk_tiles(p, w.n, w.L, rt), s1 = (int)min((long long)n_tl, w.s0 + (end - pos));
+        w.gb = p.grp_begin[w.h];
+        w.gsz = p.grp_begin[w.h + 1] - w.gb;
+        w.row0 = rt * kCM;
+        w.R = min(kCM, w.n * w.gsz - w.row0);
+        if (w.R > 0) {
+            w.lim_hi = p.causal ? w.L - w.n + (w.row0 + w.R - 1) / w.gsz : w.L - 1;
+            w.tiles = w.lim_hi < 0 ? 0 : max(0, min(s1, w.lim_hi / kCN + 1) - w.s0);
+            w.slot = -1;
+            if (w.s0 > 0 || s1 < n_tl) {
+                w.slot = w.s0 == 0 ? 1 : 0;
+                const long long x0 = pos - w.s0, c0 = x0 / per;
+                cuts[w.slot] = PagedCut{w.b, w.h | rt << 8, (int)c0, (int)((x0 + n_tl - 1) / per - c0 + 1)};
+            }
+            if (!body(w)) return;
+        }
+        pos += s1 - w.s0;
+        w.s0 = 0;
+        if (++rt == n_rt) {
+            rt = 0;
+            if (++w.h == H) fresh = true;
+        }
+    }
+}
+
+template <int VT, bool O16>
+__global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __grid_constant__ PagedAttnParams p)
+{
+    using C = ChunkCfg<VT>;
+    using T = typename C::T;
+    constexpr uint32_t kIdQK = umma_idesc_f16(kCM, kCHalf), kIdPV = umma_idesc_f16(kCM, kD);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ LineStart line;
+    __shared__ long long tmp[kChunkWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int pshift = p.pool.pshift;
+
+    pdl_wait();
+    pdl_trigger();
+    long long pos, per;
+    line_find<kChunkThreads>(p, kChunkMinTiles,
+                             [&](int n, int len) { return (long long)p.pool.n_kv_heads * chunk_head_tiles(p, n, len); }, &line, tmp, pos, per);
+    const long long end = min(pos + per, line.total);
+    PagedCut *cuts = p.cuts + (size_t)blockIdx.x * 2;
+    if (tid < 2) cuts[tid] = PagedCut{0, 0, 0, 0};
+    if (pos >= end) return;   // block-uniform
+    static_assert(sizeof(ChunkWalk) <= 64, "piece records");
+
+    const uint32_t sbase = smem_u32(smem), bars = sbase + C::BAR_OFF;
+    auto bar = [&](int k) { return bars + 8u * (uint32_t)k; };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::MISC_OFF);
+    volatile int *bad = reinterpret_cast<volatile int *>(smem + C::MISC_OFF + 4);
+    if (warp == kCQk) tmem_alloc(smem_u32(tmem_slot), 512);
+    if (tid == 0) {
+        *bad = 0;
+        for (int k = 0; k < C::NBAR; ++k)
+            mbar_init(bar(k), k < C::B_SFULL ? 1 : k < C::B_PREADY ? 2 : k < C::B_VR ? 4 : k < C::B_RAWF ? 8 : k < C::B_PFREE ? 12 : 23);
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tS = tmem, tO = tmem + 2 * kCN, tQ = tO + kD;   // S of group g at 128 g; Q high parts, then low parts
+
+    auto give_up = [&]() {   // one thread of a role; the others run out of waits in turn
+        if (atomicExch(const_cast<int *>(bad), 1) == 0) atomicAdd(p.timeouts, 1u);
+    };
+    auto wwait = [&](int k, uint32_t parity) {   // by a whole warp
+        if (__all_sync(0xffffffffu, mbar_wait(bar(k), parity))) return true;
+        if (lane == 0) give_up();
+        return false;
+    };
+    auto wait1 = [&](int k, uint32_t parity) {   // by one thread
+        if (mbar_wait(bar(k), parity)) return true;
+        give_up();
+        return false;
+    };
+
+    // Calls body(piece) for the pieces in turn; one = the calling thread is alone.
+    auto pieces = [&](bool one, auto body) {
+        for (int k = 0;; ++k) {
+            const int e = k % kCPieces;
+            if (!(one ? wait1(C::B_PIECE + e, (k / kCPieces) & 1) : wwait(C::B_PIECE + e, (k / kCPieces) & 1))) return;
+            const ChunkWalk &w = *reinterpret_cast<const ChunkWalk *>(smem + C::PIECE_OFF + 64 * e);
+            if (w.tiles < 0 || !body(w, k)) return;
+            if (!one) __syncwarp();
+            if (one || lane == 0) mbar_arrive(bar(C::B_PFREE + e));
+        }
+    };
+
+    // (each share is set inside its own branch: where branches with different
+    // shares join, the compiler would hold all of them to the smallest)
+    if (warp >= kCQk) {
+    regs_dec<kCRegsRest>();
+    if (warp == kCWalk) {
+        // ================= the pieces =================
+        if (elect_one()) {
+            int k = 0;
+            auto put = [&](const ChunkWalk &w) {
+                const int e = k % kCPieces;
+                if (k >= kCPieces && !wait1(C::B_PFREE + e, (k / kCPieces - 1) & 1)) return false;
+                *reinterpret_cast<ChunkWalk *>(smem + C::PIECE_OFF + 64 * e) = w;
+                mbar_arrive(bar(C::B_PIECE + e));
+                ++k;
+                return true;
+            };
+            chunk_pieces(p, line, pos, end, per, cuts, put);
+            ChunkWalk last = {};
+            last.tiles = -1;
+            put(last);
+        }
+        __syncwarp();
+    } else if (warp == kCQk || warp == kCPv) {
+        // ================= MMAs: one thread each =================
+        if (elect_one()) {
+            int j = 0, piece = 0;   // tiles, and pieces with any, so far
+            if (warp == kCQk) {
+                uint64_t dKH[2], dKL[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    dKH[i] = umma_desc(sbase + C::KH_OFF + i * C::KBUF, C::K_LBO, C::K_SBO);
+                    dKL[i] = umma_desc(sbase + C::KL_OFF + i * C::KBUF, C::K_LBO, C::K_SBO);
+                }
+                pieces(true, [&](const ChunkWalk &w, int) {
+                    if (w.tiles == 0) return true;
+                    if (!wait1(C::B_QR, piece & 1)) return false;
+                    ++piece;
+                    for (int k = 0; k < w.tiles; ++k, ++j) {
+                        const int g = j & 1;
+                        const uint32_t d = tS + kCN * g;
+                        if (j >= 2 && !wait1(C::B_PVD + g, ((j - 2) >> 1) & 1)) return false;   // P(j - 2) is used up
+#pragma unroll 1
+                        for (int i = 0; i < 2; ++i) {
+                            if (!wait1(C::B_KR + i, j & 1)) return false;
+                            const uint64_t kh = i ? dKH[1] : dKH[0], kl = i ? dKL[1] : dKL[0];
+                            tc_fence_after();
+#pragma unroll
+                            for (int term = 0; term < 3; ++term)
+#pragma unroll
+                                for (int ks = 0; ks < kD / 16; ++ks) {
+                                    const uint64_t o = (uint64_t)(2 * ks * (C::K_LBO / 16));
+                                    umma_ta_1(d + kCHalf * i, tQ + (term == 1 ? kD / 2 : 0) + 8 * ks, (term == 2 ? kl : kh) + o, kIdQK,
+                                              term > 0 || ks > 0);
+                                }
+                            umma_commit_1(bar(C::B_KF + i));
+                        }
+                        umma_commit_1(bar(C::B_SFULL + g));
+                        mbar_arrive(bar(C::B_SFULL + g));   // hands on what the converters published
+                    }
+                    return true;
+                });
+            } else {
+                uint64_t dVH[2], dVL[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    dVH[i] = umma_desc(sbase + C::VH_OFF + i * C::VBUF, 128, C::V_SBO);
+                    dVL[i] = umma_desc(sbase + C::VL_OFF + i * C::VBUF, 128, C::V_SBO);
+                }
+                pieces(true, [&](const ChunkWalk &w, int) {
+                    for (int k = 0; k < w.tiles; ++k, ++j) {
+                        const int g = j & 1;
+#pragma unroll 1
+                        for (int i = 0; i < 2; ++i) {
+                            if (!wait1(C::B_VR + i, j & 1) || !wait1(C::B_PREADY + 2 * g + i, (j >> 1) & 1)) return false;
+                            tc_fence_after();
+                            const uint64_t vh = i ? dVH[1] : dVH[0], vl = i ? dVL[1] : dVL[0];
+#pragma unroll
+                            for (int ks = 0; ks < kCHalf / 16; ++ks) {
+                                // chunk of 32 positions: high parts in its first 16 columns, low parts after
+                                const uint32_t ph = tS + kCN * g + kCChunk * (2 * i + (ks >> 1)) + 8 * (ks & 1), pl = ph + kCChunk / 2;
+                                const uint64_t o = (uint64_t)(16 * ks);
+                                umma_ta_1(tO, ph, vh + o, kIdPV, (k > 0 || i > 0 || ks > 0) ? 1u : 0u);
+                                if (!O16) umma_ta_1(tO, pl, vh + o, kIdPV, 1u);
+                                umma_ta_1(tO, ph, vl + o, kIdPV, 1u);
+                            }
+                            umma_commit_1(bar(C::B_VF + i));
+                        }
+                        umma_commit_1(bar(C::B_PVD + g));
+                    }
+                    return true;
+                });
+            }
+            // everything issued here is done before TMEM is freed
+            const int fin = warp == kCQk ? C::B_FIN : C::B_FIN + 1;
+            umma_commit_1(bar(fin));
+            wait1(fin, 0);
+        }
+        __syncwarp();
+    } else if (warp == kCCopy) {
+        // ================= bulk copies, half tile after half tile =================
+        int issued = 0, st = 0, ph = 0;   // halves so far, the ring's slot and its phase
+        int *rec = reinterpret_cast<int *>(smem + C::REC_OFF);
+        // pages of 64 and more: one copy a half; of 32: two; of 16: four
+        const int run = pshift >= 6 ? 4 : pshift == 5 ? 2 : 1;
+        pieces(false, [&](const ChunkWalk &w, int) {
+            const int *bt = p.block_table + (size_t)w.b * p.table_stride;
+            const int n_half = 2 * w.tiles;
+            int pg = -1;
+            for (int t = 0; t < n_half; ++t, ++issued) {
+                if ((t & 7) == 0) {   // lane l: the page of sub-tile l % 4 of half t + l / 4
+                    const int x = w.s0 * kCN + (t + (lane >> 2)) * kCHalf + (lane & 3) * kWTile;
+                    pg = t + (lane >> 2) < n_half && x < w.L ? bt[x >> pshift] : -1;
+                    if (pg >= p.pool.n_pages) pg = -1;
+                }
+                if (issued >= C::RS && !wwait(C::B_RAWF + st, ph ^ 1)) return false;
+                int ok = (int)(__ballot_sync(0xffffffffu, pg >= 0) >> (4 * (t & 7))) & 15;
+                if (run == 4) ok = ok & 1 ? 15 : 0;
+                if (run == 2) ok = (ok & 1 ? 3 : 0) | (ok & 4 ? 12 : 0);
+                if (lane == 0) rec[st] = ok;
+                __syncwarp();   // the record before the arrival that publishes it
+                const uint32_t dst = sbase + C::RAW_OFF + st * C::RAW, full = bar(C::B_RAW + st);
+                mbar_arrive_expect_tx_w(full, __popc(ok) * T::BYTES);
+                const int tile = run == 4 ? ((w.s0 * kCN + t * kCHalf) & ((1 << pshift) - 1)) >> 4 : 0;
+#pragma unroll
+                for (int q = 0; q < kCSub; ++q)
+                    if (q % run == 0 && (ok >> q & 1))
+                        bulk_g2s_w(dst + q * T::BYTES, tile_of(p.pool, __shfl_sync(0xffffffffu, pg, 4 * (t & 7) + q), w.h, tile, T::BYTES),
+                                   run * T::BYTES, full);
+                if (++st == C::RS) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+            return true;
+        });
+        for (int k = max(0, issued - C::RS); k < issued; ++k) mbar_wait(bar(C::B_RAW + k % C::RS), (k / C::RS) & 1);   // copies in flight
+    }
+    } else if (warp >= kCKConv0) {
+    regs_dec<kCRegsConv>();
+    if (warp < kCVConv0) {
+        // ================= K converters =================
+        const int i = warp - kCKConv0;   // 16-byte chunk i of each cache tile: one position's codes of two blocks
+        const int u = 8 * (i >> 1) + (lane >> 2), dg = 8 * (i & 1) + (lane & 3);
+        const int soff = T::KS_OFF + scale_off(u, 2 * (i & 1));
+        int hh = 0;
+        pieces(false, [&](const ChunkWalk &w, int) {
+            for (int t = 0; t < 2 * w.tiles; ++t, ++hh) {
+                const int st = hh % C::RS, ob = hh & 1, j = hh >> 1;
+                if (!wwait(C::B_RAW + st, (hh / C::RS) & 1) || (j >= 1 && !wwait(C::B_KF + ob, (j - 1) & 1))) return false;
+                const uint8_t *raw = smem + C::RAW_OFF + st * C::RAW;
+                uint8_t *kh = smem + C::KH_OFF + ob * C::KBUF + (u / 8) * C::K_SBO + (u % 8) * 16 + dg * C::K_LBO, *kl = kh + (C::KL_OFF - C::KH_OFF);
+#pragma unroll 2
+                for (int q = 0; q < kCSub; ++q) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(raw + q * T::BYTES + i * 512 + lane * 16);
+                    const __half s0 = __ushort_as_half(*reinterpret_cast<const uint16_t *>(raw + q * T::BYTES + soff));
+                    const __half s1 = __ushort_as_half(*reinterpret_cast<const uint16_t *>(raw + q * T::BYTES + soff + 4));
+                    const __half2 k05 = __half2half2(__ushort_as_half(kHalfBits));
+                    uint4 hi, lo;
+                    u8x8_hilo(v.x, v.y, __hmul2(__half2half2(s0), k05), hi, lo);
+                    *reinterpret_cast<uint4 *>(kh + 2 * q * C::K_SBO) = hi;
+                    *reinterpret_cast<uint4 *>(kl + 2 * q * C::K_SBO) = lo;
+                    u8x8_hilo(v.z, v.w, __hmul2(__half2half2(s1), k05), hi, lo);
+                    *reinterpret_cast<uint4 *>(kh + 2 * q * C::K_SBO + 4 * C::K_LBO) = hi;
+                    *reinterpret_cast<uint4 *>(kl + 2 * q * C::K_SBO + 4 * C::K_LBO) = lo;
+                }
+                if (i == 0 && lane == 0)
+                    reinterpret_cast<int *>(smem + C::OREC_OFF)[2 * (j & 3) + ob] = reinterpret_cast<const int *>(smem + C::REC_OFF)[st];
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(C::B_KR + ob));
+                    mbar_arrive(bar(C::B_RAWF + st));
+                }
+            }
+            return true;
+        });
+    } else {
+        // ================= V converters =================
+        const int cw = warp - kCVConv0, q = cw >> 1, half = cw & 1;   // this warp: 8 positions of sub-tile q
+        const int g = lane & 7, bb = lane >> 3;                      // this thread: block bb, code column g: four dims
+        int hh = 0;
+        pieces(false, [&](const ChunkWalk &w, int) {
+            for (int t = 0; t < 2 * w.tiles; ++t, ++hh) {
+                const int st = hh % C::RS, ob = hh & 1, j = hh >> 1;
+                if (!wwait(C::B_RAW + st, (hh / C::RS) & 1) || (j >= 1 && !wwait(C::B_VF + ob, (j - 1) & 1))) return false;
+                const uint8_t *tv = smem + C::RAW_OFF + st * C::RAW + q * T::BYTES + T::V_OFF, *ts = tv + (T::VS_OFF - T::V_OFF) + 4 * half * 16 + 4 * bb;
+                const int ok = reinterpret_cast<const int *>(smem + C::REC_OFF)[st];
+                const int x = w.s0 * kCN + t * kCHalf, p0 = x + kWTile * q + 8 * half;
+                const bool full = ok == 15 && x + kCHalf - 1 <= w.lim_hi;
+                const __half2 k05 = __half2half2(__ushort_as_half(kHalfBits));
+                uint32_t hi[4][4], lo[4][4];   // [dim of four][position pair]
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t dw = *reinterpret_cast<const uint32_t *>(ts + 16 * c);   // scales of positions 2c, 2c + 1
+                    if (!full) {   // 0 where no row sees them
+                        const bool live = ok >> q & 1;
+                        dw &= (live && p0 + 2 * c <= w.lim_hi ? 0xffffu : 0u) | (live && p0 + 2 * c + 1 <= w.lim_hi ? 0xffff0000u : 0u);
+                    }
+                    const __half2 d2 = __hmul2(*reinterpret_cast<const __half2 *>(&dw), k05);
+                    uint32_t r[2][2];
+                    if (VT == KVQ_V_Q4_0) {
+                        v_codes<VT>(*reinterpret_cast<const uint32_t *>(tv + half * 512 + (4 * g + c) * 16 + 4 * bb), 0u, r);
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(tv + (2 * half + (bb >> 1)) * 512 + (4 * g + c) * 16 + 8 * (bb & 1));
+                        v_codes<VT>(v.x, v.y, r);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v_hilo(r[e >> 1][e & 1], d2, hi[e][c], lo[e][c]);
+                }
+                uint8_t *vh = smem + C::VH_OFF + ob * C::VBUF + cw * 128, *vl = vh + (C::VL_OFF - C::VH_OFF);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {   // r[h2][half] of v_codes: dim v_dim(2 bb + h2, g) + half
+                    const int dim = v_dim<VT>(2 * bb + (e >> 1), g) + (e & 1);
+                    const int o = (dim >> 3) * C::V_SBO + (dim & 7) * 16;
+                    *reinterpret_cast<uint4 *>(vh + o) = make_uint4(hi[e][0], hi[e][1], hi[e][2], hi[e][3]);
+                    *reinterpret_cast<uint4 *>(vl + o) = make_uint4(lo[e][0], lo[e][1], lo[e][2], lo[e][3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(C::B_VR + ob));
+                    mbar_arrive(bar(C::B_RAWF + st));
+                }
+            }
+            return true;
+        });
+    }
+    } else {
+        // ================= softmax: one query row per thread =================
+        regs_inc<kCRegsSoft>();
+        const int grp = warp >> 2, quarter = warp & 3;
+        const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
+        const int row = 32 * quarter + lane;
+        const uint32_t tSg = tS + lane_base + kCN * grp;
+        float *xm = reinterpret_cast<float *>(smem + C::XM_OFF);
+        float2 *xe = reinterpret_cast<float2 *>(smem + C::XE_OFF);
+        // Q and K went in halved, the sign is in Q; a scale of 0 stays finite times -inf
+        const float c4 = fmaxf(4.0f * fabsf(p.qk_scale_log2), 1e-30f);
+        int j = 0, ends = 0;
+        bool lost = false;
+        pieces(false, [&](const ChunkWalk &w, int) {
+            const bool whole = w.slot < 0;
+            const bool row_ok = row < w.R;
+            const int tok = row_ok ? (w.row0 + row) / w.gsz : 0, head = row_ok ? p.grp_q[w.gb + (w.row0 + row) % w.gsz] : 0;
+            const int lim = row_ok ? (p.causal ? w.L - w.n + tok : w.L - 1) : -1;
+            float m = -INFINITY, l = 0.f;
+            if (w.tiles > 0 && !lost) {
+                // ---- blocks 2 grp, 2 grp + 1 of this row: int8 rule, q/2 in two fp16 parts into TMEM ----
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (size_t)(w.t0 + tok) * p.q_stride + (size_t)head * kD);
+                const float sgn = p.qk_scale_log2 < 0.f ? -0.5f : 0.5f;
+#pragma unroll 1
+                for (int b2 = 0; b2 < 2; ++b2) {
+                    const int bb = 2 * grp + b2;
+                    uint4 raw[4];
+                    float a = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        raw[k] = row_ok ? src[4 * bb + k] : make_uint4(0u, 0u, 0u, 0u);
+                        const uint32_t ws[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&ws[e]));
+                            a = fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y)));
+                        }
+                    }
+                    const float sc = __half2float(__float2half_rn(__fdiv_rn(a, 127.f)));
+                    uint32_t hv[16], lv[16];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t ws[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&ws[e]));
+                            const float2 v = make_float2((float)quant_i8(f.x, sc) * sc * sgn, (float)quant_i8(f.y, sc) * sc * sgn);   // exact: 18 bits
+                            hv[4 * k + e] = pack_half2(v.x, v.y);
+                            const float2 y = sub2(v, __half22float2(*reinterpret_cast<const __half2 *>(&hv[4 * k + e])));
+                            lv[4 * k + e] = pack_half2(y.x, y.y);
+                        }
+                    }
+                    tmem_st16(tQ + lane_base + 16 * bb, hv);
+                    tmem_st16(tQ + lane_base + kD / 2 + 16 * bb, lv);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::B_QR));
+                const bool idle_warp = 32 * quarter >= w.R;   // no row here: keep the barriers in step
+
+                const int j1 = j + w.tiles, j0 = j;
+                for (; j < j1; ++j) {
+                    if ((j & 1) != grp) continue;   // the other group's tile
+                    const uint32_t ph = (j >> 1) & 1;
+                    if (!wwait(C::B_SFULL + grp, ph)) {
+                        lost = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (idle_warp) {
+                        if (lane == 0) {
+                            mbar_arrive(bar(C::B_M + 4 * grp + quarter));
+                            mbar_arrive(bar(C::B_PREADY + 2 * grp));
+                            mbar_arrive(bar(C::B_PREADY + 2 * grp + 1));
+                        }
+                        continue;
+                    }
+                    const int x = (w.s0 + j - j0) * kCN;
+                    const int2 rec = reinterpret_cast<const int2 *>(smem + C::OREC_OFF)[j & 3];
+                    const int ok = rec.x | rec.y << 4;                     // 16-position sub-tiles with a page
+                    if (__any_sync(0xffffffffu, ok != 255 || x + kCN - 1 > lim)) {   // some position is masked: -inf into S
+#pragma unroll 1
+                        for (int c0 = 0; c0 < kCN; c0 += kWTile) {
+                            uint32_t v[16];
+                            tmem_ld16(tSg + c0, v);
+                            tmem_wait_ld();
+                            const int top = ok >> (c0 / kWTile) & 1 ? lim - x - c0 : -1;
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) v[k] = k <= top ? v[k] : 0xff800000u;
+                            tmem_st16(tSg + c0, v);
+                        }
+                        tmem_wait_st();
+                    }
+
+                    // ---- first pass: the row's maximum ----
+                    // (loops over pairs of chunks, not unrolled further: with every role's code
+                    // unrolled the warps waited for instructions)
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    uint32_t a[2][32];
+                    tmem_ld32(tSg, a[0]);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kCN; c0 += 2 * kCChunk)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t(&v)[32] = a[c];
+                            tmem_wait_ld32(v);
+                            if (c == 0 || c0 + 2 * kCChunk < kCN) tmem_ld32(tSg + c0 + kCChunk * (c + 1), a[c ^ 1]);
+#pragma unroll
+                            for (int k = 0; k < kCChunk; k += 4)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], __uint_as_float(v[k + e]));
+                        }
+                    float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    tmem_ld32(tSg, a[0]);   // the second pass's first chunk
+                    mx = mx == -INFINITY ? mx : mx * c4;
+
+                    // ---- the row's zero point after the tile before this one, handed on by the other group ----
+                    float mp = -INFINITY;
+                    if (j > 0) {
+                        if (!wwait(C::B_M + 4 * (grp ^ 1) + quarter, ((j - 1) >> 1) & 1)) {
+                            lost = true;
+                            break;
+                        }
+                        if (j > j0) mp = xm[(grp ^ 1) * kCM + row];
+                    }
+                    const bool need = mx > mp + (kCShift + kCSlack);
+                    const float mn = need ? mx - kCShift : mp;
+                    xm[grp * kCM + row] = mn;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::B_M + 4 * grp + quarter));
+                    if (mn != m) {   // raised by either group since this group's last tile
+                        l *= m == -INFINITY ? 0.f : fast_exp2(m - mn);
+                        m = mn;
+                    }
+                    if (j > j0 && __any_sync(0xffffffffu, need)) {   // O is stable once P.V(j - 1) is done
+                        if (!wwait(C::B_PVD + (grp ^ 1), ((j - 1) >> 1) & 1)) {
+                            lost = true;
+                            break;
+                        }
+                        tc_fence_after();
+                        const float alpha = need ? (mp == -INFINITY ? 0.f : fast_exp2(mp - mn)) : 1.f;
+#pragma unroll 1
+                        for (int c0 = 0; c0 < kD; c0 += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(tO + lane_base + c0, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                            tmem_st16(tO + lane_base + c0, o);
+                        }
+                    }
+
+                    // ---- second pass: P over S, 32 positions at a time ----
+                    const float mu = m == -INFINITY ? 0.f : m;
+                    const float2 cc = make_float2(c4, c4), nm = make_float2(-mu, -mu);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kCN; c0 += 2 * kCChunk) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t(&v)[32] = a[c];
+                            tmem_wait_ld32(v);
+                            if (c == 0 || c0 + 2 * kCChunk < kCN) tmem_ld32(tSg + c0 + kCChunk * (c + 1), a[c ^ 1]);
+                            uint32_t hw[16], lw[O16 ? 1 : 16];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const float2 e = fma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), cc, nm);
+                                const float2 pv = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+                                sum[k & 1] = add2(sum[k & 1], pv);
+                                hw[k] = pack_half2(pv.x, pv.y);
+                                if (!O16) {
+                                    const float2 y = sub2(pv, __half22float2(*reinterpret_cast<const __half2 *>(&hw[k])));
+                                    lw[O16 ? 0 : k] = pack_half2(y.x, y.y);
+                                }
+                            }
+                            tmem_st16(tSg + c0 + kCChunk * c, hw);
+                            if constexpr (!O16) tmem_st16(tSg + c0 + kCChunk * c + kCChunk / 2, lw);
+                        }
+                        tmem_wait_st();   // a half is whole
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(C::B_PREADY + 2 * grp + (c0 ? 1 : 0)));
+                    }
+                    const float2 s2 = add2(sum[0], sum[1]);
+                    l += s2.x + s2.y;
+                }
+                // ---- the end of the piece: both groups' sums, and P.V done ----
+                if (!lost) {
+                    xe[grp * kCM + row] = make_float2(m, l);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::B_END + 4 * grp + quarter));
+                    if (!wwait(C::B_END + 4 * (grp ^ 1) + quarter, ends & 1) || !wwait(C::B_PVD + ((j - 1) & 1), ((j - 1) >> 1) & 1)) lost = true;
+                    ++ends;
+                    tc_fence_after();
+                    const float2 o = xe[(grp ^ 1) * kCM + row];
+                    const float mm = fmaxf(m, o.x);   // O is at the later, higher zero point
+                    l = (m == -INFINITY ? 0.f : l * fast_exp2(m - mm)) + (o.x == -INFINITY ? 0.f : o.y * fast_exp2(o.x - mm));
+                    m = mm;
+                }
+            }
+            lost = lost || __any_sync(0xffffffffu, *bad != 0);
+            // ---- this group's 64 columns of the row out ----
+            const bool any = w.tiles > 0 && !(l <= 0.f);
+            const float nan = __int_as_float(0x7fc00000);
+            float lg;
+            asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(l));
+            const float f = lost ? nan : any ? 2.0f / l : 0.f;   // V went in halved
+            const float lse = lost ? nan : any ? (m + lg) * 0.69314718055994531f : -INFINITY;
+            const size_t part = ((size_t)blockIdx.x * 2 + max(0, w.slot)) * kCM + row, orow = (size_t)(w.t0 + tok) * p.n_q_heads + head;
+            const bool have_o = w.tiles > 0 && !lost;
+#pragma unroll 1
+            for (int c0 = (kD / 2) * grp; c0 < (kD / 2) * (grp + 1); c0 += 16) {
+                uint32_t o[16];
+                if (have_o) {   // warp-uniform
+                    tmem_ld16(tO + lane_base + c0, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] = 0u;
+                }
+                if (!row_ok) continue;
+                float y[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) y[k] = lost ? nan : any ? __uint_as_float(o[k]) * f : 0.f;
+                if (whole && O16) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + orow * kD + c0);
+#pragma unroll
+                    for (int k = 0; k < 16; k += 8)
+                        dst[k / 8] = make_uint4(pack_half2(y[k], y[k + 1]), pack_half2(y[k + 2], y[k + 3]), pack_half2(y[k + 4], y[k + 5]), pack_half2(y[k + 6], y[k + 7]));
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>((whole ? static_cast<float *>(p.out) + orow * kD : p.ws_o + part * kD) + c0);
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4) dst[k / 4] = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+                }
+            }
+            if (row_ok && grp == 0) {
+                if (!whole) p.ws_lse[part] = lse;
+                else if (p.lse) p.lse[orow] = lse;
+            }
+            tc_fence_before();
+            __syncwarp();
+            return true;
+        });
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kCQk) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int VT>
+cudaError_t prepare_chunk_t()
+{
+    const cudaError_t e = cudaFuncSetAttribute(paged_chunk_kernel<VT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkCfg<VT>::SMEM);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(paged_chunk_kernel<VT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkCfg<VT>::SMEM);
+}
+
+template <int VT>
+cudaError_t launch_chunk_t(const PagedAttnParams &p, int out_type, int n_ctas, cudaStream_t s, bool pdl)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n_ctas);
+    cfg.blockDim = dim3(kChunkThreads);
+    cfg.dynamicSmemBytes = ChunkCfg<VT>::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (out_type == KVQ_OUT_F16) return cudaLaunchKernelEx(&cfg, paged_chunk_kernel<VT, true>, p);
+    return cudaLaunchKernelEx(&cfg, paged_chunk_kernel<VT, false>, p);
+}
+
+}  // namespace kvq
