@@ -78,11 +78,11 @@ struct ChunkCfg {
     static constexpr int PIECE_OFF = OREC_OFF + 32;                 // ChunkWalk [kCPieces], 64 bytes each
     static constexpr int BAR_OFF = PIECE_OFF + kCPieces * 64;
     // barriers; [i] by half, [g] by group (tile parity), [q] by lane quarter
-    static constexpr int B_RAW = 0, B_KF = B_RAW + RS, B_VF = B_KF + 2, B_PVD = B_VF + 2, B_FIN = B_PVD + 2,
-                         B_PIECE = B_FIN + 2,                                               // one arrival so far, and
+    static constexpr int B_RAW = 0, B_KF = B_RAW + RS, B_VF = B_KF + 2, B_PVD = B_VF + 2, B_FIN = B_PVD + 4,
+                         B_PIECE = B_FIN + 2,                                               // one arrival: -, [i], [i], [g][i], -, -, and
                          B_M = B_PIECE + kCPieces, B_END = B_M + 8,                         // [g][q]
-                         B_SFULL = B_END + 8,                                               // two: the QK thread and its commit
-                         B_PREADY = B_SFULL + 2, B_KR = B_PREADY + 4,                       // four warps: [g][i], [i]
+                         B_SFULL = B_END + 8,                                               // two, the QK thread and its commit: [g][i]
+                         B_PREADY = B_SFULL + 4, B_KR = B_PREADY + 4,                       // four warps: [g][i], [i]
                          B_VR = B_KR + 2, B_QR = B_VR + 2,                                  // eight warps
                          B_RAWF = B_QR + 1,                                                 // twelve warps
                          B_PFREE = B_RAWF + RS, NBAR = B_PFREE + kCPieces;                  // all 23 roles
@@ -336,9 +336,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                     for (int k = 0; k < w.tiles; ++k, ++j) {
                         const int g = j & 1;
                         const uint32_t d = tS + kCN * g;
-                        if (j >= 2 && !wait1(C::B_PVD + g, ((j - 2) >> 1) & 1)) return false;   // P(j - 2) is used up
 #pragma unroll 1
                         for (int i = 0; i < 2; ++i) {
+                            // this half of P(j - 2) is used up, and K is there
+                            if (j >= 2 && !wait1(C::B_PVD + 2 * g + i, ((j - 2) >> 1) & 1)) return false;
                             if (!wait1(C::B_KR + i, j & 1)) return false;
                             const uint64_t kh = i ? dKH[1] : dKH[0], kl = i ? dKL[1] : dKL[0];
                             tc_fence_after();
@@ -351,9 +352,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                                               term > 0 || ks > 0);
                                 }
                             umma_commit_1(bar(C::B_KF + i));
+                            umma_commit_1(bar(C::B_SFULL + 2 * g + i));
+                            mbar_arrive(bar(C::B_SFULL + 2 * g + i));   // hands on what the converters published
                         }
-                        umma_commit_1(bar(C::B_SFULL + g));
-                        mbar_arrive(bar(C::B_SFULL + g));   // hands on what the converters published
                     }
                     return true;
                 });
@@ -382,8 +383,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                                 umma_ta_1(tO, ph, vl + o, kIdPV, 1u);
                             }
                             umma_commit_1(bar(C::B_VF + i));
+                            umma_commit_1(bar(C::B_PVD + 2 * g + i));
                         }
-                        umma_commit_1(bar(C::B_PVD + g));
                     }
                     return true;
                 });
@@ -588,12 +589,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                 for (; j < j1; ++j) {
                     if ((j & 1) != grp) continue;   // the other group's tile
                     const uint32_t ph = (j >> 1) & 1;
-                    if (!wwait(C::B_SFULL + grp, ph)) {
-                        lost = true;
-                        break;
-                    }
-                    tc_fence_after();
                     if (idle_warp) {
+                        if (!wwait(C::B_SFULL + 2 * grp, ph) || !wwait(C::B_SFULL + 2 * grp + 1, ph)) {
+                            lost = true;
+                            break;
+                        }
                         if (lane == 0) {
                             mbar_arrive(bar(C::B_M + 4 * grp + quarter));
                             mbar_arrive(bar(C::B_PREADY + 2 * grp));
@@ -602,40 +602,47 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                         continue;
                     }
                     const int x = (w.s0 + j - j0) * kCN;
-                    const int2 rec = reinterpret_cast<const int2 *>(smem + C::OREC_OFF)[j & 3];
-                    const int ok = rec.x | rec.y << 4;                     // 16-position sub-tiles with a page
-                    if (__any_sync(0xffffffffu, ok != 255 || x + kCN - 1 > lim)) {   // some position is masked: -inf into S
-#pragma unroll 1
-                        for (int c0 = 0; c0 < kCN; c0 += kWTile) {
-                            uint32_t v[16];
-                            tmem_ld16(tSg + c0, v);
-                            tmem_wait_ld();
-                            const int top = ok >> (c0 / kWTile) & 1 ? lim - x - c0 : -1;
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) v[k] = k <= top ? v[k] : 0xff800000u;
-                            tmem_st16(tSg + c0, v);
-                        }
-                        tmem_wait_st();
-                    }
 
-                    // ---- first pass: the row's maximum ----
-                    // (loops over pairs of chunks, not unrolled further: with every role's code
+                    // ---- first pass: the row's maximum, each half as its QK is done ----
+                    // (loops are not unrolled beyond a pair of chunks: with every role's code
                     // unrolled the warps waited for instructions)
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     uint32_t a[2][32];
-                    tmem_ld32(tSg, a[0]);
 #pragma unroll 1
-                    for (int c0 = 0; c0 < kCN; c0 += 2 * kCChunk)
+                    for (int i = 0; i < 2; ++i) {
+                        if (!wwait(C::B_SFULL + 2 * grp + i, ph)) {
+                            lost = true;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t ts = tSg + kCHalf * i;
+                        const int ok = reinterpret_cast<const int *>(smem + C::OREC_OFF)[2 * (j & 3) + i], left = lim - x - kCHalf * i;
+                        if (__any_sync(0xffffffffu, ok != 15 || left < kCHalf - 1)) {   // some position is masked: -inf into S
+#pragma unroll 1
+                            for (int q = 0; q < kCSub; ++q) {
+                                uint32_t v[16];
+                                tmem_ld16(ts + kWTile * q, v);
+                                tmem_wait_ld();
+                                const int top = ok >> q & 1 ? left - kWTile * q : -1;
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) v[k] = k <= top ? v[k] : 0xff800000u;
+                                tmem_st16(ts + kWTile * q, v);
+                            }
+                            tmem_wait_st();
+                        }
+                        tmem_ld32(ts, a[0]);
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             uint32_t(&v)[32] = a[c];
                             tmem_wait_ld32(v);
-                            if (c == 0 || c0 + 2 * kCChunk < kCN) tmem_ld32(tSg + c0 + kCChunk * (c + 1), a[c ^ 1]);
+                            if (c == 0) tmem_ld32(ts + kCChunk, a[1]);
 #pragma unroll
                             for (int k = 0; k < kCChunk; k += 4)
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], __uint_as_float(v[k + e]));
                         }
+                    }
+                    if (lost) break;
                     float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     tmem_ld32(tSg, a[0]);   // the second pass's first chunk
                     mx = mx == -INFINITY ? mx : mx * c4;
@@ -659,7 +666,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                         m = mn;
                     }
                     if (j > j0 && __any_sync(0xffffffffu, need)) {   // O is stable once P.V(j - 1) is done
-                        if (!wwait(C::B_PVD + (grp ^ 1), ((j - 1) >> 1) & 1)) {
+                        if (!wwait(C::B_PVD + 2 * (grp ^ 1) + 1, ((j - 1) >> 1) & 1)) {
                             lost = true;
                             break;
                         }
@@ -715,7 +722,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                     xe[grp * kCM + row] = make_float2(m, l);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(C::B_END + 4 * grp + quarter));
-                    if (!wwait(C::B_END + 4 * (grp ^ 1) + quarter, ends & 1) || !wwait(C::B_PVD + ((j - 1) & 1), ((j - 1) >> 1) & 1)) lost = true;
+                    if (!wwait(C::B_END + 4 * (grp ^ 1) + quarter, ends & 1) || !wwait(C::B_PVD + 2 * ((j - 1) & 1) + 1, ((j - 1) >> 1) & 1)) lost = true;
                     ++ends;
                     tc_fence_after();
                     const float2 o = xe[(grp ^ 1) * kCM + row];
