@@ -14,8 +14,9 @@
 //   8-11  K converters: k/2 = code * (scale/2) as an fp16 high and low part.
 //   12-19 V converters: v/2 likewise, turned to [dim][position].
 //   20    QK, 21 P.V: one thread each issues and waits.
-//   22    the bulk copies of 64-position half tiles, three ahead.
-//   23    walks the CTA's pieces of the line and hands them out as records.
+//   22    walks the CTA's pieces of the line, hands them out as records, and
+//         issues the bulk copies of the K parts of 64-position half tiles; 23 those
+//         of the V parts.
 // Tensor memory: S of two tiles (128 columns each), O, the query's high and low
 // parts.  Shared memory: K and V operands of two half tiles.
 // QK: S = Qh Kh + Ql Kh + Qh Kl, Q and K being code * scale to 22 bits: within
@@ -43,7 +44,7 @@ constexpr int kCN = kChunkPositions;      // positions per KV tile: 128
 constexpr int kCHalf = kCN / 2;           // positions per copied and converted half tile
 constexpr int kCSub = kCHalf / kWTile;    // cache tiles per half
 constexpr int kCChunk = 32;               // positions per softmax chunk
-constexpr int kCKConv0 = 8, kCVConv0 = 12, kCQk = 20, kCPv = 21, kCCopy = 22, kCWalk = 23;
+constexpr int kCKConv0 = 8, kCVConv0 = 12, kCQk = 20, kCPv = 21, kCKCopy = 22, kCVCopy = 23;
 constexpr int kChunkWarps = 24, kChunkThreads = kChunkWarps * 32;
 // Registers per thread: the launch gives every thread kCRegs (768 threads); the
 // warpgroups then trade: 256 * 104 + 384 * 64 + 128 * 80 = 768 * 80.
@@ -60,36 +61,35 @@ constexpr uint16_t kHalfBits = 0x3800;    // 1/2: 127 * 516 (the largest code * 
 template <int VT>
 struct ChunkCfg {
     using T = PageTile<VT, KVQ_K_I8>;
-    // raw half tiles in flight: K is converted two to four halves ahead of V, so
-    // a half stays until V has taken it (three: 582 us on the chunk named above;
-    // separate K and V rings of part copies: 887 us, bound by the copies' issue)
-    static constexpr int RS = VT == KVQ_V_Q4_0 ? 5 : 4, RAW = kCSub * T::BYTES;
+    // raw half tiles in flight: the K parts (codes, scales) and V parts of the
+    // tile records in rings of their own, since K is converted ahead of V
+    static constexpr int KPART = T::V_OFF, VPART = T::BYTES - T::V_OFF;
+    static constexpr int RSK = VT == KVQ_V_Q4_0 ? 5 : 4, RSV = RSK, RAWK = kCSub * KPART, RAWV = kCSub * VPART;
     // K operand: 8-position row groups of 16 core matrices (8 positions x 8
     // dims), 160 bytes apart so that converter stores spread over the banks
     static constexpr int K_LBO = 160, K_SBO = 16 * K_LBO, KBUF = (kCHalf / 8) * K_SBO;
     // V operand [dim][position]: 8-dim row groups padded by 16 bytes, likewise
     static constexpr int V_SBO = (kCHalf / 8) * 128 + 16, VBUF = (kD / 8) * V_SBO;
     static constexpr int KH_OFF = 0, KL_OFF = KH_OFF + 2 * KBUF, VH_OFF = KL_OFF + 2 * KBUF, VL_OFF = VH_OFF + 2 * VBUF,
-                         RAW_OFF = VL_OFF + 2 * VBUF;
-    static constexpr int XM_OFF = RAW_OFF + RS * RAW;               // fp32 [group][128]: a tile's m
+                         RAWK_OFF = VL_OFF + 2 * VBUF, RAWV_OFF = RAWK_OFF + RSK * RAWK;
+    static constexpr int XM_OFF = RAWV_OFF + RSV * RAWV;              // fp32 [group][128]: a tile's m
     static constexpr int XE_OFF = XM_OFF + 2 * kCM * 4;             // float2 [group][128]: m, l at the end of a piece
-    static constexpr int REC_OFF = XE_OFF + 2 * kCM * 8;            // int [RS]: sub-tiles with a page
-    static constexpr int OREC_OFF = REC_OFF + 32;                   // int [4 tiles][half]: the same, for the softmax
+    static constexpr int REC_OFF = XE_OFF + 2 * kCM * 8;            // int [RSK], [RSV]: sub-tiles with a page
+    static constexpr int OREC_OFF = REC_OFF + 48;                   // int [4 tiles][half]: the same, for the softmax
     static constexpr int PIECE_OFF = OREC_OFF + 32;                 // ChunkWalk [kCPieces], 64 bytes each
     static constexpr int BAR_OFF = PIECE_OFF + kCPieces * 64;
     // barriers; [i] by half, [g] by group (tile parity), [q] by lane quarter
-    static constexpr int B_RAW = 0, B_KF = B_RAW + RS, B_VF = B_KF + 2, B_PVD = B_VF + 2, B_FIN = B_PVD + 4,
+    static constexpr int B_RAWK = 0, B_RAWV = B_RAWK + RSK, B_KF = B_RAWV + RSV, B_VF = B_KF + 2, B_PVD = B_VF + 2, B_FIN = B_PVD + 4,
                          B_PIECE = B_FIN + 2,                                               // one arrival: -, [i], [i], [g][i], -, -, and
                          B_M = B_PIECE + kCPieces, B_END = B_M + 8,                         // [g][q]
                          B_SFULL = B_END + 8,                                               // two, the QK thread and its commit: [g][i]
-                         B_PREADY = B_SFULL + 4, B_KR = B_PREADY + 4,                       // four warps: [g][i], [i]
-                         B_VR = B_KR + 2, B_QR = B_VR + 2,                                  // eight warps
-                         B_RAWF = B_QR + 1,                                                 // twelve warps
-                         B_PFREE = B_RAWF + RS, NBAR = B_PFREE + kCPieces;                  // all 23 roles
+                         B_PREADY = B_SFULL + 4, B_KR = B_PREADY + 4, B_RAWKF = B_KR + 2,   // four warps: [g][i], [i], K ring
+                         B_VR = B_RAWKF + RSK, B_QR = B_VR + 2, B_RAWVF = B_QR + 1,         // eight warps: [i], -, V ring
+                         B_PFREE = B_RAWVF + RSV, NBAR = B_PFREE + kCPieces;                  // all 23 roles
     static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;             // TMEM base, bad flag
     static constexpr int SMEM = MISC_OFF + 16;
-    static_assert(RAW % 128 == 0 && RAW_OFF % 128 == 0 && BAR_OFF % 8 == 0, "alignment");
-    static_assert(RAW_OFF < (1 << 18) && SMEM + 1024 <= 232448, "descriptor range, shared memory");
+    static_assert(KPART % 16 == 0 && VPART % 16 == 0 && RAWK_OFF % 128 == 0 && OREC_OFF % 8 == 0 && BAR_OFF % 8 == 0, "alignment");
+    static_assert(RAWK_OFF < (1 << 18) && SMEM + 1024 <= 232448, "descriptor range, shared memory");
 };
 
 // 32 consecutive columns of this thread's TMEM lane; the wait passes the
@@ -112,6 +112,22 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32])
 #undef KVQ_R8
 }
 
+// mbar_wait of a thread that runs alone: a loop of three instructions (the
+// general one, inside a branch that one lane takes, slowed the MMA threads:
+// 503 against 491 us on the chunk named above, 562 against 515 us on the
+// verify shape).
+__device__ __forceinline__ bool mbar_wait_alone(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, %3;\n"
+                 "again:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra over;\n"
+                 " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra again;\n"
+                 "over:\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity), "n"(kMbarSpins)
+                 : "memory");
+    return done != 0;
+}
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one()
 {
@@ -261,7 +277,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
     if (tid == 0) {
         *bad = 0;
         for (int k = 0; k < C::NBAR; ++k)
-            mbar_init(bar(k), k < C::B_SFULL ? 1 : k < C::B_PREADY ? 2 : k < C::B_VR ? 4 : k < C::B_RAWF ? 8 : k < C::B_PFREE ? 12 : 23);
+            mbar_init(bar(k), k < C::B_SFULL ? 1 : k < C::B_PREADY ? 2 : k < C::B_VR ? 4 : k < C::B_PFREE ? 8 : 23);
         fence_mbar_init();
     }
     tc_fence_before();
@@ -279,7 +295,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
         return false;
     };
     auto wait1 = [&](int k, uint32_t parity) {   // by one thread
-        if (mbar_wait(bar(k), parity)) return true;
+        if (mbar_wait_alone(bar(k), parity)) return true;
         give_up();
         return false;
     };
@@ -300,24 +316,66 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
     // shares join, the compiler would hold all of them to the smallest)
     if (warp >= kCQk) {
     regs_dec<kCRegsRest>();
-    if (warp == kCWalk) {
-        // ================= the pieces =================
-        if (elect_one()) {
+    if (warp == kCKCopy || warp == kCVCopy) {
+        // ================= bulk copies: a warp for the K parts, one for the V parts; the first
+        // also walks the pieces and hands them out =================
+        const bool kside = warp == kCKCopy;
+        const int rs = kside ? C::RSK : C::RSV, part = kside ? C::KPART : C::VPART;
+        const int b_full = kside ? C::B_RAWK : C::B_RAWV, b_free = kside ? C::B_RAWKF : C::B_RAWVF;
+        const uint32_t raw = sbase + (kside ? C::RAWK_OFF : C::RAWV_OFF);
+        int *rec = reinterpret_cast<int *>(smem + C::REC_OFF) + (kside ? 0 : C::RSK);
+        int issued = 0, st = 0, ph = 0;   // halves so far, the ring's slot and its phase
+        const size_t page_bytes = ((size_t)p.pool.n_kv_heads << (pshift - 4)) * T::BYTES;
+        auto copy_piece = [&](const ChunkWalk &w) {
+            const int *bt = p.block_table + (size_t)w.b * p.table_stride;
+            const uint8_t *head = p.pool.data + ((size_t)w.h << (pshift - 4)) * T::BYTES + (kside ? 0 : T::V_OFF);
+            const int n_half = 2 * w.tiles;
+            const uint8_t *src = nullptr;   // lane l: sub-tile l % 4 of half t + l / 4, for eight halves at a time
+            for (int t = 0; t < n_half; ++t, ++issued) {
+                if ((t & 7) == 0) {
+                    const int x = w.s0 * kCN + (t + (lane >> 2)) * kCHalf + (lane & 3) * kWTile;
+                    const int page = t + (lane >> 2) < n_half && x < w.L ? bt[x >> pshift] : -1;
+                    src = page >= 0 && page < p.pool.n_pages ? head + page * page_bytes + ((x & ((1 << pshift) - 1)) >> 4) * T::BYTES : nullptr;
+                }
+                if (issued >= rs && !wwait(b_free + st, ph ^ 1)) return false;
+                const int ok = (int)(__ballot_sync(0xffffffffu, src != nullptr) >> (4 * (t & 7))) & 15;
+                const uint32_t full = bar(b_full + st);
+                if (lane == 0) rec[st] = ok;
+                __syncwarp();   // the record before the arrival that publishes it
+                mbar_arrive_expect_tx_w(full, __popc(ok) * part);
+                if ((lane >> 2) == (t & 7) && src)
+                    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                     raw + (st * kCSub + (lane & 3)) * part),
+                                 "l"(src), "r"(part), "r"(full)
+                                 : "memory");
+                __syncwarp();
+                if (++st == rs) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+            return true;
+        };
+        if (kside) {
             int k = 0;
             auto put = [&](const ChunkWalk &w) {
                 const int e = k % kCPieces;
-                if (k >= kCPieces && !wait1(C::B_PFREE + e, (k / kCPieces - 1) & 1)) return false;
-                *reinterpret_cast<ChunkWalk *>(smem + C::PIECE_OFF + 64 * e) = w;
-                mbar_arrive(bar(C::B_PIECE + e));
+                if (k >= kCPieces && !wwait(C::B_PFREE + e, (k / kCPieces - 1) & 1)) return false;
+                if (lane == 0) {
+                    *reinterpret_cast<ChunkWalk *>(smem + C::PIECE_OFF + 64 * e) = w;
+                    mbar_arrive(bar(C::B_PIECE + e));
+                }
                 ++k;
-                return true;
+                return w.tiles <= 0 || copy_piece(w);
             };
             chunk_pieces(p, line, pos, end, per, cuts, put);
             ChunkWalk last = {};
             last.tiles = -1;
             put(last);
+        } else {
+            pieces(false, [&](const ChunkWalk &w, int) { return copy_piece(w); });
         }
-        __syncwarp();
+        for (int k = max(0, issued - rs); k < issued; ++k) mbar_wait(bar(b_full + k % rs), (k / rs) & 1);   // copies in flight
     } else if (warp == kCQk || warp == kCPv) {
         // ================= MMAs: one thread each =================
         if (elect_one()) {
@@ -395,44 +453,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
             wait1(fin, 0);
         }
         __syncwarp();
-    } else if (warp == kCCopy) {
-        // ================= bulk copies, half tile after half tile =================
-        int issued = 0, st = 0, ph = 0;   // halves so far, the ring's slot and its phase
-        int *rec = reinterpret_cast<int *>(smem + C::REC_OFF);
-        // pages of 64 and more: one copy a half; of 32: two; of 16: four
-        const int run = pshift >= 6 ? 4 : pshift == 5 ? 2 : 1;
-        pieces(false, [&](const ChunkWalk &w, int) {
-            const int *bt = p.block_table + (size_t)w.b * p.table_stride;
-            const int n_half = 2 * w.tiles;
-            int pg = -1;
-            for (int t = 0; t < n_half; ++t, ++issued) {
-                if ((t & 7) == 0) {   // lane l: the page of sub-tile l % 4 of half t + l / 4
-                    const int x = w.s0 * kCN + (t + (lane >> 2)) * kCHalf + (lane & 3) * kWTile;
-                    pg = t + (lane >> 2) < n_half && x < w.L ? bt[x >> pshift] : -1;
-                    if (pg >= p.pool.n_pages) pg = -1;
-                }
-                if (issued >= C::RS && !wwait(C::B_RAWF + st, ph ^ 1)) return false;
-                int ok = (int)(__ballot_sync(0xffffffffu, pg >= 0) >> (4 * (t & 7))) & 15;
-                if (run == 4) ok = ok & 1 ? 15 : 0;
-                if (run == 2) ok = (ok & 1 ? 3 : 0) | (ok & 4 ? 12 : 0);
-                if (lane == 0) rec[st] = ok;
-                __syncwarp();   // the record before the arrival that publishes it
-                const uint32_t dst = sbase + C::RAW_OFF + st * C::RAW, full = bar(C::B_RAW + st);
-                mbar_arrive_expect_tx_w(full, __popc(ok) * T::BYTES);
-                const int tile = run == 4 ? ((w.s0 * kCN + t * kCHalf) & ((1 << pshift) - 1)) >> 4 : 0;
-#pragma unroll
-                for (int q = 0; q < kCSub; ++q)
-                    if (q % run == 0 && (ok >> q & 1))
-                        bulk_g2s_w(dst + q * T::BYTES, tile_of(p.pool, __shfl_sync(0xffffffffu, pg, 4 * (t & 7) + q), w.h, tile, T::BYTES),
-                                   run * T::BYTES, full);
-                if (++st == C::RS) {
-                    st = 0;
-                    ph ^= 1;
-                }
-            }
-            return true;
-        });
-        for (int k = max(0, issued - C::RS); k < issued; ++k) mbar_wait(bar(C::B_RAW + k % C::RS), (k / C::RS) & 1);   // copies in flight
     }
     } else if (warp >= kCKConv0) {
     regs_dec<kCRegsConv>();
@@ -444,15 +464,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
         int hh = 0;
         pieces(false, [&](const ChunkWalk &w, int) {
             for (int t = 0; t < 2 * w.tiles; ++t, ++hh) {
-                const int st = hh % C::RS, ob = hh & 1, j = hh >> 1;
-                if (!wwait(C::B_RAW + st, (hh / C::RS) & 1) || (j >= 1 && !wwait(C::B_KF + ob, (j - 1) & 1))) return false;
-                const uint8_t *raw = smem + C::RAW_OFF + st * C::RAW;
+                const int st = hh % C::RSK, ob = hh & 1, j = hh >> 1;
+                if (!wwait(C::B_RAWK + st, (hh / C::RSK) & 1) || (j >= 1 && !wwait(C::B_KF + ob, (j - 1) & 1))) return false;
+                const uint8_t *raw = smem + C::RAWK_OFF + st * C::RAWK;
                 uint8_t *kh = smem + C::KH_OFF + ob * C::KBUF + (u / 8) * C::K_SBO + (u % 8) * 16 + dg * C::K_LBO, *kl = kh + (C::KL_OFF - C::KH_OFF);
 #pragma unroll 2
                 for (int q = 0; q < kCSub; ++q) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(raw + q * T::BYTES + i * 512 + lane * 16);
-                    const __half s0 = __ushort_as_half(*reinterpret_cast<const uint16_t *>(raw + q * T::BYTES + soff));
-                    const __half s1 = __ushort_as_half(*reinterpret_cast<const uint16_t *>(raw + q * T::BYTES + soff + 4));
+                    const uint4 v = *reinterpret_cast<const uint4 *>(raw + q * C::KPART + i * 512 + lane * 16);
+                    const __half s0 = __ushort_as_half(*reinterpret_cast<const uint16_t *>(raw + q * C::KPART + soff));
+                    const __half s1 = __ushort_as_half(*reinterpret_cast<const uint16_t *>(raw + q * C::KPART + soff + 4));
                     const __half2 k05 = __half2half2(__ushort_as_half(kHalfBits));
                     uint4 hi, lo;
                     u8x8_hilo(v.x, v.y, __hmul2(__half2half2(s0), k05), hi, lo);
@@ -468,7 +488,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(bar(C::B_KR + ob));
-                    mbar_arrive(bar(C::B_RAWF + st));
+                    mbar_arrive(bar(C::B_RAWKF + st));
                 }
             }
             return true;
@@ -480,10 +500,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
         int hh = 0;
         pieces(false, [&](const ChunkWalk &w, int) {
             for (int t = 0; t < 2 * w.tiles; ++t, ++hh) {
-                const int st = hh % C::RS, ob = hh & 1, j = hh >> 1;
-                if (!wwait(C::B_RAW + st, (hh / C::RS) & 1) || (j >= 1 && !wwait(C::B_VF + ob, (j - 1) & 1))) return false;
-                const uint8_t *tv = smem + C::RAW_OFF + st * C::RAW + q * T::BYTES + T::V_OFF, *ts = tv + (T::VS_OFF - T::V_OFF) + 4 * half * 16 + 4 * bb;
-                const int ok = reinterpret_cast<const int *>(smem + C::REC_OFF)[st];
+                const int st = hh % C::RSV, ob = hh & 1, j = hh >> 1;
+                if (!wwait(C::B_RAWV + st, (hh / C::RSV) & 1) || (j >= 1 && !wwait(C::B_VF + ob, (j - 1) & 1))) return false;
+                const uint8_t *tv = smem + C::RAWV_OFF + st * C::RAWV + q * C::VPART, *ts = tv + (T::VS_OFF - T::V_OFF) + 4 * half * 16 + 4 * bb;
+                const int ok = reinterpret_cast<const int *>(smem + C::REC_OFF)[C::RSK + st];
                 const int x = w.s0 * kCN + t * kCHalf, p0 = x + kWTile * q + 8 * half;
                 const bool full = ok == 15 && x + kCHalf - 1 <= w.lim_hi;
                 const __half2 k05 = __half2half2(__ushort_as_half(kHalfBits));
@@ -518,7 +538,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(bar(C::B_VR + ob));
-                    mbar_arrive(bar(C::B_RAWF + st));
+                    mbar_arrive(bar(C::B_RAWVF + st));
                 }
             }
             return true;
