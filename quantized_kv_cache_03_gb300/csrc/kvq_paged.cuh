@@ -101,6 +101,15 @@ struct PagedCut {
     int c0, np;   // pieces: slot 1 of CTA c0, slot 0 of CTAs c0 + 1 .. c0 + np - 1
 };
 
+// The cut tiles and pieces of one attention launch, for the combine.
+struct PagedPieces {
+    const PagedCut *cuts;
+    const float *lse, *o;
+    int rows;     // rows of a tile
+    int ctas;     // of the launch; 0: it cut nothing
+    int spread;   // combine blocks per CTA
+};
+
 struct PagedAttnParams {
     PoolDesc pool;
     const uint16_t *q;
@@ -143,15 +152,13 @@ cudaError_t launch_page_tables(const TableParams &p, cudaStream_t s, bool pdl);
 cudaError_t launch_paged_append(const PagedRowsParams &p, int v_type, int k_type, cudaStream_t s, bool pdl);
 cudaError_t launch_paged_gather(const PagedRowsParams &p, int v_type, int k_type, int out_type, cudaStream_t s,
                                 bool pdl);
-cudaError_t launch_paged_combine(const PagedAttnParams &p, int n_ctas, int tile_rows, int out_type, cudaStream_t s,
-                                 bool pdl);
+cudaError_t launch_paged_combine(const PagedAttnParams &p, const PagedPieces &g0, const PagedPieces &g1, int out_type,
+                                 cudaStream_t s, bool pdl);
 // Row-tile attention (kvq_paged_attn_q4.cu / _q8.cu): nt = 8-row tiles per CTA (1 or 2).
 cudaError_t prepare_paged_q4(int nt, int k_type, int out_type, int *ctas_per_sm);
 cudaError_t prepare_paged_q8(int nt, int k_type, int out_type, int *ctas_per_sm);
-cudaError_t launch_paged_q4(const PagedAttnParams &p, int nt, int k_type, int out_type, int n_ctas, cudaStream_t s,
-                            bool pdl);
-cudaError_t launch_paged_q8(const PagedAttnParams &p, int nt, int k_type, int out_type, int n_ctas, cudaStream_t s,
-                            bool pdl);
+cudaError_t launch_paged_q4(const PagedAttnParams &p, int nt, int k_type, int out_type, int n_ctas, cudaStream_t s);
+cudaError_t launch_paged_q8(const PagedAttnParams &p, int nt, int k_type, int out_type, int n_ctas, cudaStream_t s);
 
 // Chunk attention on tcgen05 (kvq_paged_chunk_q4.cu / _q8.cu), int8 K.
 constexpr int kChunkRows = 128;

@@ -350,28 +350,30 @@ kvq_status kvq_paged_attn(const kvq_paged_desc *a, void *workspace, size_t works
     const bool pdl = pdl_on();
     const kvq_pages *g = a->pages;
     const bool q4 = g->v_type == KVQ_V_Q4_0;
-    auto pieces = [&](const Part &pt) {
+    PagedPieces cut[2] = {};
+    auto pieces = [&](const Part &pt, PagedPieces &c) {
         char *w = static_cast<char *>(workspace);
         p.cuts = reinterpret_cast<PagedCut *>(w + pt.cut_off);
         p.ws_lse = reinterpret_cast<float *>(w + pt.lse_off);
         p.ws_o = reinterpret_cast<float *>(w + pt.o_off);
+        // a cut tile is merged by at least two CTAs' blocks of eight warps
+        c = PagedPieces{p.cuts, p.ws_lse, p.ws_o, pt.rows, pt.n_ctas > 1 ? pt.n_ctas : 0, (pt.rows + 15) / 16};
     };
     cudaError_t e = cudaSuccess;
     if (pl.tile.n_ctas > 0) {
-        pieces(pl.tile);
+        pieces(pl.tile, cut[0]);
         p.min_rows = 1;
         p.max_rows = pl.chunk_rows - 1;
-        e = q4 ? launch_paged_q4(p, pl.nt, g->k_type, a->out_type, pl.tile.n_ctas, s, pdl)
-               : launch_paged_q8(p, pl.nt, g->k_type, a->out_type, pl.tile.n_ctas, s, pdl);
-        if (e == cudaSuccess && pl.tile.n_ctas > 1) e = launch_paged_combine(p, pl.tile.n_ctas, pl.tile.rows, a->out_type, s, pdl);
+        e = q4 ? launch_paged_q4(p, pl.nt, g->k_type, a->out_type, pl.tile.n_ctas, s)
+               : launch_paged_q8(p, pl.nt, g->k_type, a->out_type, pl.tile.n_ctas, s);
     }
     if (e == cudaSuccess && pl.chunk.n_ctas > 0) {
-        pieces(pl.chunk);
+        pieces(pl.chunk, cut[1]);
         p.min_rows = pl.chunk_rows;
         p.max_rows = INT_MAX;
         e = q4 ? launch_chunk_q4(p, a->out_type, pl.chunk.n_ctas, s, pdl) : launch_chunk_q8(p, a->out_type, pl.chunk.n_ctas, s, pdl);
-        if (e == cudaSuccess && pl.chunk.n_ctas > 1) e = launch_paged_combine(p, pl.chunk.n_ctas, pl.chunk.rows, a->out_type, s, pdl);
     }
+    if (e == cudaSuccess) e = launch_paged_combine(p, cut[0], cut[1], a->out_type, s, pdl);
     return done(e);
 }
 

@@ -14,17 +14,18 @@
 // per stage, two when pages hold 16 positions).  Nothing but the ring's
 // barriers synchronizes the main loop.
 //
-// Arithmetic per stage, for rows g and (NT = 2) g + 8 of the lane 4g + c:
-//   S = Q K^T   m16n8k16, A = query codes (rows 8..15 zero when NT = 1), B = K
-//               codes entered as 1152 + code; per 32-block an accumulator that
+// Arithmetic per stage (m16n8k16 throughout):
+//   scores      K codes enter as 1152 + code; per 32-block an accumulator that
 //               starts at -1152 * (sum of the row's codes), so it ends exactly
 //               at the integer block dot; score = sum_b I_b * sq_b * sk_b.
-//   O^T += V^T P^T   m16n8k16, A = V codes (exact fp16 integers), B = p * d
-//               per block.  The accumulator layout of S (row g, positions 2c,
-//               2c + 1) is the B layout of P^T (k 2c, 2c + 1, n = g): no
-//               transpose.  KVQ_OUT_F32 splits p * d into an fp16 high and low
-//               part (two MMAs, about 22 bits), KVQ_OUT_F16 rounds it once
-//               (2^-12 relative to each term, below the output's own rounding).
+//               NT = 2: S = Q K^T, 16 query rows by 8 positions; NT = 1: S^T =
+//               K Q^T, 16 positions by 8 query rows (Q as A would leave half of
+//               every MMA and fragment empty).
+//   O^T += V^T P^T   A = V codes (exact fp16 integers), B = p * d per block.  S
+//               (row g, positions 2c, 2c + 1) already has P^T's B layout (k 2c,
+//               2c + 1, n = g); S^T is turned by movmatrix.  KVQ_OUT_F32 splits
+//               p * d into an fp16 high and low part (two MMAs, about 22 bits),
+//               KVQ_OUT_F16 rounds it once (2^-11 at most of each term).
 // Softmax in base 2.  A row's reference maximum is raised only when a score
 // passes it by more than kSlack = 1, and exponents are taken kShift above it:
 // p reaches 2^(kShift + 1), which with the largest V scale (516 for q8_0, 8188
@@ -83,9 +84,9 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const 
         for (int st = 0; st < S; ++st) mbar_init(bar_s + st * 8, 1);
         fence_mbar_init();
     }
-    pdl_wait();
     pdl_trigger();
 
+    const uint32_t pick = g & 1 ? 0x3232u : 0x1010u;   // NT = 1: the lane's half of a K scale pair, twice
     auto seq_tiles = [&](int n) { return (n * p.gmax + C::ROWS - 1) / C::ROWS; };   // row tiles per kv head
     auto seq_stages = [&](int len) { return max(1, (len + kStagePos - 1) / kStagePos); };
     long long pos, per;
@@ -176,10 +177,12 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const 
 
             // ---- query rows -> fragments ----
             uint32_t qa[8][2 * NT];            // [k16 step][row g: k 2c.., k 2c + 8..; row g + 8 likewise]
-            float seed[kNB][NT], sq[kNB][NT];  // int8 K: accumulator seeds and row scales per block
+            // the two rows whose scores the lane holds: 2c, 2c + 1 (NT = 1), g, g + 8 (NT = 2)
+            const int lrow[2] = {NT == 1 ? 2 * c : g, NT == 1 ? 2 * c + 1 : g + 8};
+            // int8 K: scales and accumulator seeds [row][block]; read again for each stage, the registers hold enough
+            float *qs = reinterpret_cast<float *>(smem + C::QS_OFF), *qsum = reinterpret_cast<float *>(smem + C::QSUM_OFF);
             {
                 uint32_t *qw = reinterpret_cast<uint32_t *>(smem + C::Q_OFF);
-                float *qs = reinterpret_cast<float *>(smem + C::QS_OFF), *qsum = reinterpret_cast<float *>(smem + C::QSUM_OFF);
 #pragma unroll
                 for (int k = 0; k < C::ROWS / W; ++k) {
                     const int r = warp + W * k;
@@ -227,26 +230,25 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const 
                                 qa[2 * bb + kk][2 * nt] = code_pair(w, 0);
                                 qa[2 * bb + kk][2 * nt + 1] = code_pair(w, 2);
                             }
-                            seed[bb][nt] = qsum[r * kNB + bb];
-                            sq[bb][nt] = qs[r * kNB + bb];
                         }
                     }
                 }
             }
-            float m[NT], l[NT], mu[NT];
-            int lim[NT];
+            float m[2], l[2], mu[2];
+            int lim[2];
             float acc[8][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int r = g + 8 * nt;
-                lim[nt] = r < R ? (p.causal ? L - n + (row0 + r) / gsz : L - 1) : -1;
-                m[nt] = -INFINITY;
-                mu[nt] = l[nt] = 0.f;
+            for (int e = 0; e < 2; ++e) {
+                lim[e] = lrow[e] < R ? (p.causal ? L - n + (row0 + lrow[e]) / gsz : L - 1) : -1;
+                m[e] = -INFINITY;
+                mu[e] = l[e] = 0.f;
+            }
 #pragma unroll
-                for (int mt = 0; mt < 8; ++mt)
+            for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) acc[mt][nt][k] = 0.f;
-            }
 
             bool lost = false;
 #pragma unroll 1
@@ -256,11 +258,14 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const 
                     lost = true;
                     break;
                 }
-                const uint8_t *stg = ring + sl * C::STAGE;
+                uint8_t *stg = ring + sl * C::STAGE;
                 const int x = (s0 + warp + W * j) * kStagePos, ok = (okm >> (2 * sl)) & 3;
-                auto stage = [&](auto full_tag) {
-                    constexpr bool FULL = decltype(full_tag)::value;
-                    float2 s[NT][4];   // [8-position group]: positions 8i + 2c, + 1 of row g + 8 nt
+                const bool full = ok == 3 && x + kStagePos - 1 <= lim_lo;   // every row sees the whole stage
+                {
+                    // scores of 8-position group i (of four): NT = 1 position 8i + g, rows (2c, 2c + 1);
+                    // NT = 2 positions (8i + 2c, + 1), [row g, row g + 8]
+                    float2 s[NT][4];
+                    auto h2f = [](uint32_t w) { return half2_of(w); };
 #pragma unroll
                     for (int t = 0; t < C::TPS; ++t) {
                         const uint8_t *tk = stg + t * T::BYTES;
@@ -269,79 +274,140 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const 
 #pragma unroll
                             for (int ks = 0; ks < 8; ++ks) {
                                 const uint4 k4 = *reinterpret_cast<const uint4 *>(tk + ks * 512 + lane * 16);
-                                const uint32_t a[4] = {qa[ks][0], NT == 2 ? qa[ks][2 * NT - 2] : 0u, qa[ks][1], NT == 2 ? qa[ks][2 * NT - 1] : 0u};
-                                mma_f16_16816(d[0], a, k4.x, k4.z);
-                                mma_f16_16816(d[1], a, k4.y, k4.w);
+                                if constexpr (NT == 1) {
+                                    const uint32_t a[4] = {k4.x, k4.y, k4.z, k4.w};
+                                    mma_f16_16816(d[0], a, qa[ks][0], qa[ks][1]);
+                                } else {
+                                    const uint32_t a[4] = {qa[ks][0], qa[ks][2 * NT - 2], qa[ks][1], qa[ks][2 * NT - 1]};
+                                    mma_f16_16816(d[0], a, k4.x, k4.z);
+                                    mma_f16_16816(d[1], a, k4.y, k4.w);
+                                }
                             }
+                            const float2 sc = make_float2(p.qk_scale_log2, p.qk_scale_log2);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int i = 0; i < 2; ++i)
-                                    s[nt][2 * t + i] = mul2(make_float2(d[i][2 * nt], d[i][2 * nt + 1]), make_float2(p.qk_scale_log2, p.qk_scale_log2));
+                            for (int i = 0; i < 2; ++i) {
+                                if constexpr (NT == 1) {
+                                    s[0][2 * t + i] = mul2(make_float2(d[0][2 * i], d[0][2 * i + 1]), sc);
+                                } else {
+                                    s[0][2 * t + i] = mul2(make_float2(d[i][0], d[i][1]), sc);
+                                    s[NT - 1][2 * t + i] = mul2(make_float2(d[i][2], d[i][3]), sc);
+                                }
+                            }
                         } else {
                             uint4 kk[2][2], sk[2];
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
 #pragma unroll
                                 for (int hb = 0; hb < 2; ++hb) kk[i][hb] = *reinterpret_cast<const uint4 *>(tk + (2 * i + hb) * 512 + lane * 16);
-                                sk[i] = *reinterpret_cast<const uint4 *>(tk + T::KS_OFF + (4 * i + c) * 16);
+                                // NT = 1: the scale pairs of positions 2 (g/2), + 1; NT = 2: of 2c, 2c + 1
+                                sk[i] = *reinterpret_cast<const uint4 *>(tk + T::KS_OFF + (4 * i + (NT == 1 ? g >> 1 : c)) * 16);
                             }
 #pragma unroll
                             for (int bb = 0; bb < kNB; ++bb) {
+                                __syncwarp();                  // as below
+                                uint32_t lo[2][2], hi[2][2];   // [position group][k16 step]: K bytes 0, 1 and 2, 3 as 1152 + code
 #pragma unroll
                                 for (int i = 0; i < 2; ++i) {
                                     const uint4 &kw = kk[i][bb >> 1];
                                     const uint32_t w0 = (bb & 1) ? kw.z : kw.x, w1 = (bb & 1) ? kw.w : kw.y;
-                                    const uint32_t a0[4] = {qa[2 * bb][0], NT == 2 ? qa[2 * bb][2 * NT - 2] : 0u, qa[2 * bb][1], NT == 2 ? qa[2 * bb][2 * NT - 1] : 0u};
-                                    const uint32_t a1[4] = {qa[2 * bb + 1][0], NT == 2 ? qa[2 * bb + 1][2 * NT - 2] : 0u, qa[2 * bb + 1][1], NT == 2 ? qa[2 * bb + 1][2 * NT - 1] : 0u};
-                                    const uint32_t sd0 = __float_as_uint(seed[bb][0]), sd1 = __float_as_uint(NT == 2 ? seed[bb][NT - 1] : 0.f);
+                                    lo[i][0] = __byte_perm(w0, 0x64646464u, 0x4140);
+                                    hi[i][0] = __byte_perm(w0, 0x64646464u, 0x4342);
+                                    lo[i][1] = __byte_perm(w1, 0x64646464u, 0x4140);
+                                    hi[i][1] = __byte_perm(w1, 0x64646464u, 0x4342);
+                                }
+                                const uint32_t sd0 = __float_as_uint(qsum[lrow[0] * kNB + bb]), sd1 = __float_as_uint(qsum[lrow[1] * kNB + bb]);
+                                const float sq[2] = {qs[lrow[0] * kNB + bb], qs[lrow[1] * kNB + bb]};
+                                if constexpr (NT == 1) {   // S^T = K Q^T: rows are the 16 positions
                                     float d[4];
-                                    mma_f16_16816_c4(d, a0, __byte_perm(w0, 0x64646464u, 0x4140), __byte_perm(w0, 0x64646464u, 0x4342), make_uint4(sd0, sd0, sd1, sd1));
-                                    mma_f16_16816(d, a1, __byte_perm(w1, 0x64646464u, 0x4140), __byte_perm(w1, 0x64646464u, 0x4342));
-                                    const uint32_t sw = bb == 0 ? sk[i].x : bb == 1 ? sk[i].y : bb == 2 ? sk[i].z : sk[i].w;
-                                    const float2 s2 = half2_of(sw);
+                                    const uint32_t a0[4] = {lo[0][0], lo[1][0], hi[0][0], hi[1][0]}, a1[4] = {lo[0][1], lo[1][1], hi[0][1], hi[1][1]};
+                                    mma_f16_16816_c4(d, a0, qa[2 * bb][0], qa[2 * bb][1], make_uint4(sd0, sd1, sd0, sd1));
+                                    mma_f16_16816(d, a1, qa[2 * bb + 1][0], qa[2 * bb + 1][1]);
+                                    const float2 q2 = make_float2(sq[0], sq[1]);
 #pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt) {
-                                        const float2 v = mul2(make_float2(d[2 * nt], d[2 * nt + 1]), make_float2(sq[bb][nt], sq[bb][nt]));
-                                        s[nt][2 * t + i] = bb == 0 ? mul2(v, s2) : fma2(v, s2, s[nt][2 * t + i]);
+                                    for (int i = 0; i < 2; ++i) {
+                                        const uint32_t sw = bb == 0 ? sk[i].x : bb == 1 ? sk[i].y : bb == 2 ? sk[i].z : sk[i].w;
+                                        const float f = half2_of(__byte_perm(sw, sw, pick)).x;
+                                        const float2 v = mul2(make_float2(d[2 * i], d[2 * i + 1]), q2), s2 = make_float2(f, f);
+                                        s[0][2 * t + i] = bb == 0 ? mul2(v, s2) : fma2(v, s2, s[0][2 * t + i]);
+                                    }
+                                } else {                   // S = Q K^T: rows are the query rows
+#pragma unroll
+                                    for (int i = 0; i < 2; ++i) {
+                                        float d[4];
+                                        const uint32_t a0[4] = {qa[2 * bb][0], qa[2 * bb][2 * NT - 2], qa[2 * bb][1], qa[2 * bb][2 * NT - 1]};
+                                        const uint32_t a1[4] = {qa[2 * bb + 1][0], qa[2 * bb + 1][2 * NT - 2], qa[2 * bb + 1][1], qa[2 * bb + 1][2 * NT - 1]};
+                                        mma_f16_16816_c4(d, a0, lo[i][0], hi[i][0], make_uint4(sd0, sd0, sd1, sd1));
+                                        mma_f16_16816(d, a1, lo[i][1], hi[i][1]);
+                                        const float2 s2 = h2f(bb == 0 ? sk[i].x : bb == 1 ? sk[i].y : bb == 2 ? sk[i].z : sk[i].w);
+#pragma unroll
+                                        for (int nt = 0; nt < NT; ++nt) {
+                                            const float2 v = mul2(make_float2(d[2 * nt], d[2 * nt + 1]), make_float2(sq[nt], sq[nt]));
+                                            s[nt][2 * t + i] = bb == 0 ? mul2(v, s2) : fma2(v, s2, s[nt][2 * t + i]);
+                                        }
                                     }
                                 }
                             }
                         }
                     }
-                    if (!FULL) {
+                    if (!full) {
+                        // V scales of positions that no row sees may hold anything: p is 0 there, make d so too
+                        const int t = lane >> 4, q1 = x + 16 * t + 2 * ((lane & 15) >> 1);
+                        const uint32_t keep = !((ok >> t) & 1) ? 0u : (q1 <= lim_hi ? 0xffffu : 0u) | (q1 + 1 <= lim_hi ? 0xffff0000u : 0u);
+                        uint2 *d4 = reinterpret_cast<uint2 *>(stg + t * T::BYTES + T::VS_OFF + 8 * (lane & 15));
+                        *d4 = make_uint2(d4->x & keep, d4->y & keep);
+                        __syncwarp();
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const int q0 = x + 8 * i + 2 * c;
+                            const int q0 = x + 8 * i + (NT == 1 ? g : 2 * c);
                             const bool live = (ok >> (i >> 1)) & 1;
+                            if constexpr (NT == 1) {
+                                s[0][i].x = live && q0 <= lim[0] ? s[0][i].x : -INFINITY;
+                                s[0][i].y = live && q0 <= lim[1] ? s[0][i].y : -INFINITY;
+                            } else {
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                s[nt][i].x = live && q0 <= lim[nt] ? s[nt][i].x : -INFINITY;
-                                s[nt][i].y = live && q0 + 1 <= lim[nt] ? s[nt][i].y : -INFINITY;
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    s[nt][i].x = live && q0 <= lim[nt] ? s[nt][i].x : -INFINITY;
+                                    s[nt][i].y = live && q0 + 1 <= lim[nt] ? s[nt][i].y : -INFINITY;
+                                }
                             }
                         }
                     }
-                    // ---- softmax: a row's scores sit in the four lanes of one g ----
-                    float mx[NT];
-                    bool need = false;
+                    // ---- softmax: a row's scores sit in the eight lanes of one c (NT = 1) or the four of one g ----
+                    float mx[2];
+                    if constexpr (NT == 1) {
+                        mx[0] = fmaxf(fmaxf(s[0][0].x, s[0][1].x), fmaxf(s[0][2].x, s[0][3].x));
+                        mx[1] = fmaxf(fmaxf(s[0][0].y, s[0][1].y), fmaxf(s[0][2].y, s[0][3].y));
+                    } else {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mx[nt] = fmaxf(fmaxf(fmaxf(s[nt][0].x, s[nt][0].y), fmaxf(s[nt][1].x, s[nt][1].y)),
-                                       fmaxf(fmaxf(s[nt][2].x, s[nt][2].y), fmaxf(s[nt][3].x, s[nt][3].y)));
-                        need |= mx[nt] > m[nt] + (kShift + kSlack);
+                        for (int nt = 0; nt < NT; ++nt)
+                            mx[nt] = fmaxf(fmaxf(fmaxf(s[nt][0].x, s[nt][0].y), fmaxf(s[nt][1].x, s[nt][1].y)),
+                                           fmaxf(fmaxf(s[nt][2].x, s[nt][2].y), fmaxf(s[nt][3].x, s[nt][3].y)));
                     }
+                    const bool need = mx[0] > m[0] + (kShift + kSlack) || mx[1] > m[1] + (kShift + kSlack);
                     if (__any_sync(0xffffffffu, need)) {
+                        float al[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float v = mx[e];
+                            if constexpr (NT == 1) {
+                                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                            } else {
+                                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                            }
+                            v = fmaxf(m[e], v - kShift);   // m: the exponents' zero
+                            al[e] = v == -INFINITY ? 1.f : fast_exp2(m[e] - v);
+                            l[e] *= al[e];
+                            m[e] = v;
+                            mu[e] = v == -INFINITY ? 0.f : v;
+                        }
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            float v = fmaxf(mx[nt], __shfl_xor_sync(0xffffffffu, mx[nt], 1));
-                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-                            v = fmaxf(m[nt], v - kShift);   // m: the exponents' zero
-                            const float al = v == -INFINITY ? 1.f : fast_exp2(m[nt] - v);
-                            l[nt] *= al;
-                            m[nt] = v;
-                            mu[nt] = v == -INFINITY ? 0.f : v;
-                            // the accumulator's columns are rows 2c, 2c + 1: their factors sit in lanes 8c, 8c + 4
-                            const float2 a2 = make_float2(__shfl_sync(0xffffffffu, al, 8 * c), __shfl_sync(0xffffffffu, al, 8 * c + 4));
+                            // the accumulator's columns are rows 8 nt + 2c, + 1; with NT = 2 their factors sit in lanes 8c, 8c + 4
+                            float2 a2 = make_float2(al[0], al[1]);
+                            if constexpr (NT == 2) a2 = make_float2(__shfl_sync(0xffffffffu, al[nt], 8 * c), __shfl_sync(0xffffffffu, al[nt], 8 * c + 4));
 #pragma unroll
                             for (int mt = 0; mt < 8; ++mt) {
                                 const float2 lo = mul2(make_float2(acc[mt][nt][0], acc[mt][nt][1]), a2);
@@ -353,46 +419,62 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const 
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
+                        const float2 m2 = NT == 1 ? make_float2(mu[0], mu[1]) : make_float2(mu[nt], mu[nt]);
                         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float2 e = sub2(s[nt][i], make_float2(mu[nt], mu[nt]));
+                            const float2 e = sub2(s[nt][i], m2);
                             s[nt][i] = make_float2(fast_exp2(e.x), fast_exp2(e.y));
                             sum = add2(sum, s[nt][i]);
                         }
-                        l[nt] += sum.x + sum.y;
-                    }
-                    // ---- O^T += V^T P^T ----
-#pragma unroll
-                    for (int t = 0; t < C::TPS; ++t) {
-                        const uint8_t *tv = stg + t * T::BYTES + T::V_OFF, *ts = stg + t * T::BYTES + T::VS_OFF;
-                        constexpr int NVL = VT == KVQ_V_Q4_0 ? 1 : 2;
-                        uint4 vv[2][NVL], sv4[2];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                            for (int hb = 0; hb < NVL; ++hb) vv[i][hb] = *reinterpret_cast<const uint4 *>(tv + (NVL * i + hb) * 512 + lane * 16);
-                            sv4[i] = *reinterpret_cast<const uint4 *>(ts + (4 * i + c) * 16);
-                            if (!FULL) {   // scales of invisible positions may hold anything: p is 0 there, make d so too
-                                const int q0 = x + 16 * t + 8 * i + 2 * c;
-                                const bool live = (ok >> t) & 1;
-                                const uint32_t keep = (live && q0 <= lim_hi ? 0xffffu : 0u) | (live && q0 + 1 <= lim_hi ? 0xffff0000u : 0u);
-                                sv4[i].x &= keep; sv4[i].y &= keep; sv4[i].z &= keep; sv4[i].w &= keep;
-                            }
+                        if constexpr (NT == 1) {
+                            l[0] += sum.x;
+                            l[1] += sum.y;
+                        } else {
+                            l[nt] += sum.x + sum.y;
                         }
+                    }
+                    if constexpr (NT == 1) {   // (position, row) to (row, position): each fp32's halves turned as 8x8 matrices
 #pragma unroll
-                        for (int bb = 0; bb < kNB; ++bb) {
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t a = __float_as_uint(s[0][i].x), b2 = __float_as_uint(s[0][i].y);
+                            const uint32_t lo = movmatrix_t(__byte_perm(a, b2, 0x5410)), hi = movmatrix_t(__byte_perm(a, b2, 0x7632));
+                            s[0][i] = make_float2(__uint_as_float(__byte_perm(lo, hi, 0x5410)), __uint_as_float(__byte_perm(lo, hi, 0x7632)));
+                        }
+                    }
+                    // ---- O^T += V^T P^T, block by block ----
+#pragma unroll
+                    for (int hb = 0; hb < 2; ++hb) {   // blocks 2hb, 2hb + 1
+                        __syncwarp();                  // keeps the scheduler from loading the next blocks early and spilling
+                        uint4 vv[C::TPS][2];           // their V codes: q4 in x, y only
+                        uint2 sv[C::TPS][2];
+#pragma unroll
+                        for (int t = 0; t < C::TPS; ++t)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint8_t *tv = stg + t * T::BYTES + T::V_OFF, *ts = stg + t * T::BYTES + T::VS_OFF;
+                                if (VT == KVQ_V_Q4_0) {
+                                    const uint2 w = *reinterpret_cast<const uint2 *>(tv + i * 512 + lane * 16 + 8 * hb);
+                                    vv[t][i] = make_uint4(w.x, w.y, 0u, 0u);
+                                } else {
+                                    vv[t][i] = *reinterpret_cast<const uint4 *>(tv + (2 * i + hb) * 512 + lane * 16);
+                                }
+                                sv[t][i] = *reinterpret_cast<const uint2 *>(ts + (4 * i + c) * 16 + 8 * hb);
+                            }
+#pragma unroll
+                      for (int bb = 2 * hb; bb < 2 * hb + 2; ++bb) {
+                        // fp32 output: the stage's part is summed from zero and then added, so that the MMA's
+                        // truncating additions do not run over the whole sum (twice the plain form's error)
+                        float part[2][NT][4];
+#pragma unroll
+                        for (int t = 0; t < C::TPS; ++t) {
                             uint32_t a[2][4];
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 uint32_t r[2][2];
-                                if (VT == KVQ_V_Q4_0) {
-                                    const uint4 &v = vv[i][0];
-                                    v_codes<VT>(bb == 0 ? v.x : bb == 1 ? v.y : bb == 2 ? v.z : v.w, 0u, r);
-                                } else {
-                                    const uint4 &v = vv[i][NVL == 1 ? 0 : (bb >> 1)];
-                                    v_codes<VT>((bb & 1) ? v.z : v.x, (bb & 1) ? v.w : v.y, r);
-                                }
+                                const uint4 &v = vv[t][i];
+                                if (VT == KVQ_V_Q4_0) v_codes<VT>((bb & 1) ? v.y : v.x, 0u, r);
+                                else v_codes<VT>((bb & 1) ? v.z : v.x, (bb & 1) ? v.w : v.y, r);
                                 a[0][2 * i] = r[0][0];
                                 a[0][2 * i + 1] = r[0][1];
                                 a[1][2 * i] = r[1][0];
@@ -400,13 +482,16 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const 
                             }
                             float2 d2[2];
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) d2[i] = half2_of(bb == 0 ? sv4[i].x : bb == 1 ? sv4[i].y : bb == 2 ? sv4[i].z : sv4[i].w);
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t dw = (bb & 1) ? sv[t][i].y : sv[t][i].x;
+                                d2[i] = h2f(dw);
+                            }
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
                                 uint32_t hi[2], lo[2];
 #pragma unroll
                                 for (int i = 0; i < 2; ++i) {
-                                    const float2 xv = mul2(s[nt][2 * t + i], d2[i]);
+                                    float2 xv = mul2(s[nt][2 * t + i], d2[i]);
                                     hi[i] = pack_half2(xv.x, xv.y);
                                     if (!O16) {   // x - hi is exact in fp32
                                         const float2 y = sub2(xv, half2_of(hi[i]));
@@ -415,17 +500,29 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const 
                                 }
 #pragma unroll
                                 for (int h2 = 0; h2 < 2; ++h2) {
-                                    mma_f16_16816(acc[2 * bb + h2][nt], a[h2], hi[0], hi[1]);
-                                    if (!O16) mma_f16_16816(acc[2 * bb + h2][nt], a[h2], lo[0], lo[1]);
+                                    if (O16) {
+                                        mma_f16_16816(acc[2 * bb + h2][nt], a[h2], hi[0], hi[1]);
+                                    } else {
+                                        if (t == 0) mma_f16_16816_c4(part[h2][nt], a[h2], hi[0], hi[1], make_uint4(0u, 0u, 0u, 0u));
+                                        else mma_f16_16816(part[h2][nt], a[h2], hi[0], hi[1]);
+                                        mma_f16_16816(part[h2][nt], a[h2], lo[0], lo[1]);
+                                    }
                                 }
                             }
                         }
+                        if (!O16)
+#pragma unroll
+                            for (int h2 = 0; h2 < 2; ++h2)
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+                                    float(&o)[4] = acc[2 * bb + h2][nt];
+                                    const float2 u0 = add2(make_float2(o[0], o[1]), make_float2(part[h2][nt][0], part[h2][nt][1]));
+                                    const float2 u1 = add2(make_float2(o[2], o[3]), make_float2(part[h2][nt][2], part[h2][nt][3]));
+                                    o[0] = u0.x; o[1] = u0.y; o[2] = u1.x; o[3] = u1.y;
+                                }
+                      }
                     }
-                };
-                if (ok == 3 && x + kStagePos - 1 <= lim_lo)
-                    stage(std::integral_constant<bool, true>());
-                else
-                    stage(std::integral_constant<bool, false>());
+                }
                 __syncwarp();   // every lane has read the slot
                 if (issued < nj_live) {
                     fence_proxy_async_smem();
@@ -443,18 +540,19 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const 
 
             // ---- merge the warps in a fixed order and write ----
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 1);
-                l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 2);
+            for (int e = 0; e < 2; ++e) {
+                l[e] += __shfl_xor_sync(0xffffffffu, l[e], NT == 1 ? 4 : 1);
+                l[e] += __shfl_xor_sync(0xffffffffu, l[e], NT == 1 ? 8 : 2);
+                if (NT == 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
             }
             __syncthreads();   // every warp is done with its ring
             float *sm_o = reinterpret_cast<float *>(smem), *sm_m = reinterpret_cast<float *>(smem + C::ML_OFF);
             float *sm_l = sm_m + W * C::ROWS, *sm_inv = sm_l + W * C::ROWS, *sm_lse = sm_inv + C::ROWS;
-            if (c == 0)
+            if (NT == 1 ? g == 0 : c == 0)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    sm_m[warp * C::ROWS + g + 8 * nt] = m[nt];
-                    sm_l[warp * C::ROWS + g + 8 * nt] = l[nt];
+                for (int e = 0; e < 2; ++e) {
+                    sm_m[warp * C::ROWS + lrow[e]] = m[e];
+                    sm_l[warp * C::ROWS + lrow[e]] = l[e];
                 }
             __syncthreads();
             if (tid < R) {
@@ -535,8 +633,12 @@ cudaError_t prepare_paged_t(int *ctas)
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, fn, C::THREADS, C::SMEM);
 }
 
+// Never placed before the launch in front of it is through: beside that one's
+// last blocks the CTAs (three or four to an SM fill its shared memory) can leave
+// a hole that the last of them does not fit, and it then starts only when
+// another has finished (64 sequences, 456 CTAs: 370 us or up to 480 us).
 template <int NT, int VT, int KT, bool O16>
-cudaError_t launch_paged_t(const PagedAttnParams &p, int n_ctas, cudaStream_t s, bool pdl)
+cudaError_t launch_paged_t(const PagedAttnParams &p, int n_ctas, cudaStream_t s)
 {
     using C = PagedCfg<NT, VT, KT>;
     cudaLaunchConfig_t cfg = {};
@@ -544,11 +646,6 @@ cudaError_t launch_paged_t(const PagedAttnParams &p, int n_ctas, cudaStream_t s,
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, paged_attn_kernel<NT, VT, KT, O16>, p);
 }
 
@@ -565,9 +662,9 @@ cudaError_t launch_paged_t(const PagedAttnParams &p, int n_ctas, cudaStream_t s,
         return KVQ_PAGED_PICK(prepare_paged_t, VT, nt, k_type, out_type, ctas);                                      \
     }                                                                                                                \
     cudaError_t launch_paged_##SUFFIX(const PagedAttnParams &p, int nt, int k_type, int out_type, int n_ctas,        \
-                                      cudaStream_t s, bool pdl)                                                      \
+                                      cudaStream_t s)                                                                \
     {                                                                                                                \
-        return KVQ_PAGED_PICK(launch_paged_t, VT, nt, k_type, out_type, p, n_ctas, s, pdl);                          \
+        return KVQ_PAGED_PICK(launch_paged_t, VT, nt, k_type, out_type, p, n_ctas, s);                               \
     }
 
 }  // namespace kvq

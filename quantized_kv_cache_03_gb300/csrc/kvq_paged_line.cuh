@@ -14,6 +14,15 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w, int k0)
 }
 __device__ __forceinline__ float2 half2_of(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
 
+// (a & mask) | bits in one instruction (left to itself the compiler uses two,
+// each with a constant of its own).
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(mask), "r"(bits));
+    return r;
+}
+
 // V A-fragment registers of one 32-block for the position pair (t, t + 1):
 // reg[h2][half] = the exact codes of head dim g + 8 half of m-tile 2 bb + h2
 // (dims as pv_dim: q4_0 32bb + 16h2 + 2g + half, q8_0 32bb + 4g + 2h2 + half).
@@ -26,10 +35,10 @@ __device__ __forceinline__ void v_codes(uint32_t w0, uint32_t w1, uint32_t (&reg
         const __half2 k1032 = __half2half2(__ushort_as_half(0x6408)), k16th = __half2half2(__ushort_as_half(0x2c00)),
                       km72 = __half2half2(__ushort_as_half(0xd480));
         const uint32_t w8 = w0 >> 8;
-        put(reg[0][0], __hsub2(h2((w0 & 0x000F000Fu) | 0x64006400u), k1032));
-        put(reg[0][1], __hsub2(h2((w8 & 0x000F000Fu) | 0x64006400u), k1032));
-        put(reg[1][0], __hfma2(h2((w0 & 0x00F000F0u) | 0x64006400u), k16th, km72));
-        put(reg[1][1], __hfma2(h2((w8 & 0x00F000F0u) | 0x64006400u), k16th, km72));
+        put(reg[0][0], __hsub2(h2(and_or(w0, 0x000F000Fu, 0x64006400u)), k1032));
+        put(reg[0][1], __hsub2(h2(and_or(w8, 0x000F000Fu, 0x64006400u)), k1032));
+        put(reg[1][0], __hfma2(h2(and_or(w0, 0x00F000F0u, 0x64006400u)), k16th, km72));
+        put(reg[1][1], __hfma2(h2(and_or(w8, 0x00F000F0u, 0x64006400u)), k16th, km72));
     } else {                  // code + 128 under the exponent of 1024, minus 1152
         const __half2 k1152 = __half2half2(__ushort_as_half(0x6480));
         put(reg[0][0], __hsub2(h2(__byte_perm(w0, 0x64646464u, 0x4140)), k1152));

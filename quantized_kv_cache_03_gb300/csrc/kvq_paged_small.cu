@@ -299,128 +299,136 @@ cudaError_t launch_paged_gather(const PagedRowsParams &p, int v_type, int k_type
 }
 
 // ---------------------------------------------------------------------------
-// Combine: the pieces of a row tile that several CTAs of the attention launch
-// attended.  Block i shares the merge of the cut tile its CTA's slot 1 began
-// and of the one its slot 0 went on with, so a tile cut into np pieces is
-// merged by np blocks.  Few pieces: a warp per row, the pieces one after
-// another.  Many: a block per row, the pieces dealt to the warps, merged in
-// warp order.  Both orders are fixed by the lengths alone.
+// Combine: the pieces of the row tiles that several CTAs of an attention launch
+// attended, for both launches of a call at once.  The pieces of a tile are
+// weighted by exp(lse_i - max lse) / sum; what bounds it is the latency of its
+// rounds of loads.  The blocks of CTA i share the merge of the tile its slot 1
+// began and of the one its slot 0 went on with, so a tile cut into np pieces is
+// merged by np * spread blocks; the chunk launch's tiles of 128 rows have a
+// spread that leaves each warp about one row.  Few pieces: a warp per row, the
+// pieces one after another.  Many: a block per row, 16 dims to a warp, eight
+// pieces side by side in its lanes, joined by shuffles.  Both orders are fixed
+// by the lengths alone.  Four loads in flight at 64 registers measured better
+// than eight at 80: more blocks fit beside the attention's last CTAs (512-token
+// chunk over 32768 positions: 463 against 466 us for the whole call).
 // ---------------------------------------------------------------------------
 constexpr int kPcWarps = 8;
-constexpr int kPcFew = 8;   // pieces up to which a warp takes a row alone
+constexpr int kPcFew = 8;    // pieces up to which a warp takes a row alone
+constexpr int kPcLoads = 4;  // pieces in flight per lane
 
 struct Merged {
     float m, w;
     float4 o;
+    bool poisoned;
+
+    __device__ __forceinline__ Merged() : m(-INFINITY), w(0.f), o(make_float4(0.f, 0.f, 0.f, 0.f)), poisoned(false) {}
+    // joins weight w2 at maximum m2, with its sums
+    __device__ __forceinline__ void join(float m2, float w2, const float4 &v)
+    {
+        if (!(m2 > -INFINITY)) return;
+        const float mx = fmaxf(m, m2);
+        const float f = m == -INFINITY ? 0.f : expf(m - mx), e = expf(m2 - mx);
+        w = fmaf(w, f, w2 * e);
+        o.x = fmaf(e, v.x, o.x * f);
+        o.y = fmaf(e, v.y, o.y * f);
+        o.z = fmaf(e, v.z, o.z * f);
+        o.w = fmaf(e, v.w, o.w * f);
+        m = mx;
+    }
 };
 
-// Pieces first, first + step, ... of a row: running maximum, weight and sum.
-__device__ __forceinline__ Merged merge_pieces(const PagedAttnParams &p, const PagedCut &c, int rows, int r, int first,
-                                               int step, int lane)
+// Pieces first, first + step, ... of a row, four dims from d on.
+__device__ __forceinline__ Merged merge_pieces(const PagedPieces &g, const PagedCut &c, int r, int first, int step, int d)
 {
-    Merged a{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    bool poisoned = false;
-    for (int k0 = first; k0 < c.np; k0 += 4 * step) {
-        float lv[4];
-        float4 v[4];
+    Merged a;
+    for (int k0 = first; k0 < c.np; k0 += kPcLoads * step) {
+        float lv[kPcLoads];
+        float4 v[kPcLoads];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kPcLoads; ++k) {
             const int j = k0 + k * step;
             lv[k] = -INFINITY;
             v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (j < c.np) {
-                const size_t at = ((size_t)(c.c0 + j) * 2 + (j == 0 ? 1 : 0)) * rows + r;
-                lv[k] = p.ws_lse[at];
-                v[k] = reinterpret_cast<const float4 *>(p.ws_o + at * kD)[lane];
+                const size_t at = ((size_t)(c.c0 + j) * 2 + (j == 0 ? 1 : 0)) * g.rows + r;
+                lv[k] = g.lse[at];
+                v[k] = *reinterpret_cast<const float4 *>(g.o + at * kD + d);
             }
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            poisoned |= lv[k] != lv[k];
-            if (!(lv[k] > -INFINITY)) continue;
-            const float mx = fmaxf(a.m, lv[k]);
-            const float f = (a.m == -INFINITY) ? 0.f : expf(a.m - mx), w = expf(lv[k] - mx);
-            a.w = fmaf(a.w, f, w);
-            a.o.x = fmaf(w, v[k].x, a.o.x * f);
-            a.o.y = fmaf(w, v[k].y, a.o.y * f);
-            a.o.z = fmaf(w, v[k].z, a.o.z * f);
-            a.o.w = fmaf(w, v[k].w, a.o.w * f);
-            a.m = mx;
+        for (int k = 0; k < kPcLoads; ++k) {
+            a.poisoned |= lv[k] != lv[k];   // a piece whose CTA lost a copy: the row is NaN
+            a.join(lv[k], 1.f, v[k]);
         }
-    }
-    if (poisoned) {   // a piece whose CTA lost a copy: the row is NaN
-        a.m = INFINITY;
-        a.w = __int_as_float(0x7fc00000);
     }
     return a;
 }
 
 template <bool O16>
-__device__ __forceinline__ void put_merged(const PagedAttnParams &p, size_t row, const Merged &a, int lane)
+__device__ __forceinline__ void put_merged(const PagedAttnParams &p, size_t row, const Merged &a, int d)
 {
-    const bool any = !(a.w <= 0.f);
-    const float inv = any ? 1.f / a.w : 0.f;
+    const float nan = __int_as_float(0x7fc00000);
+    const bool any = a.w > 0.f;
+    const float inv = a.poisoned ? nan : any ? 1.f / a.w : 0.f;
     const float x[4] = {a.o.x * inv, a.o.y * inv, a.o.z * inv, a.o.w * inv};
-    put4<O16>(p.out, row * kD + 4 * lane, x);
-    if (lane == 0 && p.lse) p.lse[row] = any ? a.m + logf(a.w) : -INFINITY;
+    put4<O16>(p.out, row * kD + d, x);
+    if (d == 0 && p.lse) p.lse[row] = a.poisoned ? nan : any ? a.m + logf(a.w) : -INFINITY;
 }
 
 template <bool O16>
-__global__ void __launch_bounds__(kPcWarps * 32) paged_combine_kernel(const __grid_constant__ PagedAttnParams p, int rows)
+__global__ void __launch_bounds__(kPcWarps * 32, 4) paged_combine_kernel(const __grid_constant__ PagedAttnParams p,
+                                                                      const __grid_constant__ PagedPieces g0,
+                                                                      const __grid_constant__ PagedPieces g1)
 {
-    __shared__ Merged part[kPcWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n0 = g0.ctas * g0.spread;
+    const PagedPieces &g = (int)blockIdx.x < n0 ? g0 : g1;
+    const int block = (int)blockIdx.x - ((int)blockIdx.x < n0 ? 0 : n0), cta = block / g.spread;
     pdl_wait();
     pdl_trigger();
     for (int slot = 0; slot < 2; ++slot) {
-        const PagedCut c = p.cuts[(size_t)blockIdx.x * 2 + slot];
+        const PagedCut c = g.cuts[(size_t)cta * 2 + slot];
         if (c.np < 2) continue;   // block-uniform
-        const int h = c.h_rt & 255, rt = c.h_rt >> 8, share = (int)blockIdx.x - c.c0;
+        const int h = c.h_rt & 255, rt = c.h_rt >> 8;
+        const int share = (cta - c.c0) * g.spread + block % g.spread, shares = c.np * g.spread;
         int t0, n, len;
         seq_shape(p, c.b, t0, n, len);
         const int gb = p.grp_begin[h], gsz = p.grp_begin[h + 1] - gb;
-        const int row0 = rt * rows, R = min(rows, n * gsz - row0);
+        const int row0 = rt * g.rows, R = min(g.rows, n * gsz - row0);
         auto out_row = [&](int r) {
             return (size_t)(t0 + (row0 + r) / gsz) * p.n_q_heads + p.grp_q[gb + (row0 + r) % gsz];
         };
         if (c.np <= kPcFew) {
-            for (int r = share * kPcWarps + warp; r < R; r += c.np * kPcWarps)
-                put_merged<O16>(p, out_row(r), merge_pieces(p, c, rows, r, 0, 1, lane), lane);
+            for (int r = share * kPcWarps + warp; r < R; r += shares * kPcWarps)
+                put_merged<O16>(p, out_row(r), merge_pieces(g, c, r, 0, 1, 4 * lane), 4 * lane);
         } else {
-            for (int r = share; r < R; r += c.np) {
-                part[warp][lane] = merge_pieces(p, c, rows, r, warp, kPcWarps, lane);
-                __syncthreads();
-                if (warp == 0) {
-                    Merged t = part[0][lane];
-                    float M = -INFINITY;
+            const int d = kD / kPcWarps * warp + 4 * (lane & 3);
+            for (int r = share; r < R; r += shares) {
+                Merged a = merge_pieces(g, c, r, lane >> 2, 8, d);
+                a.poisoned = __any_sync(0xffffffffu, a.poisoned);
 #pragma unroll
-                    for (int w = 0; w < kPcWarps; ++w) M = fmaxf(M, part[w][lane].m);
-                    t.m = M;
-                    t.w = 0.f;
-                    t.o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int w = 0; w < kPcWarps; ++w) {
-                        const Merged q = part[w][lane];
-                        if (q.m == -INFINITY) continue;
-                        const float f = expf(q.m - M);
-                        t.w = fmaf(q.w, f, t.w);
-                        t.o.x = fmaf(q.o.x, f, t.o.x);
-                        t.o.y = fmaf(q.o.y, f, t.o.y);
-                        t.o.z = fmaf(q.o.z, f, t.o.z);
-                        t.o.w = fmaf(q.o.w, f, t.o.w);
-                    }
-                    put_merged<O16>(p, out_row(r), t, lane);
+                for (int k = 4; k < 32; k <<= 1) {
+                    float4 v;
+                    v.x = __shfl_xor_sync(0xffffffffu, a.o.x, k);
+                    v.y = __shfl_xor_sync(0xffffffffu, a.o.y, k);
+                    v.z = __shfl_xor_sync(0xffffffffu, a.o.z, k);
+                    v.w = __shfl_xor_sync(0xffffffffu, a.o.w, k);
+                    const float m2 = __shfl_xor_sync(0xffffffffu, a.m, k), w2 = __shfl_xor_sync(0xffffffffu, a.w, k);
+                    a.join(m2, w2, v);
                 }
-                __syncthreads();
+                if (lane < 4) put_merged<O16>(p, out_row(r), a, d);
             }
         }
     }
 }
 
-cudaError_t launch_paged_combine(const PagedAttnParams &p, int n_ctas, int tile_rows, int out_type, cudaStream_t s, bool pdl)
+cudaError_t launch_paged_combine(const PagedAttnParams &p, const PagedPieces &g0, const PagedPieces &g1, int out_type,
+                                 cudaStream_t s, bool pdl)
 {
+    const int blocks = g0.ctas * g0.spread + g1.ctas * g1.spread;
+    if (blocks == 0) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(n_ctas);
+    cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(kPcWarps * 32);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -428,8 +436,8 @@ cudaError_t launch_paged_combine(const PagedAttnParams &p, int n_ctas, int tile_
     at[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (out_type == KVQ_OUT_F16) return cudaLaunchKernelEx(&cfg, paged_combine_kernel<true>, p, tile_rows);
-    return cudaLaunchKernelEx(&cfg, paged_combine_kernel<false>, p, tile_rows);
+    if (out_type == KVQ_OUT_F16) return cudaLaunchKernelEx(&cfg, paged_combine_kernel<true>, p, g0, g1);
+    return cudaLaunchKernelEx(&cfg, paged_combine_kernel<false>, p, g0, g1);
 }
 
 }  // namespace kvq
