@@ -89,8 +89,10 @@ struct PagedRowsParams {      // append and gather
 
 // ------------------------------------------------------- paged attention --
 constexpr int kStagePos = 32;           // positions per work unit ("stage")
-constexpr int kChunkPositions = 128;    // the chunk kernel: positions per tile,
+constexpr int kChunkRows = 128;         // the chunk kernel: query rows per tile,
+constexpr int kChunkPositions = 128;    // positions per tile,
 constexpr int kChunkMinTiles = 3;       // and the least piece in tiles
+constexpr int kChunkSums = kChunkRows * (kD + 1);   // fp32: a row tile's sums and their zero points
 constexpr int kPagedMinStages = 4;      // a CTA's least piece of the line: one stage per warp
 
 // A query-row tile of one kv head that several CTAs attend: what the combine
@@ -120,6 +122,7 @@ struct PagedAttnParams {
     PagedCut *cuts;                     // [CTAs][2]
     float *ws_lse;                      // [CTAs][2][row tile]
     float *ws_o;                        // [CTAs][2][row tile][kD]
+    float *sums;                        // chunk kernel: [CTAs][kChunkSums]
     unsigned int *timeouts;
     int n_seqs, n_tokens, max_q, n_q_heads, table_stride, max_blocks, causal;
     int gmax;                           // query heads of the busiest kv head
@@ -161,7 +164,6 @@ cudaError_t launch_paged_q4(const PagedAttnParams &p, int nt, int k_type, int ou
 cudaError_t launch_paged_q8(const PagedAttnParams &p, int nt, int k_type, int out_type, int n_ctas, cudaStream_t s);
 
 // Chunk attention on tcgen05 (kvq_paged_chunk_q4.cu / _q8.cu), int8 K.
-constexpr int kChunkRows = 128;
 cudaError_t prepare_chunk_q4();
 cudaError_t prepare_chunk_q8();
 cudaError_t launch_chunk_q4(const PagedAttnParams &p, int out_type, int n_ctas, cudaStream_t s, bool pdl);

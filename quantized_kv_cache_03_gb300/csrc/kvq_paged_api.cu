@@ -107,7 +107,7 @@ bool table_ok(int stride, int max_blocks, int page_tokens)
 // One launch and its combine: CTAs, the row tile, and where its pieces lie in the workspace.
 struct Part {
     int n_ctas = 0, rows = 0;
-    size_t cut_off = 0, lse_off = 0, o_off = 0;
+    size_t cut_off = 0, lse_off = 0, o_off = 0, sum_off = 0;
 };
 
 struct AttnPlan {
@@ -199,7 +199,11 @@ void plan_attn(const kvq_paged_desc *a, const PagedDevice *dev, int n_sms, AttnP
         const int per_sm = dev->ctas[g->k_type][g->v_type][pl.nt][a->out_type];
         size_part(a, pl, pl.tile, n_sms * (per_sm > 0 ? per_sm : 1), 8 * pl.nt, kStagePos, kPagedMinStages, pl.bytes);
     }
-    if (rows >= pl.chunk_rows) size_part(a, pl, pl.chunk, n_sms, kChunkRows, kChunkPositions, kChunkMinTiles, pl.bytes);
+    if (rows >= pl.chunk_rows) {
+        size_part(a, pl, pl.chunk, n_sms, kChunkRows, kChunkPositions, kChunkMinTiles, pl.bytes);
+        pl.chunk.sum_off = pl.bytes;
+        pl.bytes += ((size_t)pl.chunk.n_ctas * kChunkSums * sizeof(float) + 255) / 256 * 256;
+    }
 }
 
 }  // namespace
@@ -369,6 +373,7 @@ kvq_status kvq_paged_attn(const kvq_paged_desc *a, void *workspace, size_t works
     }
     if (e == cudaSuccess && pl.chunk.n_ctas > 0) {
         pieces(pl.chunk, cut[1]);
+        p.sums = reinterpret_cast<float *>(static_cast<char *>(workspace) + pl.chunk.sum_off);
         p.min_rows = pl.chunk_rows;
         p.max_rows = INT_MAX;
         e = q4 ? launch_chunk_q4(p, a->out_type, pl.chunk.n_ctas, s, pdl) : launch_chunk_q8(p, a->out_type, pl.chunk.n_ctas, s, pdl);

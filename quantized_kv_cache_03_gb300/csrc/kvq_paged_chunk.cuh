@@ -29,6 +29,13 @@
 // two fp16 parts, P_hi.V_hi + P_lo.V_hi + P_hi.V_lo (about 22 bits).
 // m is raised only when a score would take P past 2^14, so after the first tile
 // O is hardly ever rescaled; fp32 sums do not mind the range.
+// The MMA cuts its sums off where fp32 would round them, so O falls short by
+// 1e-9 to 5e-9 of itself per position (fp32 output, whose P.V takes three MMAs
+// per 16 positions: 4.5e-5 after 32768, 1.7e-4 after 131072).  So every kCFlush
+// tiles O is added to sums in memory, in fp32, and starts again from zero: 5e-6
+// for any length with fp32 output, 4e-5 with fp16 output, a sixth of that
+// type's half step.  It costs 1 to 3 us each time (512-token chunk over 32768
+// positions, fp16: 466 -> 475 us; a mixed batch with fp32 output 329 -> 351 us).
 // Every wait is bounded: a wait that gives up marks the CTA, whose rows of this
 // and later pieces come out as NaN; the roles drain what they issued and leave.
 #pragma once
@@ -56,6 +63,10 @@ template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 constexpr int kCPieces = 4;              // piece records in flight
 constexpr float kCShift = 8.0f, kCSlack = 6.0f;
+// Tiles after which O is added to the rows' fp32 sums in memory and started
+// afresh (even, so that one softmax group does it throughout a piece).
+template <bool O16>
+constexpr int kCFlush = O16 ? 64 : 8;
 constexpr uint16_t kHalfBits = 0x3800;    // 1/2: 127 * 516 (the largest code * scale) stays inside fp16
 
 template <int VT>
@@ -436,7 +447,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                                 // chunk of 32 positions: high parts in its first 16 columns, low parts after
                                 const uint32_t ph = tS + kCN * g + kCChunk * (2 * i + (ks >> 1)) + 8 * (ks & 1), pl = ph + kCChunk / 2;
                                 const uint64_t o = (uint64_t)(16 * ks);
-                                umma_ta_1(tO, ph, vh + o, kIdPV, (k > 0 || i > 0 || ks > 0) ? 1u : 0u);
+                                umma_ta_1(tO, ph, vh + o, kIdPV, (k % kCFlush<O16> || i > 0 || ks > 0) ? 1u : 0u);
                                 if (!O16) umma_ta_1(tO, pl, vh + o, kIdPV, 1u);
                                 umma_ta_1(tO, ph, vl + o, kIdPV, 1u);
                             }
@@ -555,6 +566,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
         float2 *xe = reinterpret_cast<float2 *>(smem + C::XE_OFF);
         // Q and K went in halved, the sign is in Q; a scale of 0 stays finite times -inf
         const float c4 = fmaxf(4.0f * fabsf(p.qk_scale_log2), 1e-30f);
+        // the rows' sums in memory, [dims / 4][row], and their zero points
+        auto sums = [&]() { return reinterpret_cast<float4 *>(p.sums + (size_t)blockIdx.x * kChunkSums) + row; };
+        auto sums_m = [&]() { return p.sums + (size_t)blockIdx.x * kChunkSums + kCM * kD + row; };
         int j = 0, ends = 0;
         bool lost = false;
         pieces(false, [&](const ChunkWalk &w, int) {
@@ -685,21 +699,72 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                         l *= m == -INFINITY ? 0.f : fast_exp2(m - mn);
                         m = mn;
                     }
-                    if (j > j0 && __any_sync(0xffffffffu, need)) {   // O is stable once P.V(j - 1) is done
+                    const bool flush = j > j0 && (j - j0) % kCFlush<O16> == 0;
+                    if (j > j0 && (flush || __any_sync(0xffffffffu, need))) {   // O is stable once P.V(j - 1) is done
+                        const float alpha = need ? (mp == -INFINITY ? 0.f : fast_exp2(mp - mn)) : 1.f;
+                        float4 *sums = reinterpret_cast<float4 *>(p.sums + (size_t)blockIdx.x * kChunkSums) + row;
+                        float *sums_m = p.sums + (size_t)blockIdx.x * kChunkSums + kCM * kD + row;
+                        float beta = 0.f;
+                        // half of the row's sums into the registers that the second pass will use
+                        auto sums_in = [&](int h) {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const float4 y = __ldcg(sums + (16 * h + k) * kCM);
+                                uint32_t(&v)[32] = a[k >> 3];
+                                v[4 * (k & 7)] = __float_as_uint(y.x);
+                                v[4 * (k & 7) + 1] = __float_as_uint(y.y);
+                                v[4 * (k & 7) + 2] = __float_as_uint(y.z);
+                                v[4 * (k & 7) + 3] = __float_as_uint(y.w);
+                            }
+                        };
+                        if (flush) {
+                            tmem_wait_ld32(a[0]);
+                            if (j - j0 > kCFlush<O16>) {   // there are sums
+                                const float ms = __ldcg(sums_m);
+                                beta = ms == -INFINITY ? 0.f : fast_exp2(ms - m);
+                                sums_in(0);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 64; ++k) a[k >> 5][k & 31] = 0u;
+                            }
+                        }
                         if (!wwait(C::B_PVD + 2 * (grp ^ 1) + 1, ((j - 1) >> 1) & 1)) {
                             lost = true;
                             break;
                         }
                         tc_fence_after();
-                        const float alpha = need ? (mp == -INFINITY ? 0.f : fast_exp2(mp - mn)) : 1.f;
+                        if (flush) {   // O joins the sums, P.V(j) starts from zero
 #pragma unroll 1
-                        for (int c0 = 0; c0 < kD; c0 += 16) {
-                            uint32_t o[16];
-                            tmem_ld16(tO + lane_base + c0, o);
-                            tmem_wait_ld();
+                            for (int h = 0; h < 2; ++h) {
+                                if (h == 1 && j - j0 > kCFlush<O16>) sums_in(1);
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                            tmem_st16(tO + lane_base + c0, o);
+                                for (int q = 0; q < 4; ++q) {
+                                    uint32_t o[16];
+                                    tmem_ld16(tO + lane_base + 64 * h + 16 * q, o);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        const uint32_t *v = &a[q >> 1][16 * (q & 1) + 4 * k];
+                                        __stcg(sums + (16 * h + 4 * q + k) * kCM,
+                                               make_float4(fmaf(__uint_as_float(v[0]), beta, __uint_as_float(o[4 * k]) * alpha),
+                                                           fmaf(__uint_as_float(v[1]), beta, __uint_as_float(o[4 * k + 1]) * alpha),
+                                                           fmaf(__uint_as_float(v[2]), beta, __uint_as_float(o[4 * k + 2]) * alpha),
+                                                           fmaf(__uint_as_float(v[3]), beta, __uint_as_float(o[4 * k + 3]) * alpha)));
+                                    }
+                                }
+                            }
+                            __stcg(sums_m, m);
+                            tmem_ld32(tSg, a[0]);
+                        } else {       // O to the new zero point
+#pragma unroll 1
+                            for (int c0 = 0; c0 < kD; c0 += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(tO + lane_base + c0, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                                tmem_st16(tO + lane_base + c0, o);
+                            }
                         }
                     }
 
@@ -734,12 +799,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(C::B_PREADY + 2 * grp + (c0 ? 1 : 0)));
                     }
+                    if (lost) break;
                     const float2 s2 = add2(sum[0], sum[1]);
                     l += s2.x + s2.y;
                 }
                 // ---- the end of the piece: both groups' sums, and P.V done ----
                 if (!lost) {
                     xe[grp * kCM + row] = make_float2(m, l);
+                    if (w.tiles > kCFlush<O16>) __threadfence();   // the sums, which both groups read now
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(C::B_END + 4 * grp + quarter));
                     if (!wwait(C::B_END + 4 * (grp ^ 1) + quarter, ends & 1) || !wwait(C::B_PVD + 2 * ((j - 1) & 1) + 1, ((j - 1) >> 1) & 1)) lost = true;
@@ -760,7 +827,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
             const float f = lost ? nan : any ? 2.0f / l : 0.f;   // V went in halved
             const float lse = lost ? nan : any ? (m + lg) * 0.69314718055994531f : -INFINITY;
             const size_t part = ((size_t)blockIdx.x * 2 + max(0, w.slot)) * kCM + row, orow = (size_t)(w.t0 + tok) * p.n_q_heads + head;
-            const bool have_o = w.tiles > 0 && !lost;
+            const bool have_o = w.tiles > 0 && !lost, have_sums = have_o && w.tiles > kCFlush<O16>;
+            float fs = 0.f;
+            if (have_sums) {
+                const float msum = __ldcg(sums_m());
+                fs = any && msum != -INFINITY ? f * fast_exp2(msum - m) : 0.f;
+            }
 #pragma unroll 1
             for (int c0 = (kD / 2) * grp; c0 < (kD / 2) * (grp + 1); c0 += 16) {
                 uint32_t o[16];
@@ -775,6 +847,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                 float y[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) y[k] = lost ? nan : any ? __uint_as_float(o[k]) * f : 0.f;
+                if (have_sums)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 s = __ldcg(sums() + (c0 / 4 + k) * kCM);
+                        y[4 * k] = fmaf(s.x, fs, y[4 * k]);
+                        y[4 * k + 1] = fmaf(s.y, fs, y[4 * k + 1]);
+                        y[4 * k + 2] = fmaf(s.z, fs, y[4 * k + 2]);
+                        y[4 * k + 3] = fmaf(s.w, fs, y[4 * k + 3]);
+                    }
                 if (whole && O16) {
                     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + orow * kD + c0);
 #pragma unroll

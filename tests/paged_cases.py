@@ -142,7 +142,7 @@ class Batch:
     rows, appended through slots into a pool whose other bytes are poison."""
 
     def __init__(self, lens, new, H=2, Hq=4, page=16, k_type=kvq.K_I8, v_type=kvq.V_Q4_0, seed=0, spare=3,
-                 pad_rows=0, table_pad=0, outliers=False, hide=()):
+                 pad_rows=0, table_pad=0, outliers=False, hide=(), shape=None):
         r = np.random.default_rng(seed)
         self.lens, self.new, self.H, self.Hq, self.page = list(lens), list(new), H, Hq, page
         self.k_type, self.v_type = k_type, v_type
@@ -163,7 +163,7 @@ class Batch:
             kv = r.standard_normal((2, n, H, 128)).astype(np.float32)
             if outliers and n:
                 kv[:, :, :, r.choice(128, 4, replace=False)] *= 10
-            self.kv.append(kv.astype(np.float16))
+            self.kv.append((kv if shape is None else shape(kv)).astype(np.float16))
         if sum(lens):
             slots = np.concatenate([table[b, np.arange(n) // page] * page + np.arange(n) % page for b, n in enumerate(lens)])
             k16, v16 = (np.concatenate([kv[i] for kv in self.kv]) for i in range(2))

@@ -199,6 +199,43 @@ def test_one_sequence_cut_into_pieces(new, L, out, v_type):
     Batch([L], [new], H=1, Hq=4, page=32, v_type=v_type, seed=new, pad_rows=1).check(out=out)
 
 
+@pytest.mark.parametrize("rising", [False, True])
+@pytest.mark.parametrize("new,L,out,v_type", [
+    (64, 32768, torch.float32, Q4), (64, 20000, torch.float32, Q8), (160, 32768, torch.float16, Q8), (512, 32768, torch.float16, Q4),
+    (8, 32768, torch.float32, Q8)])
+def test_long_sums(new, L, out, v_type, rising):
+    """Sums over many thousand positions, values of one sign: nothing may be
+    lost to the accumulators' rounding, nor where their parts are joined, with
+    a maximum that stays (rising = False) or keeps rising along the sequence."""
+    def shape(kv):
+        kv[1] = 1 + 0.25 * kv[1]
+        if rising:
+            kv[0] += 4 * np.arange(L, dtype=np.float32)[:, None, None] / L
+        return kv
+    b = Batch([L], [new], H=8, Hq=32, page=64, v_type=v_type, seed=new, shape=shape)
+    if rising:
+        b.q += np.float16(1)
+    o, ls = b.attn(out=out)
+    rows = sorted({0, new // 2, new - 1})
+    k, v = values(oracle.quantize_kv(*b.kv[0], v_type), v_type)
+    q = values(oracle.quantize_kv(b.q[rows], b.q[rows], Q8), Q8)[0].transpose(1, 0, 2)
+    ro, rl = np.zeros((len(rows), 32, 128)), np.zeros((len(rows), 32))
+    for i, t in enumerate(rows):
+        n = L - new + t + 1
+        for h in range(32):
+            s = k[h // 4, :n] @ q[i, h] * SM_SCALE
+            p = np.exp(s - s.max())
+            rl[i, h], ro[i, h] = s.max() + np.log(p.sum()), p @ v[h // 4, :n] / p.sum()
+    a, rel, el = b.bounds(out=out)
+    assert (np.abs(o[rows] - ro) <= a + rel * np.abs(ro)).all() and (np.abs(ls[rows] - rl) <= el).all()
+    # on the average the roundings cancel, unless they lean to one side.  At most 1024 positions (fp32
+    # output) or 8192 are summed in accumulators that cut off, by 2^-24 of the sum on the average, with
+    # three or two additions per 16 positions.  fp16 outputs are rounded, to nearest: 2^-12 over the
+    # root of some thousand values.
+    lean = (192 if out == torch.float32 else 1024) * 2.0 ** -24 + (2.0 ** -20 if out == torch.float32 else 2.0 ** -15)
+    assert abs((o[rows] - ro).sum() / ro.sum()) <= lean
+
+
 @pytest.mark.parametrize("causal", [True, False])
 def test_rows_that_see_nothing_and_more_rows_than_positions(causal):
     """len < new: the first rows of a causal chunk see no position."""
