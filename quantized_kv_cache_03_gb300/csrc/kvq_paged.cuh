@@ -33,29 +33,126 @@ __host__ __device__ constexpr int page_tile_bytes(int v_type, int k_type)
 // Byte offset of block b's scale of position u in a scale area.
 __host__ __device__ constexpr int scale_off(int u, int b) { return 2 * (((u / 8) * 4 + (u % 8) / 2) * 8 + 2 * b + u % 2); }
 
-// A quantized row (quant_token) into place u of a tile.
-template <int VT, int KT>
-__device__ __forceinline__ void store_token_paged(const TokenRow &t, int u, int lane, uint8_t *tile)
+// Codes of four fp16 values x01, x23 for the block scale s (fp32 copy of an fp16
+// number): x / s to the nearest integer, halves away from zero, held to lo..hi;
+// NaN gives lo.  As bytes of (code + bias).  Without a division: x and s have 11
+// bits, so x / s below 191 that is not a half is 2.4e-4 or more away from the
+// next one (1.3e-6 of itself), and x times 1/s, off by 2e-7 of itself, gives the
+// same integer once it is nudged by 8e-7 of itself, which takes the halves
+// outward.  The addition of 1.5 * 2^23 rounds the exact product.
+__device__ __forceinline__ uint32_t codes4(uint32_t x01, uint32_t x23, float s, float lo, float hi, int bias)
 {
-    using T = PageTile<VT, KT>;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    inv = s == 0.f ? 0.f : inv * 1.0000008f;   // s = inf: 0, and inf * 0 is NaN
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&x01)), b = __half22float2(*reinterpret_cast<const __half2 *>(&x23));
+    const float x[4] = {a.x, a.y, b.x, b.y}, zero = 12582912.f + (float)bias;
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = __float_as_uint(fminf(fmaxf(fmaf(x[k], inv, zero), zero + lo), zero + hi));
+    return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+}
+
+// quant_token for the paged cache: the same codes and scales; kw is biased by
+// 128, and so is vw for q8_0.  (a / 127, a of 11 bits, stays 1.9e-6 of itself
+// away from the middle of two fp16 numbers, so the product's rounding, 1e-7,
+// cannot change the scale.)
+template <int VT, int KT>
+__device__ __forceinline__ TokenRow paged_token(const uint16_t *k_row, const uint16_t *v_row, int lane)
+{
+    TokenRow t;
+    const uint2 k = *reinterpret_cast<const uint2 *>(k_row + 4 * lane), v = *reinterpret_cast<const uint2 *>(v_row + 4 * lane);
+    // the blocks' largest magnitudes, K's in the low half, V's in the high one
+    auto h2 = [](uint32_t w) { return *reinterpret_cast<const __half2 *>(&w); };
+    auto bits = [](const __half2 &h) { return *reinterpret_cast<const uint32_t *>(&h); };
+    const uint32_t mk = bits(__hmax2(h2(k.x & 0x7fff7fffu), h2(k.y & 0x7fff7fffu))), mv = bits(__hmax2(h2(v.x & 0x7fff7fffu), h2(v.y & 0x7fff7fffu)));
+    __half2 m = __hmax2(h2(__byte_perm(mk, mv, 0x5410)), h2(__byte_perm(mk, mv, 0x7632)));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = __hmax2(m, h2(__shfl_xor_sync(0xffffffffu, bits(m), o)));
+    const float2 a = __half22float2(m);
+    if (KT == KVQ_K_F16) {
+        t.kw = k.x;
+        t.kw2 = k.y;
+        t.ks = 0;
+    } else {
+        const __half s = __float2half_rn(a.x * (1.f / 127.f));
+        t.ks = __half_as_ushort(s);
+        t.kw = codes4(k.x, k.y, __half2float(s), -127.f, 127.f, 128);
+        t.kw2 = 0;
+    }
+    if (VT == KVQ_V_Q8_0) {
+        const __half s = __float2half_rn(a.y * (1.f / 127.f));
+        t.vs = __half_as_ushort(s);
+        t.vw = codes4(v.x, v.y, __half2float(s), -127.f, 127.f, 128);
+    } else {
+        const __half s = __float2half_rn(a.y * 0.125f);   // exact before rounding
+        t.vs = __half_as_ushort(s);
+        const uint32_t q = codes4(v.x, v.y, __half2float(s), -8.f, 7.f, 8);
+        t.vw = q | __shfl_down_sync(0xffffffffu, q, 4) << 4;   // elements 16.. of the block
+    }
+    return t;
+}
+
+// V codes of positions u, u + 1 (u even) sit in the same words: byte offset of
+// lane's word pair (q8_0: 8 bytes, both positions' codes of its four dims) or
+// word (q4_0: 4 bytes, code bytes 2g, 2g + 1 of block b for lane 8b + g).
+__device__ __forceinline__ int v8_pair_off(int u, int lane)
+{
+    return ((2 * (u / 8) + (lane >> 4)) * 32 + 4 * (lane & 7) + (u % 8) / 2) * 16 + 8 * ((lane >> 3) & 1);
+}
+__device__ __forceinline__ int v4_pair_off(int u, int b, int g) { return ((u / 8) * 32 + 4 * g + (u % 8) / 2) * 16 + 4 * b; }
+
+// K codes (and, int8, nothing else) of a quantized row into place u.
+template <int VT, int KT>
+__device__ __forceinline__ void store_k_paged(const TokenRow &t, int u, int lane, uint8_t *tile)
+{
     if (KT == KVQ_K_F16) {
         *reinterpret_cast<uint32_t *>(tile + k16_tile_off(u, 4 * lane)) = t.kw;
         *reinterpret_cast<uint32_t *>(tile + k16_tile_off(u, 4 * lane + 2)) = t.kw2;
     } else {
-        *reinterpret_cast<uint32_t *>(tile + k_tile_off(u, 4 * lane)) = t.kw ^ 0x80808080u;
-        if ((lane & 7) == 0) *reinterpret_cast<uint16_t *>(tile + T::KS_OFF + scale_off(u, lane >> 3)) = t.ks;
+        *reinterpret_cast<uint32_t *>(tile + k_tile_off(u, 4 * lane)) = t.kw;
     }
+}
+
+// A quantized row (paged_token) into place u of a tile.
+template <int VT, int KT>
+__device__ __forceinline__ void store_token_paged(const TokenRow &t, int u, int lane, uint8_t *tile)
+{
+    using T = PageTile<VT, KT>;
+    store_k_paged<VT, KT>(t, u, lane, tile);
+    if (KT != KVQ_K_F16 && (lane & 7) == 0) *reinterpret_cast<uint16_t *>(tile + T::KS_OFF + scale_off(u, lane >> 3)) = t.ks;
     uint8_t *vt = tile + T::V_OFF;
     if (VT == KVQ_V_Q8_0) {
-        const uint32_t w = t.vw ^ 0x80808080u;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) vt[v8_tile_off(u, 4 * lane + k)] = (uint8_t)(w >> (8 * k));
+        for (int k = 0; k < 4; ++k) vt[v8_tile_off(u, 4 * lane + k)] = (uint8_t)(t.vw >> (8 * k));
     } else if ((lane & 7) < 4) {
         const int j = 16 * (lane >> 3) + 4 * (lane & 3);
         *reinterpret_cast<uint16_t *>(vt + v4_tile_off(u, j)) = (uint16_t)t.vw;
         *reinterpret_cast<uint16_t *>(vt + v4_tile_off(u, j + 2)) = (uint16_t)(t.vw >> 16);
     }
     if ((lane & 7) == 0) *reinterpret_cast<uint16_t *>(tile + T::VS_OFF + scale_off(u, lane >> 3)) = t.vs;
+}
+
+// Two rows into places u, u + 1 (u even): whole words of V codes and scales.
+template <int VT, int KT>
+__device__ __forceinline__ void store_pair_paged(const TokenRow &a, const TokenRow &b, int u, int lane, uint8_t *tile)
+{
+    using T = PageTile<VT, KT>;
+    store_k_paged<VT, KT>(a, u, lane, tile);
+    store_k_paged<VT, KT>(b, u + 1, lane, tile);
+    uint8_t *vt = tile + T::V_OFF;
+    if (VT == KVQ_V_Q8_0) {
+        *reinterpret_cast<uint2 *>(vt + v8_pair_off(u, lane)) = make_uint2(__byte_perm(a.vw, b.vw, 0x5140), __byte_perm(a.vw, b.vw, 0x7362));
+    } else {   // lanes 8b .. 8b + 3 hold the block's 16 bytes
+        const int src = (lane & 24) + ((lane & 7) >> 1);
+        const uint32_t x = __shfl_sync(0xffffffffu, a.vw, src), y = __shfl_sync(0xffffffffu, b.vw, src);
+        *reinterpret_cast<uint32_t *>(vt + v4_pair_off(u, lane >> 3, lane & 7)) = __byte_perm(x, y, lane & 1 ? 0x7632 : 0x5410);
+    }
+    if ((lane & 7) == 0) {
+        const int o = scale_off(u, lane >> 3);
+        if (KT != KVQ_K_F16) *reinterpret_cast<uint32_t *>(tile + T::KS_OFF + o) = a.ks | (uint32_t)b.ks << 16;
+        *reinterpret_cast<uint32_t *>(tile + T::VS_OFF + o) = a.vs | (uint32_t)b.vs << 16;
+    }
 }
 
 struct PoolDesc {
@@ -76,6 +173,7 @@ struct TableParams {
     const int *lens, *n_new, *n_free;
     int *free_pages, *block_table, *lens_out, *n_free_out, *q_start, *slots, *status;
     int n_seqs, pshift, n_pages, stride, max_blocks, n_tokens;
+    bool slots_here;   // the table kernel fills the slots too
 };
 
 struct PagedRowsParams {      // append and gather
@@ -151,7 +249,7 @@ __device__ __forceinline__ bool seq_mine(const PagedAttnParams &p, int n)
 }
 
 cudaError_t prepare_page_tables();
-cudaError_t launch_page_tables(const TableParams &p, cudaStream_t s, bool pdl);
+cudaError_t launch_page_tables(TableParams p, cudaStream_t s, bool pdl);
 cudaError_t launch_paged_append(const PagedRowsParams &p, int v_type, int k_type, cudaStream_t s, bool pdl);
 cudaError_t launch_paged_gather(const PagedRowsParams &p, int v_type, int k_type, int out_type, cudaStream_t s,
                                 bool pdl);
@@ -160,8 +258,10 @@ cudaError_t launch_paged_combine(const PagedAttnParams &p, const PagedPieces &g0
 // Row-tile attention (kvq_paged_attn_q4.cu / _q8.cu): nt = 8-row tiles per CTA (1 or 2).
 cudaError_t prepare_paged_q4(int nt, int k_type, int out_type, int *ctas_per_sm);
 cudaError_t prepare_paged_q8(int nt, int k_type, int out_type, int *ctas_per_sm);
-cudaError_t launch_paged_q4(const PagedAttnParams &p, int nt, int k_type, int out_type, int n_ctas, cudaStream_t s);
-cudaError_t launch_paged_q8(const PagedAttnParams &p, int nt, int k_type, int out_type, int n_ctas, cudaStream_t s);
+cudaError_t launch_paged_q4(const PagedAttnParams &p, int nt, int k_type, int out_type, int n_ctas, cudaStream_t s,
+                            bool pdl);
+cudaError_t launch_paged_q8(const PagedAttnParams &p, int nt, int k_type, int out_type, int n_ctas, cudaStream_t s,
+                            bool pdl);
 
 // Chunk attention on tcgen05 (kvq_paged_chunk_q4.cu / _q8.cu), int8 K.
 cudaError_t prepare_chunk_q4();

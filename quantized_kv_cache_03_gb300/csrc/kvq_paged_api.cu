@@ -239,7 +239,7 @@ kvq_status kvq_page_tables(int32_t n_seqs, int32_t page_tokens, int32_t n_pages,
     const kvq_status st = paged_setup(&dev, &n_sms, &timeouts);
     if (st != KVQ_OK) return st;
     const TableParams p{lens, n_new, n_free, free_pages, block_table, lens_out, n_free_out, q_start, slots, status,
-                        n_seqs, page_shift(page_tokens), n_pages, table_stride, max_blocks, n_tokens};
+                        n_seqs, page_shift(page_tokens), n_pages, table_stride, max_blocks, n_tokens, true};
     return done(launch_page_tables(p, static_cast<cudaStream_t>(stream), pdl_on()));
 }
 
@@ -368,8 +368,8 @@ kvq_status kvq_paged_attn(const kvq_paged_desc *a, void *workspace, size_t works
         pieces(pl.tile, cut[0]);
         p.min_rows = 1;
         p.max_rows = pl.chunk_rows - 1;
-        e = q4 ? launch_paged_q4(p, pl.nt, g->k_type, a->out_type, pl.tile.n_ctas, s)
-               : launch_paged_q8(p, pl.nt, g->k_type, a->out_type, pl.tile.n_ctas, s);
+        e = q4 ? launch_paged_q4(p, pl.nt, g->k_type, a->out_type, pl.tile.n_ctas, s, pdl && pl.tile.n_ctas <= n_sms)
+               : launch_paged_q8(p, pl.nt, g->k_type, a->out_type, pl.tile.n_ctas, s, pdl && pl.tile.n_ctas <= n_sms);
     }
     if (e == cudaSuccess && pl.chunk.n_ctas > 0) {
         pieces(pl.chunk, cut[1]);

@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const 
         for (int st = 0; st < S; ++st) mbar_init(bar_s + st * 8, 1);
         fence_mbar_init();
     }
+    pdl_wait();
     pdl_trigger();
 
     const uint32_t pick = g & 1 ? 0x3232u : 0x1010u;   // NT = 1: the lane's half of a K scale pair, twice
@@ -500,17 +501,12 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const 
                                 }
 #pragma unroll
                                 for (int h2 = 0; h2 < 2; ++h2) {
-                                    if (O16) {
-                                        mma_f16_16816(acc[2 * bb + h2][nt], a[h2], hi[0], hi[1]);
-                                    } else {
-                                        if (t == 0) mma_f16_16816_c4(part[h2][nt], a[h2], hi[0], hi[1], make_uint4(0u, 0u, 0u, 0u));
-                                        else mma_f16_16816(part[h2][nt], a[h2], hi[0], hi[1]);
-                                        mma_f16_16816(part[h2][nt], a[h2], lo[0], lo[1]);
-                                    }
+                                    if (t == 0) mma_f16_16816_c4(part[h2][nt], a[h2], hi[0], hi[1], make_uint4(0u, 0u, 0u, 0u));
+                                    else mma_f16_16816(part[h2][nt], a[h2], hi[0], hi[1]);
+                                    if (!O16) mma_f16_16816(part[h2][nt], a[h2], lo[0], lo[1]);
                                 }
                             }
                         }
-                        if (!O16)
 #pragma unroll
                             for (int h2 = 0; h2 < 2; ++h2)
 #pragma unroll
@@ -633,12 +629,12 @@ cudaError_t prepare_paged_t(int *ctas)
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, fn, C::THREADS, C::SMEM);
 }
 
-// Never placed before the launch in front of it is through: beside that one's
-// last blocks the CTAs (three or four to an SM fill its shared memory) can leave
-// a hole that the last of them does not fit, and it then starts only when
+// pdl only for grids of one CTA per SM at most: beside the last blocks of the
+// launch in front, the three or four CTAs that fill an SM's shared memory can
+// leave a hole that the last of them does not fit, and it then starts only when
 // another has finished (64 sequences, 456 CTAs: 370 us or up to 480 us).
 template <int NT, int VT, int KT, bool O16>
-cudaError_t launch_paged_t(const PagedAttnParams &p, int n_ctas, cudaStream_t s)
+cudaError_t launch_paged_t(const PagedAttnParams &p, int n_ctas, cudaStream_t s, bool pdl)
 {
     using C = PagedCfg<NT, VT, KT>;
     cudaLaunchConfig_t cfg = {};
@@ -646,6 +642,11 @@ cudaError_t launch_paged_t(const PagedAttnParams &p, int n_ctas, cudaStream_t s)
     cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, paged_attn_kernel<NT, VT, KT, O16>, p);
 }
 
@@ -662,9 +663,9 @@ cudaError_t launch_paged_t(const PagedAttnParams &p, int n_ctas, cudaStream_t s)
         return KVQ_PAGED_PICK(prepare_paged_t, VT, nt, k_type, out_type, ctas);                                      \
     }                                                                                                                \
     cudaError_t launch_paged_##SUFFIX(const PagedAttnParams &p, int nt, int k_type, int out_type, int n_ctas,        \
-                                      cudaStream_t s)                                                                \
+                                      cudaStream_t s, bool pdl)                                                      \
     {                                                                                                                \
-        return KVQ_PAGED_PICK(launch_paged_t, VT, nt, k_type, out_type, p, n_ctas, s);                               \
+        return KVQ_PAGED_PICK(launch_paged_t, VT, nt, k_type, out_type, p, n_ctas, s, pdl);                          \
     }
 
 }  // namespace kvq

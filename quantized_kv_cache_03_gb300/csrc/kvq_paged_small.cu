@@ -1,6 +1,7 @@
 // kvq_paged_small.cu -- page tables, append, gather and the piece combine of
 // the paged cache.
 #include "kvq_paged.cuh"
+#include "kvq_paged_line.cuh"
 
 namespace kvq {
 
@@ -13,7 +14,13 @@ namespace kvq {
 // for itself (n_seqs loads, three block scans: cheaper than passing them
 // around), the cluster synchronizes once, so that lens and n_free may be
 // updated in place, and the outputs are dealt out flat over its threads with
-// a binary search each.  Latency-bound: its bytes are a few hundred KB.
+// a binary search each; a warp copies a released sequence's pages.  Latency-bound
+// (256 sequences, a row each: 6.6 us; its bytes take 0.1 us): the launch, one
+// round of loads, three scans, the cluster's barrier.  One CTA alone instead of
+// eight is no faster (6.6).  The rows' slots are filled here up to one pass of
+// the cluster's threads (16384 rows), beyond that by a second, wide launch:
+// 17942 rows 7.15 us here, 6.82 there; 272442 rows 36.8 and 10.6; 7726 rows 5.70
+// and 6.63.
 // ---------------------------------------------------------------------------
 constexpr int kTabThreads = 512;
 
@@ -137,7 +144,24 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
         const int j = ((len_s[b] + P - 1) >> p.pshift) + f - need0[b];
         p.block_table[(size_t)b * p.stride + j] = stack(avail - 1 - f);
     }
-    for (int v = n_free + at; v < n_free_out; v += all) p.free_pages[v] = stack(v);   // what stays of the returned pages
+    // what stays of the returned pages: a warp per released sequence, the warp's sequences asked 32 at a time
+    const int warp = at >> 5, warps = all >> 5, lane = tid & 31;
+    for (int b0 = warp; b0 < n; b0 += 32 * warps) {
+        const int mine = b0 + lane * warps;
+        for (unsigned set = __ballot_sync(0xffffffffu, mine < n && p.n_new[mine] < 0); set; set &= set - 1) {
+            const int b = b0 + (__ffs(set) - 1) * warps, v0 = n_free + back0[b], m = min(back0[b + 1] - back0[b], n_free_out - v0);
+            const int *from = p.block_table + (size_t)b * p.stride;
+            for (int k0 = lane; k0 < m; k0 += 256) {   // eight loads in flight
+                int v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = k0 + 32 * k < m ? from[k0 + 32 * k] : 0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k0 + 32 * k < m) p.free_pages[v0 + k0 + 32 * k] = v[k];
+            }
+        }
+    }
+    if (!p.slots_here) return;
     // slots, four rows a thread: one search, then forward
     const int owned = min(qs[n], p.n_tokens);
     for (int t = 4 * at; t < p.n_tokens; t += 4 * all) {
@@ -165,6 +189,49 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
     }
 }
 
+// The slots of many rows, from the tables as page_tables_kernel left them: a
+// row's sequence by a search over q_start, four rows a thread.
+constexpr int kSlotThreads = 256;
+
+__global__ void __launch_bounds__(kSlotThreads) page_slots_kernel(const TableParams p)
+{
+    extern __shared__ int qs[];
+    const int n = p.n_seqs;
+    const long long t0 = 4 * ((long long)blockIdx.x * kSlotThreads + threadIdx.x);
+    pdl_wait();
+    pdl_trigger();
+    for (int i = threadIdx.x; i <= n; i += kSlotThreads) qs[i] = p.q_start[i];
+    __syncthreads();
+    if (t0 >= p.n_tokens) return;
+    const int t = (int)t0, owned = min(qs[n], p.n_tokens), left = p.n_tokens - t;
+    int s4[4] = {-1, -1, -1, -1};
+    if (t < owned) {
+        int b = last_at_most(qs, n, t), at = 0;
+        const int *row = nullptr;   // the sequence's table, if its rows were granted
+        auto enter = [&]() {
+            row = p.status[b] == 0 ? p.block_table + (size_t)b * p.stride : nullptr;
+            at = p.lens_out[b] - qs[b + 1];   // position of row t: at + t
+        };
+        enter();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k >= owned - t) break;
+            if (t + k >= qs[b + 1]) {
+                do ++b;
+                while (t + k >= qs[b + 1]);
+                enter();
+            }
+            if (!row) continue;
+            const int pos = at + t + k, page = row[pos >> p.pshift];
+            if (page >= 0 && page < p.n_pages) s4[k] = (page << p.pshift) + (pos & ((1 << p.pshift) - 1));
+        }
+    }
+    if (left >= 4 && (reinterpret_cast<uintptr_t>(p.slots) & 15) == 0)
+        *reinterpret_cast<int4 *>(p.slots + t) = make_int4(s4[0], s4[1], s4[2], s4[3]);
+    else
+        for (int k = 0; k < 4 && k < left; ++k) p.slots[t + k] = s4[k];
+}
+
 cudaError_t prepare_page_tables()
 {
     constexpr int most = (4 * KVQ_MAX_PAGED_SEQS + 3) * (int)sizeof(int);
@@ -172,10 +239,11 @@ cudaError_t prepare_page_tables()
     return cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
 }
 
-cudaError_t launch_page_tables(const TableParams &p, cudaStream_t s, bool pdl)
+cudaError_t launch_page_tables(TableParams p, cudaStream_t s, bool pdl)
 {
     cudaLaunchConfig_t cfg = {};
     const int ctas = 8;   // the portable cluster size
+    p.slots_here = p.n_tokens <= 4 * ctas * kTabThreads;
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kTabThreads);
     cfg.dynamicSmemBytes = (4 * (size_t)p.n_seqs + 3) * sizeof(int);
@@ -188,49 +256,87 @@ cudaError_t launch_page_tables(const TableParams &p, cudaStream_t s, bool pdl)
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, page_tables_kernel, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, page_tables_kernel, p);
+    if (e != cudaSuccess || p.slots_here) return e;
+    return launch_pdl(page_slots_kernel, p, (int)(((long long)p.n_tokens + 4 * kSlotThreads - 1) / (4 * kSlotThreads)), kSlotThreads,
+                      (p.n_seqs + 1) * sizeof(int), s, pdl);
 }
 
 // ---------------------------------------------------------------------------
-// Append: one warp per (token, kv head) row, as append_kernel; the slot names
-// the tile.
+// Append and gather work on rows (token, kv head), a warp each, a block eight
+// tokens of one head.  Two tokens of the batch side by side whose slots are an
+// even place and the next one share their tile's V words and scale words: the
+// warp of the first takes both, that of the second leaves.
+// ---------------------------------------------------------------------------
+constexpr int kRowWarps = 8;
+
+struct RowJob {
+    int tok, h, slot;   // slot < 0: nothing to do
+    bool pair;          // and token tok + 1, slot + 1
+};
+__device__ __forceinline__ RowJob row_job(const PagedRowsParams &p)
+{
+    RowJob r;
+    const unsigned group = blockIdx.x / (unsigned)p.pool.n_kv_heads;
+    r.h = (int)(blockIdx.x - group * p.pool.n_kv_heads);
+    r.tok = (int)(group * kRowWarps + (threadIdx.x >> 5));
+    r.pair = false;
+    r.slot = -1;
+    if (r.tok >= p.n_tokens) return r;
+    const int slot = p.slots[r.tok];
+    const int before = r.tok > 0 ? p.slots[r.tok - 1] : -1, after = r.tok + 1 < p.n_tokens ? p.slots[r.tok + 1] : -1;
+    if (slot < 0 || slot >= p.pool.n_slots) return r;
+    if ((slot & 1) && before == slot - 1) return r;
+    r.slot = slot;
+    r.pair = !(slot & 1) && after == slot + 1;   // pages hold a multiple of 16: the same tile
+    return r;
+}
+static int row_blocks(const PagedRowsParams &p)   // at most 2^28: the callers hold tokens * heads below 2^30
+{
+    return (p.n_tokens + kRowWarps - 1) / kRowWarps * p.pool.n_kv_heads;
+}
+
+// ---------------------------------------------------------------------------
+// Append: paged_token's codes into the slot's tile.  It moves 512 bytes in and
+// 208 to 400 out per row; at thousands of rows bound by instructions (340 per
+// pair) and the latency of two loads in a row, at a decode step's by the
+// latency alone.  8192 tokens, 8 heads, q8_0 V: 18.8 us, 2.7 TB/s; a row alone
+// with byte stores and a division per value 37.6.
 // ---------------------------------------------------------------------------
 template <int VT, int KT>
-__global__ void __launch_bounds__(128) paged_append_kernel(const PagedRowsParams p)
+__global__ void __launch_bounds__(kRowWarps * 32) paged_append_kernel(const PagedRowsParams p)
 {
     pdl_wait();
     pdl_trigger();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 4 + warp;
-    const int H = p.pool.n_kv_heads;
-    const int tok = (int)(row / H), h = (int)(row - (long long)tok * H);
-    if (tok >= p.n_tokens) return;
-    const int slot = p.slots[tok];
-    if (slot < 0 || slot >= p.pool.n_slots) return;
-    const size_t src = (size_t)tok * p.stride + (size_t)h * kD;
-    const TokenRow t = quant_token<VT, KT>(p.k16 + src, p.v16 + src, lane);
-    const int place = slot & ((1 << p.pool.pshift) - 1);
-    store_token_paged<VT, KT>(t, place & 15, lane,
-                              tile_of(p.pool, slot >> p.pool.pshift, h, place >> 4, PageTile<VT, KT>::BYTES));
+    const int lane = threadIdx.x & 31;
+    const RowJob r = row_job(p);
+    if (r.slot < 0) return;
+    const size_t src = (size_t)r.tok * p.stride + (size_t)r.h * kD;
+    const int place = r.slot & ((1 << p.pool.pshift) - 1);
+    uint8_t *tile = tile_of(p.pool, r.slot >> p.pool.pshift, r.h, place >> 4, PageTile<VT, KT>::BYTES);
+    const TokenRow t = paged_token<VT, KT>(p.k16 + src, p.v16 + src, lane);
+    if (r.pair) {
+        const TokenRow t1 = paged_token<VT, KT>(p.k16 + src + p.stride, p.v16 + src + p.stride, lane);
+        store_pair_paged<VT, KT>(t, t1, place & 15, lane, tile);
+    } else {
+        store_token_paged<VT, KT>(t, place & 15, lane, tile);
+    }
 }
 
 cudaError_t launch_paged_append(const PagedRowsParams &p, int v_type, int k_type, cudaStream_t s, bool pdl)
 {
-    const int grid = (int)(((long long)p.n_tokens * p.pool.n_kv_heads + 3) / 4);
     void (*fn)(PagedRowsParams) =
         k_type == KVQ_K_F16 ? (v_type == KVQ_V_Q4_0 ? paged_append_kernel<KVQ_V_Q4_0, KVQ_K_F16> : paged_append_kernel<KVQ_V_Q8_0, KVQ_K_F16>)
                             : (v_type == KVQ_V_Q4_0 ? paged_append_kernel<KVQ_V_Q4_0, KVQ_K_I8> : paged_append_kernel<KVQ_V_Q8_0, KVQ_K_I8>);
-    return launch_pdl(fn, p, grid, 128, 0, s, pdl);
+    return launch_pdl(fn, p, row_blocks(p), kRowWarps * 32, 0, s, pdl);
 }
 
 // ---------------------------------------------------------------------------
-// Gather: one warp per (token, kv head) row, four values a lane.
+// Gather: four values a lane of a row's K and V, for a pair of both rows.
+// Bound by the writes (1 KB per row with fp32 output): 131072 tokens, 8 heads,
+// q8_0 V: 225 us, 6.0 TB/s, nine tenths of a copy's rate (284 us with a warp per
+// row, which fetches the V words of eight positions to use one's).
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float half_at(const uint8_t *p)
-{
-    return __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t *>(p)));
-}
-
 template <bool O16>
 __device__ __forceinline__ void put4(void *base, size_t elem, const float (&x)[4])
 {
@@ -240,57 +346,77 @@ __device__ __forceinline__ void put4(void *base, size_t elem, const float (&x)[4
         *reinterpret_cast<float4 *>(static_cast<float *>(base) + elem) = make_float4(x[0], x[1], x[2], x[3]);
 }
 
+// The lane's four values of code bytes w (biased by bias) times s.
+__device__ __forceinline__ void scaled4(uint32_t w, int bias, float s, float (&x)[4])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = (float)((int)(w >> (8 * k) & 0xff) - bias) * s;
+}
+
 template <int VT, int KT, bool O16>
-__global__ void __launch_bounds__(128) paged_gather_kernel(const PagedRowsParams p)
+__global__ void __launch_bounds__(kRowWarps * 32) paged_gather_kernel(const PagedRowsParams p)
 {
     using T = PageTile<VT, KT>;
     pdl_wait();
     pdl_trigger();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 4 + warp;
-    const int H = p.pool.n_kv_heads;
-    const int tok = (int)(row / H), h = (int)(row - (long long)tok * H);
-    if (tok >= p.n_tokens) return;
-    const int slot = p.slots[tok];
-    if (slot < 0 || slot >= p.pool.n_slots) return;
-    const int place = slot & ((1 << p.pool.pshift) - 1), u = place & 15, b = lane >> 3;
-    const uint8_t *tile = tile_of(p.pool, slot >> p.pool.pshift, h, place >> 4, T::BYTES);
-    float x[4];
-    const size_t dst = (size_t)row * kD + 4 * lane;
-    if (KT == KVQ_K_F16) {
-        const float2 lo = __half22float2(*reinterpret_cast<const __half2 *>(tile + k16_tile_off(u, 4 * lane)));
-        const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(tile + k16_tile_off(u, 4 * lane + 2)));
-        x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
-    } else {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(tile + k_tile_off(u, 4 * lane));
-        const float s = half_at(tile + T::KS_OFF + scale_off(u, b));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = (float)((int)(w >> (8 * k) & 0xff) - 128) * s;
-    }
-    put4<O16>(p.k_out, dst, x);
-    const float d = half_at(tile + T::VS_OFF + scale_off(u, b));
+    const int lane = threadIdx.x & 31, b = lane >> 3;
+    const RowJob r = row_job(p);
+    if (r.slot < 0) return;
+    const int place = r.slot & ((1 << p.pool.pshift) - 1), u = place & 15, ue = u & ~1;
+    const uint8_t *tile = tile_of(p.pool, r.slot >> p.pool.pshift, r.h, place >> 4, T::BYTES);
+    // V words and scales of places ue, ue + 1; K of the rows asked for
     const uint8_t *vt = tile + T::V_OFF;
+    uint32_t va, vb;
+    if (VT == KVQ_V_Q8_0) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(vt + v8_pair_off(ue, lane));
+        va = __byte_perm(w.x, w.y, 0x6420);
+        vb = __byte_perm(w.x, w.y, 0x7531);
+    } else {   // bytes 4 (lane % 4) .. + 3 of the block, the low nibbles first
+        const uint32_t x = *reinterpret_cast<const uint32_t *>(vt + v4_pair_off(ue, b, 2 * (lane & 3)));
+        const uint32_t y = *reinterpret_cast<const uint32_t *>(vt + v4_pair_off(ue, b, 2 * (lane & 3) + 1));
+        const int sh = lane & 4;
+        va = __byte_perm(x, y, 0x5410) >> sh & 0x0f0f0f0fu;
+        vb = __byte_perm(x, y, 0x7632) >> sh & 0x0f0f0f0fu;
+    }
+    const float2 d = half2_of(*reinterpret_cast<const uint32_t *>(tile + T::VS_OFF + scale_off(ue, b)));
+    float2 ks = make_float2(0.f, 0.f);
+    if (KT != KVQ_K_F16) ks = half2_of(*reinterpret_cast<const uint32_t *>(tile + T::KS_OFF + scale_off(ue, b)));
+    uint32_t k0[2], k1[2];   // row u; row u + 1 of a pair
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        if (VT == KVQ_V_Q8_0) {
-            x[k] = (float)((int)vt[v8_tile_off(u, 4 * lane + k)] - 128) * d;
-        } else {   // element e of block b: byte e % 16, low nibble below 16
-            const int e = (4 * lane + k) & 31;
-            const int byte = vt[v4_tile_off(u, 16 * b + (e & 15))];
-            x[k] = (float)(((e < 16) ? byte & 15 : byte >> 4) - 8) * d;
+    for (int e = 0; e < 2; ++e) {
+        if (e == 1 && !r.pair) break;
+        if (KT == KVQ_K_F16) {
+            k0[e] = *reinterpret_cast<const uint32_t *>(tile + k16_tile_off(u + e, 4 * lane));
+            k1[e] = *reinterpret_cast<const uint32_t *>(tile + k16_tile_off(u + e, 4 * lane + 2));
+        } else {
+            k0[e] = *reinterpret_cast<const uint32_t *>(tile + k_tile_off(u + e, 4 * lane));
         }
     }
-    put4<O16>(p.v_out, dst, x);
+    size_t dst = ((size_t)r.tok * p.pool.n_kv_heads + r.h) * kD + 4 * lane;
+#pragma unroll
+    for (int e = 0; e < 2; ++e, dst += (size_t)p.pool.n_kv_heads * kD) {
+        if (e == 1 && !r.pair) break;
+        const bool odd = (u + e) & 1;
+        float x[4];
+        if (KT == KVQ_K_F16) {
+            const float2 lo = half2_of(k0[e]), hi = half2_of(k1[e]);
+            x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
+        } else {
+            scaled4(k0[e], 128, odd ? ks.y : ks.x, x);
+        }
+        put4<O16>(p.k_out, dst, x);
+        scaled4(odd ? vb : va, VT == KVQ_V_Q8_0 ? 128 : 8, odd ? d.y : d.x, x);
+        put4<O16>(p.v_out, dst, x);
+    }
 }
 
 template <bool O16>
 static cudaError_t gather_t(const PagedRowsParams &p, int v_type, int k_type, cudaStream_t s, bool pdl)
 {
-    const int grid = (int)(((long long)p.n_tokens * p.pool.n_kv_heads + 3) / 4);
     void (*fn)(PagedRowsParams) =
         k_type == KVQ_K_F16 ? (v_type == KVQ_V_Q4_0 ? paged_gather_kernel<KVQ_V_Q4_0, KVQ_K_F16, O16> : paged_gather_kernel<KVQ_V_Q8_0, KVQ_K_F16, O16>)
                             : (v_type == KVQ_V_Q4_0 ? paged_gather_kernel<KVQ_V_Q4_0, KVQ_K_I8, O16> : paged_gather_kernel<KVQ_V_Q8_0, KVQ_K_I8, O16>);
-    return launch_pdl(fn, p, grid, 128, 0, s, pdl);
+    return launch_pdl(fn, p, row_blocks(p), kRowWarps * 32, 0, s, pdl);
 }
 
 cudaError_t launch_paged_gather(const PagedRowsParams &p, int v_type, int k_type, int out_type, cudaStream_t s, bool pdl)

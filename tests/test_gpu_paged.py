@@ -155,6 +155,43 @@ def test_append_and_gather(tokens, H, page, k_type, v_type):
                 assert np.array_equal(o.cpu().numpy()[:-3], ref[:-3]) and (o[-3:] == 777).all()
 
 
+@pytest.mark.parametrize("v_type", [Q4, Q8])
+def test_append_rounds_halves_as_the_rule_says(v_type):
+    """Blocks full of values at, just below and just above the halves of their
+    scale, at scales from fp16's subnormals to its largest, and with
+    infinities and NaN among them (whose own codes say nothing)."""
+    r = np.random.default_rng(3)
+    n, H = 512, 4
+    top = np.exp2(r.uniform(-25, 16, (n, H, 4, 1))).clip(0, 65504).astype(np.float16)
+    top[:8] = np.array([0, 2.0 ** -24, 3 * 2.0 ** -24, 190 * 2.0 ** -24, 2.0 ** -14, 65504, 1, 127], np.float16)[:, None, None, None]
+    kv = []
+    for most in (127, 8 if v_type == Q4 else 127):
+        s = (top.astype(np.float32) / np.float32(most)).astype(np.float16).astype(np.float64)
+        x = ((r.integers(0, most, (n, H, 4, 32)) + 0.5) * s).clip(0, 65504).astype(np.float16)
+        x = np.abs(x).view(np.int16) + r.integers(-1, 2, x.shape).astype(np.int16)
+        x = np.minimum(x.clip(0).astype(np.int16), top.view(np.int16)).view(np.float16)
+        x = np.where(r.random(x.shape) < 0.5, x, -x)
+        x[..., 5:6] = top * np.where(r.random(top.shape) < 0.5, 1, -1).astype(np.float16)
+        x[20:23, :, 1, 7] = np.array([np.inf, -np.inf, np.nan], np.float16)[:, None]
+        kv.append(np.ascontiguousarray(x.reshape(n, H, 128)))
+    for first in (0, 7):   # in pairs, and at an odd place first
+        pool = kvq.PagePool(9, 64, H, v_type)
+        pool.data.fill_(POISON)
+        slots = first + np.arange(n)
+        kvq.kvq_paged_append(pool, to_dev(kv[0]), to_dev(kv[1]), i32(slots))
+        rows = pool_rows(pool)
+        for name, ref in oracle.quantize_kv(kv[0], kv[1], v_type).items():
+            got = rows[name][slots // 64, :, slots % 64]
+            ref = np.ascontiguousarray(ref.transpose(1, 0, 2))
+            if name in ("kq", "vq"):
+                for a in (got, ref):
+                    a.view(np.uint8)[20:23, :, 32 + 7 if a.shape[2] == 128 else 16 + 7] &= 0xF0 if a.shape[2] == 64 else 0
+            else:   # infinity / 127 or 8 is infinity (the oracle takes an infinity's exponent, which C leaves open)
+                ref.view(np.uint16)[20:22, :, 1] = 0x7C00
+            bad = np.argwhere(got.view(np.uint8) != ref.view(np.uint8))
+            assert not len(bad), (name, len(bad), bad[:4], got.view(np.uint8)[tuple(bad[0])], ref.view(np.uint8)[tuple(bad[0])])
+
+
 def test_append_skips_rows_without_a_slot():
     pool = kvq.PagePool(2, 16, 2, Q8)
     pool.data.fill_(POISON)
