@@ -209,6 +209,10 @@ struct PagedPieces {
     int ctas;     // of the launch; 0: it cut nothing
     int spread;   // combine blocks per CTA
 };
+constexpr int kAttnParts = 3;   // launches of a call: row tiles of 8 rows, of 16, the chunk kernel
+struct PagedCuts {
+    PagedPieces part[kAttnParts];
+};
 
 struct PagedAttnParams {
     PoolDesc pool;
@@ -241,7 +245,7 @@ __device__ __forceinline__ void seq_shape(const PagedAttnParams &p, int b, int &
 
 // Work of a sequence, in stages of kStagePos positions for every row tile of
 // every kv head (at least one each: rows that see nothing are still written);
-// 0 when its rows belong to the other kernel.
+// 0 when its rows belong to another launch.
 __device__ __forceinline__ bool seq_mine(const PagedAttnParams &p, int n)
 {
     const long long rows = (long long)n * p.gmax;
@@ -253,8 +257,7 @@ cudaError_t launch_page_tables(TableParams p, cudaStream_t s, bool pdl);
 cudaError_t launch_paged_append(const PagedRowsParams &p, int v_type, int k_type, cudaStream_t s, bool pdl);
 cudaError_t launch_paged_gather(const PagedRowsParams &p, int v_type, int k_type, int out_type, cudaStream_t s,
                                 bool pdl);
-cudaError_t launch_paged_combine(const PagedAttnParams &p, const PagedPieces &g0, const PagedPieces &g1, int out_type,
-                                 cudaStream_t s, bool pdl);
+cudaError_t launch_paged_combine(const PagedAttnParams &p, const PagedCuts &cuts, int out_type, cudaStream_t s, bool pdl);
 // Row-tile attention (kvq_paged_attn_q4.cu / _q8.cu): nt = 8-row tiles per CTA (1 or 2).
 cudaError_t prepare_paged_q4(int nt, int k_type, int out_type, int *ctas_per_sm);
 cudaError_t prepare_paged_q8(int nt, int k_type, int out_type, int *ctas_per_sm);

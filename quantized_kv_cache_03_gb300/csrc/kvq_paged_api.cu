@@ -104,18 +104,17 @@ bool table_ok(int stride, int max_blocks, int page_tokens)
 }
 
 // ---- attention ----
-// One launch and its combine: CTAs, the row tile, and where its pieces lie in the workspace.
+// One launch: its CTAs (0: not made), its row tile, the rows per kv head of the
+// sequences it takes, and where its pieces lie in the workspace.
 struct Part {
-    int n_ctas = 0, rows = 0;
+    int n_ctas = 0, rows = 0, least = 0, most = 0;
     size_t cut_off = 0, lse_off = 0, o_off = 0, sum_off = 0;
 };
 
 struct AttnPlan {
-    int nt;              // 8-row tiles per CTA of the row-tile kernel
     int gmax;            // query heads of the busiest kv head
     int uniform;
-    int chunk_rows;      // sequences with at least this many rows per kv head go to the chunk kernel
-    Part tile, chunk;    // the two launches (n_ctas 0: not made)
+    Part part[kAttnParts];   // row tiles of 8 rows, of 16 rows, the chunk kernel
     size_t bytes;
     uint16_t grp_begin[KVQ_MAX_HEADS + 1];
     uint8_t grp_q[KVQ_MAX_HEADS];
@@ -190,19 +189,30 @@ void plan_attn(const kvq_paged_desc *a, const PagedDevice *dev, int n_sms, AttnP
 {
     const kvq_pages *g = a->pages;
     const long long rows = (long long)a->max_q * pl.gmax;   // most rows of a sequence per kv head
-    pl.chunk_rows = chunk_min_rows(g);
+    const int chunk = chunk_min_rows(g), bound[kAttnParts + 1] = {1, chunk < 9 ? chunk : 9, chunk, INT_MAX};
+    int top = 0;   // the kind that the longest sequence goes to
+    while (top < kAttnParts - 1 && rows >= bound[top + 1]) ++top;
+    // A batch of sequences of the same number of rows is one launch (an idle
+    // one costs 3 us).  What q_start holds is known on the device alone, so the
+    // launch takes fewer rows too.  Otherwise each sequence goes to its kind (40
+    // single tokens beside four chunks: 315 us, with row tiles of 16 for all the
+    // short ones 351).
+    const bool alike = (long long)a->n_seqs * a->max_q <= a->n_tokens;
     pl.bytes = 0;
-    pl.tile = pl.chunk = Part();
-    if (pl.chunk_rows > 1) {
-        const long long most = rows < pl.chunk_rows ? rows : pl.chunk_rows - 1;
-        pl.nt = most <= 8 ? 1 : 2;
-        const int per_sm = dev->ctas[g->k_type][g->v_type][pl.nt][a->out_type];
-        size_part(a, pl, pl.tile, n_sms * (per_sm > 0 ? per_sm : 1), 8 * pl.nt, kStagePos, kPagedMinStages, pl.bytes);
-    }
-    if (rows >= pl.chunk_rows) {
-        size_part(a, pl, pl.chunk, n_sms, kChunkRows, kChunkPositions, kChunkMinTiles, pl.bytes);
-        pl.chunk.sum_off = pl.bytes;
-        pl.bytes += ((size_t)pl.chunk.n_ctas * kChunkSums * sizeof(float) + 255) / 256 * 256;
+    for (int k = 0; k < kAttnParts; ++k) {
+        Part &pt = pl.part[k];
+        pt = Part();
+        if (k > top || (alike && k != top) || bound[k] >= bound[k + 1]) continue;
+        pt.least = alike ? 1 : bound[k];
+        pt.most = k == top ? INT_MAX : bound[k + 1] - 1;
+        if (k < 2) {
+            const int per_sm = dev->ctas[g->k_type][g->v_type][k + 1][a->out_type];
+            size_part(a, pl, pt, n_sms * (per_sm > 0 ? per_sm : 1), 8 * (k + 1), kStagePos, kPagedMinStages, pl.bytes);
+        } else {
+            size_part(a, pl, pt, n_sms, kChunkRows, kChunkPositions, kChunkMinTiles, pl.bytes);
+            pt.sum_off = pl.bytes;
+            pl.bytes += ((size_t)pt.n_ctas * kChunkSums * sizeof(float) + 255) / 256 * 256;
+        }
     }
 }
 
@@ -354,31 +364,27 @@ kvq_status kvq_paged_attn(const kvq_paged_desc *a, void *workspace, size_t works
     const bool pdl = pdl_on();
     const kvq_pages *g = a->pages;
     const bool q4 = g->v_type == KVQ_V_Q4_0;
-    PagedPieces cut[2] = {};
-    auto pieces = [&](const Part &pt, PagedPieces &c) {
+    PagedCuts cuts = {};
+    cudaError_t e = cudaSuccess;
+    for (int k = 0; k < kAttnParts && e == cudaSuccess; ++k) {
+        const Part &pt = pl.part[k];
+        if (pt.n_ctas == 0) continue;
         char *w = static_cast<char *>(workspace);
         p.cuts = reinterpret_cast<PagedCut *>(w + pt.cut_off);
         p.ws_lse = reinterpret_cast<float *>(w + pt.lse_off);
         p.ws_o = reinterpret_cast<float *>(w + pt.o_off);
+        p.sums = reinterpret_cast<float *>(w + pt.sum_off);
+        p.min_rows = pt.least;
+        p.max_rows = pt.most;
         // a cut tile is merged by at least two CTAs' blocks of eight warps
-        c = PagedPieces{p.cuts, p.ws_lse, p.ws_o, pt.rows, pt.n_ctas > 1 ? pt.n_ctas : 0, (pt.rows + 15) / 16};
-    };
-    cudaError_t e = cudaSuccess;
-    if (pl.tile.n_ctas > 0) {
-        pieces(pl.tile, cut[0]);
-        p.min_rows = 1;
-        p.max_rows = pl.chunk_rows - 1;
-        e = q4 ? launch_paged_q4(p, pl.nt, g->k_type, a->out_type, pl.tile.n_ctas, s, pdl && pl.tile.n_ctas <= n_sms)
-               : launch_paged_q8(p, pl.nt, g->k_type, a->out_type, pl.tile.n_ctas, s, pdl && pl.tile.n_ctas <= n_sms);
+        cuts.part[k] = PagedPieces{p.cuts, p.ws_lse, p.ws_o, pt.rows, pt.n_ctas > 1 ? pt.n_ctas : 0, (pt.rows + 15) / 16};
+        if (k < 2)
+            e = q4 ? launch_paged_q4(p, k + 1, g->k_type, a->out_type, pt.n_ctas, s, pdl && pt.n_ctas <= n_sms)
+                   : launch_paged_q8(p, k + 1, g->k_type, a->out_type, pt.n_ctas, s, pdl && pt.n_ctas <= n_sms);
+        else
+            e = q4 ? launch_chunk_q4(p, a->out_type, pt.n_ctas, s, pdl) : launch_chunk_q8(p, a->out_type, pt.n_ctas, s, pdl);
     }
-    if (e == cudaSuccess && pl.chunk.n_ctas > 0) {
-        pieces(pl.chunk, cut[1]);
-        p.sums = reinterpret_cast<float *>(static_cast<char *>(workspace) + pl.chunk.sum_off);
-        p.min_rows = pl.chunk_rows;
-        p.max_rows = INT_MAX;
-        e = q4 ? launch_chunk_q4(p, a->out_type, pl.chunk.n_ctas, s, pdl) : launch_chunk_q8(p, a->out_type, pl.chunk.n_ctas, s, pdl);
-    }
-    if (e == cudaSuccess) e = launch_paged_combine(p, cut[0], cut[1], a->out_type, s, pdl);
+    if (e == cudaSuccess) e = launch_paged_combine(p, cuts, a->out_type, s, pdl);
     return done(e);
 }
 

@@ -426,7 +426,7 @@ cudaError_t launch_paged_gather(const PagedRowsParams &p, int v_type, int k_type
 
 // ---------------------------------------------------------------------------
 // Combine: the pieces of the row tiles that several CTAs of an attention launch
-// attended, for both launches of a call at once.  The pieces of a tile are
+// attended, for all launches of a call at once.  The pieces of a tile are
 // weighted by exp(lse_i - max lse) / sum; what bounds it is the latency of its
 // rounds of loads.  The blocks of CTA i share the merge of the tile its slot 1
 // began and of the one its slot 0 went on with, so a tile cut into np pieces is
@@ -503,13 +503,13 @@ __device__ __forceinline__ void put_merged(const PagedAttnParams &p, size_t row,
 
 template <bool O16>
 __global__ void __launch_bounds__(kPcWarps * 32, 4) paged_combine_kernel(const __grid_constant__ PagedAttnParams p,
-                                                                      const __grid_constant__ PagedPieces g0,
-                                                                      const __grid_constant__ PagedPieces g1)
+                                                                      const __grid_constant__ PagedCuts cuts)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n0 = g0.ctas * g0.spread;
-    const PagedPieces &g = (int)blockIdx.x < n0 ? g0 : g1;
-    const int block = (int)blockIdx.x - ((int)blockIdx.x < n0 ? 0 : n0), cta = block / g.spread;
+    int block = blockIdx.x, k = 0;
+    while (k < kAttnParts - 1 && block >= cuts.part[k].ctas * cuts.part[k].spread) block -= cuts.part[k].ctas * cuts.part[k].spread, ++k;
+    const PagedPieces &g = cuts.part[k];
+    const int cta = block / g.spread;
     pdl_wait();
     pdl_trigger();
     for (int slot = 0; slot < 2; ++slot) {
@@ -548,10 +548,10 @@ __global__ void __launch_bounds__(kPcWarps * 32, 4) paged_combine_kernel(const _
     }
 }
 
-cudaError_t launch_paged_combine(const PagedAttnParams &p, const PagedPieces &g0, const PagedPieces &g1, int out_type,
-                                 cudaStream_t s, bool pdl)
+cudaError_t launch_paged_combine(const PagedAttnParams &p, const PagedCuts &cuts, int out_type, cudaStream_t s, bool pdl)
 {
-    const int blocks = g0.ctas * g0.spread + g1.ctas * g1.spread;
+    int blocks = 0;
+    for (const PagedPieces &g : cuts.part) blocks += g.ctas * g.spread;
     if (blocks == 0) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks);
@@ -562,8 +562,8 @@ cudaError_t launch_paged_combine(const PagedAttnParams &p, const PagedPieces &g0
     at[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (out_type == KVQ_OUT_F16) return cudaLaunchKernelEx(&cfg, paged_combine_kernel<true>, p, g0, g1);
-    return cudaLaunchKernelEx(&cfg, paged_combine_kernel<false>, p, g0, g1);
+    if (out_type == KVQ_OUT_F16) return cudaLaunchKernelEx(&cfg, paged_combine_kernel<true>, p, cuts);
+    return cudaLaunchKernelEx(&cfg, paged_combine_kernel<false>, p, cuts);
 }
 
 }  // namespace kvq
