@@ -52,15 +52,18 @@ struct PagedCfg {
     static constexpr int ROWS = 8 * NT;
     static constexpr int KROW = F16K ? 2 * kD : kD;           // bytes of a query row's codes
     static constexpr int Q_OFF = WARPS * RING;
-    static constexpr int QS_OFF = Q_OFF + ROWS * KROW;        // fp32 [ROWS][kNB]
-    static constexpr int QSUM_OFF = QS_OFF + ROWS * kNB * 4;  // fp32 [ROWS][kNB]: accumulator seeds
-    static constexpr int BAR_OFF = QSUM_OFF + ROWS * kNB * 4;
+    // int8 K, by block and pair of rows that a lane holds: the accumulators'
+    // starts as the MMA takes them, the scales
+    static constexpr int PAIRS = ROWS / 2;
+    static constexpr int QSEED_OFF = Q_OFF + ROWS * KROW;            // fp32 [kNB][PAIRS][4]
+    static constexpr int QS_OFF = QSEED_OFF + kNB * PAIRS * 16;      // fp32 [kNB][PAIRS][2]
+    static constexpr int BAR_OFF = QS_OFF + kNB * PAIRS * 8;
     static constexpr int MISC_OFF = BAR_OFF + WARPS * STAGES * 8;
     static constexpr int SMEM = MISC_OFF + 128;
     static constexpr int OROW = kD + 4;
     static constexpr int ML_OFF = WARPS * ROWS * OROW * 4;    // merge: slices, then m, l per warp, then 1/L, lse
     static_assert(ML_OFF + (2 * WARPS + 2) * ROWS * 4 <= WARPS * RING, "the merge reuses the rings");
-    static_assert(T::BYTES % 128 == 0 && BAR_OFF % 8 == 0 && QS_OFF % 16 == 0, "alignment");
+    static_assert(T::BYTES % 128 == 0 && BAR_OFF % 8 == 0 && QSEED_OFF % 16 == 0, "alignment");
 };
 
 template <int NT, int VT, int KT, bool O16>
@@ -180,8 +183,10 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const 
             uint32_t qa[8][2 * NT];            // [k16 step][row g: k 2c.., k 2c + 8..; row g + 8 likewise]
             // the two rows whose scores the lane holds: 2c, 2c + 1 (NT = 1), g, g + 8 (NT = 2)
             const int lrow[2] = {NT == 1 ? 2 * c : g, NT == 1 ? 2 * c + 1 : g + 8};
-            // int8 K: scales and accumulator seeds [row][block]; read again for each stage, the registers hold enough
-            float *qs = reinterpret_cast<float *>(smem + C::QS_OFF), *qsum = reinterpret_cast<float *>(smem + C::QSUM_OFF);
+            // int8 K: read again for each stage, the registers hold enough
+            float4 *qseed = reinterpret_cast<float4 *>(smem + C::QSEED_OFF);
+            float2 *qs = reinterpret_cast<float2 *>(smem + C::QS_OFF);
+            const int pair = NT == 1 ? c : g;
             {
                 uint32_t *qw = reinterpret_cast<uint32_t *>(smem + C::Q_OFF);
 #pragma unroll
@@ -208,8 +213,10 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const 
                     sum += __shfl_xor_sync(0xffffffffu, sum, 4);
                     qw[r * (kD / 4) + lane] = word;
                     if ((lane & 7) == 0) {
-                        qs[r * kNB + (lane >> 3)] = __half2float(__ushort_as_half(s16)) * p.qk_scale_log2;
-                        qsum[r * kNB + (lane >> 3)] = -kBias * (float)sum;
+                        const int x = (lane >> 3) * C::PAIRS + (NT == 1 ? r >> 1 : r & 7), e = NT == 1 ? r & 1 : r >> 3;
+                        float *sd = reinterpret_cast<float *>(qseed + x);
+                        reinterpret_cast<float *>(qs + x)[e] = __half2float(__ushort_as_half(s16)) * p.qk_scale_log2;
+                        sd[NT == 1 ? e : 2 * e] = sd[NT == 1 ? e + 2 : 2 * e + 1] = -kBias * (float)sum;
                     }
                 }
                 __syncthreads();
@@ -266,15 +273,13 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const 
                     // scores of 8-position group i (of four): NT = 1 position 8i + g, rows (2c, 2c + 1);
                     // NT = 2 positions (8i + 2c, + 1), [row g, row g + 8]
                     float2 s[NT][4];
-                    auto h2f = [](uint32_t w) { return half2_of(w); };
+                    if constexpr (C::F16K) {
 #pragma unroll
-                    for (int t = 0; t < C::TPS; ++t) {
-                        const uint8_t *tk = stg + t * T::BYTES;
-                        if constexpr (C::F16K) {
+                        for (int t = 0; t < C::TPS; ++t) {
                             float d[2][4] = {};
 #pragma unroll
                             for (int ks = 0; ks < 8; ++ks) {
-                                const uint4 k4 = *reinterpret_cast<const uint4 *>(tk + ks * 512 + lane * 16);
+                                const uint4 k4 = *reinterpret_cast<const uint4 *>(stg + t * T::BYTES + ks * 512 + lane * 16);
                                 if constexpr (NT == 1) {
                                     const uint32_t a[4] = {k4.x, k4.y, k4.z, k4.w};
                                     mma_f16_16816(d[0], a, qa[ks][0], qa[ks][1]);
@@ -294,56 +299,64 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const 
                                     s[NT - 1][2 * t + i] = mul2(make_float2(d[i][2], d[i][3]), sc);
                                 }
                             }
-                        } else {
-                            uint4 kk[2][2], sk[2];
+                        }
+                    } else {
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
+                        for (int hb = 0; hb < 2; ++hb) {   // blocks 2hb, 2hb + 1
+                            __syncwarp();                  // keeps the scheduler from loading the next blocks early and spilling
+                            uint4 kk[C::TPS][2];
+                            uint2 sk[C::TPS][2];           // NT = 1: the scale pairs of positions 2 (g/2), + 1; NT = 2: of 2c, 2c + 1
 #pragma unroll
-                                for (int hb = 0; hb < 2; ++hb) kk[i][hb] = *reinterpret_cast<const uint4 *>(tk + (2 * i + hb) * 512 + lane * 16);
-                                // NT = 1: the scale pairs of positions 2 (g/2), + 1; NT = 2: of 2c, 2c + 1
-                                sk[i] = *reinterpret_cast<const uint4 *>(tk + T::KS_OFF + (4 * i + (NT == 1 ? g >> 1 : c)) * 16);
-                            }
-#pragma unroll
-                            for (int bb = 0; bb < kNB; ++bb) {
-                                __syncwarp();                  // as below
-                                uint32_t lo[2][2], hi[2][2];   // [position group][k16 step]: K bytes 0, 1 and 2, 3 as 1152 + code
+                            for (int t = 0; t < C::TPS; ++t)
 #pragma unroll
                                 for (int i = 0; i < 2; ++i) {
-                                    const uint4 &kw = kk[i][bb >> 1];
-                                    const uint32_t w0 = (bb & 1) ? kw.z : kw.x, w1 = (bb & 1) ? kw.w : kw.y;
-                                    lo[i][0] = __byte_perm(w0, 0x64646464u, 0x4140);
-                                    hi[i][0] = __byte_perm(w0, 0x64646464u, 0x4342);
-                                    lo[i][1] = __byte_perm(w1, 0x64646464u, 0x4140);
-                                    hi[i][1] = __byte_perm(w1, 0x64646464u, 0x4342);
+                                    const uint8_t *tk = stg + t * T::BYTES;
+                                    kk[t][i] = *reinterpret_cast<const uint4 *>(tk + (2 * i + hb) * 512 + lane * 16);
+                                    sk[t][i] = *reinterpret_cast<const uint2 *>(tk + T::KS_OFF + (4 * i + (NT == 1 ? g >> 1 : c)) * 16 + 8 * hb);
                                 }
-                                const uint32_t sd0 = __float_as_uint(qsum[lrow[0] * kNB + bb]), sd1 = __float_as_uint(qsum[lrow[1] * kNB + bb]);
-                                const float sq[2] = {qs[lrow[0] * kNB + bb], qs[lrow[1] * kNB + bb]};
-                                if constexpr (NT == 1) {   // S^T = K Q^T: rows are the 16 positions
-                                    float d[4];
-                                    const uint32_t a0[4] = {lo[0][0], lo[1][0], hi[0][0], hi[1][0]}, a1[4] = {lo[0][1], lo[1][1], hi[0][1], hi[1][1]};
-                                    mma_f16_16816_c4(d, a0, qa[2 * bb][0], qa[2 * bb][1], make_uint4(sd0, sd1, sd0, sd1));
-                                    mma_f16_16816(d, a1, qa[2 * bb + 1][0], qa[2 * bb + 1][1]);
-                                    const float2 q2 = make_float2(sq[0], sq[1]);
+#pragma unroll
+                            for (int bb = 2 * hb; bb < 2 * hb + 2; ++bb) {
+                                const uint4 seed = *reinterpret_cast<const uint4 *>(qseed + bb * C::PAIRS + pair);
+                                const float2 sq = qs[bb * C::PAIRS + pair];
+#pragma unroll
+                                for (int t = 0; t < C::TPS; ++t) {
+                                    uint32_t lo[2][2], hi[2][2];   // [position group][k16 step]: K bytes 0, 1 and 2, 3 as 1152 + code
 #pragma unroll
                                     for (int i = 0; i < 2; ++i) {
-                                        const uint32_t sw = bb == 0 ? sk[i].x : bb == 1 ? sk[i].y : bb == 2 ? sk[i].z : sk[i].w;
-                                        const float f = half2_of(__byte_perm(sw, sw, pick)).x;
-                                        const float2 v = mul2(make_float2(d[2 * i], d[2 * i + 1]), q2), s2 = make_float2(f, f);
-                                        s[0][2 * t + i] = bb == 0 ? mul2(v, s2) : fma2(v, s2, s[0][2 * t + i]);
+                                        const uint4 &kw = kk[t][i];
+                                        const uint32_t w0 = (bb & 1) ? kw.z : kw.x, w1 = (bb & 1) ? kw.w : kw.y;
+                                        lo[i][0] = __byte_perm(w0, 0x64646464u, 0x4140);
+                                        hi[i][0] = __byte_perm(w0, 0x64646464u, 0x4342);
+                                        lo[i][1] = __byte_perm(w1, 0x64646464u, 0x4140);
+                                        hi[i][1] = __byte_perm(w1, 0x64646464u, 0x4342);
                                     }
-                                } else {                   // S = Q K^T: rows are the query rows
-#pragma unroll
-                                    for (int i = 0; i < 2; ++i) {
+                                    if constexpr (NT == 1) {   // S^T = K Q^T: rows are the 16 positions
                                         float d[4];
-                                        const uint32_t a0[4] = {qa[2 * bb][0], qa[2 * bb][2 * NT - 2], qa[2 * bb][1], qa[2 * bb][2 * NT - 1]};
-                                        const uint32_t a1[4] = {qa[2 * bb + 1][0], qa[2 * bb + 1][2 * NT - 2], qa[2 * bb + 1][1], qa[2 * bb + 1][2 * NT - 1]};
-                                        mma_f16_16816_c4(d, a0, lo[i][0], hi[i][0], make_uint4(sd0, sd0, sd1, sd1));
-                                        mma_f16_16816(d, a1, lo[i][1], hi[i][1]);
-                                        const float2 s2 = h2f(bb == 0 ? sk[i].x : bb == 1 ? sk[i].y : bb == 2 ? sk[i].z : sk[i].w);
+                                        const uint32_t a0[4] = {lo[0][0], lo[1][0], hi[0][0], hi[1][0]}, a1[4] = {lo[0][1], lo[1][1], hi[0][1], hi[1][1]};
+                                        mma_f16_16816_c4(d, a0, qa[2 * bb][0], qa[2 * bb][1], seed);
+                                        mma_f16_16816(d, a1, qa[2 * bb + 1][0], qa[2 * bb + 1][1]);
 #pragma unroll
-                                        for (int nt = 0; nt < NT; ++nt) {
-                                            const float2 v = mul2(make_float2(d[2 * nt], d[2 * nt + 1]), make_float2(sq[nt], sq[nt]));
-                                            s[nt][2 * t + i] = bb == 0 ? mul2(v, s2) : fma2(v, s2, s[nt][2 * t + i]);
+                                        for (int i = 0; i < 2; ++i) {
+                                            const uint32_t sw = (bb & 1) ? sk[t][i].y : sk[t][i].x;
+                                            const float f = half2_of(__byte_perm(sw, sw, pick)).x;
+                                            const float2 v = mul2(make_float2(d[2 * i], d[2 * i + 1]), sq), s2 = make_float2(f, f);
+                                            s[0][2 * t + i] = bb == 0 ? mul2(v, s2) : fma2(v, s2, s[0][2 * t + i]);
+                                        }
+                                    } else {                   // S = Q K^T: rows are the query rows
+#pragma unroll
+                                        for (int i = 0; i < 2; ++i) {
+                                            float d[4];
+                                            const uint32_t a0[4] = {qa[2 * bb][0], qa[2 * bb][2 * NT - 2], qa[2 * bb][1], qa[2 * bb][2 * NT - 1]};
+                                            const uint32_t a1[4] = {qa[2 * bb + 1][0], qa[2 * bb + 1][2 * NT - 2], qa[2 * bb + 1][1], qa[2 * bb + 1][2 * NT - 1]};
+                                            mma_f16_16816_c4(d, a0, lo[i][0], hi[i][0], seed);
+                                            mma_f16_16816(d, a1, lo[i][1], hi[i][1]);
+                                            const float2 s2 = half2_of((bb & 1) ? sk[t][i].y : sk[t][i].x);
+#pragma unroll
+                                            for (int nt = 0; nt < NT; ++nt) {
+                                                const float q1 = nt == 0 ? sq.x : sq.y;
+                                                const float2 v = mul2(make_float2(d[2 * nt], d[2 * nt + 1]), make_float2(q1, q1));
+                                                s[nt][2 * t + i] = bb == 0 ? mul2(v, s2) : fma2(v, s2, s[nt][2 * t + i]);
+                                            }
                                         }
                                     }
                                 }
@@ -446,7 +459,7 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const 
                     // ---- O^T += V^T P^T, block by block ----
 #pragma unroll
                     for (int hb = 0; hb < 2; ++hb) {   // blocks 2hb, 2hb + 1
-                        __syncwarp();                  // keeps the scheduler from loading the next blocks early and spilling
+                        __syncwarp();                  // as above
                         uint4 vv[C::TPS][2];           // their V codes: q4 in x, y only
                         uint2 sv[C::TPS][2];
 #pragma unroll
@@ -485,7 +498,7 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const 
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const uint32_t dw = (bb & 1) ? sv[t][i].y : sv[t][i].x;
-                                d2[i] = h2f(dw);
+                                d2[i] = half2_of(dw);
                             }
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {

@@ -174,6 +174,17 @@ __device__ __forceinline__ void u8x8_hilo(uint32_t w0, uint32_t w1, __half2 s2, 
     lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
+// w[(k + r) % 4] = w[k].
+__device__ __forceinline__ void turn4(uint32_t (&w)[4], int r)
+{
+    const bool one = r & 1, two = r & 2;
+    const uint32_t a = one ? w[3] : w[0], b = one ? w[0] : w[1], c = one ? w[1] : w[2], d = one ? w[2] : w[3];
+    w[0] = two ? c : a;
+    w[1] = two ? d : b;
+    w[2] = two ? a : c;
+    w[3] = two ? b : d;
+}
+
 // A piece of the line, as the roles read it from shared memory.
 struct ChunkWalk {
     int tiles;               // KV tiles with a visible position among those of the piece; negative: no more pieces
@@ -471,7 +482,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
         // ================= K converters =================
         const int i = warp - kCKConv0;   // 16-byte chunk i of each cache tile: one position's codes of two blocks
         const int u = 8 * (i >> 1) + (lane >> 2), dg = 8 * (i & 1) + (lane & 3);
-        const int soff = T::KS_OFF + scale_off(u, 2 * (i & 1));
+        const int soff = T::KS_OFF + (u >> 1) * 16 + 8 * (i & 1);   // both blocks' scales of positions u & ~1, u | 1
+        const uint32_t mine = u & 1 ? 0x3232u : 0x1010u;
         int hh = 0;
         pieces(false, [&](const ChunkWalk &w, int) {
             for (int t = 0; t < 2 * w.tiles; ++t, ++hh) {
@@ -482,14 +494,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
 #pragma unroll 2
                 for (int q = 0; q < kCSub; ++q) {
                     const uint4 v = *reinterpret_cast<const uint4 *>(raw + q * C::KPART + i * 512 + lane * 16);
-                    const __half s0 = __ushort_as_half(*reinterpret_cast<const uint16_t *>(raw + q * C::KPART + soff));
-                    const __half s1 = __ushort_as_half(*reinterpret_cast<const uint16_t *>(raw + q * C::KPART + soff + 4));
+                    const uint2 sc = *reinterpret_cast<const uint2 *>(raw + q * C::KPART + soff);
+                    const uint32_t s0 = __byte_perm(sc.x, 0u, mine), s1 = __byte_perm(sc.y, 0u, mine);
                     const __half2 k05 = __half2half2(__ushort_as_half(kHalfBits));
                     uint4 hi, lo;
-                    u8x8_hilo(v.x, v.y, __hmul2(__half2half2(s0), k05), hi, lo);
+                    u8x8_hilo(v.x, v.y, __hmul2(*reinterpret_cast<const __half2 *>(&s0), k05), hi, lo);
                     *reinterpret_cast<uint4 *>(kh + 2 * q * C::K_SBO) = hi;
                     *reinterpret_cast<uint4 *>(kl + 2 * q * C::K_SBO) = lo;
-                    u8x8_hilo(v.z, v.w, __hmul2(__half2half2(s1), k05), hi, lo);
+                    u8x8_hilo(v.z, v.w, __hmul2(*reinterpret_cast<const __half2 *>(&s1), k05), hi, lo);
                     *reinterpret_cast<uint4 *>(kh + 2 * q * C::K_SBO + 4 * C::K_LBO) = hi;
                     *reinterpret_cast<uint4 *>(kl + 2 * q * C::K_SBO + 4 * C::K_LBO) = lo;
                 }
@@ -519,6 +531,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                 const bool full = ok == 15 && x + kCHalf - 1 <= w.lim_hi;
                 const __half2 k05 = __half2half2(__ushort_as_half(kHalfBits));
                 uint32_t hi[4][4], lo[4][4];   // [dim of four][position pair]
+                // The words of position pair c are 64 bytes apart over the columns, so the columns begin
+                // with different pairs (a warp's load in one wavefront, or two for q8_0, instead of four
+                // and eight) and the words are put in order afterwards.
+                uint32_t vw[4], vx[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int c = (k + (g >> 1)) & 3;
+                    vx[k] = 0u;
+                    if (VT == KVQ_V_Q4_0) {
+                        vw[k] = *reinterpret_cast<const uint32_t *>(tv + half * 512 + (4 * g + c) * 16 + 4 * bb);
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(tv + (2 * half + (bb >> 1)) * 512 + (4 * g + c) * 16 + 8 * (bb & 1));
+                        vw[k] = v.x;
+                        vx[k] = v.y;
+                    }
+                }
+                turn4(vw, g >> 1);
+                if (VT == KVQ_V_Q8_0) turn4(vx, g >> 1);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t dw = *reinterpret_cast<const uint32_t *>(ts + 16 * c);   // scales of positions 2c, 2c + 1
@@ -528,12 +558,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                     }
                     const __half2 d2 = __hmul2(*reinterpret_cast<const __half2 *>(&dw), k05);
                     uint32_t r[2][2];
-                    if (VT == KVQ_V_Q4_0) {
-                        v_codes<VT>(*reinterpret_cast<const uint32_t *>(tv + half * 512 + (4 * g + c) * 16 + 4 * bb), 0u, r);
-                    } else {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(tv + (2 * half + (bb >> 1)) * 512 + (4 * g + c) * 16 + 8 * (bb & 1));
-                        v_codes<VT>(v.x, v.y, r);
-                    }
+                    v_codes<VT>(vw[c], vx[c], r);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v_hilo(r[e >> 1][e & 1], d2, hi[e][c], lo[e][c]);
                 }
