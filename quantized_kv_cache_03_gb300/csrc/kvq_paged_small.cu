@@ -15,12 +15,12 @@ namespace kvq {
 // around), the cluster synchronizes once, so that lens and n_free may be
 // updated in place, and the outputs are dealt out flat over its threads with
 // a binary search each; a warp copies a released sequence's pages.  Latency-bound
-// (256 sequences, a row each: 6.6 us; its bytes take 0.1 us): the launch, one
+// (256 sequences, a row each: 6.3 us; its bytes take 0.1 us): the launch, one
 // round of loads, three scans, the cluster's barrier.  One CTA alone instead of
-// eight is no faster (6.6).  The rows' slots are filled here up to one pass of
+// eight is no faster.  The rows' slots are filled here up to one pass of
 // the cluster's threads (16384 rows), beyond that by a second, wide launch:
-// 17942 rows 7.15 us here, 6.82 there; 272442 rows 36.8 and 10.6; 7726 rows 5.70
-// and 6.63.
+// 17942 rows 7.15 us here, 6.6 there; 272442 rows 36.8 and 10.5; 7726 rows 5.6
+// and 6.6.
 // ---------------------------------------------------------------------------
 constexpr int kTabThreads = 512;
 
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
     __shared__ long long tmp[kTabThreads / 32];
     __shared__ int popped_s;
     const int n = p.n_seqs, tid = threadIdx.x, P = 1 << p.pshift;
-    int *qs = tab, *need0 = qs + n + 1, *back0 = need0 + n + 1, *len_s = back0 + n + 1;
+    int *qs = tab, *need0 = qs + n + 1, *back0 = need0 + n + 1, *len_s = back0 + n + 1, *add_s = len_s + n;
     uint32_t rank, ranks;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
@@ -79,6 +79,7 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
     for (int i = i0; i < i1; ++i) {
         const int len = (int)min(max((long long)p.lens[i], 0ll), lmax), add = p.n_new[i];
         len_s[i] = len;
+        add_s[i] = add;
         rows += max(add, 0);
         if (add < 0) back += (len + P - 1) >> p.pshift;
     }
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
     auto pages = [&](int len, int add) { return (int)((((long long)len + add + P - 1) >> p.pshift) - ((len + P - 1) >> p.pshift)); };
     long long need = 0, r = rows0, bk = backs0;
     for (int i = i0; i < i1; ++i) {
-        const int len = len_s[i], add = p.n_new[i];
+        const int len = len_s[i], add = add_s[i];
         qs[i] = (int)min(r, 0x7fffffffll);
         back0[i] = (int)min(bk, 0x7fffffffll);
         r += max(add, 0);
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
     long long nd = needs0;
     r = rows0;
     for (int i = i0; i < i1; ++i) {
-        const int len = len_s[i], add = p.n_new[i];
+        const int len = len_s[i], add = add_s[i];
         r += max(add, 0);
         need0[i] = (int)min(nd, 0x7fffffffll);
         if (add > 0 && fits(len, add, r)) {
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
     };
     const int at = rank * kTabThreads + tid, all = ranks * kTabThreads;
     for (int b = at; b < n; b += all) {
-        const int add = p.n_new[b], st = add > 0 ? granted(b, add) : 0;
+        const int add = add_s[b], st = add > 0 ? granted(b, add) : 0;
         p.status[b] = st;
         p.lens_out[b] = add < 0 ? 0 : st == 0 ? len_s[b] + add : len_s[b];
     }
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
     const int warp = at >> 5, warps = all >> 5, lane = tid & 31;
     for (int b0 = warp; b0 < n; b0 += 32 * warps) {
         const int mine = b0 + lane * warps;
-        for (unsigned set = __ballot_sync(0xffffffffu, mine < n && p.n_new[mine] < 0); set; set &= set - 1) {
+        for (unsigned set = __ballot_sync(0xffffffffu, mine < n && add_s[mine] < 0); set; set &= set - 1) {
             const int b = b0 + (__ffs(set) - 1) * warps, v0 = n_free + back0[b], m = min(back0[b + 1] - back0[b], n_free_out - v0);
             const int *from = p.block_table + (size_t)b * p.stride;
             for (int k0 = lane; k0 < m; k0 += 256) {   // eight loads in flight
@@ -167,14 +168,14 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
     for (int t = 4 * at; t < p.n_tokens; t += 4 * all) {
         int s4[4] = {-1, -1, -1, -1};
         if (t < owned) {
-            int b = last_at_most(qs, n, t), st = granted(b, p.n_new[b]);
+            int b = last_at_most(qs, n, t), st = granted(b, add_s[b]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 if (t + k >= owned) break;
                 if (t + k >= qs[b + 1]) {
                     do ++b;
                     while (t + k >= qs[b + 1]);
-                    st = granted(b, p.n_new[b]);
+                    st = granted(b, add_s[b]);
                 }
                 if (st) continue;
                 const int len = len_s[b], pos = len + (t + k - qs[b]), j = pos >> p.pshift, have = (len + P - 1) >> p.pshift;
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kSlotThreads) page_slots_kernel(const TablePar
 
 cudaError_t prepare_page_tables()
 {
-    constexpr int most = (4 * KVQ_MAX_PAGED_SEQS + 3) * (int)sizeof(int);
+    constexpr int most = (5 * KVQ_MAX_PAGED_SEQS + 3) * (int)sizeof(int);
     static_assert(most <= 100 * 1024, "the sums of every sequence fit in shared memory");
     return cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
 }
@@ -246,7 +247,7 @@ cudaError_t launch_page_tables(TableParams p, cudaStream_t s, bool pdl)
     p.slots_here = p.n_tokens <= 4 * ctas * kTabThreads;
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kTabThreads);
-    cfg.dynamicSmemBytes = (4 * (size_t)p.n_seqs + 3) * sizeof(int);
+    cfg.dynamicSmemBytes = (5 * (size_t)p.n_seqs + 3) * sizeof(int);
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
