@@ -66,8 +66,12 @@ struct PagedCfg {
     static_assert(T::BYTES % 128 == 0 && BAR_OFF % 8 == 0 && QSEED_OFF % 16 == 0, "alignment");
 };
 
+// Three CTAs of 8-row tiles per SM, two of 16-row tiles: with a warp more per
+// scheduler the accumulators and fragments spill or are loaded too late to
+// overlap (131072 positions, 5 rows: 48 us at three, 53 at four, 49 at two;
+// 16 sequences of 32 rows: 419 us at two, 442 at three).
 template <int NT, int VT, int KT, bool O16>
-__global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const __grid_constant__ PagedAttnParams p)
+__global__ void __launch_bounds__(128, NT == 1 ? 3 : 2) paged_attn_kernel(const __grid_constant__ PagedAttnParams p)
 {
     using C = PagedCfg<NT, VT, KT>;
     using T = PageTile<VT, KT>;
@@ -303,7 +307,6 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const 
                     } else {
 #pragma unroll
                         for (int hb = 0; hb < 2; ++hb) {   // blocks 2hb, 2hb + 1
-                            __syncwarp();                  // keeps the scheduler from loading the next blocks early and spilling
                             uint4 kk[C::TPS][2];
                             uint2 sk[C::TPS][2];           // NT = 1: the scale pairs of positions 2 (g/2), + 1; NT = 2: of 2c, 2c + 1
 #pragma unroll
@@ -459,7 +462,6 @@ __global__ void __launch_bounds__(128, NT == 1 ? 4 : 3) paged_attn_kernel(const 
                     // ---- O^T += V^T P^T, block by block ----
 #pragma unroll
                     for (int hb = 0; hb < 2; ++hb) {   // blocks 2hb, 2hb + 1
-                        __syncwarp();                  // as above
                         uint4 vv[C::TPS][2];           // their V codes: q4 in x, y only
                         uint2 sv[C::TPS][2];
 #pragma unroll
