@@ -55,7 +55,7 @@ constexpr int kCKConv0 = 8, kCVConv0 = 12, kCQk = 20, kCPv = 21, kCKCopy = 22, k
 constexpr int kChunkWarps = 24, kChunkThreads = kChunkWarps * 32;
 // Registers per thread: the launch gives every thread kCRegs (768 threads); the
 // warpgroups then trade: 256 * 104 + 384 * 64 + 128 * 80 = 768 * 80.
-constexpr int kCRegs = 80, kCRegsSoft = 104, kCRegsConv = 64, kCRegsRest = 80;
+constexpr int kCRegs = 80, kCRegsSoft = 120, kCRegsConv = 56, kCRegsRest = 72;
 static_assert(256 * kCRegsSoft + 384 * kCRegsConv + 128 * kCRegsRest <= kChunkThreads * kCRegs, "register shares");
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
