@@ -110,7 +110,7 @@ kvq_status kvq_page_bytes(const kvq_pages *p, size_t *bytes);
  * *n_free is held to [0, n_pages].  A new token whose page entry lies outside
  * [0, n_pages) gets slot -1.  A page given back twice is the caller's error;
  * pushes past n_pages entries are dropped.
- * One launch.  The pages of the method's description leave paging as future work
+ * One launch, two for more than 16384 rows.  The pages of the method's description leave paging as future work
  * (BitLLM summary, limits); the interface is the library's own.
  */
 kvq_status kvq_page_tables(int32_t n_seqs, int32_t page_tokens, int32_t n_pages, const int32_t *lens,
@@ -160,7 +160,8 @@ kvq_status kvq_paged_gather(const kvq_pages *p, const int32_t *slots, int32_t n_
  *              values are held to [0, n_tokens].  Rows no sequence owns (behind
  *              q_start[n_seqs]) are not touched.
  *  max_q       host: upper bound of the rows of one sequence, 1..n_tokens.  Rows of a
- *              sequence past max_q are not computed (left as they were).
+ *              sequence past max_q are not computed (left as they were).  At most
+ *              2^26 rows per kv head (max_q times its query heads).
  *  seq_lens    device int32 [n_seqs]: positions of each sequence, the new ones
  *              included (held to [0, max_blocks * page_tokens]).
  *  block_table, table_stride, max_blocks  as kvq_page_tables.
@@ -171,7 +172,12 @@ kvq_status kvq_paged_gather(const kvq_pages *p, const int32_t *slots, int32_t n_
  *  out_type    kvq_out_type of out.
  *  out         device [n_tokens][n_q_heads][head_dim], 16-byte aligned.
  *  lse         device fp32 [n_tokens][n_q_heads], natural log, or NULL.
- * A row that sees no position gets out = 0 and lse = -inf.
+ * A row that sees no position gets out = 0 and lse = -inf.  Whatever positions
+ * that no row of the sequence sees hold (behind len, in hidden pages, never
+ * written) has no effect.  A position that some rows see and others do not
+ * enters the latter with weight 0, so a V that is not finite there makes their
+ * out NaN too, as it does in a product of matrices; a K that is not finite has
+ * no effect on rows that do not see it.
  */
 typedef struct kvq_paged_desc {
     const kvq_pages *pages;
@@ -199,7 +205,9 @@ typedef struct kvq_paged_desc {
  * step, a few to verify, a chunk of a prompt, none) over its pages, for a
  * ragged batch in one call.  The split of the work over the GPU is derived
  * from the device lengths by the kernels themselves, in a fixed way: the same
- * inputs give the same bits.
+ * inputs give the same bits.  Sequences go to a kernel by their rows per kv
+ * head (up to 8, up to 32, more), each kind in a launch of its own; where n_seqs *
+ * max_q <= n_tokens says that all have max_q rows, one launch takes them all.
  *  workspace   device, 256-byte aligned, kvq_paged_attn_workspace_size() bytes.
  *              Its contents need no preparation and mean nothing after the
  *              call; calls that may overlap on the GPU need one each.
@@ -208,9 +216,9 @@ typedef struct kvq_paged_desc {
  */
 kvq_status kvq_paged_attn(const kvq_paged_desc *a, void *workspace, size_t workspace_bytes, void *stream);
 
-/* Bytes of workspace kvq_paged_attn needs for a (device pointers are not read;
- * depends on the device, the pool's shape, the heads and max_q, not on the
- * lengths).  bytes: host out. */
+/* Bytes of workspace kvq_paged_attn needs for a.  Device pointers are not read:
+ * it depends on the device and on the numbers in a (n_tokens among them), not on
+ * what device memory holds.  bytes: host out. */
 kvq_status kvq_paged_attn_workspace_size(const kvq_paged_desc *a, size_t *bytes);
 
 #ifdef __cplusplus

@@ -160,6 +160,7 @@ kvq_status check_attn(const kvq_paged_desc *a, AttnPlan &pl)
     pl.uniform = 1;
     for (int k = 0; k < H; ++k) pl.uniform = pl.uniform && cnt[k] == pl.gmax;
     if (a->n_tokens > 0 && a->n_seqs > 0 && (a->max_q < 1 || a->max_q > a->n_tokens)) return KVQ_ERR_INVALID_ARG;
+    if ((long long)a->max_q * pl.gmax > 1 << 26) return KVQ_ERR_INVALID_ARG;   // PagedCut: a row tile's number has 23 bits
     return KVQ_OK;
 }
 

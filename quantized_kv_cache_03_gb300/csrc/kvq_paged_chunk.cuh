@@ -33,9 +33,15 @@
 // 1e-9 to 5e-9 of itself per position (fp32 output, whose P.V takes three MMAs
 // per 16 positions: 4.5e-5 after 32768, 1.7e-4 after 131072).  So every kCFlush
 // tiles O is added to sums in memory, in fp32, and starts again from zero: 5e-6
-// for any length with fp32 output, 4e-5 with fp16 output, a sixth of that
-// type's half step.  It costs 1 to 3 us each time (512-token chunk over 32768
+// for any length with fp32 output, 4e-5 with fp16 output, whose own rounding is
+// up to 4.9e-4.  It costs 1 to 3 us each time (512-token chunk over 32768
 // positions, fp16: 466 -> 475 us; a mixed batch with fp32 output 329 -> 351 us).
+// Measured: that chunk, 32 heads on 8 kv heads, q4_0 V, fp16 output, takes 463 us
+// (589 TFLOP/s counted as four times head_dim per visible pair of position and
+// head), fp32 output 557.  The tensor pipe is active 56 % of the time; the K
+// converters are busy 80 % of it, the softmax two thirds (fp32 output: four
+// fifths), and the tile's chain QK, maximum, exponents, P.V hides only as far as
+// two tiles of S in tensor memory allow.  Shared memory moves at 40 % of its rate.
 // Every wait is bounded: a wait that gives up marks the CTA, whose rows of this
 // and later pieces come out as NaN; the roles drain what they issued and leave.
 #pragma once
@@ -54,7 +60,9 @@ constexpr int kCChunk = 32;               // positions per softmax chunk
 constexpr int kCKConv0 = 8, kCVConv0 = 12, kCQk = 20, kCPv = 21, kCKCopy = 22, kCVCopy = 23;
 constexpr int kChunkWarps = 24, kChunkThreads = kChunkWarps * 32;
 // Registers per thread: the launch gives every thread kCRegs (768 threads); the
-// warpgroups then trade: 256 * 104 + 384 * 64 + 128 * 80 = 768 * 80.
+// warpgroups then trade: 256 * 120 + 384 * 56 + 128 * 72 = 768 * 80.  (104, 64
+// and 80: the softmax with fp32 output spills in its loop, 617 against 560 us on
+// the chunk named above.)
 constexpr int kCRegs = 80, kCRegsSoft = 120, kCRegsConv = 56, kCRegsRest = 72;
 static_assert(256 * kCRegsSoft + 384 * kCRegsConv + 128 * kCRegsRest <= kChunkThreads * kCRegs, "register shares");
 template <int N>

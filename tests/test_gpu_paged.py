@@ -95,6 +95,22 @@ def test_tables_short_of_pages_rows_and_tokens(seed):
     _same_tables(_run_tables(page, pages, lens, n_new, free, n_free, table, most, n_tokens), ref)
 
 
+@pytest.mark.parametrize("seed", range(3))
+def test_tables_of_many_rows(seed):
+    """More rows than one pass of the table launch fills, some of them refused."""
+    r = np.random.default_rng(seed)
+    B, page, most, pages = 300, 64, 40, 6000
+    lens, table, free, n_free = _table_state(r, B, page, most, 6000, 1000)
+    n_free = min(n_free, [6000, 1100, 6000][seed])
+    n_new = r.choice([-1, 0, 1, 100, 399, 2000], B)
+    n_tokens = int(np.maximum(n_new, 0).sum()) + [37, 0, -20000][seed]
+    assert n_tokens > 16384
+    ref = tables_ref(page, pages, lens, n_new, free, n_free, table, most, n_tokens)
+    assert ref["status"].any()
+    for kw in (dict(), dict(in_place=True), dict(slot_shift=1)):
+        _same_tables(_run_tables(page, pages, lens, n_new, free, n_free, table, most, n_tokens, **kw), ref)
+
+
 def test_tables_hold_bad_values_to_their_bounds():
     """Negative and too long lengths, a stack size out of range, page entries outside the pool."""
     page, pages, most = 16, 30, 4
@@ -320,6 +336,38 @@ def test_strided_queries_missing_lse_scale_and_bound():
         t0, n = b.q_start[s], b.new[s]
         assert (o3[t0 + 5:t0 + n] == 777).all() and (ls3[t0 + 5:t0 + n] == 777).all()
     assert np.array_equal(ls3[:3] != 777, ls[:3] != 777)
+
+
+@pytest.mark.parametrize("k_type,v_type", [(I8, Q4), (I8, Q8), (F16, Q8)])
+@pytest.mark.parametrize("max_q", [2, 7, 40])
+def test_fewer_rows_than_announced(max_q, k_type, v_type):
+    """A batch whose n_tokens leaves room for max_q rows of every sequence is
+    taken by one launch, whatever q_start then holds."""
+    new = [1, max_q, 0, 1, max_q - 1]
+    b = Batch([300, 129, 40, 1, 77], new, H=2, Hq=8, page=32, k_type=k_type, v_type=v_type, seed=max_q,
+              pad_rows=5 * max_q - sum(new))
+    for out in (torch.float32, torch.float16):
+        b.check(out=out)
+
+
+@pytest.mark.parametrize("new", [2, 6, 40])
+def test_a_key_that_is_not_finite_stays_with_the_rows_that_see_it(new):
+    for bad in (np.inf, -np.inf, np.nan):
+        def shape(kv):
+            kv[0][-1, :, 7::32] = bad
+            return kv
+        clean, b = (Batch([200], [new], H=2, Hq=8, page=16, seed=new, shape=f) for f in (None, shape))
+        o, ls = b.attn()
+        ro, rl = clean.reference(0, True)
+        a, rel, el = clean.bounds()
+        assert (np.abs(o[:-1] - ro[:-1]) <= a + rel * np.abs(ro[:-1])).all() and (np.abs(ls[:-1] - rl[:-1]) <= el).all()
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    b = Batch([20], [1], H=1, Hq=2, page=16)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="current device"):
+        b.attn()
 
 
 def test_bad_row_ranges_touch_nothing_else():

@@ -105,7 +105,7 @@ def _attn(lib, size_only=False, ws=0, wsb=0, pool=None, **over):
 
 
 SHAPES = [dict(heads=0), dict(heads=257), dict(heads=3), dict(tokens=-1), dict(seqs=-1), dict(seqs=4097), dict(max_q=0),
-          dict(max_q=9), dict(ts=7), dict(blocks=-1), dict(blocks=1 << 27, ts=1 << 27), dict(scale=float("nan")),
+          dict(max_q=9), dict(max_q=(1 << 26) + 1, tokens=(1 << 26) + 1), dict(ts=7), dict(blocks=-1), dict(blocks=1 << 27, ts=1 << 27), dict(scale=float("nan")),
           dict(scale=float("inf")), dict(ot=2), dict(hm=[0, 1, 2, 0]), dict(hm=[0, -1, 0, 0]), dict(tokens=1 << 29)]
 
 
