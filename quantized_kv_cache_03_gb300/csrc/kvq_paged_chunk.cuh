@@ -32,13 +32,14 @@
 // The MMA cuts its sums off where fp32 would round them, so O falls short by
 // 1e-9 to 5e-9 of itself per position (fp32 output, whose P.V takes three MMAs
 // per 16 positions: 4.5e-5 after 32768, 1.7e-4 after 131072).  So every kCFlush
-// tiles O is added to sums in memory, in fp32, and starts again from zero: 5e-6
-// for any length with fp32 output, 4e-5 with fp16 output, whose own rounding is
-// up to 4.9e-4.  It costs 1 to 3 us each time (512-token chunk over 32768
-// positions, fp16: 466 -> 475 us; a mixed batch with fp32 output 329 -> 351 us).
+// tiles O is added to sums in memory, in fp32, and starts again from zero: 2e-6
+// for any length with fp32 output (every 8 tiles 3.5e-6), 4e-5 with fp16 output,
+// whose own rounding is up to 4.9e-4.  It costs 1 to 3 us each time (512-token
+// chunk over 32768 positions, fp16: 466 -> 475 us; fp32 output, every 8 tiles 557
+// us, every 4 592; a mixed batch 298 and 301).
 // Measured: that chunk, 32 heads on 8 kv heads, q4_0 V, fp16 output, takes 463 us
 // (589 TFLOP/s counted as four times head_dim per visible pair of position and
-// head), fp32 output 557.  The tensor pipe is active 56 % of the time; the K
+// head), fp32 output 592.  The tensor pipe is active 56 % of the time; the K
 // converters are busy 80 % of it, the softmax two thirds (fp32 output: four
 // fifths), and the tile's chain QK, maximum, exponents, P.V hides only as far as
 // two tiles of S in tensor memory allow.  Shared memory moves at 40 % of its rate.
@@ -62,7 +63,7 @@ constexpr int kChunkWarps = 24, kChunkThreads = kChunkWarps * 32;
 // Registers per thread: the launch gives every thread kCRegs (768 threads); the
 // warpgroups then trade: 256 * 120 + 384 * 56 + 128 * 72 = 768 * 80.  (104, 64
 // and 80: the softmax with fp32 output spills in its loop, 617 against 560 us on
-// the chunk named above.)
+// that chunk, with sums every 8 tiles.)
 constexpr int kCRegs = 80, kCRegsSoft = 120, kCRegsConv = 56, kCRegsRest = 72;
 static_assert(256 * kCRegsSoft + 384 * kCRegsConv + 128 * kCRegsRest <= kChunkThreads * kCRegs, "register shares");
 template <int N>
@@ -74,7 +75,7 @@ constexpr float kCShift = 8.0f, kCSlack = 6.0f;
 // Tiles after which O is added to the rows' fp32 sums in memory and started
 // afresh (even, so that one softmax group does it throughout a piece).
 template <bool O16>
-constexpr int kCFlush = O16 ? 64 : 8;
+constexpr int kCFlush = O16 ? 64 : 4;
 constexpr uint16_t kHalfBits = 0x3800;    // 1/2: 127 * 516 (the largest code * scale) stays inside fp16
 
 template <int VT>
@@ -431,12 +432,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                             if (!wait1(C::B_KR + i, j & 1)) return false;
                             const uint64_t kh = i ? dKH[1] : dKH[0], kl = i ? dKL[1] : dKL[0];
                             tc_fence_after();
+                            // the small terms first: the sum is cut off at each addition, by little while it is small
 #pragma unroll
-                            for (int term = 0; term < 3; ++term)
+                            for (int term = 0; term < 3; ++term)   // Ql Kh, Qh Kl, Qh Kh
 #pragma unroll
                                 for (int ks = 0; ks < kD / 16; ++ks) {
                                     const uint64_t o = (uint64_t)(2 * ks * (C::K_LBO / 16));
-                                    umma_ta_1(d + kCHalf * i, tQ + (term == 1 ? kD / 2 : 0) + 8 * ks, (term == 2 ? kl : kh) + o, kIdQK,
+                                    umma_ta_1(d + kCHalf * i, tQ + (term == 0 ? kD / 2 : 0) + 8 * ks, (term == 1 ? kl : kh) + o, kIdQK,
                                               term > 0 || ks > 0);
                                 }
                             umma_commit_1(bar(C::B_KF + i));
