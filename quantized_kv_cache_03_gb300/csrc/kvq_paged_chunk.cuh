@@ -37,8 +37,8 @@
 // whose own rounding is up to 4.9e-4.  It costs 1 to 3 us each time (512-token
 // chunk over 32768 positions, fp16: 466 -> 475 us; fp32 output, every 8 tiles 557
 // us, every 4 592; a mixed batch 298 and 301).
-// Measured: that chunk, 32 heads on 8 kv heads, q4_0 V, fp16 output, takes 463 us
-// (589 TFLOP/s counted as four times head_dim per visible pair of position and
+// Measured: that chunk, 32 heads on 8 kv heads, q4_0 V, fp16 output, takes 450 us
+// (606 TFLOP/s counted as four times head_dim per visible pair of position and
 // head), fp32 output 592.  The tensor pipe is active 56 % of the time; the K
 // converters are busy 80 % of it, the softmax two thirds (fp32 output: four
 // fifths), and the tile's chain QK, maximum, exponents, P.V hides only as far as
@@ -501,10 +501,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                 if (!wwait(C::B_RAWK + st, (hh / C::RSK) & 1) || (j >= 1 && !wwait(C::B_KF + ob, (j - 1) & 1))) return false;
                 const uint8_t *raw = smem + C::RAWK_OFF + st * C::RAWK;
                 uint8_t *kh = smem + C::KH_OFF + ob * C::KBUF + (u / 8) * C::K_SBO + (u % 8) * 16 + dg * C::K_LBO, *kl = kh + (C::KL_OFF - C::KH_OFF);
-#pragma unroll 2
+                uint4 va[kCSub];   // every load first: this role is the busiest (fp16 output, the chunk named above 460 -> 450 us)
+                uint2 sa[kCSub];
+#pragma unroll
                 for (int q = 0; q < kCSub; ++q) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(raw + q * C::KPART + i * 512 + lane * 16);
-                    const uint2 sc = *reinterpret_cast<const uint2 *>(raw + q * C::KPART + soff);
+                    va[q] = *reinterpret_cast<const uint4 *>(raw + q * C::KPART + i * 512 + lane * 16);
+                    sa[q] = *reinterpret_cast<const uint2 *>(raw + q * C::KPART + soff);
+                }
+#pragma unroll
+                for (int q = 0; q < kCSub; ++q) {
+                    const uint4 v = va[q];
+                    const uint2 sc = sa[q];
                     const uint32_t s0 = __byte_perm(sc.x, 0u, mine), s1 = __byte_perm(sc.y, 0u, mine);
                     const __half2 k05 = __half2half2(__ushort_as_half(kHalfBits));
                     uint4 hi, lo;
