@@ -11,12 +11,12 @@ namespace kvq {
 // whose row range holds it, new page f to the sequence whose range of needed
 // pages holds it, and entry v of the stack past the free pages to the released
 // sequence whose range holds it.  Every CTA of one cluster computes the sums
-// for itself (n_seqs loads, three block scans: cheaper than passing them
+// for itself (n_seqs loads, two block scans: cheaper than passing them
 // around), the cluster synchronizes once, so that lens and n_free may be
 // updated in place, and the outputs are dealt out flat over its threads with
 // a binary search each; a warp copies a released sequence's pages.  Latency-bound
 // (256 sequences, a row each: 6.3 us; its bytes take 0.1 us): the launch, one
-// round of loads, three scans, the cluster's barrier.  One CTA alone instead of
+// round of loads, two scans, the cluster's barrier.  One CTA alone instead of
 // eight is no faster.  The rows' slots are filled here up to one pass of
 // the cluster's threads (16384 rows), beyond that by a second, wide launch:
 // 17942 rows 7.15 us here, 6.6 there; 272442 rows 36.8 and 10.5; 7726 rows 5.6
@@ -24,26 +24,37 @@ namespace kvq {
 // ---------------------------------------------------------------------------
 constexpr int kTabThreads = 512;
 
-__device__ __forceinline__ long long block_scan(long long v, long long *tmp, long long &total)
+// Exclusive sums of N values over the block's threads, and the totals.
+template <int N>
+__device__ __forceinline__ void block_scan(long long (&v)[N], long long (&total)[N], long long (*tmp)[kTabThreads / 32])
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long x = v;
+    long long x[N];
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
-    }
+    for (int k = 0; k < N; ++k) x[k] = v[k];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const long long y = __shfl_up_sync(0xffffffffu, x[k], d);
+            if (lane >= d) x[k] += y;
+        }
     __syncthreads();   // tmp may still be read by the previous scan
-    if (lane == 31) tmp[warp] = x;
-    __syncthreads();
-    long long base = 0;
-    total = 0;
+    if (lane == 31)
 #pragma unroll
-    for (int w = 0; w < kTabThreads / 32; ++w) {
-        if (w < warp) base += tmp[w];
-        total += tmp[w];
+        for (int k = 0; k < N; ++k) tmp[k][warp] = x[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        long long base = 0;
+        total[k] = 0;
+#pragma unroll
+        for (int w = 0; w < kTabThreads / 32; ++w) {
+            if (w < warp) base += tmp[k][w];
+            total[k] += tmp[k][w];
+        }
+        v[k] = base + x[k] - v[k];
     }
-    return base + x - v;   // exclusive
 }
 
 // Last i in [0, n) with a[i] <= x (a non-decreasing, a[0] <= x).
@@ -61,7 +72,7 @@ __device__ __forceinline__ int last_at_most(const int *a, int n, int x)
 __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TableParams p)
 {
     extern __shared__ int tab[];
-    __shared__ long long tmp[kTabThreads / 32];
+    __shared__ long long tmp[2][kTabThreads / 32];
     __shared__ int popped_s;
     const int n = p.n_seqs, tid = threadIdx.x, P = 1 << p.pshift;
     int *qs = tab, *need0 = qs + n + 1, *back0 = need0 + n + 1, *len_s = back0 + n + 1, *add_s = len_s + n;
@@ -83,8 +94,9 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
         rows += max(add, 0);
         if (add < 0) back += (len + P - 1) >> p.pshift;
     }
-    long long rows_all, back_all, need_all;
-    const long long rows0 = block_scan(rows, tmp, rows_all), backs0 = block_scan(back, tmp, back_all);
+    long long first[2] = {rows, back}, all2[2];
+    block_scan(first, all2, tmp);
+    const long long rows0 = first[0], backs0 = first[1], rows_all = all2[0], back_all = all2[1];
     // pages needed by the sequences that fit their row of the table and the batch
     auto fits = [&](int len, int add, long long end) { return (long long)len + add <= lmax && end <= p.n_tokens; };
     auto pages = [&](int len, int add) { return (int)((((long long)len + add + P - 1) >> p.pshift) - ((len + P - 1) >> p.pshift)); };
@@ -97,7 +109,9 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
         if (add < 0) bk += (len + P - 1) >> p.pshift;
         if (add > 0 && fits(len, add, r)) need += pages(len, add);
     }
-    const long long needs0 = block_scan(need, tmp, need_all);
+    long long needs[1] = {need}, all1[1];
+    block_scan(needs, all1, tmp);
+    const long long needs0 = needs[0], need_all = all1[0];
     const int avail = (int)min((long long)n_free + back_all, (long long)p.n_pages);
     // the grant: pages in order, and nothing after the first that does not fit
     long long nd = needs0;

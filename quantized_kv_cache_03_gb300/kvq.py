@@ -184,14 +184,6 @@ def _stream(stream):
     return c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
-def _raw_stream(device):
-    """Handle of torch's current stream on `device`, without the Stream object
-    that torch.cuda.current_stream() makes (3 us)."""
-    if device.type != "cuda":
-        return None
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
 def _i32(vals):
     vals = [int(v) for v in vals]
     return (c_int32 * max(1, len(vals)))(*vals)
@@ -561,15 +553,21 @@ class _PreparedCall:
 
     def _bind(self, device, *args):
         self.device = device
+        self._index = device.index if device.type == "cuda" else None
         self._fn = fn = getattr(load(), self.name)
         # converted once: a call of a few microseconds' work is bound by its marshalling
         self._args = tuple(t(a) if isinstance(a, int) else a for t, a in zip(fn.argtypes, args))
 
     def __call__(self, stream=None):
-        if self.device.type == "cuda" and self.device.index != torch.cuda.current_device():
+        index = self._index
+        if index is not None and index != torch.cuda.current_device():
             raise ValueError("%s: the tensors are on %s, the current device is cuda:%d"
                              % (self.name, self.device, torch.cuda.current_device()))
-        st = self._fn(*self._args, _raw_stream(self.device) if stream is None else _stream(stream))
+        if stream is not None:
+            stream = _stream(stream)
+        elif index is not None:   # the handle without the Stream object of torch.cuda.current_stream() (3 us)
+            stream = torch._C._cuda_getCurrentRawStream(index)
+        st = self._fn(*self._args, stream)
         if st:
             raise KvqError(st, self.name)
 
