@@ -164,7 +164,9 @@ __global__ void __launch_bounds__(kTabThreads) page_tables_kernel(const TablePar
     for (int b0 = warp; b0 < n; b0 += 32 * warps) {
         const int mine = b0 + lane * warps;
         for (unsigned set = __ballot_sync(0xffffffffu, mine < n && add_s[mine] < 0); set; set &= set - 1) {
-            const int b = b0 + (__ffs(set) - 1) * warps, v0 = n_free + back0[b], m = min(back0[b + 1] - back0[b], n_free_out - v0);
+            const int b = b0 + (__ffs(set) - 1) * warps;
+            const long long v0 = (long long)n_free + back0[b];   // past 2^31 if lens claims more pages than there are
+            const int m = (int)max(0ll, min((long long)(back0[b + 1] - back0[b]), n_free_out - v0));
             const int *from = p.block_table + (size_t)b * p.stride;
             for (int k0 = lane; k0 < m; k0 += 256) {   // eight loads in flight
                 int v[8];

@@ -111,6 +111,21 @@ def test_tables_of_many_rows(seed):
         _same_tables(_run_tables(page, pages, lens, n_new, free, n_free, table, most, n_tokens, **kw), ref)
 
 
+def test_tables_given_back_more_pages_than_an_int_counts():
+    """33 sequences that claim 2^26 pages each end: the stack fills up with the
+    first ones' and what follows is dropped."""
+    B, page, most, n_pages = 33, 16, 1 << 26, 64
+    table = torch.empty((B, most), dtype=torch.int32, device=dev())
+    table[:, :n_pages] = torch.arange(n_pages, dtype=torch.int32, device=dev())
+    free = i32(np.full(n_pages, -5))
+    n_free, lens_out, q_start, slots, status = i32([3]), i32(np.full(B, 9)), i32(np.full(B + 1, 9)), i32([]), i32(np.full(B, 9))
+    kvq.kvq_page_tables(page, n_pages, i32(np.full(B, 1 << 30)), i32(np.full(B, -1)), free, n_free, table, lens_out, n_free, q_start,
+                        slots, status)
+    torch.cuda.synchronize()
+    assert free.tolist() == [-5] * 3 + list(range(n_pages - 3)) and n_free.tolist() == [n_pages]
+    assert not lens_out.any() and not q_start.any() and not status.any()
+
+
 def test_tables_hold_bad_values_to_their_bounds():
     """Negative and too long lengths, a stack size out of range, page entries outside the pool."""
     page, pages, most = 16, 30, 4
