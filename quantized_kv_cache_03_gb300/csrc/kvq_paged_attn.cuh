@@ -42,8 +42,6 @@
 // half would have one bit left).  l carries the same factor, so it cancels.
 #pragma once
 
-#include <type_traits>
-
 #include "kvq_paged.cuh"
 #include "kvq_paged_line.cuh"
 

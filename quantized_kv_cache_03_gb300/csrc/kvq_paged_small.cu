@@ -15,7 +15,7 @@ namespace kvq {
 // around), the cluster synchronizes once, so that lens and n_free may be
 // updated in place, and the outputs are dealt out flat over its threads with
 // a binary search each; a warp copies a released sequence's pages.  Latency-bound
-// (256 sequences, a row each: 6.3 us; its bytes take 0.1 us): the launch, one
+// (256 sequences, a row each: 6.2 us; its bytes take 0.1 us): the launch, one
 // round of loads, two scans, the cluster's barrier.  One CTA alone instead of
 // eight is no faster.  The rows' slots are filled here up to one pass of
 // the cluster's threads (16384 rows), beyond that by a second, wide launch:
