@@ -24,7 +24,8 @@
 //   O^T += V^T P^T   A = V codes (exact fp16 integers), B = p * d per block.  S
 //               (row g, positions 2c, 2c + 1) already has P^T's B layout (k 2c,
 //               2c + 1, n = g); S^T is turned by movmatrix.  KVQ_OUT_F32 splits
-//               p * d into an fp16 high and low part (two MMAs, about 22 bits),
+//               p * d into its upper 11 bits and the rest as fp16 (two MMAs; the
+//               rest is rounded to 2^-21 of p * d),
 //               KVQ_OUT_F16 rounds it once (2^-11 at most of each term).
 // Both outputs sum a stage's P.V from zero and add it in fp32: the MMA's own
 // running sum cuts off where fp32 rounds (error against 64 bits on the first batch
@@ -32,7 +33,7 @@
 // Measured: 64 sequences of 1024 to 32768 positions, 4 rows, q8_0 V: 375 us, 0.91
 // of the bytes' time at the measured copy rate; one of 131072 positions, 5 rows,
 // q4_0: 48 us (0.67: prologue, merge and combine are a third of it); 16 of 32768,
-// 32 rows, fp32 output: 419 us (0.31: 920 instructions per 16 rows and 32
+// 32 rows, fp32 output: 407 us (0.32: 920 instructions per 16 rows and 32
 // positions at 46 % issue, two warps per scheduler).
 // Softmax in base 2.  A row's reference maximum is raised only when a score
 // passes it by more than kSlack = 1, and exponents are taken kShift above it:
@@ -514,9 +515,12 @@ __global__ void __launch_bounds__(128, NT == 1 ? 3 : 2) paged_attn_kernel(const 
 #pragma unroll
                                 for (int i = 0; i < 2; ++i) {
                                     float2 xv = mul2(s[nt][2 * t + i], d2[i]);
-                                    hi[i] = pack_half2(xv.x, xv.y);
-                                    if (!O16) {   // x - hi is exact in fp32
-                                        const float2 y = sub2(xv, half2_of(hi[i]));
+                                    if (O16) {
+                                        hi[i] = pack_half2(xv.x, xv.y);
+                                    } else {   // the upper 11 bits by a mask (the ALU has room: 419 -> 407 us), and what they leave out
+                                        const float2 h = make_float2(__uint_as_float(__float_as_uint(xv.x) & 0xffffe000u), __uint_as_float(__float_as_uint(xv.y) & 0xffffe000u));
+                                        const float2 y = sub2(xv, h);
+                                        hi[i] = pack_half2(h.x, h.y);
                                         lo[i] = pack_half2(y.x, y.y);
                                     }
                                 }
