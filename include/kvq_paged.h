@@ -207,7 +207,8 @@ typedef struct kvq_paged_desc {
  * from the device lengths by the kernels themselves, in a fixed way: the same
  * inputs give the same bits.  Sequences go to a kernel by their rows per kv
  * head (up to 8, up to 32, more), each kind in a launch of its own; where n_seqs *
- * max_q <= n_tokens says that all have max_q rows, one launch takes them all.
+ * max_q == n_tokens says that all have max_q rows (at most 32 per kv head, or a
+ * single sequence), one launch takes them all, whatever q_start holds.
  *  workspace   device, 256-byte aligned, kvq_paged_attn_workspace_size() bytes.
  *              Its contents need no preparation and mean nothing after the
  *              call; calls that may overlap on the GPU need one each.

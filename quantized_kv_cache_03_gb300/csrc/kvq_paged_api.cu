@@ -193,12 +193,14 @@ void plan_attn(const kvq_paged_desc *a, const PagedDevice *dev, int n_sms, AttnP
     const int chunk = chunk_min_rows(g), bound[kAttnParts + 1] = {1, chunk < 9 ? chunk : 9, chunk, INT_MAX};
     int top = 0;   // the kind that the longest sequence goes to
     while (top < kAttnParts - 1 && rows >= bound[top + 1]) ++top;
-    // A batch of sequences of the same number of rows is one launch (an idle
-    // one costs 3 us).  What q_start holds is known on the device alone, so the
-    // launch takes fewer rows too.  Otherwise each sequence goes to its kind (40
-    // single tokens beside four chunks: 315 us, with row tiles of 16 for all the
-    // short ones 351).
-    const bool alike = (long long)a->n_seqs * a->max_q <= a->n_tokens;
+    // Sequences that all have max_q rows, as n_tokens then says, are one launch
+    // (an idle one costs 3 to 5 us).  What q_start holds is known on the device
+    // alone, so that launch takes fewer rows too: row tiles of 16 at up to 1.4
+    // times the cost of row tiles of 8, the chunk kernel at several times, which
+    // is why it stands for others only where there is a single sequence.
+    // Otherwise each sequence goes to its kind (40 single tokens beside four
+    // chunks: 315 us, with row tiles of 16 for all the short ones 351).
+    const bool alike = (long long)a->n_seqs * a->max_q == a->n_tokens && (top < 2 || a->n_seqs == 1);
     pl.bytes = 0;
     for (int k = 0; k < kAttnParts; ++k) {
         Part &pt = pl.part[k];

@@ -361,8 +361,10 @@ def test_fewer_rows_than_announced(max_q, k_type, v_type):
     new = [1, max_q, 0, 1, max_q - 1]
     b = Batch([300, 129, 40, 1, 77], new, H=2, Hq=8, page=32, k_type=k_type, v_type=v_type, seed=max_q,
               pad_rows=5 * max_q - sum(new))
+    one = Batch([200], [max_q - 1], H=2, Hq=8, page=16, k_type=k_type, v_type=v_type, seed=max_q, pad_rows=1)
     for out in (torch.float32, torch.float16):
         b.check(out=out)
+        one.check(out=out, max_q=max_q)
 
 
 @pytest.mark.parametrize("new", [2, 6, 40])
