@@ -33,14 +33,17 @@
 // Measured: 64 sequences of 1024 to 32768 positions, 4 rows, q8_0 V: 375 us, 0.91
 // of the bytes' time at the measured copy rate; one of 131072 positions, 5 rows,
 // q4_0: 48 us (0.67: prologue, merge and combine are a third of it); 16 of 32768,
-// 32 rows, fp32 output: 407 us (0.32: 920 instructions per 16 rows and 32
+// 32 rows, fp32 output: 411 us (0.31: 920 instructions per 16 rows and 32
 // positions at 46 % issue, two warps per scheduler).
 // Softmax in base 2.  A row's reference maximum is raised only when a score
-// passes it by more than kSlack = 1, and exponents are taken kShift above it:
-// p reaches 2^(kShift + 1), which with the largest V scale (516 for q8_0, 8188
-// for q4_0) still fits fp16, and keeps p * d out of fp16's subnormals, where
-// the low part would lose its bits (p = 2^-9, d = 0.02: the product's lower
-// half would have one bit left).  l carries the same factor, so it cancels.
+// passes it by more than kSlack = 1, and exponents are taken `shift` above it,
+// so p reaches 2^(shift + 1).  That keeps p * d out of fp16's subnormals, where
+// the low part loses its bits (d = 1e-5 and p = 1: it has none).  shift follows
+// the stage's largest V scale, from the exponent of its bits: p * d_max lies in
+// 2^9..2^11 where it may, so 22 bits are kept of terms down to 2^-12 of the
+// largest; with d at the top of its range (516 for q8_0, 8188 for q4_0) kShift
+// is what still fits fp16.  l carries the same factor, so it cancels.  Shift 24,
+// the most, leaves s - m 2^-20 of rounding.
 #pragma once
 
 #include "kvq_paged.cuh"
@@ -83,7 +86,8 @@ __global__ void __launch_bounds__(128, NT == 1 ? 3 : 2) paged_attn_kernel(const 
     using C = PagedCfg<NT, VT, KT>;
     using T = PageTile<VT, KT>;
     constexpr int W = C::WARPS, S = C::STAGES;
-    constexpr float kBias = 1152.0f, kSlack = 1.0f, kShift = VT == KVQ_V_Q4_0 ? 2.0f : 5.0f;
+    constexpr float kBias = 1152.0f, kSlack = 1.0f;
+    constexpr int kShift = VT == KVQ_V_Q4_0 ? 2 : 5;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ LineStart line;
     __shared__ long long tmp[W];
@@ -281,6 +285,21 @@ __global__ void __launch_bounds__(128, NT == 1 ? 3 : 2) paged_attn_kernel(const 
                 const int x = (s0 + warp + W * j) * kStagePos, ok = (okm >> (2 * sl)) & 3;
                 const bool full = ok == 3 && x + kStagePos - 1 <= lim_lo;   // every row sees the whole stage
                 {
+                    // the lane's four of the stage's V scales
+                    uint2 *d4 = reinterpret_cast<uint2 *>(stg + (lane >> 4) * T::BYTES + T::VS_OFF + 8 * (lane & 15));
+                    uint2 dv = *d4;
+                    if (!full) {
+                        // V scales of positions that no row sees may hold anything: p is 0 there, make d so too
+                        const int t = lane >> 4, q1 = x + 16 * t + 2 * ((lane & 15) >> 1);
+                        const uint32_t keep = !((ok >> t) & 1) ? 0u : (q1 <= lim_hi ? 0xffffu : 0u) | (q1 + 1 <= lim_hi ? 0xffff0000u : 0u);
+                        dv = make_uint2(dv.x & keep, dv.y & keep);
+                        *d4 = dv;
+                        __syncwarp();
+                    }
+                    // d_max < 2^(e - 14), e its exponent bits: 2^shift * d_max in 2^9..2^10
+                    const uint32_t dm = __vmaxu2(dv.x, dv.y);
+                    const int de = (int)(__reduce_max_sync(0xffffffffu, max(dm & 0xffffu, dm >> 16)) >> 10);
+                    const float shift = (float)max(kShift, 24 - de);
                     // scores of 8-position group i (of four): NT = 1 position 8i + g, rows (2c, 2c + 1);
                     // NT = 2 positions (8i + 2c, + 1), [row g, row g + 8]
                     float2 s[NT][4];
@@ -374,12 +393,6 @@ __global__ void __launch_bounds__(128, NT == 1 ? 3 : 2) paged_attn_kernel(const 
                         }
                     }
                     if (!full) {
-                        // V scales of positions that no row sees may hold anything: p is 0 there, make d so too
-                        const int t = lane >> 4, q1 = x + 16 * t + 2 * ((lane & 15) >> 1);
-                        const uint32_t keep = !((ok >> t) & 1) ? 0u : (q1 <= lim_hi ? 0xffffu : 0u) | (q1 + 1 <= lim_hi ? 0xffff0000u : 0u);
-                        uint2 *d4 = reinterpret_cast<uint2 *>(stg + t * T::BYTES + T::VS_OFF + 8 * (lane & 15));
-                        *d4 = make_uint2(d4->x & keep, d4->y & keep);
-                        __syncwarp();
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int q0 = x + 8 * i + (NT == 1 ? g : 2 * c);
@@ -407,7 +420,7 @@ __global__ void __launch_bounds__(128, NT == 1 ? 3 : 2) paged_attn_kernel(const 
                             mx[nt] = fmaxf(fmaxf(fmaxf(s[nt][0].x, s[nt][0].y), fmaxf(s[nt][1].x, s[nt][1].y)),
                                            fmaxf(fmaxf(s[nt][2].x, s[nt][2].y), fmaxf(s[nt][3].x, s[nt][3].y)));
                     }
-                    const bool need = mx[0] > m[0] + (kShift + kSlack) || mx[1] > m[1] + (kShift + kSlack);
+                    const bool need = mx[0] > m[0] + (shift + kSlack) || mx[1] > m[1] + (shift + kSlack);
                     if (__any_sync(0xffffffffu, need)) {
                         float al[2];
 #pragma unroll
@@ -421,7 +434,7 @@ __global__ void __launch_bounds__(128, NT == 1 ? 3 : 2) paged_attn_kernel(const 
                                 v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
                                 v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
                             }
-                            v = fmaxf(m[e], v - kShift);   // m: the exponents' zero
+                            v = fmaxf(m[e], v - shift);   // m: the exponents' zero
                             al[e] = v == -INFINITY ? 1.f : fast_exp2(m[e] - v);
                             l[e] *= al[e];
                             m[e] = v;
