@@ -11,15 +11,17 @@
 //         S), then p = 2^(s - m) in 32-position chunks, which overwrite S.  The
 //         row's zero point m is handed from tile to tile through shared memory.
 //         At the end of a piece each group writes half of O out.
-//   8-11  K converters: k/2 = code * (scale/2) as an fp16 high and low part.
-//   12-19 V converters: v/2 likewise, turned to [dim][position].
+//   8-11  K converters: k = code * scale as an fp16 high and low part.
+//   12-19 V converters: v likewise, turned to [dim][position].
 //   20    QK, 21 P.V: one thread each issues and waits.
 //   22    walks the CTA's pieces of the line, hands them out as records, and
 //         issues the bulk copies of the K parts of 64-position half tiles; 23 those
 //         of the V parts.
 // Tensor memory: S of two tiles (128 columns each), O, the query's high and low
 // parts.  Shared memory: K and V operands of two half tiles.
-// QK: S = Qh Kh + Ql Kh + Qh Kl, Q and K being code * scale to 22 bits: within
+// The two parts of a value hold it exactly at any scale: code * scale has 18 bits
+// and is a multiple of 2^-24, fp16's least step (see code_hilo).
+// QK: S = Qh Kh + Ql Kh + Qh Kl, the product of the low parts left out: within
 // 2^-22 |q||k| of the exact sum of scaled integer block dots.  (The block dots
 // themselves as four accumulators cost the softmax eight fp32 operations and a
 // shared load per pair of scores and four times the tensor memory; that form
@@ -76,7 +78,7 @@ constexpr float kCShift = 8.0f, kCSlack = 6.0f;
 // afresh (even, so that one softmax group does it throughout a piece).
 template <bool O16>
 constexpr int kCFlush = O16 ? 64 : 4;
-constexpr uint16_t kHalfBits = 0x3800;    // 1/2: 127 * 516 (the largest code * scale) stays inside fp16
+constexpr uint16_t kCTopBits = 0x6007;    // 515.5: 127 * 516, 8-bit codes at fp16's largest block, is past its range
 
 template <int VT>
 struct ChunkCfg {
@@ -167,17 +169,29 @@ __device__ __forceinline__ void umma_commit_1(uint32_t bar)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// Eight codes + 128 (two words) times the scale s2 (both halves): fp16 high
-// parts, and what they miss.
-__device__ __forceinline__ void u8x8_hilo(uint32_t w0, uint32_t w1, __half2 s2, uint4 &hi, uint4 &lo)
+// code * s as hi + lo, both fp16, exactly: hi from the scale st, which is s, or
+// kCTopBits where that is less (hi then stays inside fp16's range), lo what hi
+// misses of the whole product (one rounding, of a number that fits).  Scales
+// are not halved instead: a subnormal one would lose a bit, a block of values
+// around 1e-4 two per cent of itself.
+__device__ __forceinline__ void code_hilo(uint32_t code2, __half2 st, __half2 s, uint32_t &hi, uint32_t &lo)
 {
+    const __half2 c = *reinterpret_cast<const __half2 *>(&code2);
+    const __half2 h = __hmul2(c, st), l = __hfma2(c, s, __hneg2(h));
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+// Eight codes + 128 (two words) times the scale s (both halves).
+__device__ __forceinline__ void u8x8_hilo(uint32_t w0, uint32_t w1, __half2 s, uint4 &hi, uint4 &lo)
+{
+    const __half2 st = __hmin2(s, __half2half2(__ushort_as_half(kCTopBits)));
     const __half2 k1152 = __half2half2(__ushort_as_half(0x6480));
     uint32_t r[4] = {__byte_perm(w0, 0x64646464u, 0x4140), __byte_perm(w0, 0x64646464u, 0x4342),
                      __byte_perm(w1, 0x64646464u, 0x4140), __byte_perm(w1, 0x64646464u, 0x4342)}, l[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const __half2 c = __hsub2(*reinterpret_cast<__half2 *>(&r[k]), k1152);
-        v_hilo(*reinterpret_cast<const uint32_t *>(&c), s2, r[k], l[k]);
+        code_hilo(*reinterpret_cast<const uint32_t *>(&c), st, s, r[k], l[k]);
     }
     hi = make_uint4(r[0], r[1], r[2], r[3]);
     lo = make_uint4(l[0], l[1], l[2], l[3]);
@@ -513,12 +527,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                     const uint4 v = va[q];
                     const uint2 sc = sa[q];
                     const uint32_t s0 = __byte_perm(sc.x, 0u, mine), s1 = __byte_perm(sc.y, 0u, mine);
-                    const __half2 k05 = __half2half2(__ushort_as_half(kHalfBits));
                     uint4 hi, lo;
-                    u8x8_hilo(v.x, v.y, __hmul2(*reinterpret_cast<const __half2 *>(&s0), k05), hi, lo);
+                    u8x8_hilo(v.x, v.y, *reinterpret_cast<const __half2 *>(&s0), hi, lo);
                     *reinterpret_cast<uint4 *>(kh + 2 * q * C::K_SBO) = hi;
                     *reinterpret_cast<uint4 *>(kl + 2 * q * C::K_SBO) = lo;
-                    u8x8_hilo(v.z, v.w, __hmul2(*reinterpret_cast<const __half2 *>(&s1), k05), hi, lo);
+                    u8x8_hilo(v.z, v.w, *reinterpret_cast<const __half2 *>(&s1), hi, lo);
                     *reinterpret_cast<uint4 *>(kh + 2 * q * C::K_SBO + 4 * C::K_LBO) = hi;
                     *reinterpret_cast<uint4 *>(kl + 2 * q * C::K_SBO + 4 * C::K_LBO) = lo;
                 }
@@ -546,7 +559,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                 const int ok = reinterpret_cast<const int *>(smem + C::REC_OFF)[C::RSK + st];
                 const int x = w.s0 * kCN + t * kCHalf, p0 = x + kWTile * q + 8 * half;
                 const bool full = ok == 15 && x + kCHalf - 1 <= w.lim_hi;
-                const __half2 k05 = __half2half2(__ushort_as_half(kHalfBits));
                 uint32_t hi[4][4], lo[4][4];   // [dim of four][position pair]
                 // The words of position pair c are 64 bytes apart over the columns, so the columns begin
                 // with different pairs (a warp's load in one wavefront, or two for q8_0, instead of four
@@ -573,11 +585,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                         const bool live = ok >> q & 1;
                         dw &= (live && p0 + 2 * c <= w.lim_hi ? 0xffffu : 0u) | (live && p0 + 2 * c + 1 <= w.lim_hi ? 0xffff0000u : 0u);
                     }
-                    const __half2 d2 = __hmul2(*reinterpret_cast<const __half2 *>(&dw), k05);
+                    const __half2 d2 = *reinterpret_cast<const __half2 *>(&dw);
+                    // (q4_0: 8 * 8188 is fp16's largest number)
+                    const __half2 dt = VT == KVQ_V_Q4_0 ? d2 : __hmin2(d2, __half2half2(__ushort_as_half(kCTopBits)));
                     uint32_t r[2][2];
                     v_codes<VT>(vw[c], vx[c], r);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v_hilo(r[e >> 1][e & 1], d2, hi[e][c], lo[e][c]);
+                    for (int e = 0; e < 4; ++e) code_hilo(r[e >> 1][e & 1], dt, d2, hi[e][c], lo[e][c]);
                 }
                 uint8_t *vh = smem + C::VH_OFF + ob * C::VBUF + cw * 128, *vl = vh + (C::VL_OFF - C::VH_OFF);
 #pragma unroll
@@ -606,8 +620,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
         const uint32_t tSg = tS + lane_base + kCN * grp;
         float *xm = reinterpret_cast<float *>(smem + C::XM_OFF);
         float2 *xe = reinterpret_cast<float2 *>(smem + C::XE_OFF);
-        // Q and K went in halved, the sign is in Q; a scale of 0 stays finite times -inf
-        const float c4 = fmaxf(4.0f * fabsf(p.qk_scale_log2), 1e-30f);
+        // the scale's sign is in Q; a scale of 0 stays finite times -inf
+        const float cs = fmaxf(fabsf(p.qk_scale_log2), 1e-30f);
         // the rows' sums in memory, [dims / 4][row], and their zero points
         auto sums = [&]() { return reinterpret_cast<float4 *>(p.sums + (size_t)blockIdx.x * kChunkSums) + row; };
         auto sums_m = [&]() { return p.sums + (size_t)blockIdx.x * kChunkSums + kCM * kD + row; };
@@ -620,9 +634,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
             const int lim = row_ok ? (p.causal ? w.L - w.n + tok : w.L - 1) : -1;
             float m = -INFINITY, l = 0.f;
             if (w.tiles > 0 && !lost) {
-                // ---- blocks 2 grp, 2 grp + 1 of this row: int8 rule, q/2 in two fp16 parts into TMEM ----
+                // ---- blocks 2 grp, 2 grp + 1 of this row: int8 rule, q in two fp16 parts into TMEM ----
                 const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (size_t)(w.t0 + tok) * p.q_stride + (size_t)head * kD);
-                const float sgn = p.qk_scale_log2 < 0.f ? -0.5f : 0.5f;
+                const float sgn = p.qk_scale_log2 < 0.f ? -1.f : 1.f;
 #pragma unroll 1
                 for (int b2 = 0; b2 < 2; ++b2) {
                     const int bb = 2 * grp + b2;
@@ -647,7 +661,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                         for (int e = 0; e < 4; ++e) {
                             const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&ws[e]));
                             const float2 v = make_float2((float)quant_i8(f.x, sc) * sc * sgn, (float)quant_i8(f.y, sc) * sc * sgn);   // exact: 18 bits
-                            hv[4 * k + e] = pack_half2(v.x, v.y);
+                            hv[4 * k + e] = pack_half2(fminf(fmaxf(v.x, -65504.f), 65504.f), fminf(fmaxf(v.y, -65504.f), 65504.f));   // 127 * 516 is past fp16's range
                             const float2 y = sub2(v, __half22float2(*reinterpret_cast<const __half2 *>(&hv[4 * k + e])));
                             lv[4 * k + e] = pack_half2(y.x, y.y);
                         }
@@ -721,7 +735,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                     if (lost) break;
                     float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                     tmem_ld32(tSg, a[0]);   // the second pass's first chunk
-                    mx = mx == -INFINITY ? mx : mx * c4;
+                    mx = mx == -INFINITY ? mx : mx * cs;
 
                     // ---- the row's zero point after the tile before this one, handed on by the other group ----
                     float mp = -INFINITY;
@@ -812,7 +826,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
 
                     // ---- second pass: P over S, 32 positions at a time ----
                     const float mu = m == -INFINITY ? 0.f : m;
-                    const float2 cc = make_float2(c4, c4), nm = make_float2(-mu, -mu);
+                    const float2 cc = make_float2(cs, cs), nm = make_float2(-mu, -mu);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
                     for (int c0 = 0; c0 < kCN; c0 += 2 * kCChunk) {
@@ -866,7 +880,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
             const float nan = __int_as_float(0x7fc00000);
             float lg;
             asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(l));
-            const float f = lost ? nan : any ? 2.0f / l : 0.f;   // V went in halved
+            const float f = lost ? nan : any ? 1.0f / l : 0.f;
             const float lse = lost ? nan : any ? (m + lg) * 0.69314718055994531f : -INFINITY;
             const size_t part = ((size_t)blockIdx.x * 2 + max(0, w.slot)) * kCM + row, orow = (size_t)(w.t0 + tok) * p.n_q_heads + head;
             const bool have_o = w.tiles > 0 && !lost, have_sums = have_o && w.tiles > kCFlush<O16>;

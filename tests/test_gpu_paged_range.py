@@ -56,7 +56,7 @@ AMPS = {"1e-2": 1e-2, "1e-3": 1e-3, "1e-4": 1e-4, "blocks": (1.0, 1e-2, 1e-3, 1e
 
 
 @pytest.mark.parametrize("amp", AMPS)
-@pytest.mark.parametrize("new", [1, 6])
+@pytest.mark.parametrize("new", [1, 6, 40])
 @pytest.mark.parametrize("k_type,v_type", [(I8, Q4), (I8, Q8), (F16, Q8)])
 def test_small_values(new, k_type, v_type, amp):
     """V down to fp16's subnormal scales, over the whole cache, block by block
@@ -77,7 +77,7 @@ def test_small_values(new, k_type, v_type, amp):
 
 
 @pytest.mark.parametrize("amp", [1e-2, 1e-3, 1e-4])
-@pytest.mark.parametrize("new", [1, 6])
+@pytest.mark.parametrize("new", [1, 6, 40])
 def test_small_keys_under_large_queries(new, amp):
     def shape(kv):
         kv[0] *= amp
@@ -87,7 +87,7 @@ def test_small_keys_under_large_queries(new, amp):
     _check_by_block(b, torch.float32)
 
 
-@pytest.mark.parametrize("new", [1, 6])
+@pytest.mark.parametrize("new", [1, 6, 40])
 @pytest.mark.parametrize("v_type", [Q4, Q8])
 def test_largest_values(new, v_type):
     """Blocks that hold fp16's largest numbers: 127 times their scale rounds
