@@ -78,7 +78,6 @@ constexpr float kCShift = 8.0f, kCSlack = 6.0f;
 // afresh (even, so that one softmax group does it throughout a piece).
 template <bool O16>
 constexpr int kCFlush = O16 ? 64 : 4;
-constexpr uint16_t kCTopBits = 0x6007;    // 515.5: 127 * 516, 8-bit codes at fp16's largest block, is past its range
 
 template <int VT>
 struct ChunkCfg {
@@ -169,22 +168,10 @@ __device__ __forceinline__ void umma_commit_1(uint32_t bar)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// code * s as hi + lo, both fp16, exactly: hi from the scale st, which is s, or
-// kCTopBits where that is less (hi then stays inside fp16's range), lo what hi
-// misses of the whole product (one rounding, of a number that fits).  Scales
-// are not halved instead: a subnormal one would lose a bit, a block of values
-// around 1e-4 two per cent of itself.
-__device__ __forceinline__ void code_hilo(uint32_t code2, __half2 st, __half2 s, uint32_t &hi, uint32_t &lo)
-{
-    const __half2 c = *reinterpret_cast<const __half2 *>(&code2);
-    const __half2 h = __hmul2(c, st), l = __hfma2(c, s, __hneg2(h));
-    hi = *reinterpret_cast<const uint32_t *>(&h);
-    lo = *reinterpret_cast<const uint32_t *>(&l);
-}
 // Eight codes + 128 (two words) times the scale s (both halves).
 __device__ __forceinline__ void u8x8_hilo(uint32_t w0, uint32_t w1, __half2 s, uint4 &hi, uint4 &lo)
 {
-    const __half2 st = __hmin2(s, __half2half2(__ushort_as_half(kCTopBits)));
+    const __half2 st = __hmin2(s, __half2half2(__ushort_as_half(kTopScaleBits)));
     const __half2 k1152 = __half2half2(__ushort_as_half(0x6480));
     uint32_t r[4] = {__byte_perm(w0, 0x64646464u, 0x4140), __byte_perm(w0, 0x64646464u, 0x4342),
                      __byte_perm(w1, 0x64646464u, 0x4140), __byte_perm(w1, 0x64646464u, 0x4342)}, l[4];
@@ -587,7 +574,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                     }
                     const __half2 d2 = *reinterpret_cast<const __half2 *>(&dw);
                     // (q4_0: 8 * 8188 is fp16's largest number)
-                    const __half2 dt = VT == KVQ_V_Q4_0 ? d2 : __hmin2(d2, __half2half2(__ushort_as_half(kCTopBits)));
+                    const __half2 dt = VT == KVQ_V_Q4_0 ? d2 : __hmin2(d2, __half2half2(__ushort_as_half(kTopScaleBits)));
                     uint32_t r[2][2];
                     v_codes<VT>(vw[c], vx[c], r);
 #pragma unroll

@@ -20,10 +20,9 @@
 //     the row's reference max raised only when a score passes it by more than
 //     3 (p <= 8); the P.V accumulator in TMEM is rescaled on those tiles.
 //   * P.V: V is dequantized once per tile for all 128 rows, v = d * code
-//     (exact in fp32), and each of p and v/2 is split into an fp16 high part
-//     and an fp16 low part; O += P_hi V_hi + P_lo V_hi + P_hi V_lo keeps ~22
-//     bits of every product.  (The 1/2 keeps d * code inside fp16's range
-//     when the q8_0 scale rounded up; it is undone at the end.)
+//     (exact in fp32), and each of p and v is split into an fp16 high part
+//     and an fp16 low part, which hold v exactly (code_hilo); O += P_hi V_hi +
+//     P_lo V_hi + P_hi V_lo keeps ~22 bits of every product.
 //
 // Warp roles (512 threads, one CTA per SM, all 512 TMEM columns):
 //   warps 0-7   softmax: two per TMEM lane quarter (positions 0-31 / 32-63 of
@@ -32,7 +31,7 @@
 //               final O read-out;
 //   warps 8-9   K converters: K codes to the fp16 operand layout, K scales,
 //               the slot records;
-//   warps 10-13 V converters: V codes to v/2 hi and lo;
+//   warps 10-13 V converters: V codes to v hi and lo;
 //   warp 14     QK issuer (and the TMEM allocation);
 //   warp 15     P.V issuer; it also walks the segments and issues the bulk
 //               copies of the raw tiles, three stages ahead.
@@ -70,7 +69,6 @@ constexpr int kPCtlWarp = kPVWarp0 + 4;     // QK MMAs
 constexpr int kPPvWarp = kPCtlWarp + 1;     // P.V MMAs and the bulk copies
 constexpr int kPWarps = kPPvWarp + 1;
 constexpr int kPThreads = kPWarps * 32;
-constexpr float kPVScale = 0.5f;         // V enters the MMA as v / 2
 
 template <int VT>
 struct PrefillCfg {
@@ -206,13 +204,17 @@ __device__ __forceinline__ uint4 i8x8_to_f16(uint32_t w0, uint32_t w1)
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// v = code * d2 (per position of the pair), as hi = fp16(v) and lo = fp16(v - hi)
-// (the fused fp16 multiply-add rounds the exact v - hi once).
-__device__ __forceinline__ void v_hilo(uint32_t code2, __half2 d2, uint32_t &hi, uint32_t &lo)
+constexpr uint16_t kTopScaleBits = 0x6007;   // 515.5: 127 * 516, 8-bit codes at fp16's largest block, is past its range
+
+// code * s as hi + lo, both fp16, exactly: hi from the scale st, which is s, or
+// kTopScaleBits where that is less (hi then stays inside fp16's range), lo what hi
+// misses of the whole product (one rounding, of a number that fits).  Scales
+// are not halved instead: a subnormal one would lose a bit, a block of values
+// around 1e-4 two per cent of itself.
+__device__ __forceinline__ void code_hilo(uint32_t code2, __half2 st, __half2 s, uint32_t &hi, uint32_t &lo)
 {
     const __half2 c = *reinterpret_cast<const __half2 *>(&code2);
-    const __half2 h = __hmul2(c, d2);
-    const __half2 l = __hfma2(c, d2, __hneg2(h));
+    const __half2 h = __hmul2(c, st), l = __hfma2(c, s, __hneg2(h));
     hi = *reinterpret_cast<const uint32_t *>(&h);
     lo = *reinterpret_cast<const uint32_t *>(&l);
 }
@@ -569,11 +571,12 @@ __global__ void __launch_bounds__(kPThreads, 1) prefill_attn_kernel(const __grid
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::B_KR + ob));
             } else {
-            // V: v / 2 = code * (d / 2) as fp16 hi + lo, stored [dim][position]
+            // V: v = code * d as fp16 hi + lo, stored [dim][position]
             uint8_t *vh = smem + C::VH_OFF + ob * C::VBUF, *vl = smem + C::VL_OFF + ob * C::VBUF;
             auto put = [&](int dim, int pos, uint32_t code2, __half2 d2) {
                 uint32_t hi, lo;
-                v_hilo(code2, d2, hi, lo);
+                // (q4_0: 8 * 8188 is fp16's largest number)
+                code_hilo(code2, VT == KVQ_V_Q4_0 ? d2 : __hmin2(d2, __half2half2(__ushort_as_half(kTopScaleBits))), d2, hi, lo);
                 const int o = (dim / 8) * C::V_SBO + (pos / 8) * 128 + (dim % 8) * 16 + (pos % 8) * 2;
                 *reinterpret_cast<uint32_t *>(vh + o) = hi;
                 *reinterpret_cast<uint32_t *>(vl + o) = lo;
@@ -587,7 +590,7 @@ __global__ void __launch_bounds__(kPThreads, 1) prefill_attn_kernel(const __grid
                 const uint4 w = *reinterpret_cast<const uint4 *>(raw + C::R_V + t4 * C::TILE_V + ci * 16);
                 const int t = (VT == KVQ_V_Q4_0) ? 8 * i + 2 * c : 8 * (i >> 1) + 2 * c;
                 const int pos = kWTile * t4 + t;
-                // scales of positions t, t + 1 (0 where the slot holds no visible row), times 1/2
+                // scales of positions t, t + 1 (0 where the slot holds no visible row)
                 float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
                 const uint16_t *vs = reinterpret_cast<const uint16_t *>(raw + C::R_VS + t4 * C::TILE_S);
                 if (slot_ok(t4, t)) load4h(vs + t * kNB, d0);
@@ -599,7 +602,7 @@ __global__ void __launch_bounds__(kPThreads, 1) prefill_attn_kernel(const __grid
                     const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                     for (int bb = 0; bb < kNB; ++bb) {
-                        const __half2 d2 = __floats2half2_rn(d0[bb] * kPVScale, d1[bb] * kPVScale);
+                        const __half2 d2 = __floats2half2_rn(d0[bb], d1[bb]);
                         const uint32_t w0 = ws[bb], w23 = w0 >> 8;
                         uint32_t x;
                         __half2 cv;
@@ -624,7 +627,7 @@ __global__ void __launch_bounds__(kPThreads, 1) prefill_attn_kernel(const __grid
                     for (int half = 0; half < 2; ++half) {
                         const int bb = 2 * hb + half;
                         const float e0 = hb ? d0[2 + half] : d0[half], e1 = hb ? d1[2 + half] : d1[half];
-                        const __half2 d2 = __floats2half2_rn(e0 * kPVScale, e1 * kPVScale);
+                        const __half2 d2 = __floats2half2_rn(e0, e1);
 #pragma unroll
                         for (int wd = 0; wd < 2; ++wd) {
                             const uint32_t xw = ws[2 * half + wd] ^ 0x80808080u;
@@ -862,7 +865,7 @@ __global__ void __launch_bounds__(kPThreads, 1) prefill_attn_kernel(const __grid
             float inv, lg;
             asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(lt));
             asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(lt));
-            const float f = any ? inv / kPVScale : 0.f;
+            const float f = any ? inv : 0.f;
             const float lse = any ? (m + lg) * 0.69314718055994531f : -INFINITY;
             float *dst = ((G.n_split == 1) ? G.out + orow * kD : G.ws_o + (orow * G.n_split + split) * kD) + (kD / 2) * hf;
 #pragma unroll
