@@ -172,7 +172,9 @@ kvq_status kvq_paged_gather(const kvq_pages *p, const int32_t *slots, int32_t n_
  *  out_type    kvq_out_type of out.
  *  out         device [n_tokens][n_q_heads][head_dim], 16-byte aligned.
  *  lse         device fp32 [n_tokens][n_q_heads], natural log, or NULL.
- * A row that sees no position gets out = 0 and lse = -inf.  Whatever positions
+ * A row that sees no position gets out = 0 and lse = -inf.  One that sees some
+ * and whose query holds an infinity or NaN, or a score of which is NaN or
+ * +inf, gets NaN in both.  Whatever positions
  * that no row of the sequence sees hold (behind len, in hidden pages, never
  * written) has no effect.  A position that some rows see and others do not
  * enters the latter with weight 0, so a V that is not finite there makes their

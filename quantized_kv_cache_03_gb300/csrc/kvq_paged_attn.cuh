@@ -212,8 +212,11 @@ __global__ void __launch_bounds__(128, NT == 1 ? 3 : 2) paged_attn_kernel(const 
                         const size_t t = t0 + (row0 + r) / gsz;
                         raw = *reinterpret_cast<const uint2 *>(p.q + t * p.q_stride + (size_t)p.grp_q[gb + (row0 + r) % gsz] * kD + 4 * lane);
                     }
+                    // a row with an infinity or NaN gets scores of NaN, whatever its codes would be
+                    const __half2 top = __hmax2_nan(__habs2(*reinterpret_cast<const __half2 *>(&raw.x)), __habs2(*reinterpret_cast<const __half2 *>(&raw.y)));
+                    const bool wild = __any_sync(0xffffffffu, !__hble2(top, __half2half2(__ushort_as_half(0x7bff))));
                     if (C::F16K) {
-                        *reinterpret_cast<uint2 *>(qw + r * (kD / 2) + 2 * lane) = raw;
+                        *reinterpret_cast<uint2 *>(qw + r * (kD / 2) + 2 * lane) = wild ? make_uint2(0x7fff7fffu, 0x7fff7fffu) : raw;
                         continue;
                     }
                     const float2 lo = half2_of(raw.x), hi = half2_of(raw.y);
@@ -230,7 +233,7 @@ __global__ void __launch_bounds__(128, NT == 1 ? 3 : 2) paged_attn_kernel(const 
                     if ((lane & 7) == 0) {
                         const int x = (lane >> 3) * C::PAIRS + (NT == 1 ? r >> 1 : r & 7), e = NT == 1 ? r & 1 : r >> 3;
                         float *sd = reinterpret_cast<float *>(qseed + x);
-                        reinterpret_cast<float *>(qs + x)[e] = __half2float(__ushort_as_half(s16)) * p.qk_scale_log2;
+                        reinterpret_cast<float *>(qs + x)[e] = wild ? __int_as_float(0x7fc00000) : __half2float(__ushort_as_half(s16)) * p.qk_scale_log2;
                         sd[NT == 1 ? e : 2 * e] = sd[NT == 1 ? e + 2 : 2 * e + 1] = -kBias * (float)sum;
                     }
                 }
@@ -596,7 +599,8 @@ __global__ void __launch_bounds__(128, NT == 1 ? 3 : 2) paged_attn_kernel(const 
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
                     const float mw = sm_m[w * C::ROWS + tid];
-                    if (mw != -INFINITY) sum += sm_l[w * C::ROWS + tid] * fast_exp2(mw - M);
+                    const float lw = sm_l[w * C::ROWS + tid];   // without a maximum: 0, or NaN if there were scores
+                    sum += mw == -INFINITY ? lw : lw * fast_exp2(mw - M);
                 }
                 float lg;
                 asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(sum));

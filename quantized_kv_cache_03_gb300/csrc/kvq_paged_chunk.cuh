@@ -628,18 +628,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                 for (int b2 = 0; b2 < 2; ++b2) {
                     const int bb = 2 * grp + b2;
                     uint4 raw[4];
-                    float a = 0.f;
+                    __half2 top = __half2half2(__ushort_as_half(0));
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         raw[k] = row_ok ? src[4 * bb + k] : make_uint4(0u, 0u, 0u, 0u);
                         const uint32_t ws[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&ws[e]));
-                            a = fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y)));
-                        }
+                        for (int e = 0; e < 4; ++e) top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __half2 *>(&ws[e])));
                     }
-                    const float sc = __half2float(__float2half_rn(__fdiv_rn(a, 127.f)));
+                    // an infinity or NaN in the query: scores of NaN, whatever its codes would be
+                    const float2 a2 = __half22float2(top);
+                    const float a = fmaxf(a2.x, a2.y);
+                    const float sc = a2.x <= 65504.f && a2.y <= 65504.f ? __half2float(__float2half_rn(__fdiv_rn(a, 127.f))) : __int_as_float(0x7fc00000);
                     uint32_t hv[16], lv[16];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -857,7 +857,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                     tc_fence_after();
                     const float2 o = xe[(grp ^ 1) * kCM + row];
                     const float mm = fmaxf(m, o.x);   // O is at the later, higher zero point
-                    l = (m == -INFINITY ? 0.f : l * fast_exp2(m - mm)) + (o.x == -INFINITY ? 0.f : o.y * fast_exp2(o.x - mm));
+                    // without a maximum a sum is 0, or NaN if there were scores
+                    l = (m == -INFINITY ? l : l * fast_exp2(m - mm)) + (o.x == -INFINITY ? o.y : o.y * fast_exp2(o.x - mm));
                     m = mm;
                 }
             }

@@ -103,3 +103,46 @@ def test_largest_values(new, v_type):
     keys = Batch([300], [new], H=2, Hq=8, page=64, v_type=v_type, seed=new, shape=lambda kv: np.stack([kv[0] * 0 + 65504 * np.sign(kv[0]), kv[1]]))
     keys.q = (keys.q * 2e-5).astype(np.float16)
     _check_by_block(keys, torch.float32)
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("L", [90, 3000])   # whole row tiles, and tiles cut over CTAs
+@pytest.mark.parametrize("new", [1, 6, 40])
+@pytest.mark.parametrize("k_type", [I8, F16])
+def test_a_query_that_is_not_finite_gives_nan(k_type, new, L, bad):
+    """Rows whose query holds one value that is not finite: NaN in out and lse,
+    every other row what it is without them; a row that sees nothing stays empty."""
+    for at in (0, 77, 127):
+        b = Batch([L, new - 1], [new, new], H=2, Hq=8, page=32, k_type=k_type, v_type=Q8, seed=new)
+        want = b.attn()
+        a, _, el = b.bounds()
+        hit = np.zeros((b.T, b.Hq), bool)
+        hit[[0, new // 2, new, b.T - 1], [0, 3, 1, 5]] = True
+        b.q[hit, at] = bad
+        o, ls = b.attn()
+        seen = np.ones(b.T, bool)
+        seen[new] = False          # the first of new rows over new - 1 positions
+        assert np.isnan(o[hit & seen[:, None]]).all() and np.isnan(ls[hit & seen[:, None]]).all()
+        assert (o[new] == 0).all() and np.isneginf(ls[new]).all()
+        # the rows of a tile move their zero points together, so the others need not keep their bits: each run
+        # is within the bounds of the exact values
+        fin = ~hit & seen[:, None]
+        assert (np.abs(o[fin] - want[0][fin]) <= 2 * a).all() and (np.abs(ls[fin] - want[1][fin]) <= 2 * el).all()
+
+
+@pytest.mark.parametrize("L", [90, 3000])
+@pytest.mark.parametrize("new", [1, 6, 40])
+@pytest.mark.parametrize("k_type", [I8, F16])
+def test_an_infinite_score_gives_nan(k_type, new, L):
+    """The newest key holds infinities that the query turns into scores of
+    +inf (an int8 key's infinity has code -127): the last row is NaN."""
+    def shape(kv):
+        kv[0][-1, :, 7::32] = np.inf
+        return kv
+    b = Batch([L], [new], H=2, Hq=8, page=32, k_type=k_type, v_type=Q4, seed=new, shape=shape)
+    b.q[:, :, 7::32] = np.abs(b.q[:, :, 7::32]) + np.float16(0.5)
+    if k_type == I8:
+        b.q[:, :, 7::32] *= -1
+    o, ls = b.attn()
+    assert np.isnan(o[-1]).all() and np.isnan(ls[-1]).all()
+    assert np.isfinite(o[:-1]).all() and np.isfinite(ls[:-1]).all()
