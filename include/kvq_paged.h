@@ -165,7 +165,8 @@ kvq_status kvq_paged_gather(const kvq_pages *p, const int32_t *slots, int32_t n_
  *  seq_lens    device int32 [n_seqs]: positions of each sequence, the new ones
  *              included (held to [0, max_blocks * page_tokens]).
  *  block_table, table_stride, max_blocks  as kvq_page_tables.
- *  causal      nonzero: row i of n sees positions 0 .. len - n + i; zero: all
+ *  causal      nonzero: row i of the n that q_start gives the sequence (rows
+ *              past max_q counted) sees positions 0 .. len - n + i; zero: all
  *              len positions.
  *  head_map    host int32 [n_q_heads] or NULL, as kvq_decode_attn.
  *  sm_scale    softmax scale.

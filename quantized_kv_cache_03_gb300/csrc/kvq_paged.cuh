@@ -235,12 +235,16 @@ struct PagedAttnParams {
     uint8_t grp_q[KVQ_MAX_HEADS];
 };
 
-// New rows and visible length of sequence b, held to the arrays' bounds.
-__device__ __forceinline__ void seq_shape(const PagedAttnParams &p, int b, int &t0, int &n, int &len)
+// New rows and visible length of sequence b, held to the arrays' bounds, and
+// the last position its first row sees under the causal mask, row i being the
+// sequence's i-th also where rows past max_q are left out.
+__device__ __forceinline__ void seq_shape(const PagedAttnParams &p, int b, int &t0, int &n, int &len, int &lim0)
 {
     t0 = min(max(p.q_start[b], 0), p.n_tokens);
-    n = min(min(max(p.q_start[b + 1], 0), p.n_tokens) - t0, p.max_q);
+    const int rows = min(max(p.q_start[b + 1], 0), p.n_tokens) - t0;
+    n = min(rows, p.max_q);
     len = max(0, (int)min((long long)p.seq_lens[b], (long long)p.max_blocks << p.pool.pshift));
+    lim0 = len - rows;
 }
 
 // Work of a sequence, in stages of kStagePos positions for every row tile of

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(128, NT == 1 ? 3 : 2) paged_attn_kernel(const 
     auto seq_tiles = [&](int n) { return (n * p.gmax + C::ROWS - 1) / C::ROWS; };   // row tiles per kv head
     auto seq_stages = [&](int len) { return max(1, (len + kStagePos - 1) / kStagePos); };
     long long pos, per;
-    line_find<C::THREADS>(p, kPagedMinStages, [&](int n, int len) { return (long long)H * seq_tiles(n) * seq_stages(len); },
+    line_find<C::THREADS>(p, kPagedMinStages, [&](int n, int len, int) { return (long long)H * seq_tiles(n) * seq_stages(len); },
                           &line, tmp, pos, per);
     const long long end = min(pos + per, line.total);
     PagedCut *cuts = p.cuts + (size_t)blockIdx.x * 2;
@@ -117,14 +117,14 @@ __global__ void __launch_bounds__(128, NT == 1 ? 3 : 2) paged_attn_kernel(const 
     __syncthreads();
     if (pos >= end) return;
 
-    int b = line.b - 1, t0 = 0, n = 0, L = 0, n_st = 0, n_rt = 0, h = 0, rt = 0, s0 = 0;
+    int b = line.b - 1, t0 = 0, n = 0, L = 0, lim0 = 0, n_st = 0, n_rt = 0, h = 0, rt = 0, s0 = 0;
     bool fresh = true;
     int done = 0;   // stages this warp has taken since the kernel began: ring slot and phase
     for (bool first = true; pos < end; first = false) {
         if (fresh) {   // next sequence of this launch
             do {
                 ++b;
-                seq_shape(p, b, t0, n, L);
+                seq_shape(p, b, t0, n, L, lim0);
             } while (!seq_mine(p, n));
             n_st = seq_stages(L);
             n_rt = seq_tiles(n);
@@ -148,8 +148,8 @@ __global__ void __launch_bounds__(128, NT == 1 ? 3 : 2) paged_attn_kernel(const 
                 cuts[slot] = PagedCut{b, h | rt << 8, (int)c0, (int)((x0 + n_st - 1) / per - c0 + 1)};
             }
             // positions the tile's last and first rows see end at lim_hi, lim_lo
-            const int lim_hi = p.causal ? L - n + (row0 + R - 1) / gsz : L - 1;
-            const int lim_lo = p.causal ? L - n + row0 / gsz : L - 1;
+            const int lim_hi = p.causal ? lim0 + (row0 + R - 1) / gsz : L - 1;
+            const int lim_lo = p.causal ? lim0 + row0 / gsz : L - 1;
             const int sv = min(s1, (lim_hi + kStagePos) / kStagePos);       // stages past sv show nothing (lim_hi >= -kStagePos)
             const int nj = lim_hi < 0 ? 0 : max(0, (sv - s0 - warp + W - 1) / W);   // this warp's stages
 
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(128, NT == 1 ? 3 : 2) paged_attn_kernel(const 
             float acc[8][NT][4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                lim[e] = lrow[e] < R ? (p.causal ? L - n + (row0 + lrow[e]) / gsz : L - 1) : -1;
+                lim[e] = lrow[e] < R ? (p.causal ? lim0 + (row0 + lrow[e]) / gsz : L - 1) : -1;
                 m[e] = -INFINITY;
                 mu[e] = l[e] = 0.f;
             }

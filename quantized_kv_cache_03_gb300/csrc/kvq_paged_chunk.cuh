@@ -200,23 +200,24 @@ struct ChunkWalk {
     int tiles;               // KV tiles with a visible position among those of the piece; negative: no more pieces
     int s0;                  // first KV tile
     int b, h, t0, n, L;      // sequence, kv head, first row and rows of the batch, length
+    int lim0;                // last position the sequence's first row sees under the causal mask
     int gb, gsz, row0, R;    // query heads of the kv head, first row and rows of the tile
     int lim_hi;              // last position the tile's last row sees
     int slot;                // where the result goes: -1 out, else the CTA's slot of partials
 };
 // KV tiles a row tile counts for: those its last row sees (all, when the kv
 // heads have query groups of different sizes), at least one.
-__device__ __forceinline__ int chunk_tiles(const PagedAttnParams &p, int n, int L, int rt)
+__device__ __forceinline__ int chunk_tiles(const PagedAttnParams &p, int n, int L, int lim0, int rt)
 {
     const int last = min(n - 1, (int)(((long long)rt * kCM + kCM - 1) / p.gmax));
-    const int vis = p.causal && p.uniform ? min(L, L - n + 1 + last) : L;
+    const int vis = p.causal && p.uniform ? min(L, lim0 + 1 + last) : L;
     return max(1, (vis + kCN - 1) / kCN);
 }
-__device__ __forceinline__ long long chunk_head_tiles(const PagedAttnParams &p, int n, int L)
+__device__ __forceinline__ long long chunk_head_tiles(const PagedAttnParams &p, int n, int L, int lim0)
 {
     const int n_rt = (int)(((long long)n * p.gmax + kCM - 1) / kCM);
     long long s = 0;
-    for (int rt = 0; rt < n_rt; ++rt) s += chunk_tiles(p, n, L, rt);
+    for (int rt = 0; rt < n_rt; ++rt) s += chunk_tiles(p, n, L, lim0, rt);
     return s;
 }
 
@@ -235,16 +236,16 @@ __device__ __forceinline__ void chunk_pieces(const PagedAttnParams &p, const Lin
         if (fresh) {
             do {
                 ++w.b;
-                seq_shape(p, w.b, w.t0, w.n, w.L);
+                seq_shape(p, w.b, w.t0, w.n, w.L, w.lim0);
             } while (!seq_mine(p, w.n));
             n_rt = (int)(((long long)w.n * p.gmax + kCM - 1) / kCM);
             w.h = rt = w.s0 = 0;
             if (first) {
-                const long long per_head = chunk_head_tiles(p, w.n, w.L);
+                const long long per_head = chunk_head_tiles(p, w.n, w.L, w.lim0);
                 w.h = (int)(line.off / per_head);
                 long long x = line.off - w.h * per_head;
                 for (;; ++rt) {
-                    const int k = chunk_tiles(p, w.n, w.L, rt);
+                    const int k = chunk_tiles(p, w.n, w.L, w.lim0, rt);
                     if (x < k) break;
                     x -= k;
                 }
@@ -253,13 +254,13 @@ __device__ __forceinline__ void chunk_pieces(const PagedAttnParams &p, const Lin
             }
             fresh = false;
         }
-        const int n_tl = chunk_tiles(p, w.n, w.L, rt), s1 = (int)min((long long)n_tl, w.s0 + (end - pos));
+        const int n_tl = chunk_tiles(p, w.n, w.L, w.lim0, rt), s1 = (int)min((long long)n_tl, w.s0 + (end - pos));
         w.gb = p.grp_begin[w.h];
         w.gsz = p.grp_begin[w.h + 1] - w.gb;
         w.row0 = rt * kCM;
         w.R = min(kCM, w.n * w.gsz - w.row0);
         if (w.R > 0) {
-            w.lim_hi = p.causal ? w.L - w.n + (w.row0 + w.R - 1) / w.gsz : w.L - 1;
+            w.lim_hi = p.causal ? w.lim0 + (w.row0 + w.R - 1) / w.gsz : w.L - 1;
             w.tiles = w.lim_hi < 0 ? 0 : max(0, min(s1, w.lim_hi / kCN + 1) - w.s0);
             w.slot = -1;
             if (w.s0 > 0 || s1 < n_tl) {
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
     pdl_trigger();
     long long pos, per;
     line_find<kChunkThreads>(p, kChunkMinTiles,
-                             [&](int n, int len) { return (long long)p.pool.n_kv_heads * chunk_head_tiles(p, n, len); }, &line, tmp, pos, per);
+                             [&](int n, int len, int lim0) { return (long long)p.pool.n_kv_heads * chunk_head_tiles(p, n, len, lim0); }, &line, tmp, pos, per);
     const long long end = min(pos + per, line.total);
     PagedCut *cuts = p.cuts + (size_t)blockIdx.x * 2;
     if (tid < 2) cuts[tid] = PagedCut{0, 0, 0, 0};
@@ -618,7 +619,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
             const bool whole = w.slot < 0;
             const bool row_ok = row < w.R;
             const int tok = row_ok ? (w.row0 + row) / w.gsz : 0, head = row_ok ? p.grp_q[w.gb + (w.row0 + row) % w.gsz] : 0;
-            const int lim = row_ok ? (p.causal ? w.L - w.n + tok : w.L - 1) : -1;
+            const int lim = row_ok ? (p.causal ? w.lim0 + tok : w.L - 1) : -1;
             float m = -INFINITY, l = 0.f;
             if (w.tiles > 0 && !lost) {
                 // ---- blocks 2 grp, 2 grp + 1 of this row: int8 rule, q in two fp16 parts into TMEM ----

@@ -60,7 +60,7 @@ struct LineStart {
     long long total;     // stages of the line
 };
 
-// stages(n, len): the sequence's stages over all kv heads and row tiles.
+// stages(n, len, lim0): the sequence's stages over all kv heads and row tiles.
 template <int THREADS, typename F>
 __device__ __forceinline__ void line_find(const PagedAttnParams &p, long long gmin, F stages, LineStart *res,
                                           long long *tmp, long long &begin, long long &per)
@@ -69,9 +69,9 @@ __device__ __forceinline__ void line_find(const PagedAttnParams &p, long long gm
     const int each = (p.n_seqs + THREADS - 1) / THREADS, i0 = min(p.n_seqs, tid * each), i1 = min(p.n_seqs, i0 + each);
     long long sum = 0;
     for (int i = i0; i < i1; ++i) {
-        int t0, n, len;
-        seq_shape(p, i, t0, n, len);
-        if (seq_mine(p, n)) sum += stages(n, len);
+        int t0, n, len, lim0;
+        seq_shape(p, i, t0, n, len, lim0);
+        if (seq_mine(p, n)) sum += stages(n, len, lim0);
     }
     long long x = sum;
 #pragma unroll
@@ -92,9 +92,9 @@ __device__ __forceinline__ void line_find(const PagedAttnParams &p, long long gm
     long long at = base + x - sum;
     if (begin >= at && begin < at + sum)
         for (int i = i0; i < i1; ++i) {
-            int t0, n, len;
-            seq_shape(p, i, t0, n, len);
-            const long long s = seq_mine(p, n) ? stages(n, len) : 0;
+            int t0, n, len, lim0;
+            seq_shape(p, i, t0, n, len, lim0);
+            const long long s = seq_mine(p, n) ? stages(n, len, lim0) : 0;
             if (begin < at + s) {
                 res->b = i;
                 res->off = begin - at;

@@ -534,8 +534,8 @@ __global__ void __launch_bounds__(kPcWarps * 32, 4) paged_combine_kernel(const _
         if (c.np < 2) continue;   // block-uniform
         const int h = c.h_rt & 255, rt = c.h_rt >> 8;
         const int share = (cta - c.c0) * g.spread + block % g.spread, shares = c.np * g.spread;
-        int t0, n, len;
-        seq_shape(p, c.b, t0, n, len);
+        int t0, n, len, lim0;
+        seq_shape(p, c.b, t0, n, len, lim0);
         const int gb = p.grp_begin[h], gsz = p.grp_begin[h + 1] - gb;
         const int row0 = rt * g.rows, R = min(g.rows, n * gsz - row0);
         auto out_row = [&](int r) {

@@ -146,3 +146,20 @@ def test_an_infinite_score_gives_nan(k_type, new, L):
     o, ls = b.attn()
     assert np.isnan(o[-1]).all() and np.isnan(ls[-1]).all()
     assert np.isfinite(o[:-1]).all() and np.isfinite(ls[:-1]).all()
+
+
+@pytest.mark.parametrize("max_q", [1, 5, 33])
+@pytest.mark.parametrize("k_type", [I8, F16])
+def test_rows_past_max_q_do_not_move_the_others(k_type, max_q):
+    """The first max_q rows of a longer sequence see what they see without the
+    bound; the rest is left alone."""
+    b = Batch([90, 700, 17, 60], [3, 60, 17, 60], H=2, Hq=8, page=16, k_type=k_type, seed=max_q, pad_rows=1)
+    for causal in (True, False):
+        o, ls = b.attn(causal=causal, max_q=max_q)
+        a, _, el = b.bounds()
+        for s, n in enumerate(b.new):
+            t0, m = b.q_start[s], min(n, max_q)
+            ro, rl = b.reference(s, causal)
+            assert (np.abs(o[t0:t0 + m] - ro[:m]) <= a).all() and (np.abs(ls[t0:t0 + m] - rl[:m]) <= el).all()
+            assert (o[t0 + m:t0 + n] == 777).all() and (ls[t0 + m:t0 + n] == 777).all()
+        assert (o[-1] == 777).all()
