@@ -225,6 +225,23 @@ kvq_status kvq_paged_attn(const kvq_paged_desc *a, void *workspace, size_t works
  * what device memory holds.  bytes: host out. */
 kvq_status kvq_paged_attn_workspace_size(const kvq_paged_desc *a, size_t *bytes);
 
+/*
+ * kvq_debug_paged_lose_copy -- TEST HOOK, the counterpart of
+ * kvq_debug_lose_stage: kvq_paged_attn (same arguments and rules) on test
+ * flavours of its kernels in which the first CTA arms the barrier of one copy
+ * without issuing the copy.  The bounded wait for it (a short limit here) runs
+ * out; the CTA waits for the copies it did issue, the wait counter of
+ * kvq_wait_timeouts grows by one, and the rows of the CTA's pieces come out as
+ * NaN: in row tiles those of the piece that lost the copy and of the later ones,
+ * in the chunk kernel all of them.  Nothing faults and nothing waits without a
+ * limit.  Of the launches of a call those for up to 8 rows per kv head (copy:
+ * which stage of 32 positions of the first warp) and for more than 32 (copy / 2:
+ * which half tile of 64 positions; even: its K part, odd: its V part) lose one.
+ * int8 K, q4_0 V and KVQ_OUT_F32; others return KVQ_ERR_UNSUPPORTED.
+ */
+kvq_status kvq_debug_paged_lose_copy(const kvq_paged_desc *a, int32_t copy, void *workspace, size_t workspace_bytes,
+                                     void *stream);
+
 #ifdef __cplusplus
 }
 #endif

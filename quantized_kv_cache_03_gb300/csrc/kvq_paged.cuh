@@ -231,6 +231,7 @@ struct PagedAttnParams {
     int uniform;                        // every kv head has gmax query heads
     int min_rows, max_rows;             // sequences with min_rows <= rows <= max_rows per kv head are this launch's
     float qk_scale_log2;
+    int lose;                           // test flavours: which copy CTA 0 leaves out
     uint16_t grp_begin[KVQ_MAX_HEADS + 1];   // kv head h owns grp_q[grp_begin[h] .. grp_begin[h + 1])
     uint8_t grp_q[KVQ_MAX_HEADS];
 };
@@ -275,6 +276,13 @@ cudaError_t prepare_chunk_q4();
 cudaError_t prepare_chunk_q8();
 cudaError_t launch_chunk_q4(const PagedAttnParams &p, int out_type, int n_ctas, cudaStream_t s, bool pdl);
 cudaError_t launch_chunk_q8(const PagedAttnParams &p, int out_type, int n_ctas, cudaStream_t s, bool pdl);
+
+// Test flavours (int8 K, q4_0 V, fp32 output; row tiles of 8 rows, chunks) in
+// which CTA 0 arms one copy's barrier and leaves the copy out, so that the wait
+// for it, given a short limit, runs out: kvq_debug_paged_lose_copy.
+constexpr uint32_t kLostCopySpins = 1 << 15;   // of the lost stage's wait; in the chunk kernel of every wait but those for copies and MMAs in flight
+cudaError_t launch_paged_lose(const PagedAttnParams &p, int n_ctas, cudaStream_t s, bool pdl);
+cudaError_t launch_chunk_lose(const PagedAttnParams &p, int n_ctas, cudaStream_t s, bool pdl);
 
 // The current device's SM count and the address of the bounded waits' counter
 // (kvq_api.cu).

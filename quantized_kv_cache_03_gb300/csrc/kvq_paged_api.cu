@@ -219,6 +219,81 @@ void plan_attn(const kvq_paged_desc *a, const PagedDevice *dev, int n_sms, AttnP
     }
 }
 
+// kvq_paged_attn; lose >= 0: with the test flavours, which leave out that copy.
+kvq_status run_attn(const kvq_paged_desc *a, void *workspace, size_t workspace_bytes, void *stream, int lose)
+{
+    AttnPlan pl;
+    kvq_status st = check_attn(a, pl);
+    if (st != KVQ_OK) return st;
+    st = check_pool(a->pages);
+    if (st != KVQ_OK) return st;
+    if (lose >= 0 && (a->pages->k_type != KVQ_K_I8 || a->pages->v_type != KVQ_V_Q4_0 || a->out_type != KVQ_OUT_F32)) return KVQ_ERR_UNSUPPORTED;
+    if (idle(a)) return KVQ_OK;
+    const int Hq = a->n_q_heads;
+    if (!a->q16 || !aligned(a->q16, 16) || a->q_stride % 8 || a->q_stride < (int64_t)Hq * kD) return KVQ_ERR_INVALID_ARG;
+    if (!int_ptr(a->q_start) || !int_ptr(a->seq_lens) || (a->max_blocks > 0 && !int_ptr(a->block_table))) return KVQ_ERR_INVALID_ARG;
+    if (!a->out || !aligned(a->out, 16) || !aligned(a->lse, 4)) return KVQ_ERR_INVALID_ARG;
+    PagedDevice *dev = nullptr;
+    int n_sms = 0;
+    unsigned int *timeouts = nullptr;
+    st = paged_setup(&dev, &n_sms, &timeouts);
+    if (st != KVQ_OK) return st;
+    plan_attn(a, dev, n_sms, pl);
+    if (!workspace || workspace_bytes < pl.bytes || !aligned(workspace, 256)) return KVQ_ERR_WORKSPACE;
+    static thread_local PagedAttnParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.pool = pool_of(a->pages);
+    p.q = static_cast<const uint16_t *>(a->q16);
+    p.q_stride = a->q_stride;
+    p.q_start = a->q_start;
+    p.seq_lens = a->seq_lens;
+    p.block_table = a->block_table;
+    p.out = a->out;
+    p.lse = a->lse;
+    p.timeouts = timeouts;
+    p.n_seqs = a->n_seqs;
+    p.n_tokens = a->n_tokens;
+    p.max_q = a->max_q;
+    p.n_q_heads = Hq;
+    p.table_stride = a->table_stride;
+    p.max_blocks = a->max_blocks;
+    p.causal = a->causal ? 1 : 0;
+    p.gmax = pl.gmax;
+    p.uniform = pl.uniform;
+    p.qk_scale_log2 = a->sm_scale * 1.4426950408889634f;
+    p.lose = lose;
+    std::memcpy(p.grp_begin, pl.grp_begin, sizeof(p.grp_begin));
+    std::memcpy(p.grp_q, pl.grp_q, sizeof(p.grp_q));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool pdl = pdl_on();
+    const kvq_pages *g = a->pages;
+    const bool q4 = g->v_type == KVQ_V_Q4_0;
+    PagedCuts cuts = {};
+    cudaError_t e = cudaSuccess;
+    for (int k = 0; k < kAttnParts && e == cudaSuccess; ++k) {
+        const Part &pt = pl.part[k];
+        if (pt.n_ctas == 0) continue;
+        char *w = static_cast<char *>(workspace);
+        p.cuts = reinterpret_cast<PagedCut *>(w + pt.cut_off);
+        p.ws_lse = reinterpret_cast<float *>(w + pt.lse_off);
+        p.ws_o = reinterpret_cast<float *>(w + pt.o_off);
+        p.sums = reinterpret_cast<float *>(w + pt.sum_off);
+        p.min_rows = pt.least;
+        p.max_rows = pt.most;
+        // a cut tile is merged by at least two CTAs' blocks of eight warps
+        cuts.part[k] = PagedPieces{p.cuts, p.ws_lse, p.ws_o, pt.rows, pt.n_ctas > 1 ? pt.n_ctas : 0, (pt.rows + 15) / 16};
+        if (lose >= 0 && k != 1)
+            e = k == 0 ? launch_paged_lose(p, pt.n_ctas, s, pdl && pt.n_ctas <= n_sms) : launch_chunk_lose(p, pt.n_ctas, s, pdl);
+        else if (k < 2)
+            e = q4 ? launch_paged_q4(p, k + 1, g->k_type, a->out_type, pt.n_ctas, s, pdl && pt.n_ctas <= n_sms)
+                   : launch_paged_q8(p, k + 1, g->k_type, a->out_type, pt.n_ctas, s, pdl && pt.n_ctas <= n_sms);
+        else
+            e = q4 ? launch_chunk_q4(p, a->out_type, pt.n_ctas, s, pdl) : launch_chunk_q8(p, a->out_type, pt.n_ctas, s, pdl);
+    }
+    if (e == cudaSuccess) e = launch_paged_combine(p, cuts, a->out_type, s, pdl);
+    return done(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -323,72 +398,13 @@ kvq_status kvq_paged_attn_workspace_size(const kvq_paged_desc *a, size_t *bytes)
 
 kvq_status kvq_paged_attn(const kvq_paged_desc *a, void *workspace, size_t workspace_bytes, void *stream)
 {
-    AttnPlan pl;
-    kvq_status st = check_attn(a, pl);
-    if (st != KVQ_OK) return st;
-    st = check_pool(a->pages);
-    if (st != KVQ_OK) return st;
-    if (idle(a)) return KVQ_OK;
-    const int Hq = a->n_q_heads;
-    if (!a->q16 || !aligned(a->q16, 16) || a->q_stride % 8 || a->q_stride < (int64_t)Hq * kD) return KVQ_ERR_INVALID_ARG;
-    if (!int_ptr(a->q_start) || !int_ptr(a->seq_lens) || (a->max_blocks > 0 && !int_ptr(a->block_table))) return KVQ_ERR_INVALID_ARG;
-    if (!a->out || !aligned(a->out, 16) || !aligned(a->lse, 4)) return KVQ_ERR_INVALID_ARG;
-    PagedDevice *dev = nullptr;
-    int n_sms = 0;
-    unsigned int *timeouts = nullptr;
-    st = paged_setup(&dev, &n_sms, &timeouts);
-    if (st != KVQ_OK) return st;
-    plan_attn(a, dev, n_sms, pl);
-    if (!workspace || workspace_bytes < pl.bytes || !aligned(workspace, 256)) return KVQ_ERR_WORKSPACE;
-    static thread_local PagedAttnParams p;
-    std::memset(&p, 0, sizeof(p));
-    p.pool = pool_of(a->pages);
-    p.q = static_cast<const uint16_t *>(a->q16);
-    p.q_stride = a->q_stride;
-    p.q_start = a->q_start;
-    p.seq_lens = a->seq_lens;
-    p.block_table = a->block_table;
-    p.out = a->out;
-    p.lse = a->lse;
-    p.timeouts = timeouts;
-    p.n_seqs = a->n_seqs;
-    p.n_tokens = a->n_tokens;
-    p.max_q = a->max_q;
-    p.n_q_heads = Hq;
-    p.table_stride = a->table_stride;
-    p.max_blocks = a->max_blocks;
-    p.causal = a->causal ? 1 : 0;
-    p.gmax = pl.gmax;
-    p.uniform = pl.uniform;
-    p.qk_scale_log2 = a->sm_scale * 1.4426950408889634f;
-    std::memcpy(p.grp_begin, pl.grp_begin, sizeof(p.grp_begin));
-    std::memcpy(p.grp_q, pl.grp_q, sizeof(p.grp_q));
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool pdl = pdl_on();
-    const kvq_pages *g = a->pages;
-    const bool q4 = g->v_type == KVQ_V_Q4_0;
-    PagedCuts cuts = {};
-    cudaError_t e = cudaSuccess;
-    for (int k = 0; k < kAttnParts && e == cudaSuccess; ++k) {
-        const Part &pt = pl.part[k];
-        if (pt.n_ctas == 0) continue;
-        char *w = static_cast<char *>(workspace);
-        p.cuts = reinterpret_cast<PagedCut *>(w + pt.cut_off);
-        p.ws_lse = reinterpret_cast<float *>(w + pt.lse_off);
-        p.ws_o = reinterpret_cast<float *>(w + pt.o_off);
-        p.sums = reinterpret_cast<float *>(w + pt.sum_off);
-        p.min_rows = pt.least;
-        p.max_rows = pt.most;
-        // a cut tile is merged by at least two CTAs' blocks of eight warps
-        cuts.part[k] = PagedPieces{p.cuts, p.ws_lse, p.ws_o, pt.rows, pt.n_ctas > 1 ? pt.n_ctas : 0, (pt.rows + 15) / 16};
-        if (k < 2)
-            e = q4 ? launch_paged_q4(p, k + 1, g->k_type, a->out_type, pt.n_ctas, s, pdl && pt.n_ctas <= n_sms)
-                   : launch_paged_q8(p, k + 1, g->k_type, a->out_type, pt.n_ctas, s, pdl && pt.n_ctas <= n_sms);
-        else
-            e = q4 ? launch_chunk_q4(p, a->out_type, pt.n_ctas, s, pdl) : launch_chunk_q8(p, a->out_type, pt.n_ctas, s, pdl);
-    }
-    if (e == cudaSuccess) e = launch_paged_combine(p, cuts, a->out_type, s, pdl);
-    return done(e);
+    return run_attn(a, workspace, workspace_bytes, stream, -1);
+}
+
+kvq_status kvq_debug_paged_lose_copy(const kvq_paged_desc *a, int32_t copy, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (copy < 0) return KVQ_ERR_INVALID_ARG;
+    return run_attn(a, workspace, workspace_bytes, stream, copy);
 }
 
 }  // extern "C"

@@ -80,7 +80,8 @@ struct PagedCfg {
 // scheduler the accumulators and fragments spill or are loaded too late to
 // overlap (131072 positions, 5 rows: 48 us at three, 53 at four, 49 at two;
 // 16 sequences of 32 rows: 419 us at two, 442 at three).
-template <int NT, int VT, int KT, bool O16>
+// LOSE: the test flavour; CTA 0's warp 0 leaves out its copy stage p.lose.
+template <int NT, int VT, int KT, bool O16, bool LOSE = false>
 __global__ void __launch_bounds__(128, NT == 1 ? 3 : 2) paged_attn_kernel(const __grid_constant__ PagedAttnParams p)
 {
     using C = PagedCfg<NT, VT, KT>;
@@ -120,6 +121,7 @@ __global__ void __launch_bounds__(128, NT == 1 ? 3 : 2) paged_attn_kernel(const 
     int b = line.b - 1, t0 = 0, n = 0, L = 0, lim0 = 0, n_st = 0, n_rt = 0, h = 0, rt = 0, s0 = 0;
     bool fresh = true;
     int done = 0;   // stages this warp has taken since the kernel began: ring slot and phase
+    const bool loser = LOSE && blockIdx.x == 0 && warp == 0;
     for (bool first = true; pos < end; first = false) {
         if (fresh) {   // next sequence of this launch
             do {
@@ -172,18 +174,19 @@ __global__ void __launch_bounds__(128, NT == 1 ? 3 : 2) paged_attn_kernel(const 
                 const int tile = (x & ((1 << pshift) - 1)) >> 4;
                 const bool v0 = a0 >= 0 && a0 < p.pool.n_pages;
                 const uint32_t dst = ring_s + sl * C::STAGE, bw = bar_s + sl * 8;
+                const bool drop = LOSE && loser && done + issued == p.lose;
                 int ok;
                 if (pshift == 4) {
                     const int a1 = __shfl_sync(0xffffffffu, pg1, issued & 31);
                     const bool v1 = a1 >= 0 && a1 < p.pool.n_pages;
                     ok = (v0 ? 1 : 0) | (v1 ? 2 : 0);
                     mbar_arrive_expect_tx_w(bw, ((v0 ? 1 : 0) + (v1 ? 1 : 0)) * T::BYTES);
-                    if (v0) bulk_g2s_w(dst, tile_of(p.pool, a0, h, 0, T::BYTES), T::BYTES, bw);
-                    if (v1) bulk_g2s_w(dst + T::BYTES, tile_of(p.pool, a1, h, 0, T::BYTES), T::BYTES, bw);
+                    if (v0 && !drop) bulk_g2s_w(dst, tile_of(p.pool, a0, h, 0, T::BYTES), T::BYTES, bw);
+                    if (v1 && !drop) bulk_g2s_w(dst + T::BYTES, tile_of(p.pool, a1, h, 0, T::BYTES), T::BYTES, bw);
                 } else {
                     ok = v0 ? 3 : 0;
                     mbar_arrive_expect_tx_w(bw, v0 ? C::STAGE : 0);
-                    if (v0) bulk_g2s_w(dst, tile_of(p.pool, a0, h, tile, T::BYTES), C::STAGE, bw);
+                    if (v0 && !drop) bulk_g2s_w(dst, tile_of(p.pool, a0, h, tile, T::BYTES), C::STAGE, bw);
                 }
                 okm = (okm & ~(3 << (2 * sl))) | ok << (2 * sl);
                 ++issued;
@@ -276,12 +279,13 @@ __global__ void __launch_bounds__(128, NT == 1 ? 3 : 2) paged_attn_kernel(const 
 #pragma unroll
                     for (int k = 0; k < 4; ++k) acc[mt][nt][k] = 0.f;
 
-            bool lost = false;
+            int lost = -1;   // the stage whose wait gave up
 #pragma unroll 1
             for (int j = 0; j < nj_live; ++j) {
                 const int sl = (done + j) % S;
-                if (!__all_sync(0xffffffffu, mbar_wait(bar_s + sl * 8, ((done + j) / S) & 1))) {
-                    lost = true;
+                const uint32_t spins = LOSE && loser && done + j == p.lose ? kLostCopySpins : kMbarSpins;
+                if (!__all_sync(0xffffffffu, mbar_wait(bar_s + sl * 8, ((done + j) / S) & 1, spins))) {
+                    lost = j;
                     break;
                 }
                 uint8_t *stg = ring + sl * C::STAGE;
@@ -566,8 +570,9 @@ __global__ void __launch_bounds__(128, NT == 1 ? 3 : 2) paged_attn_kernel(const 
                     issue();
                 }
             }
-            if (lost) {   // wait (bounded) for the copies in flight, then poison the piece
-                for (int k = 0; k < issued; ++k) mbar_wait(bar_s + ((done + k) % S) * 8, ((done + k) / S) & 1);
+            if (lost >= 0) {   // wait (bounded) for the copies in flight, then poison this piece and the later ones
+                for (int k = lost; k < issued; ++k)
+                    if (!(LOSE && loser && done + k == p.lose)) mbar_wait(bar_s + ((done + k) % S) * 8, ((done + k) / S) & 1);
                 if (lane == 0) {
                     atomicOr(bad_flag, 1);
                     atomicAdd(p.timeouts, 1u);
@@ -675,7 +680,7 @@ cudaError_t prepare_paged_t(int *ctas)
 // launch in front, the three or four CTAs that fill an SM's shared memory can
 // leave a hole that the last of them does not fit, and it then starts only when
 // another has finished (64 sequences, 456 CTAs: 370 us or up to 480 us).
-template <int NT, int VT, int KT, bool O16>
+template <int NT, int VT, int KT, bool O16, bool LOSE = false>
 cudaError_t launch_paged_t(const PagedAttnParams &p, int n_ctas, cudaStream_t s, bool pdl)
 {
     using C = PagedCfg<NT, VT, KT>;
@@ -689,7 +694,7 @@ cudaError_t launch_paged_t(const PagedAttnParams &p, int n_ctas, cudaStream_t s,
     at[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_attn_kernel<NT, VT, KT, O16>, p);
+    return cudaLaunchKernelEx(&cfg, paged_attn_kernel<NT, VT, KT, O16, LOSE>, p);
 }
 
 #define KVQ_PAGED_PICK(FN, VT, nt, k_type, out_type, ...)                                                              \

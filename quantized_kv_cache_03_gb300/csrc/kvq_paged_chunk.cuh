@@ -45,8 +45,9 @@
 // converters are busy 80 % of it, the softmax two thirds (fp32 output: four
 // fifths), and the tile's chain QK, maximum, exponents, P.V hides only as far as
 // two tiles of S in tensor memory allow.  Shared memory moves at 40 % of its rate.
-// Every wait is bounded: a wait that gives up marks the CTA, whose rows of this
-// and later pieces come out as NaN; the roles drain what they issued and leave.
+// Every wait is bounded: a wait that gives up marks the CTA; the roles run out of
+// waits in turn, drain what they issued and leave, and every row of the CTA's
+// pieces is then written as NaN.
 #pragma once
 
 #include "kvq_paged.cuh"
@@ -137,6 +138,7 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32])
 // general one, inside a branch that one lane takes, slowed the MMA threads:
 // 503 against 491 us on the chunk named above, 562 against 515 us on the
 // verify shape).
+template <uint32_t SPINS>
 __device__ __forceinline__ bool mbar_wait_alone(uint32_t bar, uint32_t parity)
 {
     uint32_t done;
@@ -145,7 +147,7 @@ __device__ __forceinline__ bool mbar_wait_alone(uint32_t bar, uint32_t parity)
                  " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra again;\n"
                  "over:\n selp.u32 %0, 1, 0, p;\n}"
                  : "=r"(done)
-                 : "r"(bar), "r"(parity), "n"(kMbarSpins)
+                 : "r"(bar), "r"(parity), "n"(SPINS)
                  : "memory");
     return done != 0;
 }
@@ -279,7 +281,9 @@ __device__ __forceinline__ void chunk_pieces(const PagedAttnParams &p, const Lin
     }
 }
 
-template <int VT, bool O16>
+// LOSE: the test flavour; CTA 0 leaves out the copy of the K (p.lose even) or V
+// part of half tile p.lose / 2.
+template <int VT, bool O16, bool LOSE = false>
 __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __grid_constant__ PagedAttnParams p)
 {
     using C = ChunkCfg<VT>;
@@ -319,19 +323,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
     const uint32_t tmem = *tmem_slot;
     const uint32_t tS = tmem, tO = tmem + 2 * kCN, tQ = tO + kD;   // S of group g at 128 g; Q high parts, then low parts
 
+    const bool loser = LOSE && blockIdx.x == 0;
+    constexpr uint32_t kSpins = LOSE ? kLostCopySpins : kMbarSpins;
     auto give_up = [&]() {   // one thread of a role; the others run out of waits in turn
         if (atomicExch(const_cast<int *>(bad), 1) == 0) atomicAdd(p.timeouts, 1u);
     };
     auto wwait = [&](int k, uint32_t parity) {   // by a whole warp
-        if (__all_sync(0xffffffffu, mbar_wait(bar(k), parity))) return true;
+        if (__all_sync(0xffffffffu, mbar_wait(bar(k), parity, kSpins))) return true;
         if (lane == 0) give_up();
         return false;
     };
     auto wait1 = [&](int k, uint32_t parity) {   // by one thread
-        if (mbar_wait_alone(bar(k), parity)) return true;
+        if (mbar_wait_alone<kSpins>(bar(k), parity)) return true;
         give_up();
         return false;
     };
+    auto join_roles = [] { asm volatile("bar.sync 1, %0;" ::"n"(kChunkThreads) : "memory"); };   // every role has left its loop
 
     // Calls body(piece) for the pieces in turn; one = the calling thread is alone.
     auto pieces = [&](bool one, auto body) {
@@ -376,7 +383,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                 if (lane == 0) rec[st] = ok;
                 __syncwarp();   // the record before the arrival that publishes it
                 mbar_arrive_expect_tx_w(full, __popc(ok) * part);
-                if ((lane >> 2) == (t & 7) && src)
+                if ((lane >> 2) == (t & 7) && src && !(LOSE && loser && issued == p.lose >> 1 && (p.lose & 1) == (kside ? 0 : 1)))
                     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                                      raw + (st * kCSub + (lane & 3)) * part),
                                  "l"(src), "r"(part), "r"(full)
@@ -408,7 +415,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
         } else {
             pieces(false, [&](const ChunkWalk &w, int) { return copy_piece(w); });
         }
-        for (int k = max(0, issued - rs); k < issued; ++k) mbar_wait(bar(b_full + k % rs), (k / rs) & 1);   // copies in flight
+        for (int k = max(0, issued - rs); k < issued; ++k)   // copies in flight
+            if (!(LOSE && loser && k == p.lose >> 1 && (p.lose & 1) == (kside ? 0 : 1))) mbar_wait(bar(b_full + k % rs), (k / rs) & 1);
     } else if (warp == kCQk || warp == kCPv) {
         // ================= MMAs: one thread each =================
         if (elect_one()) {
@@ -484,10 +492,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
             // everything issued here is done before TMEM is freed
             const int fin = warp == kCQk ? C::B_FIN : C::B_FIN + 1;
             umma_commit_1(bar(fin));
-            wait1(fin, 0);
+            if (!mbar_wait_alone<kMbarSpins>(bar(fin), 0)) give_up();   // (the general wait here: 466 instead of 448 us on that chunk)
         }
         __syncwarp();
     }
+    join_roles();
     } else if (warp >= kCKConv0) {
     regs_dec<kCRegsConv>();
     if (warp < kCVConv0) {
@@ -599,6 +608,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
             return true;
         });
     }
+    join_roles();
     } else {
         // ================= softmax: one query row per thread =================
         regs_inc<kCRegsSoft>();
@@ -920,6 +930,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
             __syncwarp();
             return true;
         });
+        join_roles();
+        if (*bad) {   // a wait gave up: every row of this CTA's pieces is NaN, also where no role came to
+            const float nan = __int_as_float(0x7fc00000);
+            const long long per2 = max((long long)kChunkMinTiles, (line.total + gridDim.x - 1) / gridDim.x), pos2 = per2 * blockIdx.x;
+            chunk_pieces(p, line, pos2, min(pos2 + per2, line.total), per2, cuts, [&](const ChunkWalk &w) {
+                for (int i = tid; i < w.R * (kD / 4); i += 256) {
+                    const int r = i / (kD / 4), d = 4 * (i % (kD / 4));
+                    const size_t orow = (size_t)(w.t0 + (w.row0 + r) / w.gsz) * p.n_q_heads + p.grp_q[w.gb + (w.row0 + r) % w.gsz];
+                    const size_t part = ((size_t)blockIdx.x * 2 + max(0, w.slot)) * kCM + r;
+                    if (w.slot < 0 && O16)
+                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + orow * kD + d) = make_uint2(0x7fff7fffu, 0x7fff7fffu);
+                    else
+                        *reinterpret_cast<float4 *>((w.slot < 0 ? static_cast<float *>(p.out) + orow * kD : p.ws_o + part * kD) + d) = make_float4(nan, nan, nan, nan);
+                    if (d == 0) {
+                        if (w.slot >= 0) p.ws_lse[part] = nan;
+                        else if (p.lse) p.lse[orow] = nan;
+                    }
+                }
+                return true;
+            });
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -937,7 +968,7 @@ cudaError_t prepare_chunk_t()
     return cudaFuncSetAttribute(paged_chunk_kernel<VT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkCfg<VT>::SMEM);
 }
 
-template <int VT>
+template <int VT, bool LOSE = false>
 cudaError_t launch_chunk_t(const PagedAttnParams &p, int out_type, int n_ctas, cudaStream_t s, bool pdl)
 {
     cudaLaunchConfig_t cfg = {};
@@ -950,8 +981,9 @@ cudaError_t launch_chunk_t(const PagedAttnParams &p, int out_type, int n_ctas, c
     at[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (out_type == KVQ_OUT_F16) return cudaLaunchKernelEx(&cfg, paged_chunk_kernel<VT, true>, p);
-    return cudaLaunchKernelEx(&cfg, paged_chunk_kernel<VT, false>, p);
+    if constexpr (!LOSE)
+        if (out_type == KVQ_OUT_F16) return cudaLaunchKernelEx(&cfg, paged_chunk_kernel<VT, true>, p);
+    return cudaLaunchKernelEx(&cfg, paged_chunk_kernel<VT, false, LOSE>, p);
 }
 
 }  // namespace kvq

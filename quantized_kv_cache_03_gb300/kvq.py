@@ -39,7 +39,7 @@ EXPORTED = ("kvq_append", "kvq_decode_attn", "kvq_decode_workspace_size", "kvq_d
             "kvq_reset_wait_timeouts", "kvq_status_string", "kvq_debug_qk", "kvq_debug_lose_stage",
             "kvq_debug_plan", "kvq_layout_model_default", "kvq_layout_cost", "kvq_choose_layout")
 EXPORTED_PAGED = ("kvq_page_bytes", "kvq_page_tables", "kvq_paged_append", "kvq_paged_gather", "kvq_paged_attn",
-                  "kvq_paged_attn_workspace_size")
+                  "kvq_paged_attn_workspace_size", "kvq_debug_paged_lose_copy")
 OUT_F32 = 0    # type of computed values
 OUT_F16 = 1
 MAX_PAGED_SEQS = 4096
@@ -164,6 +164,8 @@ def load():
                                              c_void_p]
             lib.kvq_paged_attn.restype = c_int32
             lib.kvq_paged_attn.argtypes = [POINTER(KvqPagedDesc), c_void_p, c_size_t, c_void_p]
+            lib.kvq_debug_paged_lose_copy.restype = c_int32
+            lib.kvq_debug_paged_lose_copy.argtypes = [POINTER(KvqPagedDesc), c_int32, c_void_p, c_size_t, c_void_p]
             lib.kvq_paged_attn_workspace_size.restype = c_int32
             lib.kvq_paged_attn_workspace_size.argtypes = [POINTER(KvqPagedDesc), POINTER(c_size_t)]
             _lib = lib
@@ -741,3 +743,12 @@ def kvq_paged_attn(pool: PagePool, q16, q_start, max_q: int, seq_lens, block_tab
     if workspace is None and call._keep[-1] is not None and stream is not None:
         # the workspace made here goes back to torch now: not before `stream` is done with it
         call._keep[-1].record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+
+
+def kvq_debug_paged_lose_copy(call: PagedAttnCall, copy: int, stream=None) -> None:
+    """kvq_debug_paged_lose_copy test hook of include/kvq_paged.h, with the arguments of a prepared attention call."""
+    ws = call._keep[-1]
+    st = load().kvq_debug_paged_lose_copy(ctypes.byref(call.desc), copy, _ptr(ws), 0 if ws is None else ws.numel(),
+                                          _stream(stream))
+    if st:
+        raise KvqError(st, "kvq_debug_paged_lose_copy")

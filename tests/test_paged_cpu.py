@@ -182,3 +182,12 @@ def test_tile_record_is_a_bijection():
     for k, v, n in ((0, 0, 3328), (0, 1, 4352), (1, 0, 5248), (1, 1, 6272)):
         rows = split_tiles(np.zeros((2, n), np.uint8), k, v)
         assert sum(a[0].nbytes for a in rows.values()) == n
+
+
+def test_the_lost_copy_hook_refuses(lib):
+    def lose(copy=0, ot=0, pool=None, **over):
+        pg = _pages(**(pool or {}))
+        d = kvq.KvqPagedDesc(ctypes.pointer(pg), 0x20000, 512, 4, 8, 2, 4, 0x30000, 0x40000, 0x50000, 8, 8, 1, None, 0.1, ot, 0x60000, 0x70000)
+        return lib.kvq_debug_paged_lose_copy(ctypes.byref(d), copy, None, 0, None)
+    assert lose(copy=-1) == BAD and lose(pool=dict(n_pages=-1)) == BAD
+    assert lose(ot=1) == UNSUP and lose(pool=dict(v_type=1)) == UNSUP and lose(pool=dict(k_type=1)) == UNSUP
