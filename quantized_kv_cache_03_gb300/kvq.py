@@ -560,14 +560,19 @@ class _PreparedCall:
         # converted once: a call of a few microseconds' work is bound by its marshalling
         self._args = tuple(t(a) if isinstance(a, int) else a for t, a in zip(fn.argtypes, args))
 
-    def __call__(self, stream=None):
-        index = self._index
-        if index is not None and index != torch.cuda.current_device():
+    def _ready(self):
+        if self._index is None:
+            raise ValueError("%s: the tensors are on %s, not on a CUDA device" % (self.name, self.device))
+        if self._index != torch.cuda.current_device():
             raise ValueError("%s: the tensors are on %s, the current device is cuda:%d"
                              % (self.name, self.device, torch.cuda.current_device()))
+
+    def __call__(self, stream=None):
+        self._ready()
+        index = self._index
         if stream is not None:
             stream = _stream(stream)
-        elif index is not None:   # the handle without the Stream object of torch.cuda.current_stream() (3 us)
+        else:   # the handle without the Stream object of torch.cuda.current_stream() (3 us)
             stream = torch._C._cuda_getCurrentRawStream(index)
         st = self._fn(*self._args, stream)
         if st:
@@ -747,6 +752,7 @@ def kvq_paged_attn(pool: PagePool, q16, q_start, max_q: int, seq_lens, block_tab
 
 def kvq_debug_paged_lose_copy(call: PagedAttnCall, copy: int, stream=None) -> None:
     """kvq_debug_paged_lose_copy test hook of include/kvq_paged.h, with the arguments of a prepared attention call."""
+    call._ready()
     ws = call._keep[-1]
     st = load().kvq_debug_paged_lose_copy(ctypes.byref(call.desc), copy, _ptr(ws), 0 if ws is None else ws.numel(),
                                           _stream(stream))

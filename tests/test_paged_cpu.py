@@ -191,3 +191,24 @@ def test_the_lost_copy_hook_refuses(lib):
         return lib.kvq_debug_paged_lose_copy(ctypes.byref(d), copy, None, 0, None)
     assert lose(copy=-1) == BAD and lose(pool=dict(n_pages=-1)) == BAD
     assert lose(ot=1) == UNSUP and lose(pool=dict(v_type=1)) == UNSUP and lose(pool=dict(k_type=1)) == UNSUP
+
+
+def test_tensors_of_the_host_are_refused(monkeypatch):
+    """Calls over host tensors can be prepared (their checks need no GPU), but not made: no pointer of theirs reaches a kernel."""
+    pool = kvq.PagePool(4, 16, 2, kvq.V_Q4_0, data=torch.zeros(4 * 2 * 3328, dtype=torch.uint8))
+    k, s, o = torch.zeros((3, 2, 128), dtype=torch.float16), torch.zeros(3, dtype=torch.int32), torch.zeros((3, 2, 128))
+    one, q4, tab = torch.zeros(1, dtype=torch.int32), torch.zeros(4, dtype=torch.int32), torch.zeros((3, 4), dtype=torch.int32)
+    attn = kvq.PagedAttnCall(pool, torch.zeros((3, 4, 128), dtype=torch.float16), q4, 1, s, tab, True, 0.1, torch.zeros((3, 4, 128)),
+                             workspace=torch.zeros(8, dtype=torch.uint8))
+    calls = [kvq.PagedAppendCall(pool, k, k, s), kvq.PagedGatherCall(pool, s, o, o), attn,
+             kvq.PageTablesCall(16, 4, s, s, q4, one, tab, s, one, q4, s, s)]
+    reached = []
+    for c in calls:
+        monkeypatch.setattr(c, "_fn", lambda *a: reached.append(a) or 0)
+        with pytest.raises(ValueError, match="not on a CUDA device"):
+            c()
+        with pytest.raises(ValueError, match="not on a CUDA device"):
+            c(0)
+    with pytest.raises(ValueError, match="not on a CUDA device"):
+        kvq.kvq_debug_paged_lose_copy(attn, 0)
+    assert not reached
