@@ -548,6 +548,13 @@ def _rows_stride(t, name, heads, device):
     return t.stride(0) if t.shape[0] > 1 else heads * HEAD_DIM
 
 
+def _fits(**numbers):
+    """The library takes these as int32; ctypes would cut them off."""
+    for name, x in numbers.items():
+        if not -2 ** 31 <= x < 2 ** 31:
+            raise ValueError("%s = %d does not fit 32 bits" % (name, x))
+
+
 class _PreparedCall:
     """A library call with its arguments marshalled; stream: None = torch's
     current stream of the tensors' device, which must be the current device."""
@@ -585,6 +592,7 @@ class PagePool:
 
     def __init__(self, n_pages: int, page_tokens: int, n_kv_heads: int, v_type: int, k_type: int = K_I8,
                  head_dim: int = HEAD_DIM, device=None, data: torch.Tensor | None = None):
+        _fits(n_pages=n_pages, page_tokens=page_tokens, n_kv_heads=n_kv_heads, head_dim=head_dim, k_type=k_type, v_type=v_type)
         self.desc = KvqPages(n_pages, page_tokens, n_kv_heads, head_dim, k_type, v_type, None)
         self.n_pages, self.page_tokens, self.n_kv_heads = n_pages, page_tokens, n_kv_heads
         self.k_type, self.v_type = k_type, v_type
@@ -614,7 +622,9 @@ def _table(t, n_seqs, device):
     _check(t, "block_table", torch.int32, device, (n_seqs, None), contiguous=False)
     if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError("block_table: the entries of a row must be contiguous")
-    return (t.stride(0) if n_seqs > 1 else t.shape[1]), t.shape[1]
+    stride = t.stride(0) if n_seqs > 1 else t.shape[1]
+    _fits(n_seqs=n_seqs, max_blocks=t.shape[1], table_stride=stride)
+    return stride, t.shape[1]
 
 
 class PageTablesCall(_PreparedCall):
@@ -633,6 +643,7 @@ class PageTablesCall(_PreparedCall):
                               (q_start, "q_start", n + 1), (slots, "slots", None), (status, "status", n)):
             _check(t, what, torch.int32, dev, (size,))
         stride, cols = _table(block_table, n, dev)
+        _fits(page_tokens=page_tokens, n_pages=n_pages, n_tokens=slots.shape[0])
         self._keep = (lens, n_new, free_pages, n_free, block_table, lens_out, n_free_out, q_start, slots, status)
         self._bind(dev, n, page_tokens, n_pages, _ptr(lens), _ptr(n_new), _ptr(free_pages), _ptr(n_free),
                    _ptr(block_table), stride, cols, _ptr(lens_out), _ptr(n_free_out), _ptr(q_start), _ptr(slots),
@@ -658,6 +669,7 @@ class PagedAppendCall(_PreparedCall):
         stride = _rows_stride(k16, "k16", pool.n_kv_heads, pool.device)
         if _rows_stride(v16, "v16", pool.n_kv_heads, pool.device) != stride or k16.shape[0] != n or v16.shape[0] != n:
             raise ValueError("k16, v16 and slots must have one row per token and k16, v16 the same token stride")
+        _fits(n_tokens=n)
         self._keep = (pool, k16, v16, slots)
         self._bind(pool.device, ctypes.byref(pool.desc), _ptr(k16), _ptr(v16), stride, _ptr(slots), n)
 
@@ -684,6 +696,7 @@ class PagedGatherCall(_PreparedCall):
         ot = _out_type(k_out, "k_out")
         for t, what in ((k_out, "k_out"), (v_out, "v_out")):
             _check(t, what, k_out.dtype, pool.device, (n, pool.n_kv_heads, HEAD_DIM))
+        _fits(n_tokens=n)
         self._keep = (pool, slots, k_out, v_out)
         self._bind(pool.device, ctypes.byref(pool.desc), _ptr(slots), n, ot, _ptr(k_out), _ptr(v_out))
 
@@ -718,8 +731,13 @@ class PagedAttnCall(_PreparedCall):
             _check(lse, "lse", torch.float32, dev, (tokens, heads))
         if head_map is not None and len(head_map) != heads:
             raise ValueError("head_map must list a kv head for each query head")
+        max_q = int(max_q)
+        _fits(max_q=max_q, n_tokens=tokens, n_q_heads=heads)
+        if head_map is not None:
+            head_map = [int(h) for h in head_map]
+            _fits(**{"head_map[%d]" % i: h for i, h in enumerate(head_map)})
         hm = None if head_map is None else _i32(head_map)
-        self.desc = KvqPagedDesc(ctypes.pointer(pool.desc), q16.data_ptr(), stride, heads, tokens, n, int(max_q),
+        self.desc = KvqPagedDesc(ctypes.pointer(pool.desc), q16.data_ptr(), stride, heads, tokens, n, max_q,
                                  q_start.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), ts, cols,
                                  int(causal), None if hm is None else ctypes.cast(hm, POINTER(c_int32)),
                                  float(sm_scale), ot, out.data_ptr(), None if lse is None else lse.data_ptr())

@@ -212,3 +212,31 @@ def test_tensors_of_the_host_are_refused(monkeypatch):
     with pytest.raises(ValueError, match="not on a CUDA device"):
         kvq.kvq_debug_paged_lose_copy(attn, 0)
     assert not reached
+
+
+def test_numbers_past_32_bits_are_refused():
+    """ctypes cuts an int32 argument off: 2^32 + 16 would arrive as 16.  (Meta tensors have the shapes without the memory.)"""
+    def t(*shape, dt=torch.int32):
+        return torch.empty(shape, dtype=dt, device="meta")
+
+    big = 2 ** 32
+    with pytest.raises(ValueError, match="32 bits"):
+        kvq.PagePool(4, big + 16, 2, kvq.V_Q4_0, data=t(4 * 2 * 3328, dt=torch.uint8))
+    pool = kvq.PagePool(4, 16, 2, kvq.V_Q4_0, data=t(4 * 2 * 3328, dt=torch.uint8))
+    wide = torch.empty_strided((3, 4), (big + 4, 1), dtype=torch.int32, device="meta")
+    for page, table, slots in ((big + 16, t(3, 4), t(3)), (16, wide, t(3)), (16, t(3, 4), t(big + 3)), (16, t(3, big + 4), t(3))):
+        with pytest.raises(ValueError, match="32 bits"):
+            kvq.PageTablesCall(page, 4, t(3), t(3), t(4), t(1), table, t(3), t(1), t(4), slots, t(3))
+    kvq.PageTablesCall(16, 4, t(3), t(3), t(4), t(1), t(3, 4), t(3), t(1), t(4), t(3), t(3))
+    h = torch.float16
+    with pytest.raises(ValueError, match="32 bits"):
+        kvq.PagedAppendCall(pool, t(big + 3, 2, 128, dt=h), t(big + 3, 2, 128, dt=h), t(big + 3))
+    with pytest.raises(ValueError, match="32 bits"):
+        kvq.PagedGatherCall(pool, t(big + 3), t(big + 3, 2, 128, dt=h), t(big + 3, 2, 128, dt=h))
+    ok = dict(q16=t(5, 4, 128, dt=h), q_start=t(4), max_q=2, seq_lens=t(3), block_table=t(3, 4), causal=True, sm_scale=0.1,
+              out=t(5, 4, 128, dt=h), workspace=t(8, dt=torch.uint8))
+    kvq.PagedAttnCall(pool, **ok)
+    for over in (dict(max_q=big + 2), dict(block_table=wide), dict(head_map=[0, big, 1, 1]),
+                 dict(q16=t(big + 5, 4, 128, dt=h), out=t(big + 5, 4, 128, dt=h))):
+        with pytest.raises(ValueError, match="32 bits"):
+            kvq.PagedAttnCall(pool, **{**ok, **over})
