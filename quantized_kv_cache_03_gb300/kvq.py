@@ -559,6 +559,7 @@ class _PreparedCall:
     """A library call with its arguments marshalled; stream: None = torch's
     current stream of the tensors' device, which must be the current device."""
     name = ""
+    _own = None    # a workspace that the call allocated
 
     def _bind(self, device, *args):
         self.device = device
@@ -567,23 +568,38 @@ class _PreparedCall:
         # converted once: a call of a few microseconds' work is bound by its marshalling
         self._args = tuple(t(a) if isinstance(a, int) else a for t, a in zip(fn.argtypes, args))
 
-    def _ready(self):
+    def _handle(self, stream):
         if self._index is None:
             raise ValueError("%s: the tensors are on %s, not on a CUDA device" % (self.name, self.device))
         if self._index != torch.cuda.current_device():
             raise ValueError("%s: the tensors are on %s, the current device is cuda:%d"
                              % (self.name, self.device, torch.cuda.current_device()))
+        if stream is None:   # the handle without the Stream object of torch.cuda.current_stream() (3 us)
+            return torch._C._cuda_getCurrentRawStream(self._index)
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+    def _lend(self, handle):
+        """The own workspace, allocated on one stream, to another: torch may have given that memory away before, to work
+        still queued on the allocating stream, and may give it away again once this call is dropped."""
+        stream = _stream_object(handle, self.device)
+        with torch.cuda.stream(stream):
+            capturing = torch.cuda.is_current_stream_capturing()
+        self._own.record_stream(stream)
+        if not capturing:
+            stream.wait_event(self._own_ready)
+            self._own_streams.add(handle)
 
     def __call__(self, stream=None):
-        self._ready()
-        index = self._index
-        if stream is not None:
-            stream = _stream(stream)
-        else:   # the handle without the Stream object of torch.cuda.current_stream() (3 us)
-            stream = torch._C._cuda_getCurrentRawStream(index)
-        st = self._fn(*self._args, stream)
+        handle = self._handle(stream)
+        if self._own is not None and handle not in self._own_streams:
+            self._lend(handle)
+        st = self._fn(*self._args, handle)
         if st:
             raise KvqError(st, self.name)
+
+
+def _stream_object(handle, device):
+    return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
 
 
 class PagePool:
@@ -713,7 +729,11 @@ class PagedAttnCall(_PreparedCall):
     int32 [n_seqs][max_blocks] (rows may be strided); out fp32 or fp16
     [tokens][q heads][128]; lse fp32 [tokens][q heads] or None; workspace: a
     uint8 device tensor of workspace_size() bytes (None: one is allocated with
-    the call and kept with it; calls that may overlap need one each)."""
+    the call and kept with it; calls that may overlap need one each).  A call's
+    own workspace may be used on any stream: the first call on another stream
+    than it was allocated on waits for that one's work so far.  Not in a capture,
+    which cannot wait (torch.cuda.graph synchronizes before it begins); and a
+    graph needs the call kept for as long as it is replayed."""
     name = "kvq_paged_attn"
 
     def __init__(self, pool: PagePool, q16, q_start, max_q: int, seq_lens, block_table, causal: bool, sm_scale: float,
@@ -744,6 +764,11 @@ class PagedAttnCall(_PreparedCall):
         if workspace is None:
             size = self.workspace_size()
             workspace = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+            if size:
+                at = torch.cuda.current_stream(dev)
+                self._own, self._own_ready, self._own_streams = workspace, torch.cuda.Event(), {at.cuda_stream}
+                if not torch.cuda.is_current_stream_capturing():
+                    self._own_ready.record(at)
         else:
             _check(workspace, "workspace", torch.uint8, dev)
         self._keep = (pool, q16, q_start, seq_lens, block_table, out, lse, hm, workspace)
@@ -760,19 +785,21 @@ class PagedAttnCall(_PreparedCall):
 def kvq_paged_attn(pool: PagePool, q16, q_start, max_q: int, seq_lens, block_table, causal: bool, sm_scale: float, out,
                    lse=None, head_map=None, workspace=None, stream=None) -> None:
     """kvq_paged_attn of include/kvq_paged.h (arguments as PagedAttnCall)."""
-    call = PagedAttnCall(pool, q16, q_start, max_q, seq_lens, block_table, causal, sm_scale, out, lse, head_map,
-                         workspace)
-    call(stream)
-    if workspace is None and call._keep[-1] is not None and stream is not None:
-        # the workspace made here goes back to torch now: not before `stream` is done with it
-        call._keep[-1].record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    args = (pool, q16, q_start, max_q, seq_lens, block_table, causal, sm_scale, out, lse, head_map, workspace)
+    if stream is None or workspace is not None or pool.device.type != "cuda":
+        PagedAttnCall(*args)(stream)
+        return
+    # a workspace made here belongs to the stream that uses it
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    with torch.cuda.stream(_stream_object(handle, pool.device)):
+        PagedAttnCall(*args)(stream)
 
 
 def kvq_debug_paged_lose_copy(call: PagedAttnCall, copy: int, stream=None) -> None:
     """kvq_debug_paged_lose_copy test hook of include/kvq_paged.h, with the arguments of a prepared attention call."""
-    call._ready()
+    handle = call._handle(stream)
     ws = call._keep[-1]
     st = load().kvq_debug_paged_lose_copy(ctypes.byref(call.desc), copy, _ptr(ws), 0 if ws is None else ws.numel(),
-                                          _stream(stream))
+                                          handle)
     if st:
         raise KvqError(st, "kvq_debug_paged_lose_copy")
