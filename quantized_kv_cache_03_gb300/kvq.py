@@ -555,6 +555,11 @@ def _fits(**numbers):
             raise ValueError("%s = %d does not fit 32 bits" % (name, x))
 
 
+# The current stream's handle: torch's private call without the Stream object (3 us),
+# or, in a torch that has no such call, the public one.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _PreparedCall:
     """A library call with its arguments marshalled; stream: None = torch's
     current stream of the tensors' device, which must be the current device."""
@@ -574,8 +579,8 @@ class _PreparedCall:
         if self._index != torch.cuda.current_device():
             raise ValueError("%s: the tensors are on %s, the current device is cuda:%d"
                              % (self.name, self.device, torch.cuda.current_device()))
-        if stream is None:   # the handle without the Stream object of torch.cuda.current_stream() (3 us)
-            return torch._C._cuda_getCurrentRawStream(self._index)
+        if stream is None:
+            return _raw_stream(self._index)
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
     def _lend(self, handle):

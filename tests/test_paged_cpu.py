@@ -240,3 +240,14 @@ def test_numbers_past_32_bits_are_refused():
                  dict(q16=t(big + 5, 4, 128, dt=h), out=t(big + 5, 4, 128, dt=h))):
         with pytest.raises(ValueError, match="32 bits"):
             kvq.PagedAttnCall(pool, **{**ok, **over})
+
+
+def test_the_current_stream_without_torchs_private_call(monkeypatch):
+    """The binding imports and finds the stream in a torch that lacks the private name."""
+    import importlib.util
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    spec = importlib.util.spec_from_file_location("kvq_again", kvq.__file__)
+    again = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(again)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index: type("S", (), {"cuda_stream": 40 + index})())
+    assert again._raw_stream(2) == 42
