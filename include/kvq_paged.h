@@ -99,7 +99,7 @@ kvq_status kvq_page_bytes(const kvq_pages *p, size_t *bytes);
  *  slots        device int32 [n_tokens]: the slot of every row; rows no
  *               sequence owns get -1.
  *  n_tokens     host: rows of the packed batch, at least the sum of the
- *               positive n_new for every sequence to be served.
+ *               positive n_new for every sequence to be served; below 2^31 - 1.
  *  status       device int32 [n_seqs]: 0, or why nothing was added: 1 the pool
  *               has too few free pages, 2 the length would pass max_blocks pages or
  *               the rows would pass n_tokens.  Pages are granted in order of

@@ -312,7 +312,8 @@ kvq_status kvq_page_tables(int32_t n_seqs, int32_t page_tokens, int32_t n_pages,
                            int32_t table_stride, int32_t max_blocks, int32_t *lens_out, int32_t *n_free_out,
                            int32_t *q_start, int32_t *slots, int32_t n_tokens, int32_t *status, void *stream)
 {
-    if (n_seqs < 0 || n_seqs > KVQ_MAX_PAGED_SEQS || page_shift(page_tokens) < 0 || n_pages < 0 || n_tokens < 0)
+    // (row sums are held to INT_MAX, so that has to stay past n_tokens)
+    if (n_seqs < 0 || n_seqs > KVQ_MAX_PAGED_SEQS || page_shift(page_tokens) < 0 || n_pages < 0 || n_tokens < 0 || n_tokens == INT_MAX)
         return KVQ_ERR_INVALID_ARG;
     if ((long long)n_pages * page_tokens > INT_MAX || !table_ok(table_stride, max_blocks, page_tokens)) return KVQ_ERR_INVALID_ARG;
     if (!int_ptr(n_free) || !int_ptr(n_free_out) || !int_ptr(q_start)) return KVQ_ERR_INVALID_ARG;

@@ -251,3 +251,8 @@ def test_the_current_stream_without_torchs_private_call(monkeypatch):
     spec.loader.exec_module(again)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda index: type("S", (), {"cuda_stream": 40 + index})())
     assert again._raw_stream(2) == 42
+
+
+def test_tables_refuse_as_many_rows_as_row_sums_are_held_to(lib):
+    """Sums past 2^31 - 1 stay there, so a batch of that many rows could not tell them from a fit."""
+    assert _tables(lib, n_tokens=2 ** 31 - 1) == BAD
