@@ -108,10 +108,12 @@ kvq_status kvq_page_bytes(const kvq_pages *p, size_t *bytes);
  *               is not served keeps its length, and its rows get slot -1.
  * Lengths below 0 count as 0 and above max_blocks * page_tokens as that;
  * *n_free is held to [0, n_pages].  A new token whose page entry lies outside
- * [0, n_pages) gets slot -1.  A page given back twice is the caller's error;
- * pushes past n_pages entries are dropped.
- * One launch, two for more than 16384 rows.  The pages of the method's description leave paging as future work
- * (BitLLM summary, limits); the interface is the library's own.
+ * [0, n_pages) gets slot -1.  Pushes past n_pages entries are dropped.
+ * Entries are given back as they stand in the table and handed out again: a
+ * sequence to be ended must list only pages that are its own to give, none that
+ * another sequence still lists (a shared prefix), none twice, and no entry
+ * outside [0, n_pages) (a hidden page).
+ * One launch, two for more than 16384 rows.
  */
 kvq_status kvq_page_tables(int32_t n_seqs, int32_t page_tokens, int32_t n_pages, const int32_t *lens,
                            const int32_t *n_new, int32_t *free_pages, const int32_t *n_free,
@@ -211,7 +213,9 @@ typedef struct kvq_paged_desc {
  * inputs give the same bits.  Sequences go to a kernel by their rows per kv
  * head (up to 8, up to 32, more), each kind in a launch of its own; where n_seqs *
  * max_q == n_tokens says that all have max_q rows (at most 32 per kv head, or a
- * single sequence), one launch takes them all, whatever q_start holds.
+ * single sequence), one launch takes them all, whatever q_start holds.  A decode
+ * step in buffers for more (64 single tokens, n_tokens 4096, max_q 512) takes 5 to
+ * 6 us longer than with max_q 1, for the launches that find nothing to do.
  *  workspace   device, 256-byte aligned, kvq_paged_attn_workspace_size() bytes.
  *              Its contents need no preparation and mean nothing after the
  *              call; calls that may overlap on the GPU need one each.

@@ -30,10 +30,11 @@
 // Both outputs sum a stage's P.V from zero and add it in fp32: the MMA's own
 // running sum cuts off where fp32 rounds (error against 64 bits on the first batch
 // below 4.7e-6 instead of 5e-7).
-// Measured: 64 sequences of 1024 to 32768 positions, 4 rows, q8_0 V: 375 us, 0.91
+// Measured: 64 sequences of 1024 to 32768 positions, 4 rows, q8_0 V: 375 us (F16 K
+// 508, 0.97 of the bytes' time), 0.91
 // of the bytes' time at the measured copy rate; one of 131072 positions, 5 rows,
 // q4_0: 48 us (0.67: prologue, merge and combine are a third of it); 16 of 32768,
-// 32 rows, fp32 output: 411 us (0.31: 920 instructions per 16 rows and 32
+// 32 rows, fp32 output: 413 us (0.31: 920 instructions per 16 rows and 32
 // positions at 46 % issue, two warps per scheduler).
 // Softmax in base 2.  A row's reference maximum is raised only when a score
 // passes it by more than kSlack = 1, and exponents are taken `shift` above it,
@@ -79,7 +80,7 @@ struct PagedCfg {
 // Three CTAs of 8-row tiles per SM, two of 16-row tiles: with a warp more per
 // scheduler the accumulators and fragments spill or are loaded too late to
 // overlap (131072 positions, 5 rows: 48 us at three, 53 at four, 49 at two;
-// 16 sequences of 32 rows: 419 us at two, 442 at three).
+// 16 sequences of 32 rows, as it was then: 419 us at two, 442 at three).
 // LOSE: the test flavour; CTA 0's warp 0 leaves out its copy stage p.lose.
 template <int NT, int VT, int KT, bool O16, bool LOSE = false>
 __global__ void __launch_bounds__(128, NT == 1 ? 3 : 2) paged_attn_kernel(const __grid_constant__ PagedAttnParams p)

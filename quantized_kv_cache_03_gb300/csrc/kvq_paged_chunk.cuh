@@ -41,7 +41,7 @@
 // us, every 4 592; a mixed batch 298 and 301).
 // Measured: that chunk, 32 heads on 8 kv heads, q4_0 V, fp16 output, takes 450 us
 // (606 TFLOP/s counted as four times head_dim per visible pair of position and
-// head), fp32 output 592.  The tensor pipe is active 56 % of the time; the K
+// head), fp32 output 584.  The tensor pipe is active 56 % of the time; the K
 // converters are busy 80 % of it, the softmax two thirds (fp32 output: four
 // fifths), and the tile's chain QK, maximum, exponents, P.V hides only as far as
 // two tiles of S in tensor memory allow.  Shared memory moves at 40 % of its rate.
@@ -136,8 +136,7 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32])
 
 // mbar_wait of a thread that runs alone: a loop of three instructions (the
 // general one, inside a branch that one lane takes, slowed the MMA threads:
-// 503 against 491 us on the chunk named above, 562 against 515 us on the
-// verify shape).
+// 503 against 491 us on the chunk named above, as it was then).
 template <uint32_t SPINS>
 __device__ __forceinline__ bool mbar_wait_alone(uint32_t bar, uint32_t parity)
 {
