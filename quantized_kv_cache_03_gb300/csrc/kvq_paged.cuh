@@ -190,7 +190,7 @@ constexpr int kStagePos = 32;           // positions per work unit ("stage")
 constexpr int kChunkRows = 128;         // the chunk kernel: query rows per tile,
 constexpr int kChunkPositions = 128;    // positions per tile,
 constexpr int kChunkMinTiles = 3;       // and the least piece in tiles
-constexpr int kChunkSums = kChunkRows * (kD + 1);   // fp32: a row tile's sums and their zero points
+constexpr int kChunkSums = kChunkRows * kD;   // fp32: a row tile's sums
 constexpr int kPagedMinStages = 4;      // a CTA's least piece of the line: one stage per warp
 
 // A query-row tile of one kv head that several CTAs attend: what the combine

@@ -34,14 +34,16 @@
 // The MMA cuts its sums off where fp32 would round them, so O falls short by
 // 1e-9 to 5e-9 of itself per position (fp32 output, whose P.V takes three MMAs
 // per 16 positions: 4.5e-5 after 32768, 1.7e-4 after 131072).  So every kCFlush
-// tiles O is added to sums in memory, in fp32, and starts again from zero: 2e-6
-// for any length with fp32 output (every 8 tiles 3.5e-6), 4e-5 with fp16 output,
-// whose own rounding is up to 4.9e-4.  It costs 1 to 3 us each time (512-token
-// chunk over 32768 positions, fp16: 466 -> 475 us; fp32 output, every 8 tiles 557
-// us, every 4 592; a mixed batch 298 and 301).
-// Measured: that chunk, 32 heads on 8 kv heads, q4_0 V, fp16 output, takes 450 us
-// (606 TFLOP/s counted as four times head_dim per visible pair of position and
-// head), fp32 output 584.  The tensor pipe is active 56 % of the time; the K
+// tiles O joins sums in memory, in fp32, and starts again from zero.  Each softmax
+// group has half of the columns: the group of the last tile does it while the
+// other one makes the next P, and that one before it hands P over.  fp32 output,
+// every 2 tiles: 1.3e-6 of the result's norm on a mixed batch (every 4 2.0e-6,
+// every 8 3.4e-6; the same in PyTorch 1.4e-6), 321 us for it (309 every 4) and 620
+// for the chunk named above (566); fp16 output, whose own rounding is 2e-4, every
+// 64.  (One group for all columns, before its P: 319 and 669 us every 2.)
+// Measured: that chunk, 32 heads on 8 kv heads, q4_0 V, fp16 output, takes 443 us
+// (615 TFLOP/s counted as four times head_dim per visible pair of position and
+// head), fp32 output 620.  The tensor pipe is active 56 % of the time; the K
 // converters are busy 80 % of it, the softmax two thirds (fp32 output: four
 // fifths), and the tile's chain QK, maximum, exponents, P.V hides only as far as
 // two tiles of S in tensor memory allow.  Shared memory moves at 40 % of its rate.
@@ -76,9 +78,9 @@ __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.a
 constexpr int kCPieces = 4;              // piece records in flight
 constexpr float kCShift = 8.0f, kCSlack = 6.0f;
 // Tiles after which O is added to the rows' fp32 sums in memory and started
-// afresh (even, so that one softmax group does it throughout a piece).
+// afresh.
 template <bool O16>
-constexpr int kCFlush = O16 ? 64 : 4;
+constexpr int kCFlush = O16 ? 64 : 2;
 
 template <int VT>
 struct ChunkCfg {
@@ -96,7 +98,8 @@ struct ChunkCfg {
                          RAWK_OFF = VL_OFF + 2 * VBUF, RAWV_OFF = RAWK_OFF + RSK * RAWK;
     static constexpr int XM_OFF = RAWV_OFF + RSV * RAWV;              // fp32 [group][128]: a tile's m
     static constexpr int XE_OFF = XM_OFF + 2 * kCM * 4;             // float2 [group][128]: m, l at the end of a piece
-    static constexpr int REC_OFF = XE_OFF + 2 * kCM * 8;            // int [RSK], [RSV]: sub-tiles with a page
+    static constexpr int XS_OFF = XE_OFF + 2 * kCM * 8;             // float2 [group][128]: zero points of the sums, and of the O that joins them next
+    static constexpr int REC_OFF = XS_OFF + 2 * kCM * 8;            // int [RSK], [RSV]: sub-tiles with a page
     static constexpr int OREC_OFF = REC_OFF + 48;                   // int [4 tiles][half]: the same, for the softmax
     static constexpr int PIECE_OFF = OREC_OFF + 32;                 // ChunkWalk [kCPieces], 64 bytes each
     static constexpr int BAR_OFF = PIECE_OFF + kCPieces * 64;
@@ -105,8 +108,8 @@ struct ChunkCfg {
                          B_PIECE = B_FIN + 2,                                               // one arrival: -, [i], [i], [g][i], -, -, and
                          B_M = B_PIECE + kCPieces, B_END = B_M + 8,                         // [g][q]
                          B_SFULL = B_END + 8,                                               // two, the QK thread and its commit: [g][i]
-                         B_PREADY = B_SFULL + 4, B_KR = B_PREADY + 4, B_RAWKF = B_KR + 2,   // four warps: [g][i], [i], K ring
-                         B_VR = B_RAWKF + RSK, B_QR = B_VR + 2, B_RAWVF = B_QR + 1,         // eight warps: [i], -, V ring
+                         B_PREADY = B_SFULL + 4, B_KR = B_PREADY + 4, B_RAWKF = B_KR + 2,   // four warps: [g][i], [i], K ring, -
+                         B_OFREE = B_RAWKF + RSK, B_VR = B_OFREE + 1, B_QR = B_VR + 2, B_RAWVF = B_QR + 1,   // eight warps: [i], -, V ring
                          B_PFREE = B_RAWVF + RSV, NBAR = B_PFREE + kCPieces;                  // all 23 roles
     static constexpr int MISC_OFF = BAR_OFF + NBAR * 8;             // TMEM base, bad flag
     static constexpr int SMEM = MISC_OFF + 16;
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
     } else if (warp == kCQk || warp == kCPv) {
         // ================= MMAs: one thread each =================
         if (elect_one()) {
-            int j = 0, piece = 0;   // tiles, and pieces with any, so far
+            int j = 0, piece = 0, joins = 0;   // tiles, pieces with any, and starts of O from zero within pieces so far
             if (warp == kCQk) {
                 uint64_t dKH[2], dKL[2];
 #pragma unroll
@@ -467,6 +470,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                 pieces(true, [&](const ChunkWalk &w, int) {
                     for (int k = 0; k < w.tiles; ++k, ++j) {
                         const int g = j & 1;
+                        // O starts from zero: the group of this tile has read its half of it (it says P is ready
+                        // after that), the other group says so here
+                        if (k > 0 && k % kCFlush<O16> == 0 && !wait1(C::B_OFREE, joins++ & 1)) return false;
 #pragma unroll 1
                         for (int i = 0; i < 2; ++i) {
                             if (!wait1(C::B_VR + i, j & 1) || !wait1(C::B_PREADY + 2 * g + i, (j >> 1) & 1)) return false;
@@ -617,11 +623,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
         const uint32_t tSg = tS + lane_base + kCN * grp;
         float *xm = reinterpret_cast<float *>(smem + C::XM_OFF);
         float2 *xe = reinterpret_cast<float2 *>(smem + C::XE_OFF);
+        float2 *xs = reinterpret_cast<float2 *>(smem + C::XS_OFF) + grp * kCM + row;   // .x: the sums' zero point, .y: that of the O to join them
         // the scale's sign is in Q; a scale of 0 stays finite times -inf
         const float cs = fmaxf(fabsf(p.qk_scale_log2), 1e-30f);
-        // the rows' sums in memory, [dims / 4][row], and their zero points
-        auto sums = [&]() { return reinterpret_cast<float4 *>(p.sums + (size_t)blockIdx.x * kChunkSums) + row; };
-        auto sums_m = [&]() { return p.sums + (size_t)blockIdx.x * kChunkSums + kCM * kD + row; };
+        // the row's sums in memory, [dims / 4][row]: this group's half of them, which no other thread touches
+        auto sums = [&]() { return reinterpret_cast<float4 *>(p.sums + (size_t)blockIdx.x * kChunkSums) + (kD / 8) * grp * kCM + row; };
         int j = 0, ends = 0;
         bool lost = false;
         pieces(false, [&](const ChunkWalk &w, int) {
@@ -673,6 +679,46 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                 const bool idle_warp = 32 * quarter >= w.R;   // no row here: keep the barriers in step
 
                 const int j1 = j + w.tiles, j0 = j;
+                uint32_t a[2][32];
+                // This group's half of O, complete with tile t, joins the sums.
+                auto join = [&](int t) {
+                    float beta = 0.f;
+                    const float2 z = *xs;
+                    if (t + 1 - j0 > kCFlush<O16>) {   // there are sums
+                        beta = z.x == -INFINITY ? 0.f : fast_exp2(z.x - z.y);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float4 y = __ldcg(sums() + k * kCM);
+                            uint32_t(&v)[32] = a[k >> 3];
+                            v[4 * (k & 7)] = __float_as_uint(y.x);
+                            v[4 * (k & 7) + 1] = __float_as_uint(y.y);
+                            v[4 * (k & 7) + 2] = __float_as_uint(y.z);
+                            v[4 * (k & 7) + 3] = __float_as_uint(y.w);
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 64; ++k) a[k >> 5][k & 31] = 0u;
+                    }
+                    xs->x = z.y;
+                    if (!wwait(C::B_PVD + 2 * (t & 1) + 1, (t >> 1) & 1)) return false;
+                    tc_fence_after();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t o[16];
+                        tmem_ld16(tO + lane_base + (kD / 2) * grp + 16 * q, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t *v = &a[q >> 1][16 * (q & 1) + 4 * k];
+                            __stcg(sums() + (4 * q + k) * kCM,
+                                   make_float4(fmaf(__uint_as_float(v[0]), beta, __uint_as_float(o[4 * k])), fmaf(__uint_as_float(v[1]), beta, __uint_as_float(o[4 * k + 1])),
+                                               fmaf(__uint_as_float(v[2]), beta, __uint_as_float(o[4 * k + 2])), fmaf(__uint_as_float(v[3]), beta, __uint_as_float(o[4 * k + 3]))));
+                        }
+                    }
+                    tc_fence_before();
+                    return true;
+                };
+                auto restarts = [&](int t) { return t > j0 && t < j1 && (t - j0) % kCFlush<O16> == 0; };   // O, with P.V(t)
                 for (; j < j1; ++j) {
                     if ((j & 1) != grp) continue;   // the other group's tile
                     const uint32_t ph = (j >> 1) & 1;
@@ -686,6 +732,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                             mbar_arrive(bar(C::B_PREADY + 2 * grp));
                             mbar_arrive(bar(C::B_PREADY + 2 * grp + 1));
                         }
+                        if (restarts(j + 1)) {   // (after P.V(j), as the warps with rows: one arrival each per phase)
+                            if (!wwait(C::B_PVD + 2 * grp + 1, ph)) {
+                                lost = true;
+                                break;
+                            }
+                            if (lane == 0) mbar_arrive(bar(C::B_OFREE));
+                        }
                         continue;
                     }
                     const int x = (w.s0 + j - j0) * kCN;
@@ -694,7 +747,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                     // (loops are not unrolled beyond a pair of chunks: with every role's code
                     // unrolled the warps waited for instructions)
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    uint32_t a[2][32];
 #pragma unroll 1
                     for (int i = 0; i < 2; ++i) {
                         if (!wwait(C::B_SFULL + 2 * grp + i, ph)) {
@@ -746,78 +798,28 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                     const bool need = mx > mp + (kCShift + kCSlack);
                     const float mn = need ? mx - kCShift : mp;
                     xm[grp * kCM + row] = mn;
+                    xs->y = restarts(j) ? mp : mn;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(C::B_M + 4 * grp + quarter));
                     if (mn != m) {   // raised by either group since this group's last tile
                         l *= m == -INFINITY ? 0.f : fast_exp2(m - mn);
                         m = mn;
                     }
-                    const bool flush = j > j0 && (j - j0) % kCFlush<O16> == 0;
-                    if (j > j0 && (flush || __any_sync(0xffffffffu, need))) {   // O is stable once P.V(j - 1) is done
+                    if (!restarts(j) && j > j0 && __any_sync(0xffffffffu, need)) {   // O to the new zero point, once P.V(j - 1) is done
                         const float alpha = need ? (mp == -INFINITY ? 0.f : fast_exp2(mp - mn)) : 1.f;
-                        float4 *sums = reinterpret_cast<float4 *>(p.sums + (size_t)blockIdx.x * kChunkSums) + row;
-                        float *sums_m = p.sums + (size_t)blockIdx.x * kChunkSums + kCM * kD + row;
-                        float beta = 0.f;
-                        // half of the row's sums into the registers that the second pass will use
-                        auto sums_in = [&](int h) {
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                const float4 y = __ldcg(sums + (16 * h + k) * kCM);
-                                uint32_t(&v)[32] = a[k >> 3];
-                                v[4 * (k & 7)] = __float_as_uint(y.x);
-                                v[4 * (k & 7) + 1] = __float_as_uint(y.y);
-                                v[4 * (k & 7) + 2] = __float_as_uint(y.z);
-                                v[4 * (k & 7) + 3] = __float_as_uint(y.w);
-                            }
-                        };
-                        if (flush) {
-                            tmem_wait_ld32(a[0]);
-                            if (j - j0 > kCFlush<O16>) {   // there are sums
-                                const float ms = __ldcg(sums_m);
-                                beta = ms == -INFINITY ? 0.f : fast_exp2(ms - m);
-                                sums_in(0);
-                            } else {
-#pragma unroll
-                                for (int k = 0; k < 64; ++k) a[k >> 5][k & 31] = 0u;
-                            }
-                        }
                         if (!wwait(C::B_PVD + 2 * (grp ^ 1) + 1, ((j - 1) >> 1) & 1)) {
                             lost = true;
                             break;
                         }
                         tc_fence_after();
-                        if (flush) {   // O joins the sums, P.V(j) starts from zero
 #pragma unroll 1
-                            for (int h = 0; h < 2; ++h) {
-                                if (h == 1 && j - j0 > kCFlush<O16>) sums_in(1);
+                        for (int c0 = 0; c0 < kD; c0 += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(tO + lane_base + c0, o);
+                            tmem_wait_ld();
 #pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    uint32_t o[16];
-                                    tmem_ld16(tO + lane_base + 64 * h + 16 * q, o);
-                                    tmem_wait_ld();
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k) {
-                                        const uint32_t *v = &a[q >> 1][16 * (q & 1) + 4 * k];
-                                        __stcg(sums + (16 * h + 4 * q + k) * kCM,
-                                               make_float4(fmaf(__uint_as_float(v[0]), beta, __uint_as_float(o[4 * k]) * alpha),
-                                                           fmaf(__uint_as_float(v[1]), beta, __uint_as_float(o[4 * k + 1]) * alpha),
-                                                           fmaf(__uint_as_float(v[2]), beta, __uint_as_float(o[4 * k + 2]) * alpha),
-                                                           fmaf(__uint_as_float(v[3]), beta, __uint_as_float(o[4 * k + 3]) * alpha)));
-                                    }
-                                }
-                            }
-                            __stcg(sums_m, m);
-                            tmem_ld32(tSg, a[0]);
-                        } else {       // O to the new zero point
-#pragma unroll 1
-                            for (int c0 = 0; c0 < kD; c0 += 16) {
-                                uint32_t o[16];
-                                tmem_ld16(tO + lane_base + c0, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                                tmem_st16(tO + lane_base + c0, o);
-                            }
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                            tmem_st16(tO + lane_base + c0, o);
                         }
                     }
 
@@ -850,16 +852,30 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                         tmem_wait_st();   // a half is whole
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(C::B_PREADY + 2 * grp + (c0 ? 1 : 0)));
+                        if (lane == 0 && !restarts(j)) mbar_arrive(bar(C::B_PREADY + 2 * grp + (c0 ? 1 : 0)));
                     }
-                    if (lost) break;
                     const float2 s2 = add2(sum[0], sum[1]);
                     l += s2.x + s2.y;
+                    // ---- O starts from zero with the P.V of this tile or of the next: its half joins the sums ----
+                    if (restarts(j) || restarts(j + 1)) {
+                        if (!join(restarts(j) ? j - 1 : j)) {
+                            lost = true;
+                            break;
+                        }
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (restarts(j)) {
+                                mbar_arrive(bar(C::B_PREADY + 2 * grp));
+                                mbar_arrive(bar(C::B_PREADY + 2 * grp + 1));
+                            } else {
+                                mbar_arrive(bar(C::B_OFREE));
+                            }
+                        }
+                    }
                 }
                 // ---- the end of the piece: both groups' sums, and P.V done ----
                 if (!lost) {
                     xe[grp * kCM + row] = make_float2(m, l);
-                    if (w.tiles > kCFlush<O16>) __threadfence();   // the sums, which both groups read now
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(C::B_END + 4 * grp + quarter));
                     if (!wwait(C::B_END + 4 * (grp ^ 1) + quarter, ends & 1) || !wwait(C::B_PVD + 2 * ((j - 1) & 1) + 1, ((j - 1) >> 1) & 1)) lost = true;
@@ -883,10 +899,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
             const size_t part = ((size_t)blockIdx.x * 2 + max(0, w.slot)) * kCM + row, orow = (size_t)(w.t0 + tok) * p.n_q_heads + head;
             const bool have_o = w.tiles > 0 && !lost, have_sums = have_o && w.tiles > kCFlush<O16>;
             float fs = 0.f;
-            if (have_sums) {
-                const float msum = __ldcg(sums_m());
-                fs = any && msum != -INFINITY ? f * fast_exp2(msum - m) : 0.f;
-            }
+            if (have_sums) fs = any && xs->x != -INFINITY ? f * fast_exp2(xs->x - m) : 0.f;
 #pragma unroll 1
             for (int c0 = (kD / 2) * grp; c0 < (kD / 2) * (grp + 1); c0 += 16) {
                 uint32_t o[16];
@@ -904,7 +917,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const __g
                 if (have_sums)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const float4 s = __ldcg(sums() + (c0 / 4 + k) * kCM);
+                        const float4 s = __ldcg(sums() + ((c0 - (kD / 2) * grp) / 4 + k) * kCM);
                         y[4 * k] = fmaf(s.x, fs, y[4 * k]);
                         y[4 * k + 1] = fmaf(s.y, fs, y[4 * k + 1]);
                         y[4 * k + 2] = fmaf(s.z, fs, y[4 * k + 2]);
