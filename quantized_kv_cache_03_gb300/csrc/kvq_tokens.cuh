@@ -1,0 +1,86 @@
+// kvq_tokens.cuh -- launch parameters and device helpers of the calls around the
+// paged cache's append and attention (include/kvq_tokens.h).
+#pragma once
+
+#include "kvq_paged.cuh"
+#include "kvq_tokens.h"
+
+namespace kvq {
+
+struct RopeDesc {
+    const unsigned long long *turns;   // [n_rot / 2]
+    int n_rot;                         // 0: no rotation
+    int pairs;                         // KVQ_ROPE_PAIRS
+    float amplitude;
+};
+
+// cos and sin of position * rate, both times amplitude.  The product of the
+// position and the rate (parts of a turn, 2^-64) wraps at full turns; its top
+// 32 bits as a signed number are the angle in (-1, 1) half turns, exact to
+// 2^-32 of a turn and rounded to 24 bits: 1.9e-7 rad at most.
+__device__ __forceinline__ float2 angle_of(unsigned long long rate, int pos, float amplitude)
+{
+    const unsigned long long t = rate * (unsigned long long)(long long)pos;
+    float s, c;
+    sincospif((float)(int)(t >> 32) * 0x1p-31f, &s, &c);
+    return make_float2(c * amplitude, s * amplitude);
+}
+
+struct PositionsParams {
+    const int *q_start, *lens;
+    int *positions;
+    int n_seqs, n_tokens;
+};
+
+struct QkvParams {
+    PoolDesc pool;              // keys and values into pages, if `paged`
+    RopeDesc rope;
+    const uint16_t *q, *k, *v;
+    long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+    uint16_t *q_out, *k_out;
+    const float *q_norm, *k_norm;   // may be null
+    const int *positions, *slots;   // slots may be null
+    float eps;
+    int n_tokens, n_q_heads, n_kv_heads;
+    int paged;
+    int kv_heads, kv_chunks;    // heads of a warp that fills pages, and such pieces of a token's kv heads
+    int kv_blocks;              // the blocks that fill pages come first
+    int row_heads, row_chunks;  // the same of rows that stay fp16
+};
+
+struct ForkParams {
+    const int *lens, *parent, *keep, *table, *n_free;
+    int *table_out, *lens_out, *free_pages, *n_free_out, *copy_from, *copy_to, *copy_held, *status;
+    uint8_t *old_mark, *full_mark, *tail_mark;   // [n_pages]: listed by an old row, by a new one as a whole page, as its last one in part
+    int *owner;                 // [n_pages], of pages with a tail mark: the first place that ends in it
+    int *kept, *tail;           // [n_seqs]: positions kept; the entry of the last page where it is kept in part
+    int *counts;                // pages given back by each CTA's share of the pool
+    int n_seqs, pshift, n_pages, stride, out_stride, max_blocks;
+};
+
+struct CopyParams {
+    uint8_t *data[KVQ_MAX_COPY_POOLS];
+    uint16_t heads[KVQ_MAX_COPY_POOLS], tile_bytes[KVQ_MAX_COPY_POOLS];
+    const int *from, *to, *held;
+    int n_pools, n_copies, n_pages, most_heads, tiles;
+};
+
+struct MoveParams {
+    PoolDesc pool;
+    RopeDesc rope;
+    const int *from, *to, *turn;   // turn: null without a rotation
+    int n_tokens;
+    int heads, chunks;             // kv heads of a warp, and such pieces of a token's
+    uint8_t *rows;                 // staged: [n_tokens][kv heads] rows of a tile's bytes / 16
+};
+
+constexpr int kForkCtas = 8, kForkThreads = 512;
+
+cudaError_t launch_positions(const PositionsParams &p, cudaStream_t s, bool pdl);
+cudaError_t launch_qkv(const QkvParams &p, int v_type, int k_type, int n_sms, cudaStream_t s, bool pdl);
+cudaError_t launch_page_fork(const ForkParams &p, cudaStream_t s, bool pdl);
+cudaError_t launch_page_copy(const CopyParams &p, cudaStream_t s, bool pdl);
+// rows null: from slots to slots; else through them.
+cudaError_t launch_paged_move(const MoveParams &p, int v_type, int k_type, int n_sms, cudaStream_t s, bool pdl);
+
+}  // namespace kvq

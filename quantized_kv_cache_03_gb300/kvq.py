@@ -1,5 +1,6 @@
-"""ctypes binding of libkvq.so (include/kvq.h, and include/kvq_paged.h for the
-paged cache): argument marshalling only.
+"""ctypes binding of libkvq.so (include/kvq.h, include/kvq_paged.h for the paged
+cache, include/kvq_tokens.h for what surrounds its calls): argument marshalling
+only.
 
 Every step of the decode path runs in the library's CUDA kernels; torch only
 provides device memory and the stream handle.  Importing this module does not
@@ -40,10 +41,20 @@ EXPORTED = ("kvq_append", "kvq_decode_attn", "kvq_decode_workspace_size", "kvq_d
             "kvq_debug_plan", "kvq_layout_model_default", "kvq_layout_cost", "kvq_choose_layout")
 EXPORTED_PAGED = ("kvq_page_bytes", "kvq_page_tables", "kvq_paged_append", "kvq_paged_gather", "kvq_paged_attn",
                   "kvq_paged_attn_workspace_size", "kvq_debug_paged_lose_copy")
+EXPORTED_TOKENS = ("kvq_rope_turns", "kvq_page_positions", "kvq_qkv", "kvq_page_fork", "kvq_page_fork_workspace_size",
+                   "kvq_page_copy", "kvq_paged_move", "kvq_paged_move_workspace_size")
 OUT_F32 = 0    # type of computed values
 OUT_F16 = 1
 MAX_PAGED_SEQS = 4096
 PAGE_RELEASE = -1
+MAX_COPY_POOLS = 128
+ROPE_HALF = 0       # pair i of a rotation: values i and i + n_rot/2
+ROPE_PAIRS = 1      # values 2i and 2i + 1
+ROPE_PLAIN = 0      # how a rotation's rates are stretched (kvq_rope_turns)
+ROPE_LINEAR = 1
+ROPE_BASE = 2
+ROPE_BY_INDEX = 3
+ROPE_BY_TURNS = 4
 MAX_CALLS = 16
 MAX_T_Q = 4096
 MAX_T_Q_APPEND = 8
@@ -89,6 +100,18 @@ class KvqPagedDesc(ctypes.Structure):
                 ("seq_lens", c_void_p), ("block_table", c_void_p), ("table_stride", c_int32),
                 ("max_blocks", c_int32), ("causal", c_int32), ("head_map", POINTER(c_int32)), ("sm_scale", c_float),
                 ("out_type", c_int32), ("out", c_void_p), ("lse", c_void_p)]
+
+
+class KvqRope(ctypes.Structure):
+    _fields_ = [("turns", c_void_p), ("n_rot", c_int32), ("layout", c_int32), ("amplitude", c_float)]
+
+
+class KvqQkvDesc(ctypes.Structure):
+    _fields_ = [("q16", c_void_p), ("k16", c_void_p), ("v16", c_void_p), ("q_stride", c_int64), ("k_stride", c_int64),
+                ("v_stride", c_int64), ("n_tokens", c_int32), ("n_q_heads", c_int32), ("n_kv_heads", c_int32),
+                ("eps", c_float), ("q_norm", c_void_p), ("k_norm", c_void_p), ("rope", POINTER(KvqRope)),
+                ("positions", c_void_p), ("q_out", c_void_p), ("q_out_stride", c_int64), ("pages", POINTER(KvqPages)),
+                ("slots", c_void_p), ("k_out", c_void_p), ("k_out_stride", c_int64)]
 
 
 class KvqError(RuntimeError):
@@ -168,6 +191,26 @@ def load():
             lib.kvq_debug_paged_lose_copy.argtypes = [POINTER(KvqPagedDesc), c_int32, c_void_p, c_size_t, c_void_p]
             lib.kvq_paged_attn_workspace_size.restype = c_int32
             lib.kvq_paged_attn_workspace_size.argtypes = [POINTER(KvqPagedDesc), POINTER(c_size_t)]
+            f64 = ctypes.c_double
+            lib.kvq_rope_turns.restype = c_int32
+            lib.kvq_rope_turns.argtypes = [c_int32, f64, c_int32, f64, f64, f64, f64, POINTER(ctypes.c_uint64), POINTER(c_float)]
+            lib.kvq_page_positions.restype = c_int32
+            lib.kvq_page_positions.argtypes = [c_int32, c_void_p, c_void_p, c_int32, c_void_p, c_void_p]
+            lib.kvq_qkv.restype = c_int32
+            lib.kvq_qkv.argtypes = [POINTER(KvqQkvDesc), c_void_p]
+            lib.kvq_page_fork.restype = c_int32
+            lib.kvq_page_fork.argtypes = [c_int32, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32,
+                                          c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                          c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]
+            lib.kvq_page_fork_workspace_size.restype = c_int32
+            lib.kvq_page_fork_workspace_size.argtypes = [c_int32, c_int32, POINTER(c_size_t)]
+            lib.kvq_page_copy.restype = c_int32
+            lib.kvq_page_copy.argtypes = [POINTER(KvqPages), c_int32, c_void_p, c_void_p, c_void_p, c_int32, c_void_p]
+            lib.kvq_paged_move.restype = c_int32
+            lib.kvq_paged_move.argtypes = [POINTER(KvqPages), c_void_p, c_void_p, c_int32, POINTER(KvqRope), c_void_p, c_int32,
+                                           c_void_p, c_size_t, c_void_p]
+            lib.kvq_paged_move_workspace_size.restype = c_int32
+            lib.kvq_paged_move_workspace_size.argtypes = [POINTER(KvqPages), c_int32, POINTER(c_size_t)]
             _lib = lib
     return _lib
 
@@ -573,6 +616,21 @@ class _PreparedCall:
         # converted once: a call of a few microseconds' work is bound by its marshalling
         self._args = tuple(t(a) if isinstance(a, int) else a for t, a in zip(fn.argtypes, args))
 
+    def _workspace(self, given, size, device):
+        """The workspace the call uses: the one given, or `size` bytes of its own."""
+        if given is not None:
+            _check(given, "workspace", torch.uint8, device)
+            return given
+        if not size:
+            return None
+        self._own = torch.empty(size, dtype=torch.uint8, device=device)
+        if device.type == "cuda":
+            at = torch.cuda.current_stream(device)
+            self._own_ready, self._own_streams = torch.cuda.Event(), {at.cuda_stream}
+            if not torch.cuda.is_current_stream_capturing():
+                self._own_ready.record(at)
+        return self._own
+
     def _handle(self, stream):
         if self._index is None:
             raise ValueError("%s: the tensors are on %s, not on a CUDA device" % (self.name, self.device))
@@ -605,6 +663,16 @@ class _PreparedCall:
 
 def _stream_object(handle, device):
     return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+
+
+def _call_once(make, device, workspace, stream):
+    """Makes a prepared call and calls it.  A workspace made here belongs to the stream that uses it."""
+    if stream is None or workspace is not None or device.type != "cuda":
+        make()(stream)
+        return
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    with torch.cuda.stream(_stream_object(handle, device)):
+        make()(stream)
 
 
 class PagePool:
@@ -766,16 +834,7 @@ class PagedAttnCall(_PreparedCall):
                                  q_start.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), ts, cols,
                                  int(causal), None if hm is None else ctypes.cast(hm, POINTER(c_int32)),
                                  float(sm_scale), ot, out.data_ptr(), None if lse is None else lse.data_ptr())
-        if workspace is None:
-            size = self.workspace_size()
-            workspace = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-            if size:
-                at = torch.cuda.current_stream(dev)
-                self._own, self._own_ready, self._own_streams = workspace, torch.cuda.Event(), {at.cuda_stream}
-                if not torch.cuda.is_current_stream_capturing():
-                    self._own_ready.record(at)
-        else:
-            _check(workspace, "workspace", torch.uint8, dev)
+        workspace = self._workspace(workspace, self.workspace_size() if workspace is None else 0, dev)
         self._keep = (pool, q16, q_start, seq_lens, block_table, out, lse, hm, workspace)
         self._bind(dev, ctypes.byref(self.desc), _ptr(workspace), 0 if workspace is None else workspace.numel())
 
@@ -791,13 +850,7 @@ def kvq_paged_attn(pool: PagePool, q16, q_start, max_q: int, seq_lens, block_tab
                    lse=None, head_map=None, workspace=None, stream=None) -> None:
     """kvq_paged_attn of include/kvq_paged.h (arguments as PagedAttnCall)."""
     args = (pool, q16, q_start, max_q, seq_lens, block_table, causal, sm_scale, out, lse, head_map, workspace)
-    if stream is None or workspace is not None or pool.device.type != "cuda":
-        PagedAttnCall(*args)(stream)
-        return
-    # a workspace made here belongs to the stream that uses it
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    with torch.cuda.stream(_stream_object(handle, pool.device)):
-        PagedAttnCall(*args)(stream)
+    _call_once(lambda: PagedAttnCall(*args), pool.device, workspace, stream)
 
 
 def kvq_debug_paged_lose_copy(call: PagedAttnCall, copy: int, stream=None) -> None:
@@ -808,3 +861,236 @@ def kvq_debug_paged_lose_copy(call: PagedAttnCall, copy: int, stream=None) -> No
                                           handle)
     if st:
         raise KvqError(st, "kvq_debug_paged_lose_copy")
+
+
+# -------------------------------------- around the paged cache's calls --
+# (include/kvq_tokens.h): prepared calls and functions as above.
+
+class Rope:
+    """A rotation of heads to positions (kvq_rope and kvq_rope_turns of
+    include/kvq_tokens.h): the rates, laid out once in device memory, for kvq_qkv
+    and kvq_paged_move.  n_rot: the first values of a head that rotate, a multiple
+    of 8; layout: ROPE_HALF or ROPE_PAIRS; scaling: ROPE_PLAIN, or for contexts
+    `factor` times as long as the `original` one ROPE_LINEAR, ROPE_BASE,
+    ROPE_BY_INDEX or ROPE_BY_TURNS (the last two with the turns within `original`
+    from which a pair keeps its rate, `fast`, and up to which it is slowed,
+    `slow`).  amplitude: None for the scaling's own."""
+
+    def __init__(self, n_rot: int = HEAD_DIM, base: float = 10000.0, layout: int = ROPE_HALF, scaling: int = ROPE_PLAIN,
+                 factor: float = 1.0, original: float = 0.0, fast: float = 0.0, slow: float = 0.0, amplitude: float | None = None,
+                 device=None):
+        _fits(n_rot=n_rot, layout=layout, scaling=scaling)
+        if layout not in (ROPE_HALF, ROPE_PAIRS):
+            raise ValueError("layout must be ROPE_HALF or ROPE_PAIRS")
+        rates, amp = (ctypes.c_uint64 * max(1, n_rot // 2))(), c_float(0.0)
+        st = load().kvq_rope_turns(n_rot, float(base), scaling, float(factor), float(original), float(fast), float(slow), rates,
+                                   ctypes.byref(amp))
+        if st:
+            raise KvqError(st, "kvq_rope_turns")
+        device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        host = torch.frombuffer(rates, dtype=torch.int64, count=max(1, n_rot // 2)).clone()
+        self.turns = host.to(device)   # (int64 holds the bits of the unsigned rates)
+        self.device, self.n_rot, self.layout = self.turns.device, n_rot, layout
+        self.amplitude = float(amp.value if amplitude is None else amplitude)
+        self.desc = KvqRope(self.turns.data_ptr(), n_rot, layout, self.amplitude)
+
+
+def _rope(rope, device):
+    if rope is None:
+        return None
+    if rope.device != device:
+        raise ValueError("rope is on %s, the call's tensors are on %s" % (rope.device, device))
+    return ctypes.pointer(rope.desc)
+
+
+class PagePositionsCall(_PreparedCall):
+    """kvq_page_positions of include/kvq_tokens.h, prepared.  q_start int32
+    [n_seqs + 1], seq_lens int32 [n_seqs] (lens_out of kvq_page_tables); positions
+    int32 [tokens]."""
+    name = "kvq_page_positions"
+
+    def __init__(self, q_start, seq_lens, positions):
+        n, dev = seq_lens.shape[0], seq_lens.device
+        _check(seq_lens, "seq_lens", torch.int32, dev, (n,))
+        _check(q_start, "q_start", torch.int32, dev, (n + 1,))
+        _check(positions, "positions", torch.int32, dev, (None,))
+        _fits(n_seqs=n, n_tokens=positions.shape[0])
+        self._keep = (q_start, seq_lens, positions)
+        self._bind(dev, n, _ptr(q_start), _ptr(seq_lens), positions.shape[0], _ptr(positions))
+
+
+def kvq_page_positions(q_start, seq_lens, positions, stream=None) -> None:
+    """kvq_page_positions of include/kvq_tokens.h (arguments as PagePositionsCall)."""
+    PagePositionsCall(q_start, seq_lens, positions)(stream)
+
+
+class QkvCall(_PreparedCall):
+    """kvq_qkv of include/kvq_tokens.h, prepared.  q16 fp16 [tokens][q heads][128],
+    k16 and v16 fp16 [tokens][kv heads][128] (tokens may be strided: views into a
+    fused projection's output will do); positions int32 [tokens]; rope: a Rope, or
+    None; q_out like q16 (q16 itself rotates in place); pool and slots, int32
+    [tokens]: keys and values go into pages; or k_out like k16, with v16 and pool
+    None (and slots, if given, telling the rows to leave out).  q_norm, k_norm: fp32
+    [128], or None.  q16 and q_out may be None (keys and values alone), and so may
+    k16, v16, pool and k_out (queries alone)."""
+    name = "kvq_qkv"
+
+    def __init__(self, q16, k16, v16, positions, rope, q_out, k_out=None, pool: PagePool | None = None, slots=None,
+                 q_norm=None, k_norm=None, eps: float = 1e-6):
+        some = q16 if q16 is not None else k16
+        if some is None:
+            raise ValueError("q16 or k16 must be given")
+        dev, n = some.device, some.shape[0]
+        if (q16 is None) != (q_out is None):
+            raise ValueError("q16 and q_out belong together")
+        if k16 is None and not (v16 is None and pool is None and k_out is None):
+            raise ValueError("v16, pool and k_out need k16")
+        if k16 is not None and (pool is None) == (k_out is None):
+            raise ValueError("keys go into a pool or to k_out: exactly one must be given")
+        if (v16 is None) != (pool is None):
+            raise ValueError("v16 and pool belong together")
+        if pool is not None and slots is None:
+            raise ValueError("a pool needs slots")
+        if pool is not None and pool.device != dev:
+            raise ValueError("the pool is on %s, the call's tensors are on %s" % (pool.device, dev))
+
+        def rows(t, name, like):
+            if t is None:
+                return 0, 0
+            heads = like.shape[1] if like.dim() == 3 else 0
+            stride = _rows_stride(t, name, heads, dev)
+            if t.shape[0] != n:
+                raise ValueError("%s must have one row per token" % name)
+            return heads, stride
+
+        hq, q_stride = rows(q16, "q16", q16)
+        _, qo_stride = rows(q_out, "q_out", q16)
+        hk, k_stride = rows(k16, "k16", k16)
+        _, v_stride = rows(v16, "v16", k16)
+        _, ko_stride = rows(k_out, "k_out", k16)
+        if pool is not None and pool.n_kv_heads != hk:
+            raise ValueError("k16 has %d heads, the pool %d" % (hk, pool.n_kv_heads))
+        for t, what, dt, shape in ((positions, "positions", torch.int32, (n,)), (slots, "slots", torch.int32, (n,)),
+                                   (q_norm, "q_norm", torch.float32, (HEAD_DIM,)), (k_norm, "k_norm", torch.float32, (HEAD_DIM,))):
+            if t is not None:
+                _check(t, what, dt, dev, shape)
+        if rope is not None and rope.n_rot > 0 and positions is None:
+            raise ValueError("a rotation needs positions")
+        _fits(n_tokens=n, n_q_heads=hq, n_kv_heads=hk)
+
+        def at(t):
+            return None if t is None else t.data_ptr()
+
+        self.desc = KvqQkvDesc(at(q16), at(k16), at(v16), q_stride, k_stride, v_stride, n, hq, hk, float(eps), at(q_norm),
+                               at(k_norm), _rope(rope, dev), at(positions), at(q_out), qo_stride,
+                               None if pool is None else ctypes.pointer(pool.desc), at(slots), at(k_out), ko_stride)
+        self._keep = (q16, k16, v16, positions, rope, q_out, k_out, pool, slots, q_norm, k_norm)
+        self._bind(dev, ctypes.byref(self.desc))
+
+
+def kvq_qkv(q16, k16, v16, positions, rope, q_out, k_out=None, pool=None, slots=None, q_norm=None, k_norm=None, eps: float = 1e-6,
+            stream=None) -> None:
+    """kvq_qkv of include/kvq_tokens.h (arguments as QkvCall)."""
+    QkvCall(q16, k16, v16, positions, rope, q_out, k_out, pool, slots, q_norm, k_norm, eps)(stream)
+
+
+class PageForkCall(_PreparedCall):
+    """kvq_page_fork of include/kvq_tokens.h, prepared.  lens, lens_out, copy_from,
+    copy_to, copy_held, status, parent, keep: int32 [n_seqs]; block_table and
+    table_out int32 [n_seqs][max_blocks] (rows may be strided); free_pages int32
+    [n_pages]; n_free, n_free_out int32 [1].  parent None: every place goes on with
+    itself (table_out may then be block_table); keep None: with all it holds.
+    lens_out may be lens and n_free_out may be n_free.  workspace as
+    PagedAttnCall's."""
+    name = "kvq_page_fork"
+
+    def __init__(self, page_tokens: int, n_pages: int, lens, block_table, free_pages, n_free, table_out, lens_out, n_free_out,
+                 copy_from, copy_to, copy_held, status, parent=None, keep=None, workspace=None):
+        n, dev = lens.shape[0], lens.device
+        for t, what, size in ((lens, "lens", n), (parent, "parent", n), (keep, "keep", n), (free_pages, "free_pages", n_pages),
+                              (n_free, "n_free", 1), (lens_out, "lens_out", n), (n_free_out, "n_free_out", 1),
+                              (copy_from, "copy_from", n), (copy_to, "copy_to", n), (copy_held, "copy_held", n), (status, "status", n)):
+            if t is not None or what not in ("parent", "keep"):
+                _check(t, what, torch.int32, dev, (size,))
+        stride, cols = _table(block_table, n, dev)
+        out_stride, out_cols = _table(table_out, n, dev)
+        if out_cols != cols:
+            raise ValueError("table_out must have block_table's columns")
+        _fits(page_tokens=page_tokens, n_pages=n_pages)
+        size = c_size_t(0)
+        st = load().kvq_page_fork_workspace_size(n, n_pages, ctypes.byref(size))
+        if st:
+            raise KvqError(st, "kvq_page_fork_workspace_size")
+        workspace = self._workspace(workspace, int(size.value), dev)
+        self._keep = (lens, parent, keep, block_table, table_out, lens_out, free_pages, n_free, n_free_out, copy_from, copy_to,
+                      copy_held, status, workspace)
+        self._bind(dev, n, page_tokens, n_pages, _ptr(lens), _ptr(parent), _ptr(keep), _ptr(block_table), stride, cols,
+                   _ptr(table_out), out_stride, _ptr(lens_out), _ptr(free_pages), _ptr(n_free), _ptr(n_free_out), _ptr(copy_from),
+                   _ptr(copy_to), _ptr(copy_held), _ptr(status), _ptr(workspace), workspace.numel())
+
+
+def kvq_page_fork(page_tokens: int, n_pages: int, lens, block_table, free_pages, n_free, table_out, lens_out, n_free_out, copy_from,
+                  copy_to, copy_held, status, parent=None, keep=None, workspace=None, stream=None) -> None:
+    """kvq_page_fork of include/kvq_tokens.h (arguments as PageForkCall)."""
+    args = (page_tokens, n_pages, lens, block_table, free_pages, n_free, table_out, lens_out, n_free_out, copy_from, copy_to,
+            copy_held, status, parent, keep, workspace)
+    _call_once(lambda: PageForkCall(*args), lens.device, workspace, stream)
+
+
+class PageCopyCall(_PreparedCall):
+    """kvq_page_copy of include/kvq_tokens.h, prepared.  pools: a list of PagePool
+    with the same pages and page size (the layers); from_pages, to_pages, held: int32 [copies] (held None:
+    whole pages), as PageForkCall's copy_from, copy_to and copy_held."""
+    name = "kvq_page_copy"
+
+    def __init__(self, pools, from_pages, to_pages, held=None):
+        pools = list(pools)
+        n, dev = from_pages.shape[0], from_pages.device
+        for t, what in ((from_pages, "from_pages"), (to_pages, "to_pages"), (held, "held")):
+            if t is not None:
+                _check(t, what, torch.int32, dev, (n,))
+        for pool in pools:
+            if pool.device != dev:
+                raise ValueError("a pool is on %s, the call's tensors are on %s" % (pool.device, dev))
+        if len(pools) > MAX_COPY_POOLS:
+            raise ValueError("at most %d pools" % MAX_COPY_POOLS)
+        _fits(n_copies=n)
+        self._pools = (KvqPages * max(1, len(pools)))(*[pool.desc for pool in pools])
+        self._keep = (pools, from_pages, to_pages, held)
+        self._bind(dev, self._pools, len(pools), _ptr(from_pages), _ptr(to_pages), _ptr(held), n)
+
+
+def kvq_page_copy(pools, from_pages, to_pages, held=None, stream=None) -> None:
+    """kvq_page_copy of include/kvq_tokens.h (arguments as PageCopyCall)."""
+    PageCopyCall(pools, from_pages, to_pages, held)(stream)
+
+
+class PagedMoveCall(_PreparedCall):
+    """kvq_paged_move of include/kvq_tokens.h, prepared.  from_slots, to_slots int32
+    [tokens]; rope and turn, int32 [tokens]: the keys' rotation and the positions to
+    turn each by, or None; staged: slots may be one token's `to` and another's
+    `from` (workspace as PagedAttnCall's)."""
+    name = "kvq_paged_move"
+
+    def __init__(self, pool: PagePool, from_slots, to_slots, rope=None, turn=None, staged: bool = True, workspace=None):
+        n, dev = from_slots.shape[0], pool.device
+        for t, what in ((from_slots, "from_slots"), (to_slots, "to_slots"), (turn, "turn")):
+            if t is not None or what != "turn":
+                _check(t, what, torch.int32, dev, (n,))
+        if (rope is None) != (turn is None):
+            raise ValueError("rope and turn belong together")
+        _fits(n_tokens=n)
+        size = c_size_t(0)
+        if staged:
+            st = load().kvq_paged_move_workspace_size(ctypes.byref(pool.desc), n, ctypes.byref(size))
+            if st:
+                raise KvqError(st, "kvq_paged_move_workspace_size")
+        workspace = self._workspace(workspace, int(size.value), dev)
+        self._keep = (pool, from_slots, to_slots, rope, turn, workspace)
+        self._bind(dev, ctypes.byref(pool.desc), _ptr(from_slots), _ptr(to_slots), n, _rope(rope, dev), _ptr(turn), int(staged),
+                   _ptr(workspace), 0 if workspace is None else workspace.numel())
+
+
+def kvq_paged_move(pool: PagePool, from_slots, to_slots, rope=None, turn=None, staged: bool = True, workspace=None, stream=None) -> None:
+    """kvq_paged_move of include/kvq_tokens.h (arguments as PagedMoveCall)."""
+    _call_once(lambda: PagedMoveCall(pool, from_slots, to_slots, rope, turn, staged, workspace), pool.device, workspace, stream)
