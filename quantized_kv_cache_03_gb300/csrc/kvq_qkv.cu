@@ -1,229 +1,477 @@
 // kvq_qkv.cu -- new tokens on their way into the paged cache: heads normalized
 // and rotated, queries (and keys, without pages) written as fp16, keys and values
 // quantized into their slots.
-#include "kvq_tokens.cuh"
+#include <cstdlib>
+
+#include "kvq_quad.cuh"
 
 namespace kvq {
 
 constexpr int kQkvWarps = 8;
+constexpr int kQkvTokens = 8;   // tokens of a block
 
-// A half-warp holds a row (token, head), eight values a lane, as two groups of
-// four dims.  The groups are chosen so that both values of a pair are the same
-// lane's: with pairs side by side (and without a rotation) the lane's groups are,
-// with pairs half of n_rot apart the groups are too, and what is not rotated is
-// shared out over the lanes behind.  Either way lanes below n_rot / 8 rotate, by
-// rates 4 * lane and on.
-template <int PAIRS>
-struct Lane {
-    int a, b;        // first dims of the groups
-    bool rotates;
-    __device__ __forceinline__ Lane(const RopeDesc &r, int l)
-    {
-        const int h4 = r.n_rot >> 3;
-        rotates = l < h4;
-        a = PAIRS ? 8 * l : rotates ? 4 * l : r.n_rot + 8 * (l - h4);
-        b = PAIRS ? a + 4 : rotates ? a + 4 * h4 : a + 4;
-    }
+constexpr int kBatch = 4;       // rows that an octet takes at a time
+
+struct QkvShared {
+    uint16_t ring[kQkvWarps][2][kBatch][4][kD];
+    float cosines[kQkvTokens + 1][kAngleRow], sines[kQkvTokens + 1][kAngleRow];
+    float norm[2][kD];          // of queries, of keys
+    uint8_t list[kQkvWarps][kQkvTokens];
 };
 
-struct Raw {
-    uint2 a, b;
-};
-template <int PAIRS>
-__device__ __forceinline__ Raw load_row(const uint16_t *row, const Lane<PAIRS> &ln)
+// 16 bytes from global to shared memory; the copies of a thread form groups, of
+// which all but the newest N have arrived.
+__device__ __forceinline__ void copy16(uint32_t to, const void *from)
 {
-    Raw r;
-    if (PAIRS) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(row + ln.a);
-        r.a = make_uint2(w.x, w.y);
-        r.b = make_uint2(w.z, w.w);
-    } else {
-        r.a = *reinterpret_cast<const uint2 *>(row + ln.a);
-        r.b = *reinterpret_cast<const uint2 *>(row + ln.b);
-    }
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// ---- eight lanes (an octet) to a row ----
+// A row's 256 bytes are read and written as whole lines, and what multiplies a
+// token's rows fits into a lane's registers.  Lane c holds values 8 c + i and
+// 64 + 8 c + i, or, where pairs lie half of fewer than 128 apart, the group pairs
+// m = c and c + 8 (PartGroups), so that both values of a pair are always its own.
+struct Oct16 {
+    uint4 b[2];
+};
+template <int ROT>
+__device__ __forceinline__ Oct16 oct_load(const uint16_t *row, int c, int n_rot)
+{
+    Oct16 r;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+        if (ROT == kRotPart) {
+            const PartGroups g(c + 8 * b, n_rot);
+            const uint2 x = *reinterpret_cast<const uint2 *>(row + g.a), y = *reinterpret_cast<const uint2 *>(row + g.b);
+            r.b[b] = make_uint4(x.x, x.y, y.x, y.y);
+        } else {
+            r.b[b] = *reinterpret_cast<const uint4 *>(row + 64 * b + 8 * c);
+        }
     return r;
 }
-template <int PAIRS>
-__device__ __forceinline__ void store_row(uint16_t *row, const Lane<PAIRS> &ln, const Raw &r)
+template <int ROT>
+__device__ __forceinline__ void oct_store(uint16_t *row, int c, int n_rot, const Oct16 &r)
 {
-    if (PAIRS) {
-        *reinterpret_cast<uint4 *>(row + ln.a) = make_uint4(r.a.x, r.a.y, r.b.x, r.b.y);
-    } else {
-        *reinterpret_cast<uint2 *>(row + ln.a) = r.a;
-        *reinterpret_cast<uint2 *>(row + ln.b) = r.b;
-    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+        if (ROT == kRotPart) {
+            const PartGroups g(c + 8 * b, n_rot);
+            *reinterpret_cast<uint2 *>(row + g.a) = make_uint2(r.b[b].x, r.b[b].y);
+            *reinterpret_cast<uint2 *>(row + g.b) = make_uint2(r.b[b].z, r.b[b].w);
+        } else {
+            *reinterpret_cast<uint4 *>(row + 64 * b + 8 * c) = r.b[b];
+        }
 }
 
-struct Weights {
-    float4 a, b;
-    template <int PAIRS>
-    __device__ __forceinline__ Weights(const float *norm, const Lane<PAIRS> &ln)
-    {
-        a = b = make_float4(1.f, 1.f, 1.f, 1.f);
-        if (norm) {
-            a = *reinterpret_cast<const float4 *>(norm + ln.a);
-            b = *reinterpret_cast<const float4 *>(norm + ln.b);
-        }
-    }
-};
-
-// The half-warp's row, normalized and rotated.  cs: the lane's four angles.
-template <int PAIRS>
-__device__ __forceinline__ Raw turn_row(const Raw &r, const Lane<PAIRS> &ln, const Weights &w, bool norm, float eps, const float2 (&cs)[4])
+// 1 / sqrt(x), 2^-22 off at most.  No argument but 0 is below 2^-55 (a square of an fp16 value over 128; eps is held to
+// the normal numbers), so nothing is flushed.
+__device__ __forceinline__ float inv_sqrt(float x)
 {
-    float x[8];
-    {
-        auto two = [](uint32_t v, float &lo, float &hi) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v));
-            lo = f.x;
-            hi = f.y;
-        };
-        two(r.a.x, x[0], x[1]);
-        two(r.a.y, x[2], x[3]);
-        two(r.b.x, x[4], x[5]);
-        two(r.b.y, x[6], x[7]);
-    }
-    if (norm) {
-        float ss = 0.f;
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// (a, b) -> (a A + b B, a C + b D) for the lane's eight pairs of values, two side by
+// side; the weights of the norm are in it, its factor of the row comes last.  Which
+// values are a pair's: those of x.b[0] and x.b[1] (half), or of one x.b's first and
+// second two float2 (quad_floats).
+struct OctCoef {
+    float2 A[4], B[4], C[4], D[4];
+    bool rotates[2];   // of x.b[0], x.b[1]
+};
+template <int ROT>
+__device__ __forceinline__ OctCoef oct_coef(const float *norm, const float *cosines, const float *sines, int c, int n_rot)
+{
+    OctCoef k;
+    float2 w[2][4];   // weights in the order of quad_floats
 #pragma unroll
-        for (int k = 0; k < 8; ++k) ss = fmaf(x[k], x[k], ss);
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float f = rsqrtf(fmaf(ss, 1.f / kD, eps));
-        const float wv[8] = {w.a.x, w.a.y, w.a.z, w.a.w, w.b.x, w.b.y, w.b.z, w.b.w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = x[k] * f * wv[k];
-    }
-    if (ln.rotates) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float &p = x[PAIRS ? 2 * i : i], &q = x[PAIRS ? 2 * i + 1 : i + 4];
-            const float u = p * cs[i].x - q * cs[i].y, v = p * cs[i].y + q * cs[i].x;
-            p = u;
-            q = v;
+    for (int b = 0; b < 2; ++b) {
+        float4 u = make_float4(1.f, 1.f, 1.f, 1.f), v = u;
+        if (norm) {
+            const PartGroups g(c + 8 * b, n_rot);
+            u = *reinterpret_cast<const float4 *>(norm + (ROT == kRotPart ? g.a : 64 * b + 8 * c));
+            v = *reinterpret_cast<const float4 *>(norm + (ROT == kRotPart ? g.b : 64 * b + 8 * c + 4));
         }
+        const bool first = ROT == kRotPairs;
+        w[b][0] = first ? make_float2(u.x, u.z) : make_float2(u.x, u.y);
+        w[b][1] = first ? make_float2(v.x, v.z) : make_float2(u.z, u.w);
+        w[b][2] = first ? make_float2(u.y, u.w) : make_float2(v.x, v.y);
+        w[b][3] = first ? make_float2(v.y, v.w) : make_float2(v.z, v.w);
     }
-    Raw o;
-    o.a = make_uint2(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]));
-    o.b = make_uint2(pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int b = i >> 1, at = ROT == kRotHalf ? 8 * c + 2 * i : ROT == kRotPairs ? 32 * b + 4 * c + 2 * (i & 1) : 4 * (c + 8 * b) + 2 * (i & 1);
+        const bool rot = ROT != kRotNone && 2 * (at & ~3) < n_rot;
+        if (i % 2 == 0) k.rotates[b] = rot;
+        float2 cs = make_float2(1.f, 1.f), sn = make_float2(0.f, 0.f);
+        if (rot) {
+            cs = *reinterpret_cast<const float2 *>(cosines + at);
+            sn = *reinterpret_cast<const float2 *>(sines + at);
+        }
+        const float2 wa = ROT == kRotHalf ? w[0][i] : w[b][i & 1], wb = ROT == kRotHalf ? w[1][i] : w[b][2 + (i & 1)];
+        k.A[i] = mul2(wa, cs);
+        k.B[i] = mul2(make_float2(-wb.x, -wb.y), sn);
+        k.C[i] = mul2(wa, sn);
+        k.D[i] = mul2(wb, cs);
+    }
+    return k;
+}
+template <int ROT>
+__device__ __forceinline__ Oct16 oct_turn(const Oct16 &raw, const OctCoef &k, bool norm, float eps)
+{
+    float2 x[2][4];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) quad_floats<ROT>(raw.b[b], x[b]);
+    float f = 1.f;
+    if (norm) {
+        float2 s2 = mul2(x[0][0], x[0][0]);
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s2 = fma2(x[i >> 2][i & 3], x[i >> 2][i & 3], s2);
+        float ss = s2.x + s2.y;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        f = inv_sqrt(fmaf(ss, 1.f / kD, eps));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 &a = ROT == kRotHalf ? x[0][i] : x[i >> 1][i & 1], &b = ROT == kRotHalf ? x[1][i] : x[i >> 1][2 + (i & 1)];
+        float2 u = mul2(a, k.A[i]), v = mul2(b, k.D[i]);
+        if (ROT == kRotHalf || (ROT != kRotNone && k.rotates[i >> 1])) {   // (elsewhere B and C are 0, and an infinity times 0 is no value of the row)
+            u = fma2(b, k.B[i], u);
+            v = fma2(a, k.C[i], v);
+        }
+        if (norm) {
+            u = mul2(u, make_float2(f, f));
+            v = mul2(v, make_float2(f, f));
+        }
+        a = u;
+        b = v;
+    }
+    Oct16 o;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) o.b[b] = quad_halves<ROT>(x[b]);
     return o;
 }
 
-__device__ __forceinline__ void angles(const QkvParams &p, int pos, int l, bool rotates, float2 (&cs)[4])
+// A token's V codes and K codes as the lanes hold them: codes 8 c .. 8 c + 7 and
+// those 64 further, the scales of their two blocks.
+struct OctCodes {
+    uint2 w[2];
+    uint32_t s;      // of block c / 4, of block 2 + c / 4
+};
+template <bool Q4>
+__device__ __forceinline__ OctCodes oct_quantize(const Oct16 &x)
 {
+    uint32_t m[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) cs[i] = make_float2(1.f, 0.f);
-    if (rotates)
+    for (int b = 0; b < 2; ++b) m[b] = top8(x.b[b]);
+    uint32_t top = bits_of(__hmax2(h2_of(__byte_perm(m[0], m[1], 0x5410)), h2_of(__byte_perm(m[0], m[1], 0x7632))));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) cs[i] = angle_of(p.rope.turns[4 * l + i], pos, p.rope.amplitude);
+    for (int o = 1; o < 4; o <<= 1) top = bits_of(__hmax2(h2_of(top), h2_of(__shfl_xor_sync(0xffffffffu, top, o))));
+    const __half2 s = scales_of<Q4>(top);
+    const float2 f = __half22float2(s);
+    OctCodes r;
+    r.s = bits_of(s);
+    r.w[0] = codes8<Q4>(x.b[0], f.x);
+    r.w[1] = codes8<Q4>(x.b[1], f.y);
+    return r;
 }
-
-// Heads [h0, h1) of a token that stay fp16: src to dst.
-template <int PAIRS>
-__device__ __forceinline__ void rows(const uint16_t *src, uint16_t *dst, const float *norm, float eps, const Lane<PAIRS> &ln,
-                                     const float2 (&cs)[4], int h0, int h1, bool mine)
+// Where a lane's parts of place u lie in a tile: its K codes (the others 64 dims
+// on), V codes, and scales of its first block (of the second 8 bytes on).
+struct OctPlace {
+    int k, v, s;
+    bool odd, paired;
+};
+template <int VT, int KT>
+__device__ __forceinline__ OctPlace oct_place(int u, int c, bool paired)
 {
-    constexpr int kDepth = 4;
-    const Weights w(norm, ln);
-    for (int h = h0; h < h1; h += kDepth) {
-        Raw r[kDepth];
-#pragma unroll
-        for (int k = 0; k < kDepth; ++k) {
-            r[k].a = r[k].b = make_uint2(0, 0);
-            if (mine && h + k < h1) r[k] = load_row<PAIRS>(src + (size_t)(h + k) * kD, ln);
-        }
-        __syncwarp();   // in place: the row is read before it is written
-#pragma unroll
-        for (int k = 0; k < kDepth; ++k) {
-            if (h + k >= h1) break;
-            const Raw o = turn_row<PAIRS>(r[k], ln, w, norm != nullptr, eps, cs);
-            if (mine) store_row<PAIRS>(dst + (size_t)(h + k) * kD, ln, o);
-        }
+    OctPlace o;
+    o.odd = u & 1;
+    o.paired = paired;
+    o.k = KT == KVQ_K_F16 ? k16_tile_off(u, 8 * c) : k_tile_off(u, 8 * c);
+    if (VT == KVQ_V_Q8_0) o.v = quad_v8_off(u, c & 3, paired && o.odd, 0) + 8 * (c >> 2) + (paired ? 0 : o.odd);
+    else o.v = quad_v4_off(u, quart_of(c & 3), paired && o.odd) + 4 * (c >> 2) + (paired ? 0 : 2 * o.odd);
+    o.v += PageTile<VT, KT>::V_OFF;
+    o.s = scale_off(u, c >> 2);
+    return o;
+}
+__device__ __forceinline__ void oct_put_scales(uint8_t *at, int c, uint32_t s)
+{
+    if ((c & 3) == 0) {
+        *reinterpret_cast<uint16_t *>(at) = (uint16_t)s;
+        *reinterpret_cast<uint16_t *>(at + 8) = (uint16_t)(s >> 16);
     }
 }
-
-template <int VT, int KT, int PAIRS>
-__global__ void __launch_bounds__(kQkvWarps * 32) qkv_kernel(const __grid_constant__ QkvParams p)
+template <int VT, int KT>
+__device__ __forceinline__ void oct_put_key(const Oct16 &x, uint8_t *tile, const OctPlace &at, int c, bool write)
 {
-    __shared__ __align__(16) uint16_t key[kQkvWarps][2][kD];
+    if (KT == KVQ_K_F16) {
+        if (!write) return;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const uint32_t w[4] = {x.b[b].x, x.b[b].y, x.b[b].z, x.b[b].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t *>(tile + at.k + 2048 * b + 16 * i) = w[i];
+        }
+    } else {
+        const OctCodes q = oct_quantize<false>(x);
+        if (!write) return;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) *reinterpret_cast<uint2 *>(tile + at.k + 512 * b) = q.w[b];
+        oct_put_scales(tile + PageTile<VT, KT>::KS_OFF + at.s, c, q.s);
+    }
+}
+// paired: octets of lanes and lanes ^ 8 hold places u (even) and u + 1 of one tile,
+// whose words of V codes they share: each writes half of them.
+template <int VT, int KT>
+__device__ __forceinline__ void oct_put_value(const Oct16 &x, uint8_t *tile, const OctPlace &at, int c, bool write)
+{
+    const OctCodes q = oct_quantize<VT == KVQ_V_Q4_0>(x);
+    uint8_t *to = tile + at.v;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        if (VT == KVQ_V_Q8_0) {
+            const uint32_t keep = at.odd ? q.w[b].y : q.w[b].x, got = __shfl_xor_sync(0xffffffffu, at.odd ? q.w[b].x : q.w[b].y, 8);
+            if (write && at.paired) {
+                *reinterpret_cast<uint2 *>(to + 512 * b) = make_uint2(__byte_perm(keep, got, at.odd ? 0x1504 : 0x5140), __byte_perm(keep, got, at.odd ? 0x3726 : 0x7362));
+            } else if (write) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    to[512 * b + 64 * (k >> 2) + 4 * ((k & 3) >> 1) + 2 * (k & 1)] = (uint8_t)((k < 4 ? q.w[b].x : q.w[b].y) >> (8 * (k & 3)));
+            }
+        } else {   // code bytes 4 quart .. + 3 of the block; high nibbles are lane c ^ 2's, or low ones
+            const uint32_t keep = c & 2 ? q.w[b].y : q.w[b].x, nib = __shfl_xor_sync(0xffffffffu, c & 2 ? q.w[b].x : q.w[b].y, 2);
+            const uint32_t w = c & 2 ? nib | keep << 4 : keep | nib << 4, got = __shfl_xor_sync(0xffffffffu, w, 8);
+            if (write && at.paired) {
+                *reinterpret_cast<uint32_t *>(to + 8 * b) = __byte_perm(w, got, at.odd ? 0x3276 : 0x5410);
+            } else if (write) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) *reinterpret_cast<uint16_t *>(to + 8 * b + 64 * i) = (uint16_t)(w >> (16 * i));
+            }
+        }
+    }
+    if (write) oct_put_scales(tile + PageTile<VT, KT>::VS_OFF + at.s, c, q.s);
+}
+
+// The rows a warp works on, one of each octet's token at a time: some neighbouring
+// heads of its queries, then of its keys, on their way into pages with its values.
+// They come through a ring of two batches in shared memory, the first of them
+// while the block still works out its angles.
+struct Stream {
+    const uint16_t *q, *k, *v;     // the lane's part of the next rows of its octet's tokens
+    int nq, nk;                    // rows of each still to come
+    uint32_t to;                   // the lane's part of the next batch, in shared memory
+    bool q_mine, k_mine;
+};
+constexpr uint32_t kBatchBytes = kBatch * 4 * kD * 2;
+__device__ __forceinline__ void stream_row(uint32_t to, const uint16_t *from, bool there)
+{
+    if (there) {
+        copy16(to, from);
+        copy16(to + kD, from + kD / 2);
+    }
+}
+template <bool PAGED>
+__device__ __forceinline__ void stream_get(Stream &w)
+{
+    if (w.nq > 0) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) stream_row(w.to + i * 8 * kD, w.q + i * kD, w.q_mine && i < w.nq);
+        w.q += kBatch * kD;
+        w.nq -= kBatch;
+    } else if (w.nk > 0) {
+        if (PAGED) {
+#pragma unroll
+            for (int i = 0; i < kBatch / 2; ++i) {
+                stream_row(w.to + 2 * i * 8 * kD, w.k + i * kD, w.k_mine && i < w.nk);
+                stream_row(w.to + (2 * i + 1) * 8 * kD, w.v + i * kD, w.k_mine && i < w.nk);
+            }
+            w.k += kBatch / 2 * kD;
+            w.v += kBatch / 2 * kD;
+            w.nk -= kBatch / 2;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) stream_row(w.to + i * 8 * kD, w.k + i * kD, w.k_mine && i < w.nk);
+            w.k += kBatch * kD;
+            w.nk -= kBatch;
+        }
+    }
+    w.to ^= kBatchBytes;
+    copy_commit();
+}
+
+// A block takes eight tokens and a share of the heads; a warp heads of four tokens
+// at a time.
+template <int VT, int KT, int ROT, bool PAGED>
+__global__ void __launch_bounds__(kQkvWarps * 32, 3) qkv_kernel(const __grid_constant__ QkvParams p)
+{
+    extern __shared__ __align__(1024) uint8_t qkv_smem[];
+    QkvShared &sh = *reinterpret_cast<QkvShared *>(qkv_smem);
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane & 15, half = lane >> 4;
-    const Lane<PAIRS> ln(p.rope, l);
-    float2 cs[4];
-    if ((int)blockIdx.x >= p.kv_blocks) {
-        // rows that stay fp16: a warp takes tokens 2i, 2i + 1, a half-warp each
-        const long long job = (long long)(blockIdx.x - p.kv_blocks) * kQkvWarps + warp;
-        const long long pair = job / p.row_chunks;
-        const int c = (int)(job - pair * p.row_chunks);
-        if (2 * pair >= p.n_tokens) return;
-        const int tok = (int)(2 * pair) + half;
-        const bool mine = tok < p.n_tokens && (!p.slots || p.slots[tok] >= 0);
-        if (!__any_sync(0xffffffffu, mine)) return;
-        angles(p, mine && p.rope.n_rot ? p.positions[tok] : 0, l, ln.rotates, cs);
-        const int heads = p.n_q_heads + (p.paged ? 0 : p.n_kv_heads), h0 = c * p.row_heads, h1 = min(heads, h0 + p.row_heads);
-        if (h0 < p.n_q_heads)
-            rows<PAIRS>(p.q + tok * p.q_stride, p.q_out + tok * p.q_out_stride, p.q_norm, p.eps, ln, cs, h0, min(h1, p.n_q_heads), mine);
-        if (h1 > p.n_q_heads)
-            rows<PAIRS>(p.k + tok * p.k_stride, p.k_out + tok * p.k_out_stride, p.k_norm, p.eps, ln, cs, max(h0, p.n_q_heads) - p.n_q_heads, h1 - p.n_q_heads, mine);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 7, oct = lane >> 3, n_rot = p.rope.n_rot;
+    const int tile = blockIdx.x / p.chunks, share = blockIdx.x - tile * p.chunks, t0 = tile * kQkvTokens;
+    // slots of the token before the block's, of its own, and of the one behind
+    const int at = t0 - 1 + lane;
+    const int slot = lane < kQkvTokens + 2 && at >= 0 && at < p.n_tokens ? (p.slots ? p.slots[at] : 0) : -1;
+    const int q1 = min(p.n_q_heads, (share + 1) * p.q_heads), k1 = min(p.n_kv_heads, (share + 1) * p.kv_heads);
+    auto piece = [](int h0, int h1, int parts, int part, int &first) {   // heads of one of the warps that share tokens
+        const int each = (max(0, h1 - h0) + parts - 1) / parts;
+        first = h0 + part * each;
+        return max(0, min(each, h1 - first));
+    };
+    Stream w;
+    const int qi = 4 * (warp & 1) + oct;
+    int q_first, k_first, ki = qi, sl = 0;
+    const int nq = piece(share * p.q_heads, q1, kQkvWarps / 2, warp >> 1, q_first);
+    w.q_mine = __shfl_sync(0xffffffffu, slot, 1 + qi) >= 0;
+    int nk;
+    bool pair = false, beyond = false;
+    if (!PAGED) {
+        nk = piece(share * p.kv_heads, k1, kQkvWarps / 2, warp >> 1, k_first);
+        w.k_mine = w.q_mine;
+    } else {
+        // pages: two octets to a token that begins a pair and its partner; without pairs an octet to each token
+        const SlotPairs q = slot_pairs(slot, slot >= 0 && slot < p.pool.n_slots, kQkvTokens);
+        slot_list(q, sh.list[warp]);
+        const bool pairs = (q.pair & q.lead) != 0;
+        beyond = q.pair & q.lead & 1u << kQkvTokens;   // with the first token of the block behind
+        const int per = pairs ? 2 : 4, groups = max(1, (q.leads + per - 1) / per), parts = kQkvWarps / groups, part = warp / groups;   // (at most four groups)
+        const int n = (warp - part * groups) * per + (pairs ? oct >> 1 : oct), e = pairs ? oct & 1 : 0;
+        const int lead = n < q.leads ? sh.list[warp][n] : 1;
+        pair = n < q.leads && (q.pair >> lead & 1);
+        w.k_mine = n < q.leads && (e == 0 || pair);
+        ki = lead - 1 + (pair ? e : 0);
+        sl = __shfl_sync(0xffffffffu, slot, 1 + ki);
+        nk = q.leads > 0 ? piece(share * p.kv_heads, k1, parts, part, k_first) : 0;
+    }
+    w.q = p.q + (t0 + qi) * p.q_stride + q_first * kD + 8 * c;
+    w.k = p.k + (t0 + ki) * p.k_stride + k_first * kD + 8 * c;
+    w.v = p.v + (t0 + ki) * p.v_stride + k_first * kD + 8 * c;
+    w.nq = nq;
+    w.nk = nk;
+    w.to = smem_u32(sh.ring[warp][0][0][oct]) + 16 * c;
+    stream_get<PAGED>(w);
+    stream_get<PAGED>(w);
+    if (ROT != kRotNone) {
+        const int n = min(kQkvTokens + (beyond ? 1 : 0), p.n_tokens - t0), j = threadIdx.x % (kD / 2);
+        if (j < n_rot / 2) {
+            const unsigned long long rate = p.rope.turns[j];
+            for (int t = threadIdx.x / (kD / 2); t < n; t += kQkvWarps * 32 / (kD / 2)) {
+                const float2 a = angle_of(rate, p.positions[t0 + t], p.rope.amplitude);
+                sh.cosines[t][j] = a.x;
+                sh.sines[t][j] = a.y;
+            }
+        }
+    }
+    {
+        const float *norm = threadIdx.x < kD ? p.q_norm : p.k_norm;
+        if (norm) sh.norm[threadIdx.x / kD][threadIdx.x % kD] = norm[threadIdx.x % kD];
+    }
+    __syncthreads();
+    const float *q_norm = p.q_norm ? sh.norm[0] : nullptr, *k_norm = p.k_norm ? sh.norm[1] : nullptr;
+    OctCoef k;
+    int at_batch = 0;
+    // rows that stay fp16: queries, and keys without pages
+    auto rows = [&](int n, uint16_t *dst, bool mine, bool norm) {
+        for (; n > 0; n -= kBatch) {
+            copy_wait<1>();
+            if (ROT == kRotPart) __syncwarp();   // (elsewhere a lane reads what it copied itself)
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (i >= n) break;
+                const Oct16 o = oct_turn<ROT>(oct_load<ROT>(sh.ring[warp][at_batch][i][oct], c, n_rot), k, norm, p.eps);
+                if (mine) oct_store<ROT>(dst + i * kD, c, n_rot, o);
+            }
+            dst += kBatch * kD;
+            at_batch ^= 1;
+            __syncwarp();   // the batch has been read: its place may be filled again
+            stream_get<PAGED>(w);
+        }
+    };
+    if (nq > 0) {
+        k = oct_coef<ROT>(q_norm, sh.cosines[qi], sh.sines[qi], c, n_rot);
+        rows(nq, p.q_out + (t0 + qi) * p.q_out_stride + q_first * kD, w.q_mine, q_norm != nullptr);
+    }
+    if (nk == 0) return;
+    k = oct_coef<ROT>(k_norm, sh.cosines[ki], sh.sines[ki], c, n_rot);
+    if (!PAGED) {
+        rows(nk, p.k_out + (t0 + ki) * p.k_out_stride + k_first * kD, w.k_mine, k_norm != nullptr);
         return;
     }
-    // pages: a warp takes a token, or two whose slots are an even place and the next
-    const long long job = (long long)blockIdx.x * kQkvWarps + warp;
-    const int c = (int)(job / ((p.n_tokens + kQkvWarps - 1) / kQkvWarps * kQkvWarps)), tok = (int)(job % ((p.n_tokens + kQkvWarps - 1) / kQkvWarps * kQkvWarps));
-    if (tok >= p.n_tokens) return;
-    const int slot = p.slots[tok], before = tok > 0 ? p.slots[tok - 1] : -1, after = tok + 1 < p.n_tokens ? p.slots[tok + 1] : -1;
-    if (slot < 0 || slot >= p.pool.n_slots || ((slot & 1) && before == slot - 1)) return;
-    const bool pair = !(slot & 1) && after == slot + 1;
-    const int my = tok + (pair ? half : 0);   // alone: both half-warps work on the one row
-    angles(p, p.rope.n_rot ? p.positions[my] : 0, l, ln.rotates, cs);
-    const Weights w(p.k_norm, ln);
-    const int place = slot & ((1 << p.pool.pshift) - 1), h1 = min(p.n_kv_heads, (c + 1) * p.kv_heads);
-    for (int h = c * p.kv_heads; h < h1; ++h) {
-        const uint16_t *vrow = p.v + tok * p.v_stride + (size_t)h * kD;
-        const Raw o = turn_row<PAIRS>(load_row<PAIRS>(p.k + my * p.k_stride + (size_t)h * kD, ln), ln, w, p.k_norm != nullptr, p.eps, cs);
-        __syncwarp();
-        store_row<PAIRS>(key[warp][half], ln, o);
-        __syncwarp();
-        uint8_t *tile = tile_of(p.pool, slot >> p.pool.pshift, h, place >> 4, PageTile<VT, KT>::BYTES);
-        const TokenRow t = paged_token<VT, KT>(key[warp][0], vrow, lane);
-        if (pair) {
-            const TokenRow t1 = paged_token<VT, KT>(key[warp][1], vrow + p.v_stride, lane);
-            store_pair_paged<VT, KT>(t, t1, place & 15, lane, tile);
-        } else {
-            store_token_paged<VT, KT>(t, place & 15, lane, tile);
+    const OctPlace place = oct_place<VT, KT>(sl & 15, c, pair);
+    uint8_t *tile16 = tile_of(p.pool, sl >> p.pool.pshift, k_first, (sl & ((1 << p.pool.pshift) - 1)) >> 4, PageTile<VT, KT>::BYTES);
+    const uint32_t head_bytes = (uint32_t)PageTile<VT, KT>::BYTES << (p.pool.pshift - 4);
+    for (int n = nk; n > 0; n -= kBatch / 2) {
+        copy_wait<1>();
+        if (ROT == kRotPart) __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kBatch / 2; ++i) {
+            if (i >= n) break;
+            uint16_t *krow = sh.ring[warp][at_batch][2 * i][oct];
+            Oct16 o = oct_turn<ROT>(oct_load<ROT>(krow, c, n_rot), k, k_norm != nullptr, p.eps);
+            if (ROT == kRotPart) {   // back to neighbours
+                __syncwarp();
+                oct_store<ROT>(krow, c, n_rot, o);
+                __syncwarp();
+                o = oct_load<kRotNone>(krow, c, 0);
+            }
+            oct_put_key<VT, KT>(o, tile16, place, c, w.k_mine);
+            oct_put_value<VT, KT>(oct_load<kRotNone>(sh.ring[warp][at_batch][2 * i + 1][oct], c, 0), tile16, place, c, w.k_mine);
+            tile16 += head_bytes;
         }
+        at_batch ^= 1;
+        __syncwarp();
+        stream_get<PAGED>(w);
     }
 }
 
-template <int VT, int KT>
-static cudaError_t qkv_t(const QkvParams &p, int blocks, cudaStream_t s, bool pdl)
+// Rows that stay fp16 know no formats.
+template <int VT, int KT, bool PAGED>
+static void (*qkv_fn(const RopeDesc &r))(QkvParams)
 {
-    return p.rope.pairs || p.rope.n_rot == 0 ? launch_pdl(qkv_kernel<VT, KT, 1>, p, blocks, kQkvWarps * 32, 0, s, pdl)
-                                             : launch_pdl(qkv_kernel<VT, KT, 0>, p, blocks, kQkvWarps * 32, 0, s, pdl);
+    return r.n_rot == 0 ? qkv_kernel<VT, KT, kRotNone, PAGED> : r.pairs ? qkv_kernel<VT, KT, kRotPairs, PAGED>
+           : r.n_rot == kD ? qkv_kernel<VT, KT, kRotHalf, PAGED> : qkv_kernel<VT, KT, kRotPart, PAGED>;
+}
+static void (*qkv_fn(const QkvParams &p, int v_type, int k_type))(QkvParams)
+{
+    if (!p.paged) return qkv_fn<KVQ_V_Q4_0, KVQ_K_I8, false>(p.rope);
+    if (v_type == KVQ_V_Q4_0) return k_type == KVQ_K_F16 ? qkv_fn<KVQ_V_Q4_0, KVQ_K_F16, true>(p.rope) : qkv_fn<KVQ_V_Q4_0, KVQ_K_I8, true>(p.rope);
+    return k_type == KVQ_K_F16 ? qkv_fn<KVQ_V_Q8_0, KVQ_K_F16, true>(p.rope) : qkv_fn<KVQ_V_Q8_0, KVQ_K_I8, true>(p.rope);
+}
+
+cudaError_t prepare_qkv()
+{
+    const int rots[4][2] = {{0, 0}, {kD, 1}, {kD, 0}, {64, 0}};
+    for (auto &r : rots)
+        for (int form = 0; form < 5; ++form) {
+            QkvParams p = {};
+            p.rope.n_rot = r[0];
+            p.rope.pairs = r[1];
+            p.paged = form < 4;
+            const cudaError_t e = cudaFuncSetAttribute(qkv_fn(p, form & 1, form >> 1 & 1), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(QkvShared));
+            if (e != cudaSuccess) return e;
+        }
+    return cudaSuccess;
 }
 
 cudaError_t launch_qkv(const QkvParams &in, int v_type, int k_type, int n_sms, cudaStream_t s, bool pdl)
 {
     QkvParams p = in;
-    const long long warps = (long long)n_sms * 48;
-    // as many heads to a warp as leaves each SM its warps
-    auto pieces = [&](int heads, long long tokens, int least, int &each, int &n) {
-        const long long want = heads * tokens / warps;
-        each = want < least ? least : want > 16 ? 16 : (int)want;
-        each = each > heads ? (heads > 0 ? heads : 1) : each;
-        n = (heads + each - 1) / each;
-    };
-    const int row_heads = p.n_q_heads + (p.paged ? 0 : p.n_kv_heads);
-    const long long pairs = ((long long)p.n_tokens + 1) / 2;
-    pieces(row_heads, pairs, 4, p.row_heads, p.row_chunks);
-    pieces(p.paged ? p.n_kv_heads : 0, pairs, 1, p.kv_heads, p.kv_chunks);
-    const long long token_blocks = ((long long)p.n_tokens + kQkvWarps - 1) / kQkvWarps;
-    p.kv_blocks = (int)(token_blocks * p.kv_chunks);
-    const long long blocks = p.kv_blocks + (pairs * p.row_chunks + kQkvWarps - 1) / kQkvWarps;
-    if (v_type == KVQ_V_Q4_0)
-        return k_type == KVQ_K_F16 ? qkv_t<KVQ_V_Q4_0, KVQ_K_F16>(p, (int)blocks, s, pdl) : qkv_t<KVQ_V_Q4_0, KVQ_K_I8>(p, (int)blocks, s, pdl);
-    return k_type == KVQ_K_F16 ? qkv_t<KVQ_V_Q8_0, KVQ_K_F16>(p, (int)blocks, s, pdl) : qkv_t<KVQ_V_Q8_0, KVQ_K_I8>(p, (int)blocks, s, pdl);
+    const int tiles = (int)(((long long)p.n_tokens + kQkvTokens - 1) / kQkvTokens);
+    const int most = (p.n_q_heads > p.n_kv_heads ? p.n_q_heads : p.n_kv_heads) / 2;
+    const char *e = getenv("KVQ_TMP");
+    const long long want = (long long)n_sms * (e ? atoi(e) : 2);
+    long long chunks = (want + tiles - 1) / tiles;
+    chunks = chunks > most ? most : chunks;
+    p.chunks = chunks < 1 ? 1 : (int)chunks;
+    p.q_heads = (p.n_q_heads + p.chunks - 1) / p.chunks;
+    p.kv_heads = (p.n_kv_heads + p.chunks - 1) / p.chunks;
+    return launch_pdl(qkv_fn(p, v_type, k_type), p, tiles * p.chunks, kQkvWarps * 32, (int)sizeof(QkvShared), s, pdl);
 }
 
 }  // namespace kvq

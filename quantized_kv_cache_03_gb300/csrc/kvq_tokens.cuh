@@ -43,9 +43,7 @@ struct QkvParams {
     float eps;
     int n_tokens, n_q_heads, n_kv_heads;
     int paged;
-    int kv_heads, kv_chunks;    // heads of a warp that fills pages, and such pieces of a token's kv heads
-    int kv_blocks;              // the blocks that fill pages come first
-    int row_heads, row_chunks;  // the same of rows that stay fp16
+    int chunks, q_heads, kv_heads;   // shares of the heads, and the heads of a share
 };
 
 struct ForkParams {
@@ -77,6 +75,7 @@ struct MoveParams {
 constexpr int kForkCtas = 8, kForkThreads = 512;
 
 cudaError_t launch_positions(const PositionsParams &p, cudaStream_t s, bool pdl);
+cudaError_t prepare_qkv();
 cudaError_t launch_qkv(const QkvParams &p, int v_type, int k_type, int n_sms, cudaStream_t s, bool pdl);
 cudaError_t launch_page_fork(const ForkParams &p, cudaStream_t s, bool pdl);
 cudaError_t launch_page_copy(const CopyParams &p, cudaStream_t s, bool pdl);

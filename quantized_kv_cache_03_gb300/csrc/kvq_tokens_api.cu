@@ -1,8 +1,10 @@
 // kvq_tokens_api.cu -- the C ABI of include/kvq_tokens.h: argument checks and
 // launches.  Nothing here allocates, throws or synchronizes.
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <mutex>
 
 #include "kvq_paged_host.cuh"
 #include "kvq_tokens.cuh"
@@ -13,11 +15,23 @@ namespace {
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 
-kvq_status sms_of(int *n_sms)
+std::mutex g_mu;
+bool g_ready[kMaxDevices];
+
+// The current device's SM count; its kernels' attributes are set by the first call.
+kvq_status tokens_setup(int *n_sms)
 {
     int dev = 0;
     unsigned int *timeouts = nullptr;
-    return device_common(&dev, n_sms, &timeouts);
+    const kvq_status st = device_common(&dev, n_sms, &timeouts);
+    if (st != KVQ_OK) return st;
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!g_ready[dev]) {
+        const cudaError_t e = prepare_qkv();
+        if (e != cudaSuccess) return done(e);
+        g_ready[dev] = true;
+    }
+    return KVQ_OK;
 }
 
 kvq_status check_rope(const kvq_rope *r)
@@ -104,7 +118,7 @@ kvq_status kvq_page_positions(int32_t n_seqs, const int32_t *q_start, const int3
     if (n_tokens == 0) return KVQ_OK;
     if (!int_ptr(q_start) || (n_seqs > 0 && !int_ptr(seq_lens)) || !int_ptr(positions)) return KVQ_ERR_INVALID_ARG;
     int n_sms = 0;
-    const kvq_status st = sms_of(&n_sms);
+    const kvq_status st = tokens_setup(&n_sms);
     if (st != KVQ_OK) return st;
     return done(launch_positions(PositionsParams{q_start, seq_lens, positions, n_seqs, n_tokens}, static_cast<cudaStream_t>(stream), pdl_on()));
 }
@@ -135,7 +149,7 @@ kvq_status kvq_qkv(const kvq_qkv_desc *a, void *stream)
     const RopeDesc rope = rope_of(a->rope);
     if (rope.n_rot > 0 && !int_ptr(a->positions)) return KVQ_ERR_INVALID_ARG;
     int n_sms = 0;
-    st = sms_of(&n_sms);
+    st = tokens_setup(&n_sms);
     if (st != KVQ_OK) return st;
     QkvParams p = {};
     if (a->pages) p.pool = pool_of(a->pages);
@@ -154,7 +168,7 @@ kvq_status kvq_qkv(const kvq_qkv_desc *a, void *stream)
     p.k_norm = a->k_norm;
     p.positions = a->positions;
     p.slots = a->slots;
-    p.eps = a->eps;
+    p.eps = a->eps > 0 && a->eps < FLT_MIN ? FLT_MIN : a->eps;   // (below every mean of squares that is not 0)
     p.n_tokens = a->n_tokens;
     p.n_q_heads = a->n_q_heads;
     p.n_kv_heads = a->n_kv_heads;
@@ -187,7 +201,7 @@ kvq_status kvq_page_fork(int32_t n_seqs, int32_t page_tokens, int32_t n_pages, c
         if (max_blocks > 0 && table_out == block_table && (parent || out_stride != table_stride)) return KVQ_ERR_INVALID_ARG;
     }
     int n_sms = 0;
-    const kvq_status st = sms_of(&n_sms);
+    const kvq_status st = tokens_setup(&n_sms);
     if (st != KVQ_OK) return st;
     const ForkPlan f = plan_fork(n_seqs, n_pages);
     if (!workspace || workspace_bytes < f.bytes || !aligned(workspace, 256)) return KVQ_ERR_WORKSPACE;
@@ -237,7 +251,7 @@ kvq_status kvq_page_copy(const kvq_pages *pools, int32_t n_pools, const int32_t 
     if (n_copies == 0 || n_pools == 0 || pools->n_pages == 0) return KVQ_OK;
     if (!int_ptr(from) || !int_ptr(to) || !aligned(held, 4)) return KVQ_ERR_INVALID_ARG;
     int n_sms = 0;
-    const kvq_status st = sms_of(&n_sms);
+    const kvq_status st = tokens_setup(&n_sms);
     if (st != KVQ_OK) return st;
     CopyParams p = {};
     for (int i = 0; i < n_pools; ++i) {
@@ -277,7 +291,7 @@ kvq_status kvq_paged_move(const kvq_pages *p, const int32_t *from, const int32_t
     if (n_tokens == 0 || p->n_pages == 0) return KVQ_OK;
     if (!int_ptr(from) || !int_ptr(to)) return KVQ_ERR_INVALID_ARG;
     int n_sms = 0;
-    st = sms_of(&n_sms);
+    st = tokens_setup(&n_sms);
     if (st != KVQ_OK) return st;
     size_t need = 0;
     if (staged) kvq_paged_move_workspace_size(p, n_tokens, &need);
