@@ -1,8 +1,6 @@
 // kvq_qkv.cu -- new tokens on their way into the paged cache: heads normalized
 // and rotated, queries (and keys, without pages) written as fp16, keys and values
 // quantized into their slots.
-#include <cstdlib>
-
 #include "kvq_quad.cuh"
 
 namespace kvq {
@@ -11,6 +9,8 @@ constexpr int kQkvWarps = 8;
 constexpr int kQkvTokens = 8;   // tokens of a block
 
 constexpr int kBatch = 4;       // rows that an octet takes at a time
+static_assert(kQkvWarps * 32 == 2 * kD, "a thread to each weight of the two norms");
+static_assert(kQkvTokens == 8 && kQkvWarps % 4 == 0, "four tokens to a warp, and four groups of them in a block at most");
 
 struct QkvShared {
     uint16_t ring[kQkvWarps][2][kBatch][4][kD];
@@ -318,6 +318,20 @@ __global__ void __launch_bounds__(kQkvWarps * 32, 3) qkv_kernel(const __grid_con
     // slots of the token before the block's, of its own, and of the one behind
     const int at = t0 - 1 + lane;
     const int slot = lane < kQkvTokens + 2 && at >= 0 && at < p.n_tokens ? (p.slots ? p.slots[at] : 0) : -1;
+    // what the thread's angles and weights are made of: asked for before anything waits for the slots
+    const int aj = threadIdx.x % (kD / 2), at0 = threadIdx.x / (kD / 2);
+    const bool turns = ROT != kRotNone && aj < n_rot / 2;
+    constexpr int kAngles = kQkvTokens * (kD / 2) / (kQkvWarps * 32);   // of a thread, and one more in some blocks
+    unsigned long long rate = 0;
+    int pos[kAngles];
+    if (turns) rate = p.rope.turns[aj];
+#pragma unroll
+    for (int i = 0; i < kAngles; ++i) {
+        const int t = t0 + at0 + i * (kQkvTokens / kAngles);
+        pos[i] = turns && t < p.n_tokens ? p.positions[t] : 0;
+    }
+    const float *norm = threadIdx.x < kD ? p.q_norm : p.k_norm;
+    const float weight = norm ? norm[threadIdx.x % kD] : 0.f;
     const int q1 = min(p.n_q_heads, (share + 1) * p.q_heads), k1 = min(p.n_kv_heads, (share + 1) * p.kv_heads);
     auto piece = [](int h0, int h1, int parts, int part, int &first) {   // heads of one of the warps that share tokens
         const int each = (max(0, h1 - h0) + parts - 1) / parts;
@@ -357,21 +371,17 @@ __global__ void __launch_bounds__(kQkvWarps * 32, 3) qkv_kernel(const __grid_con
     w.to = smem_u32(sh.ring[warp][0][0][oct]) + 16 * c;
     stream_get<PAGED>(w);
     stream_get<PAGED>(w);
-    if (ROT != kRotNone) {
-        const int n = min(kQkvTokens + (beyond ? 1 : 0), p.n_tokens - t0), j = threadIdx.x % (kD / 2);
-        if (j < n_rot / 2) {
-            const unsigned long long rate = p.rope.turns[j];
-            for (int t = threadIdx.x / (kD / 2); t < n; t += kQkvWarps * 32 / (kD / 2)) {
-                const float2 a = angle_of(rate, p.positions[t0 + t], p.rope.amplitude);
-                sh.cosines[t][j] = a.x;
-                sh.sines[t][j] = a.y;
-            }
-        }
+    if (turns) {
+        auto put = [&](int t, int position) {
+            const float2 a = angle_of(rate, position, p.rope.amplitude);
+            sh.cosines[t][aj] = a.x;
+            sh.sines[t][aj] = a.y;
+        };
+#pragma unroll
+        for (int i = 0; i < kAngles; ++i) put(at0 + i * (kQkvTokens / kAngles), pos[i]);
+        if (beyond && at0 == 0) put(kQkvTokens, p.positions[t0 + kQkvTokens]);
     }
-    {
-        const float *norm = threadIdx.x < kD ? p.q_norm : p.k_norm;
-        if (norm) sh.norm[threadIdx.x / kD][threadIdx.x % kD] = norm[threadIdx.x % kD];
-    }
+    sh.norm[threadIdx.x / kD][threadIdx.x % kD] = weight;
     __syncthreads();
     const float *q_norm = p.q_norm ? sh.norm[0] : nullptr, *k_norm = p.k_norm ? sh.norm[1] : nullptr;
     OctCoef k;
@@ -464,8 +474,10 @@ cudaError_t launch_qkv(const QkvParams &in, int v_type, int k_type, int n_sms, c
     QkvParams p = in;
     const int tiles = (int)(((long long)p.n_tokens + kQkvTokens - 1) / kQkvTokens);
     const int most = (p.n_q_heads > p.n_kv_heads ? p.n_q_heads : p.n_kv_heads) / 2;
-    const char *e = getenv("KVQ_TMP");
-    const long long want = (long long)n_sms * (e ? atoi(e) : 2);
+    // Shares of the heads until there are two blocks for every SM: what a block does before its first row costs about
+    // ten rows of a warp (777 tokens, 64 + 8 heads: 9.4 us at one block for every SM, 8.6 at two, 11.7 at four; 64
+    // tokens, 32 + 8 heads: one share for every two heads, 4.1).
+    const long long want = 2ll * n_sms;
     long long chunks = (want + tiles - 1) / tiles;
     chunks = chunks > most ? most : chunks;
     p.chunks = chunks < 1 ? 1 : (int)chunks;
