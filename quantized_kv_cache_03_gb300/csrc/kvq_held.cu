@@ -1,7 +1,6 @@
 // kvq_held.cu -- what the paged cache holds: positions of a step's rows, tables
 // forked, pages copied, tokens moved and their keys turned.
-#include "kvq_paged_line.cuh"
-#include "kvq_tokens.cuh"
+#include "kvq_quad.cuh"
 
 namespace kvq {
 
@@ -293,228 +292,293 @@ cudaError_t launch_page_copy(const CopyParams &p, cudaStream_t s, bool pdl)
 }
 
 // ---------------------------------------------------------------------------
-// Move: a warp takes a token (four values a lane), or two whose new slots are an
-// even place and the next, which share words of V codes and scales.
+// Move: a quad of lanes takes a token of a head (kvq_quad.cuh), a warp eight at a
+// time: four pairs of tokens whose new slots are an even place and the next, which
+// share words of V codes, or, where the list has no pairs, eight tokens.  A warp
+// looks at eight tokens of the list and goes over some of the heads.
 // ---------------------------------------------------------------------------
-constexpr int kMoveWarps = 8;
-
-// The row at place u of a tile, as paged_token would give it.
-template <int VT, int KT>
-__device__ __forceinline__ TokenRow load_token_paged(const uint8_t *tile, int u, int lane, bool want_v)
-{
-    using T = PageTile<VT, KT>;
-    TokenRow t;
-    const int b = lane >> 3, ue = u & ~1;
-    t.kw = *reinterpret_cast<const uint32_t *>(tile + (KT == KVQ_K_F16 ? k16_tile_off(u, 4 * lane) : k_tile_off(u, 4 * lane)));
-    t.kw2 = KT == KVQ_K_F16 ? *reinterpret_cast<const uint32_t *>(tile + k16_tile_off(u, 4 * lane + 2)) : 0;
-    t.ks = KT == KVQ_K_F16 ? 0 : *reinterpret_cast<const uint16_t *>(tile + T::KS_OFF + scale_off(u, b));
-    t.vw = 0;
-    t.vs = 0;
-    if (!want_v) return t;
-    const uint8_t *vt = tile + T::V_OFF;
-    if (VT == KVQ_V_Q8_0) {
-        const uint2 w = *reinterpret_cast<const uint2 *>(vt + v8_pair_off(ue, lane));
-        t.vw = __byte_perm(w.x, w.y, u & 1 ? 0x7531 : 0x6420);
-    } else {
-        const uint32_t x = *reinterpret_cast<const uint32_t *>(vt + v4_pair_off(ue, b, 2 * (lane & 3)));
-        const uint32_t y = *reinterpret_cast<const uint32_t *>(vt + v4_pair_off(ue, b, 2 * (lane & 3) + 1));
-        t.vw = __byte_perm(x, y, u & 1 ? 0x7632 : 0x5410);
-    }
-    t.vs = *reinterpret_cast<const uint16_t *>(tile + T::VS_OFF + scale_off(u, b));
-    return t;
-}
-
-// A lane's part in a rotation: four values of which the other half of each pair is
-// its own (pairs side by side) or those of lane `other`.
-struct MoveTurn {
-    float2 cs[4];
-    int other;
-    bool rotates, second;
-    template <int PAIRS>
-    __device__ __forceinline__ void set(const RopeDesc &r, int pos, int lane)
-    {
-        const int h4 = r.n_rot >> 3;   // lanes of first values
-        rotates = lane < 2 * h4;
-        second = !PAIRS && lane >= h4;
-        other = PAIRS || !rotates ? lane : second ? lane - h4 : lane + h4;
-#pragma unroll
-        for (int i = 0; i < (PAIRS ? 2 : 4); ++i)
-            cs[i] = rotates ? angle_of(r.turns[PAIRS ? 2 * lane + i : 4 * (second ? other : lane) + i], pos, 1.f) : make_float2(1.f, 0.f);
-    }
-};
-
-template <int KT, int PAIRS>
-__device__ __forceinline__ void turn_key(TokenRow &t, const MoveTurn &m, const RopeDesc &r, int lane)
-{
-    auto values = [&](uint32_t w, uint32_t w2, float s, float (&x)[4]) {
-        if (KT == KVQ_K_F16) {
-            const float2 a = half2_of(w), b = half2_of(w2);
-            x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = (float)((int)(w >> (8 * k) & 0xff) - 128) * s;
-        }
-    };
-    const float s = __half2float(__ushort_as_half(t.ks));
-    float x[4], y[4];
-    values(t.kw, t.kw2, s, x);
-    if (PAIRS) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            y[2 * i] = x[2 * i] * m.cs[i].x - x[2 * i + 1] * m.cs[i].y;
-            y[2 * i + 1] = x[2 * i] * m.cs[i].y + x[2 * i + 1] * m.cs[i].x;
-        }
-    } else {
-        float o[4];
-        const uint32_t w = __shfl_sync(0xffffffffu, t.kw, m.other), w2 = KT == KVQ_K_F16 ? __shfl_sync(0xffffffffu, t.kw2, m.other) : 0;
-        values(w, w2, KT == KVQ_K_F16 ? 0.f : __shfl_sync(0xffffffffu, s, m.other), o);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = m.second ? o[i] * m.cs[i].y + x[i] * m.cs[i].x : x[i] * m.cs[i].x - o[i] * m.cs[i].y;
-    }
-    const uint32_t a = pack_half2(y[0], y[1]), b = pack_half2(y[2], y[3]);
-    if (KT == KVQ_K_F16) {
-        if (m.rotates) t.kw = a, t.kw2 = b;
-        return;
-    }
-    // values of the block that do not rotate are code * scale, rounded like the others
-    auto h2 = [](uint32_t w) { return *reinterpret_cast<const __half2 *>(&w); };
-    const uint32_t a1 = m.rotates ? a : pack_half2(x[0], x[1]), b1 = m.rotates ? b : pack_half2(x[2], x[3]);
-    __half2 top = __hmax2(h2(a1 & 0x7fff7fffu), h2(b1 & 0x7fff7fffu));
-    top = __hmax2(top, __lowhigh2highlow(top));
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-        const uint32_t z = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t *>(&top), o);
-        top = __hmax2(top, h2(z));
-    }
-    const __half sn = __float2half_rn(__low2float(top) * (1.f / 127.f));
-    const uint32_t codes = codes4(a1, b1, __half2float(sn), -127.f, 127.f, 128);
-    if ((lane & ~7) * 4 < r.n_rot) {   // the block holds a value that rotates
-        t.kw = codes;
-        t.ks = __half_as_ushort(sn);
-    }
-}
+constexpr int kMoveWarps = 4;
+constexpr int kMoveTokens = 8;   // of a warp
 
 // Which half of the way: from slots to slots, from slots to the staged rows, from those to slots.
 constexpr int kMoveDirect = 0, kMoveOut = 1, kMoveIn = 2;
 
-template <int VT, int KT>
-__device__ __forceinline__ void stage_row(uint8_t *row, const TokenRow &t, int lane)
+struct alignas(16) MoveShared {   // (read in words of 16 bytes, warp after warp)
+    float cosines[kMoveTokens][kAngleRow], sines[kMoveTokens][kAngleRow];   // of the quads' turns; of row 0 alone where they are the same
+    uint8_t list[kMoveTokens];
+};
+
+// The lane's values of a held key in fp32, a block at a time as quad_floats has them.
+template <int KT, int ROT>
+__device__ __forceinline__ void key_floats(const uint32_t *w, float scale, float2 (&x)[4])
 {
-    if (KT == KVQ_K_F16) reinterpret_cast<uint2 *>(row)[lane] = make_uint2(t.kw, t.kw2);
-    else reinterpret_cast<uint32_t *>(row)[lane] = t.kw;
-    row += KT == KVQ_K_F16 ? 256 : 128;
-    if (VT == KVQ_V_Q8_0) reinterpret_cast<uint32_t *>(row)[lane] = t.vw;
-    else if ((lane & 7) < 4) reinterpret_cast<uint32_t *>(row)[(lane >> 3) * 4 + (lane & 3)] = t.vw;
-    row += VT == KVQ_V_Q8_0 ? 128 : 64;
-    if ((lane & 7) == 0) {
-        if (KT != KVQ_K_F16) reinterpret_cast<uint16_t *>(row)[4 + (lane >> 3)] = t.ks;
-        reinterpret_cast<uint16_t *>(row)[lane >> 3] = t.vs;
-    }
-}
-template <int VT, int KT>
-__device__ __forceinline__ TokenRow unstage_row(const uint8_t *row, int lane)
-{
-    TokenRow t;
     if (KT == KVQ_K_F16) {
-        const uint2 w = reinterpret_cast<const uint2 *>(row)[lane];
-        t.kw = w.x;
-        t.kw2 = w.y;
-    } else {
-        t.kw = reinterpret_cast<const uint32_t *>(row)[lane];
-        t.kw2 = 0;
+        quad_floats<ROT>(make_uint4(w[0], w[1], w[2], w[3]), x);
+    } else {   // code + 128 under the exponent of 2^23
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(__byte_perm(w[k >> 2], 0x4b000000u, 0x7440 | (k & 3)));
+        const float2 less = make_float2(-8388736.f, -8388736.f), s2 = make_float2(scale, scale);
+        if (ROT == kRotPairs) {
+            x[0] = make_float2(v[0], v[2]);
+            x[1] = make_float2(v[4], v[6]);
+            x[2] = make_float2(v[1], v[3]);
+            x[3] = make_float2(v[5], v[7]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = make_float2(v[2 * k], v[2 * k + 1]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = mul2(add2(x[k], less), s2);
     }
-    row += KT == KVQ_K_F16 ? 256 : 128;
-    t.vw = reinterpret_cast<const uint32_t *>(row)[VT == KVQ_V_Q8_0 ? lane : (lane >> 3) * 4 + (lane & 3)];
-    row += VT == KVQ_V_Q8_0 ? 128 : 64;
-    t.ks = KT == KVQ_K_F16 ? 0 : reinterpret_cast<const uint16_t *>(row)[4 + (lane >> 3)];
-    t.vs = reinterpret_cast<const uint16_t *>(row)[lane >> 3];
-    return t;
 }
 
-template <int VT, int KT, int PAIRS, int WAY>
+// The quad's key turned (where `turns`: the others' stay as they are).  scratch:
+// the quad's 128 floats in shared memory (part).
+template <int VT, int KT, int ROT>
+__device__ __forceinline__ void turn_key(QuadRow<VT, KT> &r, bool turns, const float *cosines, const float *sines, int c, int n_rot, float *scratch)
+{
+    constexpr int kWords = KT == KVQ_K_F16 ? 4 : 2;   // of a block
+    const float2 s01 = half2_of(r.ks[0]), s23 = half2_of(r.ks[1]);
+    const float scale[4] = {s01.x, s01.y, s23.x, s23.y};
+    QuadF x;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) key_floats<KT, ROT>(r.k + kWords * b, scale[b], x.b[b]);
+    if (ROT == kRotPart) {   // neighbours to group pairs, and back
+        __syncwarp();
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                *reinterpret_cast<float4 *>(scratch + 32 * b + 8 * c + 4 * k) = make_float4(x.b[b][2 * k].x, x.b[b][2 * k].y, x.b[b][2 * k + 1].x, x.b[b][2 * k + 1].y);
+        __syncwarp();
+        QuadF y;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const PartGroups g(c + 4 * b, n_rot);
+            const float4 u = *reinterpret_cast<const float4 *>(scratch + g.a), v = *reinterpret_cast<const float4 *>(scratch + g.b);
+            y.b[b][0] = make_float2(u.x, u.y);
+            y.b[b][1] = make_float2(u.z, u.w);
+            y.b[b][2] = make_float2(v.x, v.y);
+            y.b[b][3] = make_float2(v.z, v.w);
+        }
+        quad_turn<ROT>(y, cosines, sines, c, n_rot);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const PartGroups g(c + 4 * b, n_rot);
+            *reinterpret_cast<float4 *>(scratch + g.a) = make_float4(y.b[b][0].x, y.b[b][0].y, y.b[b][1].x, y.b[b][1].y);
+            *reinterpret_cast<float4 *>(scratch + g.b) = make_float4(y.b[b][2].x, y.b[b][2].y, y.b[b][3].x, y.b[b][3].y);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float4 u = *reinterpret_cast<const float4 *>(scratch + 32 * b + 8 * c + 4 * k);
+                x.b[b][2 * k] = make_float2(u.x, u.y);
+                x.b[b][2 * k + 1] = make_float2(u.z, u.w);
+            }
+    } else {
+        quad_turn<ROT>(x, cosines, sines, c, n_rot);
+    }
+    Quad16 h;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) h.b[b] = quad_halves<ROT>(x.b[b]);
+    if (KT == KVQ_K_F16) {
+        if (turns)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                r.k[kWords * b] = h.b[b].x;
+                r.k[kWords * b + 1] = h.b[b].y;
+                r.k[kWords * b + kWords - 2] = h.b[b].z;
+                r.k[kWords * b + kWords - 1] = h.b[b].w;
+            }
+        return;
+    }
+    const QuadCodes q = quad_quantize<false>(h);
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+        if (turns && 32 * b < n_rot) {   // the block holds a value that rotates
+            r.k[kWords * b] = q.w[2 * b];
+            r.k[kWords * b + 1] = q.w[2 * b + 1];
+            const uint32_t half = b & 1 ? 0xffff0000u : 0xffffu;
+            r.ks[b >> 1] = (r.ks[b >> 1] & ~half) | (q.s[b >> 1] & half);
+        }
+}
+
+// A staged row: the lanes' parts one after another, then the scales.
+template <int VT, int KT>
+struct Staged {
+    static constexpr int K = 4 * QuadRow<VT, KT>::KW, V = 4 * QuadRow<VT, KT>::VW;   // bytes of a lane
+    static constexpr int BYTES = (4 * (K + V) + (KT == KVQ_K_F16 ? 8 : 16) + 15) / 16 * 16;
+};
+template <int N>
+__device__ __forceinline__ void put_words(uint8_t *to, const uint32_t (&w)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 4) *reinterpret_cast<uint4 *>(to + 4 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+}
+template <int N>
+__device__ __forceinline__ void get_words(const uint8_t *from, uint32_t (&w)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(from + 4 * i);
+        w[i] = v.x;
+        w[i + 1] = v.y;
+        w[i + 2] = v.z;
+        w[i + 3] = v.w;
+    }
+}
+template <int VT, int KT>
+__device__ __forceinline__ void stage_put(uint8_t *row, const QuadRow<VT, KT> &r, int c)
+{
+    using S = Staged<VT, KT>;
+    put_words(row + S::K * c, r.k);
+    put_words(row + 4 * S::K + S::V * c, r.v);
+    uint8_t *scales = row + 4 * (S::K + S::V);
+    reinterpret_cast<uint16_t *>(scales)[c] = (uint16_t)r.vs;
+    if (KT != KVQ_K_F16 && c == 0) *reinterpret_cast<uint2 *>(scales + 8) = make_uint2(r.ks[0], r.ks[1]);
+}
+template <int VT, int KT>
+__device__ __forceinline__ void stage_get(const uint8_t *row, QuadRow<VT, KT> &r, int c)
+{
+    using S = Staged<VT, KT>;
+    get_words(row + S::K * c, r.k);
+    get_words(row + 4 * S::K + S::V * c, r.v);
+    const uint8_t *scales = row + 4 * (S::K + S::V);
+    r.vs = reinterpret_cast<const uint16_t *>(scales)[c];
+    r.ks[0] = r.ks[1] = 0;
+    if (KT != KVQ_K_F16) {
+        const uint2 s = *reinterpret_cast<const uint2 *>(scales + 8);
+        r.ks[0] = s.x;
+        r.ks[1] = s.y;
+    }
+}
+
+template <int VT, int KT, int ROT, int WAY>
 __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const MoveParams p)
 {
-    using T = PageTile<VT, KT>;
-    constexpr int kRow = T::BYTES / kWTile;
+    constexpr int kTile = PageTile<VT, KT>::BYTES, kRow = Staged<VT, KT>::BYTES;
+    __shared__ __align__(16) MoveShared shared[kMoveWarps];
+    __shared__ __align__(16) float scratch[ROT == kRotPart ? kMoveWarps : 1][8][ROT == kRotPart ? kD + 4 : 1];
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const unsigned token_blocks = (unsigned)(p.n_tokens + kMoveWarps - 1) / kMoveWarps;
-    const int c = blockIdx.x / token_blocks, tok = (int)(blockIdx.x - c * token_blocks) * kMoveWarps + warp;
-    if (tok >= p.n_tokens) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, quad = lane >> 2;
+    MoveShared &sh = shared[warp];
+    const long long job = (long long)blockIdx.x * kMoveWarps + warp;
+    const int window = (int)(job / p.chunks), share = (int)(job - (long long)window * p.chunks);
+    const long long t0 = (long long)window * kMoveTokens;
+    if (t0 >= p.n_tokens) return;
+    // the list's tokens: the one before the window, its own, the one behind
+    const long long at = t0 - 1 + lane;
+    const bool there = lane < kMoveTokens + 2 && at >= 0 && at < p.n_tokens;
+    const int from_all = there ? p.from[at] : -1, to_all = there ? p.to[at] : -1;
+    const int turn_all = ROT != kRotNone && there ? p.turn[at] : 0;
     auto inside = [&](int slot) { return slot >= 0 && slot < p.pool.n_slots; };
-    auto moves = [&](int i) { return i >= 0 && i < p.n_tokens && inside(p.from[i]) && inside(p.to[i]); };
-    if (!moves(tok)) return;
-    const int to = p.to[tok];
-    if ((to & 1) && tok > 0 && p.to[tok - 1] == to - 1 && moves(tok - 1)) return;   // the warp before takes it
-    const bool pair = !(to & 1) && tok + 1 < p.n_tokens && p.to[tok + 1] == to + 1 && moves(tok + 1);
-    int from[2] = {p.from[tok], pair ? p.from[tok + 1] : -1}, turn[2] = {0, 0};
-    MoveTurn m[2];
-    if (WAY != kMoveIn && p.turn) {
-        turn[0] = p.turn[tok];
-        if (pair) turn[1] = p.turn[tok + 1];
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (turn[e] != 0) m[e].template set<PAIRS>(p.rope, turn[e], lane);
-    }
-    const int P1 = (1 << p.pool.pshift) - 1;
-    const bool still = WAY == kMoveDirect && from[0] == to && (!pair || from[1] == to + 1);   // only keys change
-    if (still && turn[0] == 0 && turn[1] == 0) return;
-    const int h1 = min(p.pool.n_kv_heads, (c + 1) * p.heads);
-    for (int h = c * p.heads; h < h1; ++h) {
-        TokenRow t[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            if (e == 1 && !pair) break;
-            if (WAY == kMoveIn) {
-                t[e] = unstage_row<VT, KT>(p.rows + ((size_t)(tok + e) * p.pool.n_kv_heads + h) * kRow, lane);
-                continue;
+    const SlotPairs q = slot_pairs(to_all, inside(from_all) && inside(to_all), kMoveTokens);
+    if (q.leads == 0) return;
+    slot_list(q, sh.list);
+    const bool pairs = (q.pair & q.lead) != 0;
+    const int per = pairs ? 4 : 8, e = pairs ? quad & 1 : 0, P1 = (1 << p.pool.pshift) - 1;
+    const int h0 = share * p.heads, h1 = min(p.pool.n_kv_heads, h0 + p.heads);
+    const size_t head_bytes = (size_t)kTile << (p.pool.pshift - 4);
+    for (int g = 0; g < q.leads; g += per) {
+        const int n = g + (pairs ? quad >> 1 : quad), lead = sh.list[min(n, q.leads - 1)];
+        const bool pair = q.pair >> lead & 1, mine = n < q.leads && (e == 0 || pair);
+        const int i = lead + (pair ? e : 0);
+        const int from = __shfl_sync(0xffffffffu, from_all, i), to = __shfl_sync(0xffffffffu, to_all, i), turn = __shfl_sync(0xffffffffu, turn_all, i);
+        const bool turns = mine && turn != 0;
+        // a token that stays keeps its V, unless the other of its pair comes from elsewhere and they share words
+        const bool stays = WAY == kMoveDirect && from == to, other_stays = __shfl_xor_sync(0xffffffffu, stays, 4);
+        const bool still = stays && (!pair || other_stays);
+        // angles of the quads' turns, one row for all where they are the same
+        int row = 0;
+        bool any = false;
+        if (ROT != kRotNone) {
+            any = __any_sync(0xffffffffu, turns);
+            const int one = __shfl_sync(0xffffffffu, turn, __ffs(__ballot_sync(0xffffffffu, turns) | 0x80000000u) - 1);
+            const bool same = __all_sync(0xffffffffu, !turns || turn == one);
+            if (any) {
+                __syncwarp();   // the rows before may still be read
+                const int half_n = p.rope.n_rot / 2;
+                for (int k = 0; k < (same ? 1 : kMoveTokens); ++k) {
+                    const int t = same ? one : __shfl_sync(0xffffffffu, turn, 4 * k);
+                    for (int j = lane; j < half_n; j += 32) {
+                        const float2 a = angle_of(p.rope.turns[j], t, 1.f);
+                        sh.cosines[k][j] = a.x;
+                        sh.sines[k][j] = a.y;
+                    }
+                }
+                __syncwarp();
             }
-            const int place = from[e] & P1;
-            t[e] = load_token_paged<VT, KT>(tile_of(p.pool, from[e] >> p.pool.pshift, h, place >> 4, T::BYTES), place & 15, lane, !still);
-            if (turn[e] != 0) turn_key<KT, PAIRS>(t[e], m[e], p.rope, lane);
-            if (WAY == kMoveOut) stage_row<VT, KT>(p.rows + ((size_t)(tok + e) * p.pool.n_kv_heads + h) * kRow, t[e], lane);
+            row = same ? 0 : quad;
         }
-        if (WAY == kMoveOut) continue;
-        const int place = to & P1;
-        uint8_t *tile = tile_of(p.pool, to >> p.pool.pshift, h, place >> 4, T::BYTES);
-        if (still) {
+        const bool values = __any_sync(0xffffffffu, mine && !still);
+        if (!values && !any) continue;   // nothing changes
+        const int fu = from & 15, tu = to & 15;
+        const uint8_t *src = tile_of(p.pool, from >> p.pool.pshift, h0, (from & P1) >> 4, kTile);
+        uint8_t *dst = tile_of(p.pool, to >> p.pool.pshift, h0, (to & P1) >> 4, kTile);
+        uint8_t *staged = WAY == kMoveDirect ? nullptr : p.rows + ((size_t)(t0 + i - 1) * p.pool.n_kv_heads + h0) * kRow;
+        QuadRow<VT, KT> r;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (e == 1 && !pair) break;
-                store_k_paged<VT, KT>(t[e], (place & 15) + e, lane, tile);
-                if (KT != KVQ_K_F16 && (lane & 7) == 0) *reinterpret_cast<uint16_t *>(tile + T::KS_OFF + scale_off((place & 15) + e, lane >> 3)) = t[e].ks;
+        for (int k = 0; k < QuadRow<VT, KT>::KW; ++k) r.k[k] = 0;
+#pragma unroll
+        for (int k = 0; k < QuadRow<VT, KT>::VW; ++k) r.v[k] = 0;
+        r.ks[0] = r.ks[1] = r.vs = 0;
+        for (int h = h0; h < h1; ++h) {
+            if (WAY == kMoveIn) {
+                if (mine) stage_get<VT, KT>(staged, r, c);
+            } else if (mine) {
+                quad_get_key<VT, KT>(r, src, fu, c);
+                if (!still) quad_get_value<VT, KT>(r, src, fu, c);
             }
-        } else if (pair) {
-            store_pair_paged<VT, KT>(t[0], t[1], place & 15, lane, tile);
-        } else {
-            store_token_paged<VT, KT>(t[0], place & 15, lane, tile);
+            if (ROT != kRotNone && any) turn_key<VT, KT, ROT>(r, turns, sh.cosines[row], sh.sines[row], c, p.rope.n_rot, scratch[ROT == kRotPart ? warp : 0][ROT == kRotPart ? quad : 0]);
+            if (WAY == kMoveOut) {
+                if (mine) stage_put<VT, KT>(staged, r, c);
+            } else {
+                if (mine && (!still || turns)) quad_put_key<VT, KT>(r, dst, tu, c);
+                if (values) quad_put_value<VT, KT>(r, dst, tu, c, pair, mine && !still);
+            }
+            src += head_bytes;
+            dst += head_bytes;
+            staged += kRow;
         }
     }
 }
 
-template <int VT, int KT, int PAIRS>
+template <int VT, int KT, int ROT>
 static cudaError_t move_t(const MoveParams &p, int blocks, cudaStream_t s, bool pdl)
 {
-    if (!p.rows) return launch_pdl(move_kernel<VT, KT, PAIRS, kMoveDirect>, p, blocks, kMoveWarps * 32, 0, s, pdl);
-    const cudaError_t e = launch_pdl(move_kernel<VT, KT, PAIRS, kMoveOut>, p, blocks, kMoveWarps * 32, 0, s, pdl);
-    return e != cudaSuccess ? e : launch_pdl(move_kernel<VT, KT, PAIRS, kMoveIn>, p, blocks, kMoveWarps * 32, 0, s, pdl);
+    if (!p.rows) return launch_pdl(move_kernel<VT, KT, ROT, kMoveDirect>, p, blocks, kMoveWarps * 32, 0, s, pdl);
+    const cudaError_t e = launch_pdl(move_kernel<VT, KT, ROT, kMoveOut>, p, blocks, kMoveWarps * 32, 0, s, pdl);
+    return e != cudaSuccess ? e : launch_pdl(move_kernel<VT, KT, kRotNone, kMoveIn>, p, blocks, kMoveWarps * 32, 0, s, pdl);
+}
+
+template <int VT, int KT>
+static cudaError_t move_rot(const MoveParams &p, int blocks, cudaStream_t s, bool pdl)
+{
+    if (!p.turn) return move_t<VT, KT, kRotNone>(p, blocks, s, pdl);
+    if (p.rope.pairs) return move_t<VT, KT, kRotPairs>(p, blocks, s, pdl);
+    return p.rope.n_rot == kD ? move_t<VT, KT, kRotHalf>(p, blocks, s, pdl) : move_t<VT, KT, kRotPart>(p, blocks, s, pdl);
+}
+
+int staged_row_bytes(int v_type, int k_type)
+{
+    if (v_type == KVQ_V_Q4_0) return k_type == KVQ_K_F16 ? Staged<KVQ_V_Q4_0, KVQ_K_F16>::BYTES : Staged<KVQ_V_Q4_0, KVQ_K_I8>::BYTES;
+    return k_type == KVQ_K_F16 ? Staged<KVQ_V_Q8_0, KVQ_K_F16>::BYTES : Staged<KVQ_V_Q8_0, KVQ_K_I8>::BYTES;
 }
 
 cudaError_t launch_paged_move(const MoveParams &in, int v_type, int k_type, int n_sms, cudaStream_t s, bool pdl)
 {
     MoveParams p = in;
-    const long long want = (long long)p.pool.n_kv_heads * p.n_tokens / 2 / ((long long)n_sms * 48);
+    const long long windows = ((long long)p.n_tokens + kMoveTokens - 1) / kMoveTokens;
+    const long long want = windows * p.pool.n_kv_heads / ((long long)n_sms * 24);
     p.heads = want < 1 ? 1 : want > p.pool.n_kv_heads ? p.pool.n_kv_heads : (int)want;
     p.chunks = (p.pool.n_kv_heads + p.heads - 1) / p.heads;
-    const int blocks = (int)(((long long)p.n_tokens + kMoveWarps - 1) / kMoveWarps * p.chunks);
-    const bool pairs = p.rope.pairs, f16 = k_type == KVQ_K_F16;
-    if (v_type == KVQ_V_Q4_0) {
-        if (f16) return pairs ? move_t<KVQ_V_Q4_0, KVQ_K_F16, 1>(p, blocks, s, pdl) : move_t<KVQ_V_Q4_0, KVQ_K_F16, 0>(p, blocks, s, pdl);
-        return pairs ? move_t<KVQ_V_Q4_0, KVQ_K_I8, 1>(p, blocks, s, pdl) : move_t<KVQ_V_Q4_0, KVQ_K_I8, 0>(p, blocks, s, pdl);
-    }
-    if (f16) return pairs ? move_t<KVQ_V_Q8_0, KVQ_K_F16, 1>(p, blocks, s, pdl) : move_t<KVQ_V_Q8_0, KVQ_K_F16, 0>(p, blocks, s, pdl);
-    return pairs ? move_t<KVQ_V_Q8_0, KVQ_K_I8, 1>(p, blocks, s, pdl) : move_t<KVQ_V_Q8_0, KVQ_K_I8, 0>(p, blocks, s, pdl);
+    const int blocks = (int)((windows * p.chunks + kMoveWarps - 1) / kMoveWarps);
+    if (v_type == KVQ_V_Q4_0) return k_type == KVQ_K_F16 ? move_rot<KVQ_V_Q4_0, KVQ_K_F16>(p, blocks, s, pdl) : move_rot<KVQ_V_Q4_0, KVQ_K_I8>(p, blocks, s, pdl);
+    return k_type == KVQ_K_F16 ? move_rot<KVQ_V_Q8_0, KVQ_K_F16>(p, blocks, s, pdl) : move_rot<KVQ_V_Q8_0, KVQ_K_I8>(p, blocks, s, pdl);
 }
 
 }  // namespace kvq

@@ -69,7 +69,7 @@ struct MoveParams {
     const int *from, *to, *turn;   // turn: null without a rotation
     int n_tokens;
     int heads, chunks;             // kv heads of a warp, and such pieces of a token's
-    uint8_t *rows;                 // staged: [n_tokens][kv heads] rows of a tile's bytes / 16
+    uint8_t *rows;                 // staged: [n_tokens][kv heads] rows of staged_row_bytes()
 };
 
 constexpr int kForkCtas = 8, kForkThreads = 512;
@@ -80,6 +80,7 @@ cudaError_t launch_qkv(const QkvParams &p, int v_type, int k_type, int n_sms, cu
 cudaError_t launch_page_fork(const ForkParams &p, cudaStream_t s, bool pdl);
 cudaError_t launch_page_copy(const CopyParams &p, cudaStream_t s, bool pdl);
 // rows null: from slots to slots; else through them.
+int staged_row_bytes(int v_type, int k_type);
 cudaError_t launch_paged_move(const MoveParams &p, int v_type, int k_type, int n_sms, cudaStream_t s, bool pdl);
 
 }  // namespace kvq

@@ -276,7 +276,7 @@ kvq_status kvq_paged_move_workspace_size(const kvq_pages *p, int32_t n_tokens, s
     const kvq_status st = check_shape(p);
     if (st != KVQ_OK) return st;
     if (!move_size_ok(p, n_tokens)) return KVQ_ERR_INVALID_ARG;
-    *bytes = (size_t)n_tokens * p->n_kv_heads * (page_tile_bytes(p->v_type, p->k_type) / kWTile);
+    *bytes = (size_t)n_tokens * p->n_kv_heads * staged_row_bytes(p->v_type, p->k_type);
     return KVQ_OK;
 }
 

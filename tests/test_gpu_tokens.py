@@ -435,6 +435,32 @@ def test_moved_bytes(kind, page, H, n, k_type, v_type):
 
 
 @pytest.mark.parametrize("k_type,v_type", [(I8, Q4), (I8, Q8), (F16, Q4), (F16, Q8)])
+@pytest.mark.parametrize("turned", [False, True])
+def test_some_stay_and_some_move(turned, k_type, v_type):
+    """Pairs of neighbouring slots of which one's token stays where it is and the other's comes from elsewhere."""
+    r = np.random.default_rng(7)
+    page, H, n = 32, 3, 60
+    pool, rows = _filled(r, 6, page, H, k_type, v_type)
+    to = np.arange(n) + 1
+    frm = np.where(r.random(n) < 0.5, to, 100 + r.permutation(90)[:n])
+    turn = np.where(r.random(n) < 0.5, 0, r.integers(-99, 99, n)) if turned else np.zeros(n, int)
+    kvq.kvq_paged_move(pool, i32(frm), i32(to), rope=kvq.Rope(128, device=dev()) if turned else None, turn=i32(turn) if turned else None, staged=False)
+    got = _by_slot(pool)
+    for name, a in rows.items():
+        want, same = a.copy(), np.ones(len(a), bool)
+        want[to] = a[frm]
+        if name in ("kq", "ks", "k16"):
+            same[to[turn != 0]] = False
+        assert np.array_equal(got[name][same], want[same]), name
+    k0, k1 = values(rows, v_type)[0], values(got, v_type)[0]
+    y, size = rotated(k0[frm], turn, rates(128)[0], 1.0, HALF)
+    allowed = fp16_bound(y, size)
+    if k_type == I8:
+        allowed = allowed + 0.5 * np.repeat(got["ks"][to].copy().view(np.float16).astype(np.float64), 32, -1) * (1 + 2.0 ** -20)
+    assert (np.abs(k1[to] - y) <= allowed)[turn != 0].all()
+
+
+@pytest.mark.parametrize("k_type,v_type", [(I8, Q4), (I8, Q8), (F16, Q4), (F16, Q8)])
 @pytest.mark.parametrize("layout,n_rot", [(HALF, 128), (PAIRS, 128), (HALF, 40), (PAIRS, 40), (HALF, 8), (HALF, 64), (PAIRS, 96)])
 @pytest.mark.parametrize("way", ["still", "down", "apart"])
 def test_turned_keys(way, layout, n_rot, k_type, v_type):

@@ -191,7 +191,7 @@ def test_move_refuses(lib):
     assert lib.kvq_paged_move_workspace_size(ctypes.byref(_pages()), -1, ctypes.byref(n)) == BAD
     assert lib.kvq_paged_move_workspace_size(ctypes.byref(_pages(page_tokens=17)), 1, ctypes.byref(n)) == BAD
     assert lib.kvq_paged_move_workspace_size(ctypes.byref(_pages()), 1, None) == BAD
-    for k, v, row in ((0, 0, 208), (0, 1, 272), (1, 0, 328), (1, 1, 392)):
+    for k, v, row in ((0, 0, 208), (0, 1, 272), (1, 0, 336), (1, 1, 400)):
         assert lib.kvq_paged_move_workspace_size(ctypes.byref(_pages(k_type=k, v_type=v)), 7, ctypes.byref(n)) == OK and n.value == 7 * 2 * row
 
 
