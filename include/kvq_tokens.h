@@ -214,7 +214,7 @@ kvq_status kvq_page_fork_workspace_size(int32_t n_seqs, int32_t n_pages, size_t 
  *             page is written that another pair reads or writes.
  *  held       device int32 [n_copies]: only the tiles of the first held[i] positions
  *             are copied (whole tiles of 16).  NULL: whole pages.
- *  n_copies   0 or more; n_copies * n_pools * the most n_kv_heads at most 2^30.
+ *  n_copies   0 or more; n_copies * n_pools * the most n_kv_heads at most 2^28.
  */
 kvq_status kvq_page_copy(const kvq_pages *pools, int32_t n_pools, const int32_t *from, const int32_t *to,
                          const int32_t *held, int32_t n_copies, void *stream);

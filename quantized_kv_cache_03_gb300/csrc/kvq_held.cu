@@ -246,42 +246,48 @@ cudaError_t launch_page_fork(const ForkParams &p, cudaStream_t s, bool pdl)
 }
 
 // ---------------------------------------------------------------------------
-// Copy: a block takes one head of one page in one pool, whose tiles are one run
-// of bytes.
+// Copy: a warp takes up to 4 KB of one head of one page in one pool, whose tiles are
+// one run of bytes; all of it is on its way before the first is written.
 // ---------------------------------------------------------------------------
-constexpr int kCopyThreads = 128;
-constexpr int kCopyLoads = 8;
+constexpr int kCopyWarps = 8;
+constexpr int kCopyLoads = 8;                 // of 16 bytes a lane
+constexpr int kCopyPiece = 32 * kCopyLoads;   // words of 16 bytes
 
-__global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const __grid_constant__ CopyParams p)
+__global__ void __launch_bounds__(kCopyWarps * 32) page_copy_kernel(const __grid_constant__ CopyParams p)
 {
     pdl_wait();
     pdl_trigger();
-    const unsigned pool = blockIdx.y, i = blockIdx.x / (unsigned)p.most_heads, h = blockIdx.x - i * p.most_heads, heads = p.heads[pool];
-    if (h >= heads) return;
-    const int from = p.from[i], to = p.to[i];
+    const unsigned pool = blockIdx.y, i = blockIdx.x / (unsigned)p.blocks, unit = (blockIdx.x - i * p.blocks) * kCopyWarps + (threadIdx.x >> 5);
+    const int from = p.from[i], to = p.to[i], lane = threadIdx.x & 31;
     if (from < 0 || to < 0 || from >= p.n_pages || to >= p.n_pages || from == to) return;
+    const unsigned heads = p.heads[pool], h = unit / (unsigned)p.pieces, piece = unit - h * p.pieces;
+    if (h >= heads) return;
     int tiles = p.tiles;
     if (p.held) tiles = min(tiles, (int)(((long long)max(p.held[i], 0) + 15) >> 4));
     const int n = tiles * (p.tile_bytes[pool] / 16);
     const size_t run = (size_t)p.tiles * p.tile_bytes[pool];
     const uint4 *src = reinterpret_cast<const uint4 *>(p.data[pool] + ((size_t)from * heads + h) * run);
     uint4 *dst = reinterpret_cast<uint4 *>(p.data[pool] + ((size_t)to * heads + h) * run);
-    for (int k0 = threadIdx.x; k0 < n; k0 += kCopyThreads * kCopyLoads) {
-        uint4 v[kCopyLoads];
+    const int at = (int)piece * kCopyPiece + lane;
+    uint4 v[kCopyLoads];
 #pragma unroll
-        for (int k = 0; k < kCopyLoads; ++k)
-            if (k0 + k * kCopyThreads < n) v[k] = src[k0 + k * kCopyThreads];
+    for (int k = 0; k < kCopyLoads; ++k)
+        if (at + 32 * k < n) v[k] = __ldcs(src + at + 32 * k);
 #pragma unroll
-        for (int k = 0; k < kCopyLoads; ++k)
-            if (k0 + k * kCopyThreads < n) dst[k0 + k * kCopyThreads] = v[k];
-    }
+    for (int k = 0; k < kCopyLoads; ++k)
+        if (at + 32 * k < n) __stcs(dst + at + 32 * k, v[k]);
 }
 
-cudaError_t launch_page_copy(const CopyParams &p, cudaStream_t s, bool pdl)
+cudaError_t launch_page_copy(const CopyParams &in, cudaStream_t s, bool pdl)
 {
+    CopyParams p = in;
+    int words = 0;
+    for (int i = 0; i < p.n_pools; ++i) words = p.tiles * (p.tile_bytes[i] / 16) > words ? p.tiles * (p.tile_bytes[i] / 16) : words;
+    p.pieces = (words + kCopyPiece - 1) / kCopyPiece;
+    p.blocks = (p.most_heads * p.pieces + kCopyWarps - 1) / kCopyWarps;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.n_copies * p.most_heads, p.n_pools);
-    cfg.blockDim = dim3(kCopyThreads);
+    cfg.gridDim = dim3(p.n_copies * p.blocks, p.n_pools);
+    cfg.blockDim = dim3(kCopyWarps * 32);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -333,9 +339,9 @@ __device__ __forceinline__ void key_floats(const uint32_t *w, float scale, float
     }
 }
 
-// The quad's key turned (where `turns`: the others' stay as they are).  scratch:
-// the quad's 128 floats in shared memory (part).
-template <int VT, int KT, int ROT>
+// The quad's key turned; SOME: only where `turns`, the others' stay as they are.
+// scratch: the quad's 128 floats in shared memory (part).
+template <bool SOME, int VT, int KT, int ROT>
 __device__ __forceinline__ void turn_key(QuadRow<VT, KT> &r, bool turns, const float *cosines, const float *sines, int c, int n_rot, float *scratch)
 {
     constexpr int kWords = KT == KVQ_K_F16 ? 4 : 2;   // of a block
@@ -385,7 +391,7 @@ __device__ __forceinline__ void turn_key(QuadRow<VT, KT> &r, bool turns, const f
 #pragma unroll
     for (int b = 0; b < 4; ++b) h.b[b] = quad_halves<ROT>(x.b[b]);
     if (KT == KVQ_K_F16) {
-        if (turns)
+        if (!SOME || turns)
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 r.k[kWords * b] = h.b[b].x;
@@ -398,11 +404,10 @@ __device__ __forceinline__ void turn_key(QuadRow<VT, KT> &r, bool turns, const f
     const QuadCodes q = quad_quantize<false>(h);
 #pragma unroll
     for (int b = 0; b < 4; ++b)
-        if (turns && 32 * b < n_rot) {   // the block holds a value that rotates
+        if ((!SOME || turns) && (ROT == kRotHalf || 32 * b < n_rot)) {   // the block holds a value that rotates
             r.k[kWords * b] = q.w[2 * b];
             r.k[kWords * b + 1] = q.w[2 * b + 1];
-            const uint32_t half = b & 1 ? 0xffff0000u : 0xffffu;
-            r.ks[b >> 1] = (r.ks[b >> 1] & ~half) | (q.s[b >> 1] & half);
+            r.ks[b >> 1] = __byte_perm(r.ks[b >> 1], q.s[b >> 1], b & 1 ? 0x7610 : 0x3254);
         }
 }
 
@@ -457,7 +462,7 @@ __device__ __forceinline__ void stage_get(const uint8_t *row, QuadRow<VT, KT> &r
 }
 
 template <int VT, int KT, int ROT, int WAY>
-__global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const MoveParams p)
+__global__ void __launch_bounds__(kMoveWarps * 32, 7) move_kernel(const MoveParams p)
 {
     constexpr int kTile = PageTile<VT, KT>::BYTES, kRow = Staged<VT, KT>::BYTES;
     __shared__ __align__(16) MoveShared shared[kMoveWarps];
@@ -492,29 +497,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const MoveParams 
         // a token that stays keeps its V, unless the other of its pair comes from elsewhere and they share words
         const bool stays = WAY == kMoveDirect && from == to, other_stays = __shfl_xor_sync(0xffffffffu, stays, 4);
         const bool still = stays && (!pair || other_stays);
-        // angles of the quads' turns, one row for all where they are the same
-        int row = 0;
-        bool any = false;
-        if (ROT != kRotNone) {
-            any = __any_sync(0xffffffffu, turns);
-            const int one = __shfl_sync(0xffffffffu, turn, __ffs(__ballot_sync(0xffffffffu, turns) | 0x80000000u) - 1);
-            const bool same = __all_sync(0xffffffffu, !turns || turn == one);
-            if (any) {
-                __syncwarp();   // the rows before may still be read
-                const int half_n = p.rope.n_rot / 2;
-                for (int k = 0; k < (same ? 1 : kMoveTokens); ++k) {
-                    const int t = same ? one : __shfl_sync(0xffffffffu, turn, 4 * k);
-                    for (int j = lane; j < half_n; j += 32) {
-                        const float2 a = angle_of(p.rope.turns[j], t, 1.f);
-                        sh.cosines[k][j] = a.x;
-                        sh.sines[k][j] = a.y;
-                    }
-                }
-                __syncwarp();
-            }
-            row = same ? 0 : quad;
-        }
-        const bool values = __any_sync(0xffffffffu, mine && !still);
+        const bool values = __any_sync(0xffffffffu, mine && !still), any = ROT != kRotNone && __any_sync(0xffffffffu, turns);
         if (!values && !any) continue;   // nothing changes
         const int fu = from & 15, tu = to & 15;
         const uint8_t *src = tile_of(p.pool, from >> p.pool.pshift, h0, (from & P1) >> 4, kTile);
@@ -526,23 +509,58 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const MoveParams 
 #pragma unroll
         for (int k = 0; k < QuadRow<VT, KT>::VW; ++k) r.v[k] = 0;
         r.ks[0] = r.ks[1] = r.vs = 0;
-        for (int h = h0; h < h1; ++h) {
+        auto get = [&]() {
+            if (!mine) return;
             if (WAY == kMoveIn) {
-                if (mine) stage_get<VT, KT>(staged, r, c);
-            } else if (mine) {
+                stage_get<VT, KT>(staged, r, c);
+            } else {
                 quad_get_key<VT, KT>(r, src, fu, c);
-                if (!still) quad_get_value<VT, KT>(r, src, fu, c);
+                if (values) quad_get_value<VT, KT>(r, src, fu, c);
             }
-            if (ROT != kRotNone && any) turn_key<VT, KT, ROT>(r, turns, sh.cosines[row], sh.sines[row], c, p.rope.n_rot, scratch[ROT == kRotPart ? warp : 0][ROT == kRotPart ? quad : 0]);
+        };
+        get();   // the first head's row, on its way while the angles are worked out
+        int row = 0;
+        if (ROT != kRotNone && any) {   // angles of the quads' turns, one row for all where they are the same
+            const int one = __shfl_sync(0xffffffffu, turn, __ffs(__ballot_sync(0xffffffffu, turns)) - 1);
+            const bool same = __all_sync(0xffffffffu, !turns || turn == one);
+            __syncwarp();   // the rows before may still be read
+            for (int k = 0; k < (same ? 1 : kMoveTokens); ++k) {
+                const int t = same ? one : __shfl_sync(0xffffffffu, turn, 4 * k);
+                for (int j = lane; j < p.rope.n_rot / 2; j += 32) {
+                    const float2 a = angle_of(p.rope.turns[j], t, 1.f);
+                    sh.cosines[k][j] = a.x;
+                    sh.sines[k][j] = a.y;
+                }
+            }
+            __syncwarp();
+            row = same ? 0 : quad;
+        }
+        const float *cosines = sh.cosines[row], *sines = sh.sines[row];
+        float *const mem = scratch[ROT == kRotPart ? warp : 0][ROT == kRotPart ? quad : 0];
+        if (WAY == kMoveDirect && !values) {   // keys turn where they lie: only those that do are written
+            for (int h = h0;;) {
+                turn_key<false, VT, KT, ROT>(r, true, cosines, sines, c, p.rope.n_rot, mem);
+                if (turns) quad_put_key<VT, KT>(r, dst, tu, c);
+                if (++h >= h1) break;
+                src += head_bytes;
+                dst += head_bytes;
+                if (mine) quad_get_key<VT, KT>(r, src, fu, c);
+            }
+            continue;
+        }
+        for (int h = h0;;) {
+            if (ROT != kRotNone && any) turn_key<true, VT, KT, ROT>(r, turns, cosines, sines, c, p.rope.n_rot, mem);
             if (WAY == kMoveOut) {
                 if (mine) stage_put<VT, KT>(staged, r, c);
             } else {
-                if (mine && (!still || turns)) quad_put_key<VT, KT>(r, dst, tu, c);
-                if (values) quad_put_value<VT, KT>(r, dst, tu, c, pair, mine && !still);
+                if (mine) quad_put_key<VT, KT>(r, dst, tu, c);
+                quad_put_value<VT, KT>(r, dst, tu, c, pair, mine);
             }
+            if (++h >= h1) break;
             src += head_bytes;
             dst += head_bytes;
             staged += kRow;
+            get();
         }
     }
 }

@@ -61,6 +61,7 @@ struct CopyParams {
     uint16_t heads[KVQ_MAX_COPY_POOLS], tile_bytes[KVQ_MAX_COPY_POOLS];
     const int *from, *to, *held;
     int n_pools, n_copies, n_pages, most_heads, tiles;
+    int pieces, blocks;   // of a head's run of bytes; of a page in one pool
 };
 
 struct MoveParams {

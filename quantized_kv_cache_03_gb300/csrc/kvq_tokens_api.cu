@@ -247,7 +247,7 @@ kvq_status kvq_page_copy(const kvq_pages *pools, int32_t n_pools, const int32_t 
         if (pools[i].n_pages != pools->n_pages || pools[i].page_tokens != pools->page_tokens) return KVQ_ERR_INVALID_ARG;
         most = pools[i].n_kv_heads > most ? pools[i].n_kv_heads : most;
     }
-    if ((long long)n_pools * most * n_copies > 1 << 30) return KVQ_ERR_INVALID_ARG;
+    if ((long long)n_pools * most * n_copies > 1 << 28) return KVQ_ERR_INVALID_ARG;
     if (n_copies == 0 || n_pools == 0 || pools->n_pages == 0) return KVQ_OK;
     if (!int_ptr(from) || !int_ptr(to) || !aligned(held, 4)) return KVQ_ERR_INVALID_ARG;
     int n_sms = 0;
