@@ -51,197 +51,456 @@ cudaError_t launch_positions(const PositionsParams &p, cudaStream_t s, bool pdl)
 
 // ---------------------------------------------------------------------------
 // Fork.  Whether a page is given back, and whether a row may go on writing into
-// its last page, depends on every row's list, so the work is three launches: the
-// marks are cleared, the lists are marked and the rows copied, and one cluster
-// counts what is marked old and not new, pushes it in order and deals out pages
-// for copies.  Marks are bytes, stored without reading (any number of rows may
-// mark a page); the first place that ends inside a page is a minimum: nothing
-// depends on an order.
+// its last page, depends on every row's list.  Pages are marked in bytes, stored
+// without reading: those that a new row lists whole (an old row's entries up to the
+// longest that a place keeps of it: once, however many keep them), those that one
+// ends in, and those past all that is kept of an old row, which are given back
+// unless they are also one of the others.  The first place that ends in a page is
+// a minimum.  Nothing depends on an order.
+//
+// In phases: lengths, and marks cleared; rows marked and copied; pages to give back
+// counted and last pages that are shared listed; pages pushed, in order of
+// their numbers, and dealt out.  Small batches go through them in one cluster, with
+// marks as bits in shared memory, each CTA's own until they are joined: a scattered
+// store to global memory costs an SM a cycle a byte (256 places of 129 entries: 13 us
+// so, 7.1 with the bits).  What is left is latency: the lengths, the rows and the
+// cluster's two barriers each wait for memory once.  Large batches take a launch for
+// each phase over the whole GPU, with bytes in global memory.
 // ---------------------------------------------------------------------------
-struct ForkRow {
-    int from, keep;   // old row (-1: none), positions kept
+constexpr int kForkCtas = 8, kForkThreads = 1024;   // of the one cluster
+constexpr int kForkWide = 1024, kForkMark = 256;    // threads of a block otherwise
+
+// What the phases know about each place, in shared memory (one cluster) or in the workspace.
+struct ForkSeqs {
+    int *from, *kept;     // old row (-1: none), positions kept
+    int *tail;            // the entry of the page the place ends inside; -1: it ends with a page
+    int *olds;            // pages of the old row of that number,
+    int *whole, *used;    // and most that a place keeps of it, whole ones and all
+    int *rank;            // among the places that need a copy, in order; -1: it needs none
+    int *list;            // those places
+    static constexpr int kArrays = 8;
+    __device__ __forceinline__ ForkSeqs(int *at, int n)
+        : from(at), kept(at + n), tail(at + 2 * n), olds(at + 3 * n), whole(at + 4 * n), used(at + 5 * n), rank(at + 6 * n), list(at + 7 * n) {}
 };
-__device__ __forceinline__ int old_len(const ForkParams &p, int b)
-{
-    return (int)min(max((long long)p.lens[b], 0ll), (long long)p.max_blocks << p.pshift);
-}
-__device__ __forceinline__ ForkRow fork_row(const ForkParams &p, int b)
-{
-    ForkRow r;
-    r.from = p.parent ? p.parent[b] : b;
-    if (r.from < 0 || r.from >= p.n_seqs) r.from = -1;
-    r.keep = r.from < 0 ? 0 : old_len(p, r.from);
-    if (p.keep) r.keep = max(0, min(r.keep, p.keep[b]));
-    return r;
-}
 __device__ __forceinline__ bool is_page(const ForkParams &p, int page) { return page >= 0 && page < p.n_pages; }
 
-__global__ void __launch_bounds__(256) fork_clear_kernel(const ForkParams p)
+// Lengths, by one block (in a cluster by every one).
+template <int THREADS>
+__device__ __forceinline__ void fork_lengths(const ForkParams &p, const ForkSeqs &q)
 {
-    pdl_wait();
-    pdl_trigger();
-    const long long at = (long long)blockIdx.x * 256 + threadIdx.x, all = (long long)gridDim.x * 256;
-    const long long words = ((long long)(p.full_mark - p.old_mark)) * 3 / 16;   // the three marks lie side by side
-    for (long long i = at; i < words; i += all) reinterpret_cast<uint4 *>(p.old_mark)[i] = make_uint4(0, 0, 0, 0);
-    for (long long b = at; b < p.n_seqs; b += all) {
-        const ForkRow r = fork_row(p, (int)b);
-        p.kept[b] = r.keep;
-        if ((r.keep & ((1 << p.pshift) - 1)) == 0) continue;
-        const int tail = p.table[(size_t)r.from * p.stride + (r.keep >> p.pshift)];
-        p.tail[b] = tail;
-        if (is_page(p, tail)) p.owner[tail] = p.n_seqs;
+    const int P = 1 << p.pshift;
+    for (int b = threadIdx.x; b < p.n_seqs; b += THREADS) {
+        const int len = (int)min(max((long long)p.lens[b], 0ll), (long long)p.max_blocks << p.pshift);
+        int from = p.parent ? p.parent[b] : b;
+        if (from < 0 || from >= p.n_seqs) from = -1;
+        q.from[b] = from;
+        q.kept[b] = p.keep ? p.keep[b] : len;
+        q.olds[b] = (len + P - 1) >> p.pshift;
+        q.whole[b] = q.used[b] = 0;
+        q.rank[b] = len;   // (for the moment)
     }
+    __syncthreads();
+    for (int b = threadIdx.x; b < p.n_seqs; b += THREADS) {
+        const int from = q.from[b], len = from < 0 ? 0 : q.rank[from], keep = p.keep ? max(0, min(len, q.kept[b])) : len;
+        if (keep > 0) {
+            atomicMax(q.whole + from, keep >> p.pshift);
+            atomicMax(q.used + from, (keep + P - 1) >> p.pshift);
+        }
+        q.kept[b] = keep;
+    }
+    __syncthreads();
+}
+// The entry of the page that place b ends inside, -1 if it ends with one.
+__device__ __forceinline__ int fork_tail(const ForkParams &p, const ForkSeqs &q, int b)
+{
+    const int kept = q.kept[b];
+    return kept & ((1 << p.pshift) - 1) ? p.table[(size_t)q.from[b] * p.stride + (kept >> p.pshift)] : -1;
 }
 
-constexpr int kForkRun = 1024;   // entries of a row that a block takes
+// 128 entries of a row, marked and copied by a warp: read, then written.
+struct ForkRun {
+    int b, e0, whole, mine;
+    bool copies;
+    int old_page[4], page[4];
 
-__global__ void __launch_bounds__(256) fork_mark_kernel(const ForkParams p)
-{
-    pdl_wait();
-    pdl_trigger();
-    const int runs = (p.max_blocks + kForkRun - 1) / kForkRun;
-    const int b = blockIdx.x / runs, e0 = (blockIdx.x - b * runs) * kForkRun, P = 1 << p.pshift;
-    const ForkRow r = fork_row(p, b);
-    const int olds = (old_len(p, b) + P - 1) >> p.pshift, whole = r.keep >> p.pshift, used = (r.keep + P - 1) >> p.pshift;
-    const int *old_row = p.table + (size_t)b * p.stride, *row = p.table + (size_t)max(r.from, 0) * p.stride;
-    int *out = p.table_out + (size_t)b * p.out_stride;
-    const bool same = out == row;   // in place: the entries are there
+    __device__ __forceinline__ ForkRun(const ForkParams &p, const ForkSeqs &q, int row_of, int run) : b(row_of), e0(run * 128 + (int)(threadIdx.x & 31))
+    {
+        const int used = q.used[b], olds = q.olds[b], from = q.from[b];
+        whole = q.whole[b];
+        mine = q.kept[b] >> p.pshift;
+        const int *old_row = p.table + (size_t)b * p.stride, *row = p.table + (size_t)max(from, 0) * p.stride;
+        copies = p.table_out + (size_t)b * p.out_stride != row;   // (in place the entries are there)
 #pragma unroll
-    for (int k = 0; k < kForkRun / 256; ++k) {
-        const int e = e0 + k * 256 + (int)threadIdx.x;
-        if (e < olds) {
-            const int page = old_row[e];
-            if (is_page(p, page)) p.old_mark[page] = 1;
-        }
-        if (e < used) {
-            const int page = row[e];
-            if (e < whole) {
-                if (!same) out[e] = page;
-                if (is_page(p, page)) p.full_mark[page] = 1;
-            } else if (is_page(p, page)) {   // (its entry is written once it is known which page the row ends in)
-                p.tail_mark[page] = 1;
-                atomicMin(p.owner + page, b);
-            }
+        for (int k = 0; k < 4; ++k) {
+            const int e = e0 + 32 * k;
+            old_page[k] = e < olds && (e < whole || e >= used) ? old_row[e] : -1;
+            page[k] = copies && e < mine ? row[e] : -1;
         }
     }
-}
+    // mark(page, whole): it is one that a new row lists whole, or one that no place keeps of this row
+    template <typename F>
+    __device__ __forceinline__ void write(const ForkParams &p, F mark) const
+    {
+        int *out = p.table_out + (size_t)b * p.out_stride;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int e = e0 + 32 * k;
+            if (is_page(p, old_page[k])) mark(old_page[k], e < whole);
+            if (copies && e < mine) out[e] = page[k];
+        }
+    }
+};
+__device__ __forceinline__ int fork_runs(const ForkParams &p) { return (p.max_blocks + 127) / 128; }
 
-// Exclusive sum over the block's threads, and the total.
-__device__ __forceinline__ int fork_scan(int x, int &total, int *tmp)
+// Exclusive sums of two values over the block's threads, and the totals.
+template <int THREADS>
+__device__ __forceinline__ int2 fork_scan(int2 x, int2 &total, int2 *tmp)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int y = x;
+    int2 y = x;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int z = __shfl_up_sync(0xffffffffu, y, d);
-        if (lane >= d) y += z;
+        const int u = __shfl_up_sync(0xffffffffu, y.x, d), v = __shfl_up_sync(0xffffffffu, y.y, d);
+        if (lane >= d) y.x += u, y.y += v;
     }
     __syncthreads();   // tmp may still be read by the scan before
     if (lane == 31) tmp[warp] = y;
     __syncthreads();
-    int base = 0;
-    total = 0;
+    int2 z = lane < THREADS / 32 ? tmp[lane] : make_int2(0, 0), sum = z;   // every warp adds the warps up
 #pragma unroll
-    for (int w = 0; w < kForkThreads / 32; ++w) {
-        if (w < warp) base += tmp[w];
-        total += tmp[w];
+    for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, sum.x, d), v = __shfl_up_sync(0xffffffffu, sum.y, d);
+        if (lane >= d) sum.x += u, sum.y += v;
     }
-    return base + y - x;
+    total = make_int2(__shfl_sync(0xffffffffu, sum.x, 31), __shfl_sync(0xffffffffu, sum.y, 31));
+    return make_int2(__shfl_sync(0xffffffffu, sum.x - z.x, warp) + y.x - x.x, __shfl_sync(0xffffffffu, sum.y - z.y, warp) + y.y - x.y);
+}
+
+// The stack between the pushes and the pops: entries below n_free are the old
+// ones, `back` new ones follow; `needs` are taken off its top, the first place's first.
+struct ForkStack {
+    int n_free, avail, needs;
+    __device__ __forceinline__ ForkStack(const ForkParams &p, int n, int back, int want) : n_free(n), needs(want)
+    {
+        avail = (int)min((long long)n + back, (long long)p.n_pages);
+    }
+};
+__device__ __forceinline__ void fork_give(const ForkParams &p, const ForkSeqs &q, int b, int page)
+{
+    p.copy_to[b] = page;
+    p.table_out[(size_t)b * p.out_stride + (q.kept[b] >> p.pshift)] = page;
+}
+// A page that is given back, entry `at` of the stack.
+__device__ __forceinline__ void fork_push(const ForkParams &p, const ForkSeqs &q, const ForkStack &st, long long at, int page)
+{
+    if (at >= p.n_pages) return;
+    p.free_pages[at] = page;
+    const int r = st.avail - 1 - (int)at;
+    if (r < st.needs) fork_give(p, q, q.list[r], page);
+}
+// Every place's results but a copy's page where it was pushed just now.
+__device__ __forceinline__ void fork_results(const ForkParams &p, const ForkSeqs &q, const ForkStack &st, int at, int all)
+{
+    const int P = 1 << p.pshift;
+    for (int b = at; b < p.n_seqs; b += all) {
+        int kept = q.kept[b], from = -1, held = 0, status = 0;
+        const int rank = q.rank[b], entry = st.avail - 1 - rank;
+        const bool in_part = (kept & (P - 1)) != 0;
+        if (rank >= 0 && entry >= 0) {
+            from = q.tail[b];
+            held = kept & (P - 1);
+            if (entry < st.n_free) fork_give(p, q, b, p.free_pages[entry]);
+        } else {
+            p.copy_to[b] = -1;
+            if (rank >= 0) {
+                kept &= ~(P - 1);
+                status = 1;
+            } else if (in_part) {
+                p.table_out[(size_t)b * p.out_stride + (kept >> p.pshift)] = q.tail[b];
+            }
+        }
+        p.copy_from[b] = from;
+        p.copy_held[b] = held;
+        p.status[b] = status;
+        p.lens_out[b] = kept;
+    }
+    if (at == 0) *p.n_free_out = st.avail - min(st.needs, st.avail);
 }
 
 __device__ __forceinline__ void cluster_sync() { asm volatile("barrier.cluster.arrive;\n barrier.cluster.wait;" ::: "memory"); }
-
-__global__ void __cluster_dims__(kForkCtas, 1, 1) __launch_bounds__(kForkThreads) fork_deal_kernel(const ForkParams p)
+// A word of another CTA's shared memory.
+__device__ __forceinline__ uint32_t of_cta(const uint32_t *mine, int rank)
 {
-    __shared__ int tmp[kForkThreads / 32];
-    const int tid = threadIdx.x, rank = blockIdx.x, P = 1 << p.pshift;
+    uint32_t at, v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(mine)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void to_cta(uint32_t *mine, int rank, uint32_t v)
+{
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(mine)), "r"(rank));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+
+// The least place that ends in a page, by page: a table in shared memory, probed
+// in a row, at most half full.
+struct PageTable {
+    static constexpr int kSlots = 2048;
+    int *page, *place;
+    __device__ __forceinline__ explicit PageTable(int *at) : page(at), place(at + kSlots) {}
+    __device__ __forceinline__ void clear() const
+    {
+        for (int i = threadIdx.x; i < kSlots; i += kForkThreads) {
+            page[i] = -1;
+            place[i] = 0x7fffffff;
+        }
+    }
+    static __device__ __forceinline__ unsigned slot(int p) { return (unsigned)p * 2654435769u >> 21; }
+    __device__ __forceinline__ void least(int p, int b) const
+    {
+        for (unsigned h = slot(p);; h = (h + 1) % kSlots) {
+            const int had = atomicCAS(page + h, -1, p);
+            if (had == -1 || had == p) {
+                atomicMin(place + h, b);
+                return;
+            }
+        }
+    }
+    __device__ __forceinline__ int of(int p) const   // p is in it
+    {
+        unsigned h = slot(p);
+        while (page[h] != p) h = (h + 1) % kSlots;
+        return place[h];
+    }
+};
+
+constexpr int kForkMaxSeqs = 1024, kForkMaxPages = 64 * 1024;   // of the cluster
+static_assert(2 * kForkMaxSeqs <= PageTable::kSlots && kForkMaxSeqs <= kForkThreads && kForkMaxPages / 32 / kForkCtas <= kForkThreads, "a place and a word of marks to a thread");
+
+__global__ void __cluster_dims__(kForkCtas, 1, 1) __launch_bounds__(kForkThreads) fork_cluster_kernel(const ForkParams p)
+{
+    extern __shared__ int seqs[];
+    __shared__ int2 tmp[kForkThreads / 32];
+    __shared__ uint32_t counts[kForkCtas], needs[kForkMaxSeqs / 32];
+    const int tid = threadIdx.x, rank = blockIdx.x, at = rank * kForkThreads + tid, all = kForkCtas * kForkThreads, n = p.n_seqs, words = (p.n_pages + 31) / 32;
+    const ForkSeqs q(seqs, n);
+    uint32_t *const old = reinterpret_cast<uint32_t *>(seqs) + ForkSeqs::kArrays * n, *const full = old + words, *const tails = full + words;
+    for (int i = tid; i < 3 * words; i += kForkThreads) old[i] = 0;
+    const PageTable ends(reinterpret_cast<int *>(tails + words));
+    ends.clear();
     pdl_wait();
     pdl_trigger();
     const int n_free = min(max(*p.n_free, 0), p.n_pages);
-    // a thread's pages: a run of 16-byte words of marks
-    const int words = (p.n_pages + 15) / 16, per = (words + kForkCtas * kForkThreads - 1) / (kForkCtas * kForkThreads);
-    const int w0 = (int)min((long long)words, (long long)(rank * kForkThreads + tid) * per), w1 = min(words, w0 + per);
-    auto gone = [&](int w) {   // a bit per byte: listed before and not now (marks past the last page are clear)
-        const uint4 o = reinterpret_cast<const uint4 *>(p.old_mark)[w], f = reinterpret_cast<const uint4 *>(p.full_mark)[w],
-                    t = reinterpret_cast<const uint4 *>(p.tail_mark)[w];
-        return make_uint4(o.x & ~(f.x | t.x), o.y & ~(f.y | t.y), o.z & ~(f.z | t.z), o.w & ~(f.w | t.w));
-    };
-    int n = 0;
-    for (int w = w0; w < w1; ++w) {
-        const uint4 g = gone(w);
-        n += __popc(g.x) + __popc(g.y) + __popc(g.z) + __popc(g.w);
+    fork_lengths<kForkThreads>(p, q);   // (its barriers also order the marks' clearing)
+    // rows marked and copied, the first two of a warp read before the ends of the places are
+    auto mark = [&](int page, bool whole) { atomicOr((whole ? full : old) + (page >> 5), 1u << (page & 31)); };
+    const int runs = fork_runs(p), warps = all >> 5, items = n * runs;   // (few: the launch sees to it)
+    auto run = [&](int item) { return ForkRun(p, q, item / runs, item % runs); };
+    if (items > 0) {
+        const ForkRun one = run(min(at >> 5, items - 1)), two = run(min((at >> 5) + warps, items - 1));   // (the last one again does no harm)
+        if (tid < n) {
+            const int tail = fork_tail(p, q, tid);
+            q.tail[tid] = tail;
+            if (is_page(p, tail)) {
+                atomicOr(tails + (tail >> 5), 1u << (tail & 31));
+                ends.least(tail, tid);
+            }
+        }
+        one.write(p, mark);
+        two.write(p, mark);
+        for (int item = (at >> 5) + 2 * warps; item < items; item += warps) run(item).write(p, mark);
     }
-    int mine;
-    const int first = fork_scan(n, mine, tmp);
-    if (tid == 0) p.counts[rank] = mine;
+    cluster_sync();   // marks are set; and every CTA has read lens and n_free, which results may replace
+    // the CTA's share of the pool, a word of 32 pages a thread
+    const int share = (words + kForkCtas - 1) / kForkCtas, w = rank * share + tid;
+    uint32_t gone = 0;
+    if (tid < share && w < words) {
+        uint32_t o = 0, f = tails[w];
+#pragma unroll
+        for (int k = 0; k < kForkCtas; ++k) {
+            o |= of_cta(old + w, k);
+            f |= of_cta(full + w, k);
+        }
+        gone = o & ~f;
+    }
+    // the CTA's places that end inside a page they may not write to: one that a row lists whole, or that an earlier
+    // place ends in too; a bit each, to every CTA
+    const int places = (n + 32 * kForkCtas - 1) / (32 * kForkCtas) * 32, b = rank * places + tid;
+    if (tid < places) {
+        bool need = false;
+        const int tail = b < n ? q.tail[b] : -1;
+        if (is_page(p, tail)) {
+            uint32_t f = 0;
+#pragma unroll
+            for (int k = 0; k < kForkCtas; ++k) f |= of_cta(full + (tail >> 5), k);
+            need = (f >> (tail & 31) & 1) || ends.of(tail) != b;
+        }
+        const unsigned bits = __ballot_sync(0xffffffffu, need);
+        if ((tid & 31) < kForkCtas && b - (tid & 31) < kForkMaxSeqs) to_cta(needs + (b >> 5), tid & 31, bits);
+    }
+    int2 total;
+    const int first = fork_scan<kForkThreads>(make_int2(__popc(gone), 0), total, tmp).x;
+    if (tid < kForkCtas) to_cta(counts + rank, tid, (uint32_t)total.x);   // this CTA's count, to every other
     cluster_sync();
     int before = 0, back = 0;
 #pragma unroll
     for (int k = 0; k < kForkCtas; ++k) {
-        const int c = __ldcg(p.counts + k);
-        before += k < rank ? c : 0;
-        back += c;
+        before += k < rank ? (int)counts[k] : 0;
+        back += (int)counts[k];
     }
-    const int avail = (int)min((long long)n_free + back, (long long)p.n_pages);
-    long long at = (long long)n_free + before + first;
-    if (n > 0)
-        for (int w = w0; w < w1; ++w) {
-            const uint4 g = gone(w);
+    const bool need = tid < n && (needs[tid >> 5] >> (tid & 31) & 1);
+    const int mine = fork_scan<kForkThreads>(make_int2(need, 0), total, tmp).x;
+    if (tid < n) q.rank[tid] = need ? mine : -1;
+    if (need) q.list[mine] = tid;
+    __syncthreads();
+    const ForkStack st(p, n_free, back, total.x);
+    long long to = (long long)n_free + before + first;
+    for (; gone; gone &= gone - 1) fork_push(p, q, st, to++, 32 * w + __ffs(gone) - 1);
+    fork_results(p, q, st, at, all);
+}
+
+__global__ void __launch_bounds__(kForkWide) fork_clear_kernel(const ForkParams p)
+{
+    pdl_wait();
+    pdl_trigger();
+    if (blockIdx.x == 0) {
+        const ForkSeqs q(p.seqs, p.n_seqs);
+        fork_lengths<kForkWide>(p, q);
+        for (int b = threadIdx.x; b < p.n_seqs; b += kForkWide) {
+            const int tail = fork_tail(p, q, b);
+            q.tail[b] = tail;
+            if (is_page(p, tail)) p.owner[tail] = p.n_seqs;
+        }
+        if (threadIdx.x == 0) p.totals[0] = min(max(*p.n_free, 0), p.n_pages);
+    } else {   // the marks, three kinds side by side
+        const long long words = (long long)(p.full_mark - p.old_mark) * 3 / 16, at = (long long)(blockIdx.x - 1) * kForkWide + threadIdx.x;
+        for (long long i = at; i < words; i += (long long)(gridDim.x - 1) * kForkWide) reinterpret_cast<uint4 *>(p.old_mark)[i] = make_uint4(0, 0, 0, 0);
+    }
+}
+__global__ void __launch_bounds__(kForkMark) fork_mark_kernel(const ForkParams p)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int at = blockIdx.x * kForkMark + threadIdx.x, all = gridDim.x * kForkMark, runs = fork_runs(p);
+    const ForkSeqs q(p.seqs, p.n_seqs);
+    for (long long item = at >> 5; item < (long long)p.n_seqs * runs; item += all >> 5) {
+        const int b = (int)(item / runs);
+        ForkRun(p, q, b, (int)(item - (long long)b * runs)).write(p, [&](int page, bool whole) { (whole ? p.full_mark : p.old_mark)[page] = 1; });
+    }
+    for (int b = at; b < p.n_seqs; b += all) {
+        const int tail = q.tail[b];
+        if (is_page(p, tail)) {
+            p.tail_mark[tail] = 1;
+            atomicMin(p.owner + tail, b);
+        }
+    }
+}
+// Sixteen pages' marks: a bit per byte, listed before and not now (marks past the last page are clear).
+__device__ __forceinline__ uint4 fork_gone(const ForkParams &p, long long w)
+{
+    const uint4 o = reinterpret_cast<const uint4 *>(p.old_mark)[w], f = reinterpret_cast<const uint4 *>(p.full_mark)[w],
+                t = reinterpret_cast<const uint4 *>(p.tail_mark)[w];
+    return make_uint4(o.x & ~(f.x | t.x), o.y & ~(f.y | t.y), o.z & ~(f.z | t.z), o.w & ~(f.w | t.w));
+}
+// A thread's share of the pool: words w0 .. w1 - 1 of a block's, the first of them kept in hand.
+struct ForkShare {
+    long long w0, w1;
+    uint4 g;
+    int n;
+    __device__ __forceinline__ ForkShare(const ForkParams &p) : g(make_uint4(0, 0, 0, 0)), n(0)
+    {
+        const long long words = (p.n_pages + 15) / 16, of_block = (words + p.blocks - 1) / p.blocks, per = (of_block + kForkWide - 1) / kForkWide;
+        const long long b0 = min(words, blockIdx.x * of_block), b1 = min(words, b0 + of_block);
+        w0 = min(b1, b0 + threadIdx.x * per);
+        w1 = min(b1, w0 + per);
+        if (w0 < w1) g = fork_gone(p, w0);
+        n = count(g);
+        for (long long w = w0 + 1; w < w1; ++w) n += count(fork_gone(p, w));
+    }
+    static __device__ __forceinline__ int count(const uint4 &v) { return __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w); }
+};
+__global__ void __launch_bounds__(kForkWide) fork_count_kernel(const ForkParams p)
+{
+    __shared__ int2 tmp[kForkWide / 32];
+    pdl_wait();
+    pdl_trigger();
+    int2 total;
+    if ((int)blockIdx.x < p.blocks) {
+        fork_scan<kForkWide>(make_int2(ForkShare(p).n, 0), total, tmp);
+        if (threadIdx.x == 0) p.counts[blockIdx.x] = total.x;
+        return;
+    }
+    // one block more: places that end inside a page they may not write to
+    const ForkSeqs q(p.seqs, p.n_seqs);
+    const int each = (p.n_seqs + kForkWide - 1) / kForkWide, b0 = min(p.n_seqs, (int)threadIdx.x * each), b1 = min(p.n_seqs, b0 + each);
+    int n = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int tail = q.tail[b];
+        int needs = 0;
+        if (is_page(p, tail)) {
+            const int full = p.full_mark[tail], owner = p.owner[tail];
+            needs = full != 0 || owner != b;
+        }
+        q.rank[b] = needs - 1;   // -1 or 0
+        n += needs;
+    }
+    int at = fork_scan<kForkWide>(make_int2(0, n), total, tmp).y;
+    for (int b = b0; b < b1; ++b)
+        if (q.rank[b] >= 0) {
+            q.list[at] = b;
+            q.rank[b] = at++;
+        }
+    if (threadIdx.x == 0) p.totals[1] = total.y;
+}
+__global__ void __launch_bounds__(kForkWide) fork_deal_kernel(const ForkParams p)
+{
+    __shared__ int2 tmp[kForkWide / 32];
+    pdl_wait();
+    pdl_trigger();
+    const ForkSeqs q(p.seqs, p.n_seqs);
+    const ForkShare share(p);
+    int2 blocks = make_int2(0, 0), total;   // pages of the blocks before this one, of all
+    for (int k = threadIdx.x; k < p.blocks; k += kForkWide) {
+        const int c = p.counts[k];
+        blocks.x += k < (int)blockIdx.x ? c : 0;
+        blocks.y += c;
+    }
+    fork_scan<kForkWide>(blocks, total, tmp);
+    const ForkStack st(p, p.totals[0], total.y, p.totals[1]);
+    int2 mine;
+    long long at = (long long)st.n_free + total.x + fork_scan<kForkWide>(make_int2(share.n, 0), mine, tmp).x;
+    if (share.n > 0)
+        for (long long w = share.w0; w < share.w1; ++w) {
+            const uint4 g = w == share.w0 ? share.g : fork_gone(p, w);
             const uint32_t v[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                for (uint32_t bits = v[k]; bits; bits &= bits - 1) {
-                    if (at < p.n_pages) p.free_pages[at] = 16 * w + 4 * k + (__ffs(bits) >> 3);
-                    ++at;
-                }
+                for (uint32_t bits = v[k]; bits; bits &= bits - 1) fork_push(p, q, st, at++, (int)(16 * w) + 4 * k + (__ffs(bits) >> 3));
         }
-    cluster_sync();   // the stack is whole
-    if (rank != 0) return;
-    // pages for copies, in order of place
-    const int each = (p.n_seqs + kForkThreads - 1) / kForkThreads, b0 = min(p.n_seqs, tid * each), b1 = min(p.n_seqs, b0 + each);
-    auto shared_tail = [&](int b, int kept) {   // the row ends inside a page that it may not write to
-        if ((kept & (P - 1)) == 0) return false;
-        const int page = p.tail[b];
-        return is_page(p, page) && (p.full_mark[page] || p.owner[page] != b);
-    };
-    int need = 0;
-    for (int b = b0; b < b1; ++b) need += shared_tail(b, p.kept[b]);
-    int needs;
-    int rank_of = fork_scan(need, needs, tmp);
-    for (int b = b0; b < b1; ++b) {
-        int kept = p.kept[b], from = -1, to = -1, held = 0, st = 0;
-        const bool in_part = (kept & (P - 1)) != 0, shared = shared_tail(b, kept);
-        int *entry = p.table_out + (size_t)b * p.out_stride + (kept >> p.pshift);
-        if (shared && rank_of < avail) {
-            from = p.tail[b];
-            to = __ldcg(p.free_pages + (avail - 1 - rank_of));
-            held = kept & (P - 1);
-            *entry = to;
-        } else if (shared) {
-            kept &= ~(P - 1);
-            st = 1;
-        } else if (in_part) {
-            *entry = p.tail[b];
-        }
-        rank_of += shared;
-        p.copy_from[b] = from;
-        p.copy_to[b] = to;
-        p.copy_held[b] = held;
-        p.status[b] = st;
-        p.lens_out[b] = kept;
-    }
-    if (tid == 0) *p.n_free_out = avail - min(needs, avail);
+    fork_results(p, q, st, blockIdx.x * kForkWide + threadIdx.x, p.blocks * kForkWide);
 }
 
-cudaError_t launch_page_fork(const ForkParams &p, cudaStream_t s, bool pdl)
+constexpr int fork_cluster_smem(int n_seqs, int n_pages) { return (ForkSeqs::kArrays * n_seqs + 3 * ((n_pages + 31) / 32) + 2 * PageTable::kSlots) * (int)sizeof(int); }
+cudaError_t prepare_page_fork()
 {
-    const long long words = ((long long)(p.full_mark - p.old_mark)) * 3 / 16;
-    const long long items = words > p.n_seqs ? words : p.n_seqs;
-    const int clear = (int)(items / 256 + 1 < 608 ? items / 256 + 1 : 608);
-    cudaError_t e = launch_pdl(fork_clear_kernel, p, clear, 256, 0, s, pdl);
-    const long long runs = (p.max_blocks + kForkRun - 1) / kForkRun;
-    if (e == cudaSuccess && p.n_seqs * runs > 0) e = launch_pdl(fork_mark_kernel, p, (int)(p.n_seqs * runs), 256, 0, s, pdl);
-    if (e == cudaSuccess) e = launch_pdl(fork_deal_kernel, p, kForkCtas, kForkThreads, 0, s, pdl);
+    return cudaFuncSetAttribute(fork_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, fork_cluster_smem(kForkMaxSeqs, kForkMaxPages));
+}
+
+cudaError_t launch_page_fork(const ForkParams &in, int n_sms, cudaStream_t s, bool pdl)
+{
+    ForkParams p = in;
+    const long long entries = (long long)p.n_seqs * p.max_blocks;
+    // Eight SMs against all of them and four launches: 256 places of 129 entries 7.1 us against 10.8, 512 of 257 11.0
+    // against 12.9, 1024 of 129 15.2 against 14.6.
+    if (p.n_seqs <= kForkMaxSeqs && p.n_pages <= kForkMaxPages && entries <= 128 * 1024)
+        return launch_pdl(fork_cluster_kernel, p, kForkCtas, kForkThreads, fork_cluster_smem(p.n_seqs, p.n_pages), s, pdl);
+    auto grid = [&](long long items, int most) { return (int)(items < 1 ? 1 : items > most ? most : items); };
+    cudaError_t e = launch_pdl(fork_clear_kernel, p, 1 + grid(((long long)p.n_pages * 3 / 16 + kForkWide - 1) / kForkWide, 2 * n_sms), kForkWide, 0, s, pdl);
+    if (e == cudaSuccess) e = launch_pdl(fork_mark_kernel, p, grid((long long)p.n_seqs * ((p.max_blocks + 127) / 128) / (kForkMark / 32) + 1, 8 * n_sms), kForkMark, 0, s, pdl);
+    if (e == cudaSuccess) e = launch_pdl(fork_count_kernel, p, p.blocks + 1, kForkWide, 0, s, pdl);
+    if (e == cudaSuccess) e = launch_pdl(fork_deal_kernel, p, p.blocks, kForkWide, 0, s, pdl);
     return e;
 }
 

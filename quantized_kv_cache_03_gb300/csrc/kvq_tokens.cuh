@@ -51,8 +51,9 @@ struct ForkParams {
     int *table_out, *lens_out, *free_pages, *n_free_out, *copy_from, *copy_to, *copy_held, *status;
     uint8_t *old_mark, *full_mark, *tail_mark;   // [n_pages]: listed by an old row, by a new one as a whole page, as its last one in part
     int *owner;                 // [n_pages], of pages with a tail mark: the first place that ends in it
-    int *kept, *tail;           // [n_seqs]: positions kept; the entry of the last page where it is kept in part
-    int *counts;                // pages given back by each CTA's share of the pool
+    int *seqs;                  // [8][n_seqs]
+    int *counts, *totals;       // [blocks]: pages given back by each block's share of the pool; the old stack's size, copies needed
+    int blocks;                 // of the launches that count and push
     int n_seqs, pshift, n_pages, stride, out_stride, max_blocks;
 };
 
@@ -73,12 +74,11 @@ struct MoveParams {
     uint8_t *rows;                 // staged: [n_tokens][kv heads] rows of staged_row_bytes()
 };
 
-constexpr int kForkCtas = 8, kForkThreads = 512;
-
 cudaError_t launch_positions(const PositionsParams &p, cudaStream_t s, bool pdl);
 cudaError_t prepare_qkv();
 cudaError_t launch_qkv(const QkvParams &p, int v_type, int k_type, int n_sms, cudaStream_t s, bool pdl);
-cudaError_t launch_page_fork(const ForkParams &p, cudaStream_t s, bool pdl);
+cudaError_t prepare_page_fork();
+cudaError_t launch_page_fork(const ForkParams &p, int n_sms, cudaStream_t s, bool pdl);
 cudaError_t launch_page_copy(const CopyParams &p, cudaStream_t s, bool pdl);
 // rows null: from slots to slots; else through them.
 int staged_row_bytes(int v_type, int k_type);

@@ -27,7 +27,8 @@ kvq_status tokens_setup(int *n_sms)
     if (st != KVQ_OK) return st;
     std::lock_guard<std::mutex> lk(g_mu);
     if (!g_ready[dev]) {
-        const cudaError_t e = prepare_qkv();
+        cudaError_t e = prepare_qkv();
+        if (e == cudaSuccess) e = prepare_page_fork();
         if (e != cudaSuccess) return done(e);
         g_ready[dev] = true;
     }
@@ -58,17 +59,19 @@ bool norm_ok(const float *p) { return aligned(p, 16); }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct ForkPlan {
-    size_t marks, owner, kept, tail, counts, bytes;   // bytes of one kind of marks, offsets, and all
+    size_t marks, owner, seqs, counts, totals, bytes;   // bytes of one kind of marks, offsets, and all
+    int blocks;
 };
 ForkPlan plan_fork(int n_seqs, int n_pages)
 {
     ForkPlan f;
+    f.blocks = n_pages / 16384 + 1 < 1024 ? n_pages / 16384 + 1 : 1024;   // 16 pages a thread, more in very large pools
     f.marks = up256((size_t)n_pages);
     f.owner = 3 * f.marks;
-    f.kept = f.owner + up256((size_t)n_pages * sizeof(int));
-    f.tail = f.kept + up256((size_t)n_seqs * sizeof(int));
-    f.counts = f.tail + up256((size_t)n_seqs * sizeof(int));
-    f.bytes = f.counts + up256(kForkCtas * sizeof(int));
+    f.seqs = f.owner + up256((size_t)n_pages * sizeof(int));
+    f.counts = f.seqs + up256(8 * (size_t)n_seqs * sizeof(int));
+    f.totals = f.counts + up256((size_t)f.blocks * sizeof(int));
+    f.bytes = f.totals + up256(2 * sizeof(int));
     return f;
 }
 
@@ -224,16 +227,17 @@ kvq_status kvq_page_fork(int32_t n_seqs, int32_t page_tokens, int32_t n_pages, c
     p.full_mark = w + f.marks;
     p.tail_mark = w + 2 * f.marks;
     p.owner = reinterpret_cast<int *>(w + f.owner);
-    p.kept = reinterpret_cast<int *>(w + f.kept);
-    p.tail = reinterpret_cast<int *>(w + f.tail);
+    p.seqs = reinterpret_cast<int *>(w + f.seqs);
     p.counts = reinterpret_cast<int *>(w + f.counts);
+    p.totals = reinterpret_cast<int *>(w + f.totals);
+    p.blocks = f.blocks;
     p.n_seqs = n_seqs;
     p.pshift = page_shift(page_tokens);
     p.n_pages = n_pages;
     p.stride = table_stride;
     p.out_stride = out_stride;
     p.max_blocks = max_blocks;
-    return done(launch_page_fork(p, static_cast<cudaStream_t>(stream), pdl_on()));
+    return done(launch_page_fork(p, n_sms, static_cast<cudaStream_t>(stream), pdl_on()));
 }
 
 kvq_status kvq_page_copy(const kvq_pages *pools, int32_t n_pools, const int32_t *from, const int32_t *to, const int32_t *held,
