@@ -397,29 +397,27 @@ __global__ void __launch_bounds__(kForkMark) fork_mark_kernel(const ForkParams p
         }
     }
 }
-// Sixteen pages' marks: a bit per byte, listed before and not now (marks past the last page are clear).
-__device__ __forceinline__ uint4 fork_gone(const ForkParams &p, long long w)
+// Four pages' marks: a bit per byte, listed before and not now (marks past the last page are clear).
+__device__ __forceinline__ uint32_t fork_gone(const ForkParams &p, long long w)
 {
-    const uint4 o = reinterpret_cast<const uint4 *>(p.old_mark)[w], f = reinterpret_cast<const uint4 *>(p.full_mark)[w],
-                t = reinterpret_cast<const uint4 *>(p.tail_mark)[w];
-    return make_uint4(o.x & ~(f.x | t.x), o.y & ~(f.y | t.y), o.z & ~(f.z | t.z), o.w & ~(f.w | t.w));
+    auto of = [&](const uint8_t *marks) { return reinterpret_cast<const uint32_t *>(marks)[w]; };
+    return of(p.old_mark) & ~(of(p.full_mark) | of(p.tail_mark));
 }
 // A thread's share of the pool: words w0 .. w1 - 1 of a block's, the first of them kept in hand.
 struct ForkShare {
     long long w0, w1;
-    uint4 g;
+    uint32_t g;
     int n;
-    __device__ __forceinline__ ForkShare(const ForkParams &p) : g(make_uint4(0, 0, 0, 0)), n(0)
+    __device__ __forceinline__ ForkShare(const ForkParams &p) : g(0)
     {
-        const long long words = (p.n_pages + 15) / 16, of_block = (words + p.blocks - 1) / p.blocks, per = (of_block + kForkWide - 1) / kForkWide;
+        const long long words = ((long long)p.n_pages + 3) / 4, of_block = (words + p.blocks - 1) / p.blocks, per = (of_block + kForkWide - 1) / kForkWide;
         const long long b0 = min(words, blockIdx.x * of_block), b1 = min(words, b0 + of_block);
         w0 = min(b1, b0 + threadIdx.x * per);
         w1 = min(b1, w0 + per);
         if (w0 < w1) g = fork_gone(p, w0);
-        n = count(g);
-        for (long long w = w0 + 1; w < w1; ++w) n += count(fork_gone(p, w));
+        n = __popc(g);
+        for (long long w = w0 + 1; w < w1; ++w) n += __popc(fork_gone(p, w));
     }
-    static __device__ __forceinline__ int count(const uint4 &v) { return __popc(v.x) + __popc(v.y) + __popc(v.z) + __popc(v.w); }
 };
 __global__ void __launch_bounds__(kForkWide) fork_count_kernel(const ForkParams p)
 {
@@ -473,11 +471,7 @@ __global__ void __launch_bounds__(kForkWide) fork_deal_kernel(const ForkParams p
     long long at = (long long)st.n_free + total.x + fork_scan<kForkWide>(make_int2(share.n, 0), mine, tmp).x;
     if (share.n > 0)
         for (long long w = share.w0; w < share.w1; ++w) {
-            const uint4 g = w == share.w0 ? share.g : fork_gone(p, w);
-            const uint32_t v[4] = {g.x, g.y, g.z, g.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                for (uint32_t bits = v[k]; bits; bits &= bits - 1) fork_push(p, q, st, at++, (int)(16 * w) + 4 * k + (__ffs(bits) >> 3));
+            for (uint32_t bits = w == share.w0 ? share.g : fork_gone(p, w); bits; bits &= bits - 1) fork_push(p, q, st, at++, (int)(4 * w) + (__ffs(bits) >> 3));
         }
     fork_results(p, q, st, blockIdx.x * kForkWide + threadIdx.x, p.blocks * kForkWide);
 }
@@ -512,7 +506,8 @@ constexpr int kCopyWarps = 8;
 constexpr int kCopyLoads = 8;                 // of 16 bytes a lane
 constexpr int kCopyPiece = 32 * kCopyLoads;   // words of 16 bytes
 
-__global__ void __launch_bounds__(kCopyWarps * 32) page_copy_kernel(const __grid_constant__ CopyParams p)
+template <int POOLS>
+__global__ void __launch_bounds__(kCopyWarps * 32) page_copy_kernel(const __grid_constant__ CopyParams<POOLS> p)
 {
     pdl_wait();
     pdl_trigger();
@@ -537,9 +532,10 @@ __global__ void __launch_bounds__(kCopyWarps * 32) page_copy_kernel(const __grid
         if (at + 32 * k < n) __stcs(dst + at + 32 * k, v[k]);
 }
 
-cudaError_t launch_page_copy(const CopyParams &in, cudaStream_t s, bool pdl)
+template <int POOLS>
+cudaError_t launch_page_copy(const CopyParams<POOLS> &in, cudaStream_t s, bool pdl)
 {
-    CopyParams p = in;
+    CopyParams<POOLS> p = in;
     int words = 0;
     for (int i = 0; i < p.n_pools; ++i) words = p.tiles * (p.tile_bytes[i] / 16) > words ? p.tiles * (p.tile_bytes[i] / 16) : words;
     p.pieces = (words + kCopyPiece - 1) / kCopyPiece;
@@ -553,8 +549,10 @@ cudaError_t launch_page_copy(const CopyParams &in, cudaStream_t s, bool pdl)
     at[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, page_copy_kernel, p);
+    return cudaLaunchKernelEx(&cfg, page_copy_kernel<POOLS>, p);
 }
+template cudaError_t launch_page_copy(const CopyParams<kFewPools> &, cudaStream_t, bool);
+template cudaError_t launch_page_copy(const CopyParams<KVQ_MAX_COPY_POOLS> &, cudaStream_t, bool);
 
 // ---------------------------------------------------------------------------
 // Move: a quad of lanes takes a token of a head (kvq_quad.cuh), a warp eight at a

@@ -57,9 +57,12 @@ struct ForkParams {
     int n_seqs, pshift, n_pages, stride, out_stride, max_blocks;
 };
 
+// Two sizes: a launch carries its parameters along, and 1.5 KB of them take 0.2 us longer than 200 bytes.
+constexpr int kFewPools = 8;
+template <int POOLS>
 struct CopyParams {
-    uint8_t *data[KVQ_MAX_COPY_POOLS];
-    uint16_t heads[KVQ_MAX_COPY_POOLS], tile_bytes[KVQ_MAX_COPY_POOLS];
+    uint8_t *data[POOLS];
+    uint16_t heads[POOLS], tile_bytes[POOLS];
     const int *from, *to, *held;
     int n_pools, n_copies, n_pages, most_heads, tiles;
     int pieces, blocks;   // of a head's run of bytes; of a page in one pool
@@ -79,7 +82,8 @@ cudaError_t prepare_qkv();
 cudaError_t launch_qkv(const QkvParams &p, int v_type, int k_type, int n_sms, cudaStream_t s, bool pdl);
 cudaError_t prepare_page_fork();
 cudaError_t launch_page_fork(const ForkParams &p, int n_sms, cudaStream_t s, bool pdl);
-cudaError_t launch_page_copy(const CopyParams &p, cudaStream_t s, bool pdl);
+template <int POOLS>
+cudaError_t launch_page_copy(const CopyParams<POOLS> &p, cudaStream_t s, bool pdl);
 // rows null: from slots to slots; else through them.
 int staged_row_bytes(int v_type, int k_type);
 cudaError_t launch_paged_move(const MoveParams &p, int v_type, int k_type, int n_sms, cudaStream_t s, bool pdl);

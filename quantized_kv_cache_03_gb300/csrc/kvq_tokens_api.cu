@@ -65,7 +65,7 @@ struct ForkPlan {
 ForkPlan plan_fork(int n_seqs, int n_pages)
 {
     ForkPlan f;
-    f.blocks = n_pages / 16384 + 1 < 1024 ? n_pages / 16384 + 1 : 1024;   // 16 pages a thread, more in very large pools
+    f.blocks = n_pages / 4096 + 1 < 1024 ? n_pages / 4096 + 1 : 1024;   // 4 pages a thread, more in very large pools
     f.marks = up256((size_t)n_pages);
     f.owner = 3 * f.marks;
     f.seqs = f.owner + up256((size_t)n_pages * sizeof(int));
@@ -257,21 +257,28 @@ kvq_status kvq_page_copy(const kvq_pages *pools, int32_t n_pools, const int32_t 
     int n_sms = 0;
     const kvq_status st = tokens_setup(&n_sms);
     if (st != KVQ_OK) return st;
-    CopyParams p = {};
-    for (int i = 0; i < n_pools; ++i) {
-        p.data[i] = static_cast<uint8_t *>(pools[i].data);
-        p.heads[i] = (uint16_t)pools[i].n_kv_heads;
-        p.tile_bytes[i] = (uint16_t)page_tile_bytes(pools[i].v_type, pools[i].k_type);
+    auto run = [&](auto &p) {
+        for (int i = 0; i < n_pools; ++i) {
+            p.data[i] = static_cast<uint8_t *>(pools[i].data);
+            p.heads[i] = (uint16_t)pools[i].n_kv_heads;
+            p.tile_bytes[i] = (uint16_t)page_tile_bytes(pools[i].v_type, pools[i].k_type);
+        }
+        p.from = from;
+        p.to = to;
+        p.held = held;
+        p.n_pools = n_pools;
+        p.n_copies = n_copies;
+        p.n_pages = pools->n_pages;
+        p.most_heads = most;
+        p.tiles = pools->page_tokens / kWTile;
+        return done(launch_page_copy(p, static_cast<cudaStream_t>(stream), pdl_on()));
+    };
+    if (n_pools <= kFewPools) {
+        CopyParams<kFewPools> p;
+        return run(p);
     }
-    p.from = from;
-    p.to = to;
-    p.held = held;
-    p.n_pools = n_pools;
-    p.n_copies = n_copies;
-    p.n_pages = pools->n_pages;
-    p.most_heads = most;
-    p.tiles = pools->page_tokens / kWTile;
-    return done(launch_page_copy(p, static_cast<cudaStream_t>(stream), pdl_on()));
+    CopyParams<KVQ_MAX_COPY_POOLS> p;
+    return run(p);
 }
 
 kvq_status kvq_paged_move_workspace_size(const kvq_pages *p, int32_t n_tokens, size_t *bytes)
