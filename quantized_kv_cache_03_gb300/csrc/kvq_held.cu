@@ -555,21 +555,13 @@ template cudaError_t launch_page_copy(const CopyParams<kFewPools> &, cudaStream_
 template cudaError_t launch_page_copy(const CopyParams<KVQ_MAX_COPY_POOLS> &, cudaStream_t, bool);
 
 // ---------------------------------------------------------------------------
-// Move: a quad of lanes takes a token of a head (kvq_quad.cuh), a warp eight at a
-// time: four pairs of tokens whose new slots are an even place and the next, which
-// share words of V codes, or, where the list has no pairs, eight tokens.  A warp
-// looks at eight tokens of the list and goes over some of the heads.
+// Gather, many rows: a quad of lanes takes a token of a head (kvq_quad.cuh), a warp
+// eight tokens.  Bound by memory: 131072 tokens, 8 heads, q8_0 V: 218 us in fp32, 0.92
+// of a copy's rate (a lane's 32 bytes stored as they lie, half a sector at a time:
+// 351), 131 us in fp16, 0.92 (a warp to a pair of rows: 179); q4_0 V in fp16 121 us,
+// 0.92.
 // ---------------------------------------------------------------------------
-constexpr int kMoveWarps = 4;
-constexpr int kMoveTokens = 8;   // of a warp
-
-// Which half of the way: from slots to slots, from slots to the staged rows, from those to slots.
-constexpr int kMoveDirect = 0, kMoveOut = 1, kMoveIn = 2;
-
-struct alignas(16) MoveShared {   // (read in words of 16 bytes, warp after warp)
-    float cosines[kMoveTokens][kAngleRow], sines[kMoveTokens][kAngleRow];   // of the quads' turns; of row 0 alone where they are the same
-    uint8_t list[kMoveTokens];
-};
+constexpr int kGatherWarps = 4;
 
 // The lane's values of a held key in fp32, a block at a time as quad_floats has them.
 template <int KT, int ROT>
@@ -595,6 +587,150 @@ __device__ __forceinline__ void key_floats(const uint32_t *w, float scale, float
         for (int k = 0; k < 4; ++k) x[k] = mul2(add2(x[k], less), s2);
     }
 }
+
+// A block's words of a quad, w[0] and w[1] (N of them each) of lane c being dims 8 c and on and 8 c + 4 and on, dealt out
+// so that those of its four lanes are neighbours: dims 4 c and on, and 16 + 4 c and on.  Stores of 16 bytes a lane then
+// fill whole sectors.
+template <int N>
+__device__ __forceinline__ void spread(const uint32_t *w, int c, uint32_t (&x)[2][N])
+{
+    const int lane = (threadIdx.x & 28) + (c >> 1);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t a = __shfl_sync(0xffffffffu, w[i], lane + 2 * j), b = __shfl_sync(0xffffffffu, w[N + i], lane + 2 * j);
+            x[j][i] = c & 1 ? b : a;
+        }
+}
+// Four values, as fp16 or fp32.
+template <bool O16>
+__device__ __forceinline__ void put4(void *base, size_t elem, float2 x, float2 y)
+{
+    if (O16) *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(base) + elem) = make_uint2(pack_half2(x.x, x.y), pack_half2(y.x, y.y));
+    else *reinterpret_cast<float4 *>(static_cast<float *>(base) + elem) = make_float4(x.x, x.y, y.x, y.y);
+}
+// The four values of code bytes w (code + bias) times s.
+template <int BIAS>
+__device__ __forceinline__ void scaled4(uint32_t w, float s, float2 &x, float2 &y)
+{
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 | k));
+    const float2 less = make_float2(-8388608.f - BIAS, -8388608.f - BIAS), s2 = make_float2(s, s);
+    x = mul2(add2(make_float2(v[0], v[1]), less), s2);
+    y = mul2(add2(make_float2(v[2], v[3]), less), s2);
+}
+
+template <int VT, int KT, bool O16>
+__global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(const GatherParams p)
+{
+    using T = PageTile<VT, KT>;
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, c = lane & 3, quad = lane >> 2;
+    const long long job = (long long)blockIdx.x * kGatherWarps + (threadIdx.x >> 5);
+    const int window = (int)(job / p.chunks), h0 = (int)(job - (long long)window * p.chunks) * p.heads, h1 = min(p.pool.n_kv_heads, h0 + p.heads);
+    const long long tok = (long long)window * 8 + quad;
+    const int slot = tok < p.n_tokens ? p.slots[tok] : -1;
+    const bool mine = slot >= 0 && slot < p.pool.n_slots;
+    if (!__any_sync(0xffffffffu, mine)) return;
+    const int place = slot & ((1 << p.pool.pshift) - 1), u = place & 15;
+    const uint8_t *tile = tile_of(p.pool, mine ? slot >> p.pool.pshift : 0, h0, place >> 4, T::BYTES);
+    size_t at = ((size_t)tok * p.pool.n_kv_heads + h0) * kD;
+    QuadRow<VT, KT> r;
+#pragma unroll
+    for (int k = 0; k < QuadRow<VT, KT>::KW; ++k) r.k[k] = 0;
+#pragma unroll
+    for (int k = 0; k < QuadRow<VT, KT>::VW; ++k) r.v[k] = 0;
+    r.ks[0] = r.ks[1] = 0;
+    uint4 vs = make_uint4(0, 0, 0, 0);
+    for (int h = h0; h < h1; ++h, tile += (size_t)T::BYTES << (p.pool.pshift - 4), at += kD) {
+        if (mine) {
+            quad_get_key<VT, KT>(r, tile, u, c);
+            quad_get_value<VT, KT>(r, tile, u, c);
+            vs = *reinterpret_cast<const uint4 *>(tile + T::VS_OFF + 16 * (u / 2));
+        }
+        const uint32_t sel = u & 1 ? 0x7632 : 0x5410;
+        const float2 k01 = half2_of(r.ks[0]), k23 = half2_of(r.ks[1]), v01 = half2_of(__byte_perm(vs.x, vs.y, sel)), v23 = half2_of(__byte_perm(vs.z, vs.w, sel));
+        const float ks[4] = {k01.x, k01.y, k23.x, k23.y}, ds[4] = {v01.x, v01.y, v23.x, v23.y};
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            float2 x[4];
+            constexpr int N = KT == KVQ_K_F16 ? 2 : 1;
+            if (O16) {
+                key_floats<KT, kRotNone>(r.k + 2 * N * b, ks[b], x);
+                if (mine) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.k_out) + at + 32 * b + 8 * c) = quad_halves<kRotNone>(x);
+            } else {
+                uint32_t w[2][N];
+                spread<N>(r.k + 2 * N * b, c, w);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (KT == KVQ_K_F16) x[0] = half2_of(w[j][0]), x[1] = half2_of(w[j][N - 1]);
+                    else scaled4<128>(w[j][0], ks[b], x[0], x[1]);
+                    if (mine) put4<O16>(p.k_out, at + 32 * b + 16 * j + 4 * c, x[0], x[1]);
+                }
+            }
+            if (VT == KVQ_V_Q8_0 && O16) {
+                scaled4<128>(r.v[2 * b], ds[b], x[0], x[1]);
+                scaled4<128>(r.v[2 * b + 1], ds[b], x[2], x[3]);
+                if (mine) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.v_out) + at + 32 * b + 8 * c) = quad_halves<kRotNone>(x);
+            } else if (VT == KVQ_V_Q8_0) {
+                uint32_t w[2][1];
+                spread<1>(r.v + 2 * b, c, w);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    scaled4<128>(w[j][0], ds[b], x[0], x[1]);
+                    if (mine) put4<O16>(p.v_out, at + 32 * b + 16 * j + 4 * c, x[0], x[1]);
+                }
+            } else {   // code bytes 4 quart .. + 3: their low nibbles, their high ones 16 values on
+                scaled4<8>(r.v[b] & 0x0f0f0f0fu, ds[b], x[0], x[1]);
+                scaled4<8>(r.v[b] >> 4 & 0x0f0f0f0fu, ds[b], x[2], x[3]);
+                if (mine) {
+                    put4<O16>(p.v_out, at + 32 * b + 4 * quart_of(c), x[0], x[1]);
+                    put4<O16>(p.v_out, at + 32 * b + 16 + 4 * quart_of(c), x[2], x[3]);
+                }
+            }
+        }
+    }
+}
+
+template <bool O16>
+static cudaError_t gather_t(const GatherParams &p, int v_type, int k_type, int blocks, cudaStream_t s, bool pdl)
+{
+    void (*fn)(GatherParams) =
+        k_type == KVQ_K_F16 ? (v_type == KVQ_V_Q4_0 ? gather_kernel<KVQ_V_Q4_0, KVQ_K_F16, O16> : gather_kernel<KVQ_V_Q8_0, KVQ_K_F16, O16>)
+                            : (v_type == KVQ_V_Q4_0 ? gather_kernel<KVQ_V_Q4_0, KVQ_K_I8, O16> : gather_kernel<KVQ_V_Q8_0, KVQ_K_I8, O16>);
+    return launch_pdl(fn, p, blocks, kGatherWarps * 32, 0, s, pdl);
+}
+
+cudaError_t launch_gather_many(const PagedRowsParams &rows, int v_type, int k_type, int out_type, int n_sms, cudaStream_t s, bool pdl)
+{
+    GatherParams p = {rows.pool, rows.slots, rows.n_tokens, rows.k_out, rows.v_out, 1, 1};
+    const long long windows = ((long long)p.n_tokens + 7) / 8;
+    const long long want = windows * p.pool.n_kv_heads / ((long long)n_sms * 48);
+    p.heads = want < 1 ? 1 : want > p.pool.n_kv_heads ? p.pool.n_kv_heads : (int)want;
+    p.chunks = (p.pool.n_kv_heads + p.heads - 1) / p.heads;
+    const int blocks = (int)((windows * p.chunks + kGatherWarps - 1) / kGatherWarps);
+    return out_type == KVQ_OUT_F16 ? gather_t<true>(p, v_type, k_type, blocks, s, pdl) : gather_t<false>(p, v_type, k_type, blocks, s, pdl);
+}
+
+// ---------------------------------------------------------------------------
+// Move: a quad of lanes takes a token of a head (kvq_quad.cuh), a warp eight at a
+// time: four pairs of tokens whose new slots are an even place and the next, which
+// share words of V codes, or, where the list has no pairs, eight tokens.  A warp
+// looks at eight tokens of the list and goes over some of the heads.
+// ---------------------------------------------------------------------------
+constexpr int kMoveWarps = 4;
+constexpr int kMoveTokens = 8;   // of a warp
+
+// Which half of the way: from slots to slots, from slots to the staged rows, from those to slots.
+constexpr int kMoveDirect = 0, kMoveOut = 1, kMoveIn = 2;
+
+struct alignas(16) MoveShared {   // (read in words of 16 bytes, warp after warp)
+    float cosines[kMoveTokens][kAngleRow], sines[kMoveTokens][kAngleRow];   // of the quads' turns; of row 0 alone where they are the same
+    uint8_t list[kMoveTokens];
+};
 
 // The quad's key turned; SOME: only where `turns`, the others' stay as they are.
 // scratch: the quad's 128 floats in shared memory (part).

@@ -320,7 +320,7 @@ kvq_status kvq_paged_gather(const kvq_pages *p, const int32_t *slots, int32_t n_
     r.n_tokens = n_tokens;
     r.k_out = k_out;
     r.v_out = v_out;
-    return done(launch_paged_gather(r, p->v_type, p->k_type, out_type, static_cast<cudaStream_t>(stream), pdl_on()));
+    return done(launch_paged_gather(r, p->v_type, p->k_type, out_type, n_sms, static_cast<cudaStream_t>(stream), pdl_on()));
 }
 
 kvq_status kvq_paged_attn_workspace_size(const kvq_paged_desc *a, size_t *bytes)

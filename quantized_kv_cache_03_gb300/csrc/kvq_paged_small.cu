@@ -349,12 +349,9 @@ cudaError_t launch_paged_append(const PagedRowsParams &p, int v_type, int k_type
 }
 
 // ---------------------------------------------------------------------------
-// Gather: four values a lane of a row's K and V, for a pair of both rows.
-// Bound by the writes (1 KB per row with fp32 output): 131072 tokens, 8 heads,
-// q8_0 V: 225 us, 6.0 TB/s, nine tenths of a copy's rate (284 us with a warp per
-// row, which fetches the V words of eight positions to use one's); fp16 output
-// 179 us, 4.6 TB/s, and 186 us, 5.1 TB/s, with F16 K: the same instructions for
-// fewer bytes.
+// Gather, some rows: four values a lane of a row's K and V, for a pair of both
+// rows.  64 tokens, 8 heads: 1.6 us, launch latency.  (Many rows are bound by
+// instructions here, 140 a row, and go to gather_kernel of kvq_held.cu.)
 // ---------------------------------------------------------------------------
 template <bool O16>
 __device__ __forceinline__ void put4(void *base, size_t elem, const float (&x)[4])
@@ -438,8 +435,11 @@ static cudaError_t gather_t(const PagedRowsParams &p, int v_type, int k_type, cu
     return launch_pdl(fn, p, row_blocks(p), kRowWarps * 32, 0, s, pdl);
 }
 
-cudaError_t launch_paged_gather(const PagedRowsParams &p, int v_type, int k_type, int out_type, cudaStream_t s, bool pdl)
+cudaError_t launch_paged_gather(const PagedRowsParams &p, int v_type, int k_type, int out_type, int n_sms, cudaStream_t s, bool pdl)
 {
+    // Eight rows to a warp from 4096 rows on (8 heads, q8_0 V, fp16 / fp32 output: 512 tokens 2.2 / 2.5 us here and 1.8 /
+    // 2.2 there, 256 tokens 1.6 / 1.7 and 1.8 / 2.1).
+    if ((long long)p.n_tokens * p.pool.n_kv_heads >= 4096) return launch_gather_many(p, v_type, k_type, out_type, n_sms, s, pdl);
     return out_type == KVQ_OUT_F16 ? gather_t<true>(p, v_type, k_type, s, pdl) : gather_t<false>(p, v_type, k_type, s, pdl);
 }
 

@@ -68,6 +68,14 @@ struct CopyParams {
     int pieces, blocks;   // of a head's run of bytes; of a page in one pool
 };
 
+struct GatherParams {
+    PoolDesc pool;
+    const int *slots;
+    int n_tokens;
+    void *k_out, *v_out;
+    int heads, chunks;             // kv heads of a warp, and such pieces of a token's
+};
+
 struct MoveParams {
     PoolDesc pool;
     RopeDesc rope;

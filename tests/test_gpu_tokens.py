@@ -379,6 +379,32 @@ def test_copy_past_32_bits():
         assert np.array_equal(a[1, :, 0, 3], a[0, :, 0, 7]) and np.array_equal(a[2, :, 0, 9], a[0, :, 0, 3])
 
 
+# ---------------------------------------------------------------- gather --
+@pytest.mark.parametrize("k_type,v_type", [(I8, Q4), (I8, Q8), (F16, Q4), (F16, Q8)])
+@pytest.mark.parametrize("T,H,page", [(4096, 1, 16), (1370, 3, 64), (513, 8, 256), (5001, 8, 32)])
+def test_gather_of_many_rows(T, H, page, k_type, v_type):
+    """Rows past the size from which a warp takes eight: exact values (code * scale fits 24 bits), rounded once in fp16; slots in
+    order, scattered, listed twice, and ones that are none, whose rows stay."""
+    r = np.random.default_rng(T)
+    n_pages = 700 // page + 3
+    pool, rows = _filled(r, n_pages, page, H, k_type, v_type)
+    k, v = values(rows, v_type)
+    slots = r.integers(0, n_pages * page, T)
+    slots[:200] = np.arange(200) + 5
+    slots[r.integers(0, T, 40)] = -1
+    slots[7:9] = n_pages * page, 2 ** 31 - 1
+    slots[-1] = -2 ** 31
+    some = (slots >= 0) & (slots < n_pages * page)
+    for dt, npt in ((torch.float32, np.float32), (torch.float16, np.float16)):
+        ko, vo = (torch.full((T, H, 128), 777.0, dtype=dt, device=dev()) for _ in range(2))
+        kvq.kvq_paged_gather(pool, i32(slots), ko, vo)
+        for o, ref in ((ko, k), (vo, v)):
+            want = np.full((T, H, 128), 777, npt)
+            with np.errstate(over="ignore"):
+                want[some] = ref[slots[some]].astype(npt)
+            assert np.array_equal(o.cpu().numpy(), want)
+
+
 # ------------------------------------------------------------------ move --
 def _filled(r, n_pages, page, H, k_type, v_type, big=True):
     """A pool of quantized tokens, and its rows."""
