@@ -696,15 +696,17 @@ __global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(const GatherP
 }
 
 template <bool O16>
-static cudaError_t gather_t(const GatherParams &p, int v_type, int k_type, int blocks, cudaStream_t s, bool pdl)
+static cudaError_t gather_t(const GatherParams &p, int v_type, int k_type, int blocks, cudaStream_t s)
 {
     void (*fn)(GatherParams) =
         k_type == KVQ_K_F16 ? (v_type == KVQ_V_Q4_0 ? gather_kernel<KVQ_V_Q4_0, KVQ_K_F16, O16> : gather_kernel<KVQ_V_Q8_0, KVQ_K_F16, O16>)
                             : (v_type == KVQ_V_Q4_0 ? gather_kernel<KVQ_V_Q4_0, KVQ_K_I8, O16> : gather_kernel<KVQ_V_Q8_0, KVQ_K_I8, O16>);
-    return launch_pdl(fn, p, blocks, kGatherWarps * 32, 0, s, pdl);
+    // Never beside the last blocks of the launch in front: blocks that are placed while those still hold registers
+    // crowd on the few SMs with room for them (777 tokens after kvq_qkv: 16.5 us for the two, 11.7 so).
+    return launch_pdl(fn, p, blocks, kGatherWarps * 32, 0, s, false);
 }
 
-cudaError_t launch_gather_many(const PagedRowsParams &rows, int v_type, int k_type, int out_type, int n_sms, cudaStream_t s, bool pdl)
+cudaError_t launch_gather_many(const PagedRowsParams &rows, int v_type, int k_type, int out_type, int n_sms, cudaStream_t s)
 {
     GatherParams p = {rows.pool, rows.slots, rows.n_tokens, rows.k_out, rows.v_out, 1, 1};
     const long long windows = ((long long)p.n_tokens + 7) / 8;
@@ -712,7 +714,7 @@ cudaError_t launch_gather_many(const PagedRowsParams &rows, int v_type, int k_ty
     p.heads = want < 1 ? 1 : want > p.pool.n_kv_heads ? p.pool.n_kv_heads : (int)want;
     p.chunks = (p.pool.n_kv_heads + p.heads - 1) / p.heads;
     const int blocks = (int)((windows * p.chunks + kGatherWarps - 1) / kGatherWarps);
-    return out_type == KVQ_OUT_F16 ? gather_t<true>(p, v_type, k_type, blocks, s, pdl) : gather_t<false>(p, v_type, k_type, blocks, s, pdl);
+    return out_type == KVQ_OUT_F16 ? gather_t<true>(p, v_type, k_type, blocks, s) : gather_t<false>(p, v_type, k_type, blocks, s);
 }
 
 // ---------------------------------------------------------------------------
