@@ -147,6 +147,9 @@ kvq_status kvq_qkv(const kvq_qkv_desc *a, void *stream)
     if (keys && !rows_ok(a->k16, a->k_stride, a->n_kv_heads)) return KVQ_ERR_INVALID_ARG;
     if (a->pages && !rows_ok(a->v16, a->v_stride, a->n_kv_heads)) return KVQ_ERR_INVALID_ARG;
     if (a->k_out && !rows_ok(a->k_out, a->k_out_stride, a->n_kv_heads)) return KVQ_ERR_INVALID_ARG;
+    // in place a row is read and written by the same lanes, so the rows have to be the same ones
+    if ((a->n_q_heads > 0 && a->q_out == a->q16 && a->q_out_stride != a->q_stride) || (a->k_out && a->k_out == a->k16 && a->k_out_stride != a->k_stride))
+        return KVQ_ERR_INVALID_ARG;
     if (!norm_ok(a->q_norm) || !norm_ok(a->k_norm)) return KVQ_ERR_INVALID_ARG;
     if ((a->pages && !int_ptr(a->slots)) || !aligned(a->slots, 4)) return KVQ_ERR_INVALID_ARG;
     const RopeDesc rope = rope_of(a->rope);

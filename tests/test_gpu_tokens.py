@@ -180,6 +180,55 @@ def test_values_that_are_not_finite_and_large_ones():
                 assert np.isnan(o[bad]).any(-1).all()
 
 
+@pytest.mark.parametrize("k_type,v_type", [(I8, Q4), (I8, Q8), (F16, Q4), (F16, Q8)])
+def test_quantized_as_append_does(k_type, v_type):
+    """Values at, just below and just above the halves of their scale, at scales from fp16's subnormals to its largest, zeros,
+    infinities and NaN among them: the bytes of kvq_paged_append, from pairs of places and single ones."""
+    r = np.random.default_rng(3)
+    n, H = 256, 4
+    top = np.exp2(r.uniform(-25, 16, (n, H, 4, 1))).clip(0, 65504).astype(np.float16)
+    top[:8] = np.array([0, 2.0 ** -24, 3 * 2.0 ** -24, 190 * 2.0 ** -24, 2.0 ** -14, 65504, 1, 127], np.float16)[:, None, None, None]
+    kv = []
+    for most in (127, 8 if v_type == Q4 else 127):
+        s = (top.astype(np.float32) / np.float32(most)).astype(np.float16).astype(np.float64)
+        x = ((r.integers(0, most, (n, H, 4, 32)) + 0.5) * s).clip(0, 65504).astype(np.float16)
+        x = np.abs(x).view(np.int16) + r.integers(-1, 2, x.shape).astype(np.int16)
+        x = np.minimum(x.clip(0).astype(np.int16), top.view(np.int16)).view(np.float16)
+        x = np.where(r.random(x.shape) < 0.5, x, -x)
+        x[..., 5:6] = top * np.where(r.random(top.shape) < 0.5, 1, -1).astype(np.float16)
+        x[20:23, :, 1, 7] = np.array([np.inf, -np.inf, np.nan], np.float16)[:, None]
+        x[23, :, 2] = np.nan
+        kv.append(to_dev(np.ascontiguousarray(x.reshape(n, H, 128))))
+    ka = torch.zeros_like(kv[0])
+    kvq.kvq_qkv(None, kv[0], None, None, None, None, k_out=ka)   # the fp16 keys: as they were, NaN with bits of its own
+    assert torch.equal(torch.nan_to_num(ka), torch.nan_to_num(kv[0])) and torch.equal(ka.isnan(), kv[0].isnan())
+    for slots in (np.arange(n), np.arange(n) + 7, 2 * np.arange(n) % 509):
+        one, two = (kvq.PagePool(9, 64, H, v_type, k_type=k_type) for _ in range(2))
+        one.data.fill_(POISON)
+        two.data.fill_(POISON)
+        kvq.kvq_qkv(None, kv[0], kv[1], None, None, None, pool=one, slots=i32(slots))
+        kvq.kvq_paged_append(two, ka, kv[1], i32(slots))
+        assert torch.equal(one.data, two.data)
+
+
+def test_into_pages_past_32_bits():
+    H, page = 8, 256
+    n_pages = (5 << 30) // (H * 16 * 4352)
+    pool = kvq.PagePool(n_pages, page, H, Q8)
+    r = np.random.default_rng(8)
+    x = to_dev(_tokens(r, 20, 1, H))
+    slots = np.concatenate([np.arange(10) + (n_pages - 1) * page + 3, np.arange(10)])
+    rope, pos, q = kvq.Rope(128, device=dev()), i32(np.arange(20) + 9), torch.zeros((20, 1, 128), dtype=torch.float16, device=dev())
+    kvq.kvq_qkv(x[:, :1], x[:, 1:1 + H], x[:, 1 + H:], pos, rope, q, pool=pool, slots=i32(slots))
+    small, ka = kvq.PagePool(2, page, H, Q8), torch.zeros((20, H, 128), dtype=torch.float16, device=dev())
+    kvq.kvq_qkv(None, x[:, 1:1 + H], None, pos, rope, None, k_out=ka)
+    kvq.kvq_paged_append(small, ka, x[:, 1 + H:].contiguous(), i32(np.where(slots >= page, slots - (n_pages - 2) * page, slots)))
+    outs = [torch.zeros((20, H, 128), device=dev()) for _ in range(4)]
+    kvq.kvq_paged_gather(pool, i32(slots), outs[0], outs[1])
+    kvq.kvq_paged_gather(small, i32(np.where(slots >= page, slots - (n_pages - 2) * page, slots)), outs[2], outs[3])
+    assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3]) and outs[0].any()
+
+
 def test_a_large_step():
     """More tokens and heads than one pass of the launch holds."""
     T, Hq, H = 5001, 20, 4

@@ -113,7 +113,7 @@ PLAIN = dict(pages=False, ko=0x90000, kos=256, v=0)
                                   dict(q=0), dict(k=0), dict(v=0), dict(q=0x20008), dict(k=0x30002), dict(v=0x40008), dict(qs=504), dict(qs=516), dict(ks=248),
                                   dict(vs=252), dict(qn=0x50004), dict(kn=0x50008), dict(pos=0), dict(pos=0x60002), dict(qo=0), dict(qo=0x70008), dict(qos=500),
                                   dict(slots=0), dict(slots=0x80001), dict(ko=0x90000, kos=256), dict(pages=False), dict(hk=3, ks=384, vs=384), dict(hk=0),
-                                  dict(n=1 << 28), dict(PLAIN, ko=0x90008), dict(PLAIN, kos=248), dict(PLAIN, hk=0), dict(PLAIN, slots=0x80002)])
+                                  dict(n=1 << 28), dict(PLAIN, ko=0x90008), dict(PLAIN, kos=248), dict(PLAIN, hk=0), dict(PLAIN, slots=0x80002), dict(qo=0x20000, qos=520), dict(PLAIN, ko=0x30000, kos=264)])
 def test_qkv_refuses(lib, over):
     assert _qkv(lib, **over) == BAD
 
