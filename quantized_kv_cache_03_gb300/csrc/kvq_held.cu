@@ -742,49 +742,61 @@ __device__ __forceinline__ void turn_key(QuadRow<VT, KT> &r, bool turns, const f
     constexpr int kWords = KT == KVQ_K_F16 ? 4 : 2;   // of a block
     const float2 s01 = half2_of(r.ks[0]), s23 = half2_of(r.ks[1]);
     const float scale[4] = {s01.x, s01.y, s23.x, s23.y};
-    QuadF x;
+    Quad16 h;
+    if (ROT == kRotHalf) {
 #pragma unroll
-    for (int b = 0; b < 4; ++b) key_floats<KT, ROT>(r.k + kWords * b, scale[b], x.b[b]);
-    if (ROT == kRotPart) {   // neighbours to group pairs, and back
+        for (int b = 0; b < 2; ++b) {
+            float2 x[4], y[4];
+            key_floats<KT, ROT>(r.k + kWords * b, scale[b], x);
+            key_floats<KT, ROT>(r.k + kWords * (b + 2), scale[b + 2], y);
+            quad_turn8(x, y, cosines, sines, 32 * b + 8 * c);
+            h.b[b] = quad_halves<ROT>(x);
+            h.b[b + 2] = quad_halves<ROT>(y);
+        }
+    } else if (ROT == kRotPairs) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            float2 x[4];
+            key_floats<KT, ROT>(r.k + kWords * b, scale[b], x);
+            if (32 * b + 8 * c < n_rot) quad_turn4(x, cosines, sines, 16 * b + 4 * c);   // all of the lane's four pairs or none
+            h.b[b] = quad_halves<ROT>(x);
+        }
+    } else {   // neighbours to group pairs, and back
+        float2 x[4];
         __syncwarp();
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
+        for (int b = 0; b < 4; ++b) {
+            key_floats<KT, ROT>(r.k + kWords * b, scale[b], x);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-                *reinterpret_cast<float4 *>(scratch + 32 * b + 8 * c + 4 * k) = make_float4(x.b[b][2 * k].x, x.b[b][2 * k].y, x.b[b][2 * k + 1].x, x.b[b][2 * k + 1].y);
-        __syncwarp();
-        QuadF y;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const PartGroups g(c + 4 * b, n_rot);
-            const float4 u = *reinterpret_cast<const float4 *>(scratch + g.a), v = *reinterpret_cast<const float4 *>(scratch + g.b);
-            y.b[b][0] = make_float2(u.x, u.y);
-            y.b[b][1] = make_float2(u.z, u.w);
-            y.b[b][2] = make_float2(v.x, v.y);
-            y.b[b][3] = make_float2(v.z, v.w);
-        }
-        quad_turn<ROT>(y, cosines, sines, c, n_rot);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const PartGroups g(c + 4 * b, n_rot);
-            *reinterpret_cast<float4 *>(scratch + g.a) = make_float4(y.b[b][0].x, y.b[b][0].y, y.b[b][1].x, y.b[b][1].y);
-            *reinterpret_cast<float4 *>(scratch + g.b) = make_float4(y.b[b][2].x, y.b[b][2].y, y.b[b][3].x, y.b[b][3].y);
+                *reinterpret_cast<float4 *>(scratch + 32 * b + 8 * c + 4 * k) = make_float4(x[2 * k].x, x[2 * k].y, x[2 * k + 1].x, x[2 * k + 1].y);
         }
         __syncwarp();
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
+        for (int b = 0; b < 4; ++b) {
+            const PartGroups g(c + 4 * b, n_rot);
+            float4 *const first = reinterpret_cast<float4 *>(scratch + g.a), *const second = reinterpret_cast<float4 *>(scratch + g.b);
+            const float4 u = *first, v = *second;
+            x[0] = make_float2(u.x, u.y);
+            x[1] = make_float2(u.z, u.w);
+            x[2] = make_float2(v.x, v.y);
+            x[3] = make_float2(v.z, v.w);
+            if (g.rotates) quad_turn4(x, cosines, sines, 4 * (c + 4 * b));
+            *first = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+            *second = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const float4 u = *reinterpret_cast<const float4 *>(scratch + 32 * b + 8 * c + 4 * k);
-                x.b[b][2 * k] = make_float2(u.x, u.y);
-                x.b[b][2 * k + 1] = make_float2(u.z, u.w);
+                x[2 * k] = make_float2(u.x, u.y);
+                x[2 * k + 1] = make_float2(u.z, u.w);
             }
-    } else {
-        quad_turn<ROT>(x, cosines, sines, c, n_rot);
+            h.b[b] = quad_halves<kRotNone>(x);
+        }
     }
-    Quad16 h;
-#pragma unroll
-    for (int b = 0; b < 4; ++b) h.b[b] = quad_halves<ROT>(x.b[b]);
     if (KT == KVQ_K_F16) {
         if (!SOME || turns)
 #pragma unroll

@@ -74,9 +74,6 @@ __device__ __forceinline__ void quad_store(uint16_t *row, int c, int n_rot, cons
 // The same values in fp32, as pairs for packed arithmetic: of neighbours
 // (x0 x1), (x2 x3), ..., or, where pairs side by side rotate, of their first
 // values and of their second ones: (x0 x2), (x4 x6), (x1 x3), (x5 x7).
-struct QuadF {
-    float2 b[4][4];
-};
 template <int ROT>
 __device__ __forceinline__ void quad_floats(const uint4 &w, float2 (&x)[4])
 {
@@ -110,29 +107,21 @@ __device__ __forceinline__ void quad_turn2(float2 &a, float2 &b, float2 c, float
     a = u;
     b = v;
 }
-template <int ROT>
-__device__ __forceinline__ void quad_turn(QuadF &x, const float *cosines, const float *sines, int c, int n_rot)
+// Four pairs at `at` of a token's table: x[0], x[1] their first values, x[2], x[3] the second.
+__device__ __forceinline__ void quad_turn4(float2 (&x)[4], const float *cosines, const float *sines, int at)
 {
-    auto four = [](const float *p) { return *reinterpret_cast<const float4 *>(p); };
-    if (ROT == kRotPairs || ROT == kRotPart) {
+    const float4 cs = *reinterpret_cast<const float4 *>(cosines + at), sn = *reinterpret_cast<const float4 *>(sines + at);
+    quad_turn2(x[0], x[2], make_float2(cs.x, cs.y), make_float2(sn.x, sn.y));
+    quad_turn2(x[1], x[3], make_float2(cs.z, cs.w), make_float2(sn.z, sn.w));
+}
+// Eight pairs: x the first values, y the second.
+__device__ __forceinline__ void quad_turn8(float2 (&x)[4], float2 (&y)[4], const float *cosines, const float *sines, int at)
+{
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int at = ROT == kRotPairs ? 16 * b + 4 * c : 4 * (c + 4 * b);   // the lane's four pairs
-            if (2 * at < n_rot) {                                                   // rotate, all or none
-                const float4 cs = four(cosines + at), sn = four(sines + at);
-                quad_turn2(x.b[b][0], x.b[b][2], make_float2(cs.x, cs.y), make_float2(sn.x, sn.y));
-                quad_turn2(x.b[b][1], x.b[b][3], make_float2(cs.z, cs.w), make_float2(sn.z, sn.w));
-            }
-        }
-    } else if (ROT == kRotHalf) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int k = 0; k < 4; k += 2) {
-                const float4 cs = four(cosines + 32 * b + 8 * c + 2 * k), sn = four(sines + 32 * b + 8 * c + 2 * k);
-                quad_turn2(x.b[b][k], x.b[b + 2][k], make_float2(cs.x, cs.y), make_float2(sn.x, sn.y));
-                quad_turn2(x.b[b][k + 1], x.b[b + 2][k + 1], make_float2(cs.z, cs.w), make_float2(sn.z, sn.w));
-            }
+    for (int k = 0; k < 4; k += 2) {
+        const float4 cs = *reinterpret_cast<const float4 *>(cosines + at + 2 * k), sn = *reinterpret_cast<const float4 *>(sines + at + 2 * k);
+        quad_turn2(x[k], y[k], make_float2(cs.x, cs.y), make_float2(sn.x, sn.y));
+        quad_turn2(x[k + 1], y[k + 1], make_float2(cs.z, cs.w), make_float2(sn.z, sn.w));
     }
 }
 
