@@ -304,8 +304,29 @@ __device__ __forceinline__ void stream_get(Stream &w)
     copy_commit();
 }
 
-// A block takes eight tokens and a share of the heads; a warp heads of four tokens
-// at a time.
+// y = x * rsqrt(mean(x^2) + eps) * w for a head's row, then its pairs (a, b) turned:
+// (a cos - b sin, a sin + b cos), then, for keys and values in pages, a scale of
+// fp16 for every 32 values and codes.  Sums, norms and rotations are fp32; a row
+// that stays fp16 is rounded once, and so is a key before it is quantized, so that
+// its codes are those of an append of the fp16 row.
+//
+// Bound by memory, with the arithmetic close behind: 8192 tokens of 40 + 2 * 8 heads
+// (q4_0 V, norms, halves) 38.0 us for 215 MB, 5.7 TB/s, 0.83 of a copy's rate, at half
+// of the issue slots and 20 warps on an SM.  What a row costs in instructions decides
+// how much of a copy's rate is left, so
+//  - a block takes eight tokens and a share of the heads: angles are worked out once
+//    for all heads (by 64-bit turns and one sincospif each), and so are norms;
+//  - an octet takes rows of one token, its cosines, sines and weights in registers
+//    (a warp to a pair of rows 62.7 us; half-warps, angles from shared memory 46;
+//    quads, eight rows to a warp, 44);
+//  - rows come in through a ring in shared memory, two batches of four rows to an
+//    octet, because loads into registers leave too few registers for the warps (a row
+//    ahead in registers 52; a ring of eight rows with a wait for each 41.4; this 38.6,
+//    and 38.0 with the rates and positions asked for before the slots are looked at);
+//  - queries and then keys and values go through one stream of batches (a loop for
+//    keys and one for values 46; two blocks on an SM with no spill 40.8, three 38.0).
+// 777 tokens (64 + 2 * 8 heads, F16 K) take 8 us, 64 tokens 3.7: a launch, slots, rows
+// and angles each waiting for memory once.
 template <int VT, int KT, int ROT, bool PAGED>
 __global__ void __launch_bounds__(kQkvWarps * 32, 3) qkv_kernel(const __grid_constant__ QkvParams p)
 {
@@ -476,7 +497,7 @@ cudaError_t launch_qkv(const QkvParams &in, int v_type, int k_type, int n_sms, c
     const int most = (p.n_q_heads > p.n_kv_heads ? p.n_q_heads : p.n_kv_heads) / 2;
     // Shares of the heads until there are two blocks for every SM: what a block does before its first row costs about
     // ten rows of a warp (777 tokens, 64 + 8 heads: 9.4 us at one block for every SM, 8.6 at two, 11.7 at four; 64
-    // tokens, 32 + 8 heads: one share for every two heads, 4.1).
+    // tokens, 32 + 8 heads: 3.7, a share for every two heads).
     const long long want = 2ll * n_sms;
     long long chunks = (want + tiles - 1) / tiles;
     chunks = chunks > most ? most : chunks;
