@@ -262,7 +262,8 @@ struct PageTable {
     static __device__ __forceinline__ unsigned slot(int p) { return (unsigned)p * 2654435769u >> 21; }
     __device__ __forceinline__ void least(int p, int b) const
     {
-        for (unsigned h = slot(p);; h = (h + 1) % kSlots) {
+        unsigned h = slot(p);
+        for (int k = 0; k < kSlots; ++k, h = (h + 1) % kSlots) {
             const int had = atomicCAS(page + h, -1, p);
             if (had == -1 || had == p) {
                 atomicMin(place + h, b);
@@ -273,7 +274,7 @@ struct PageTable {
     __device__ __forceinline__ int of(int p) const   // p is in it
     {
         unsigned h = slot(p);
-        while (page[h] != p) h = (h + 1) % kSlots;
+        for (int k = 0; k < kSlots && page[h] != p; ++k) h = (h + 1) % kSlots;
         return place[h];
     }
 };
@@ -313,6 +314,8 @@ __global__ void __cluster_dims__(kForkCtas, 1, 1) __launch_bounds__(kForkThreads
         one.write(p, mark);
         two.write(p, mark);
         for (int item = (at >> 5) + 2 * warps; item < items; item += warps) run(item).write(p, mark);
+    } else if (tid < n) {   // rows without entries
+        q.tail[tid] = -1;
     }
     cluster_sync();   // marks are set; and every CTA has read lens and n_free, which results may replace
     // the CTA's share of the pool, a word of 32 pages a thread

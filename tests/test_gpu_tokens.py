@@ -355,6 +355,17 @@ def test_fork_of_one_place_into_all(left):
     _same(_run_fork(page, n_pages, lens, table, free, left, most, np.full(B, 5)), ref)
 
 
+@pytest.mark.parametrize("B,n_pages", [(1, 5), (3, 0), (200, 40), (1024, 7), (1500, 40)])
+def test_fork_of_rows_without_entries(B, n_pages):
+    """A table of no columns: every length is held to 0, nothing is copied or given back."""
+    lens, free = np.arange(B) % 50, np.arange(n_pages, dtype=np.int32)
+    table = np.zeros((B, 0), np.int32)
+    for parent, keep in ((None, None), (np.arange(B)[::-1].copy(), np.full(B, 3))):
+        ref = fork_ref(16, n_pages, lens, table, free, n_pages // 2, table, 0, parent, keep)
+        assert not ref["lens"].any() and not ref["status"].any()
+        _same(_run_fork(16, n_pages, lens, table, free, n_pages // 2, 0, parent, keep), ref)
+
+
 def test_fork_over_a_large_pool():
     """A million pages, most of them in no list."""
     r = np.random.default_rng(8)
