@@ -7,6 +7,7 @@ namespace kvq {
 
 constexpr int kQkvWarps = 8;
 constexpr int kQkvTokens = 8;   // tokens of a block
+constexpr int kQkvBlocks = 3;   // on an SM
 
 constexpr int kBatch = 4;       // rows that an octet takes at a time
 static_assert(kQkvWarps * 32 == 2 * kD, "a thread to each weight of the two norms");
@@ -311,7 +312,7 @@ __device__ __forceinline__ void stream_get(Stream &w)
 // its codes are those of an append of the fp16 row.
 //
 // Bound by memory, with the arithmetic close behind: 8192 tokens of 40 + 2 * 8 heads
-// (q4_0 V, norms, halves) 38.0 us for 215 MB, 5.7 TB/s, 0.83 of a copy's rate, at half
+// (q4_0 V, norms, halves) 36.1 us for 215 MB, 6.0 TB/s, 0.88 of a copy's rate, at half
 // of the issue slots and 20 warps on an SM.  What a row costs in instructions decides
 // how much of a copy's rate is left, so
 //  - a block takes eight tokens and a share of the heads: angles are worked out once
@@ -322,20 +323,23 @@ __device__ __forceinline__ void stream_get(Stream &w)
 //  - rows come in through a ring in shared memory, two batches of four rows to an
 //    octet, because loads into registers leave too few registers for the warps (a row
 //    ahead in registers 52; a ring of eight rows with a wait for each 41.4; this 38.6,
-//    and 38.0 with the rates and positions asked for before the slots are looked at);
+//    38.0 with the rates and positions asked for before the slots are looked at, 36.1
+//    with the last wave cut up);
 //  - queries and then keys and values go through one stream of batches (a loop for
 //    keys and one for values 46; two blocks on an SM with no spill 40.8, three 38.0).
 // 777 tokens (64 + 2 * 8 heads, F16 K) take 8 us, 64 tokens 3.7: a launch, slots, rows
 // and angles each waiting for memory once.
 template <int VT, int KT, int ROT, bool PAGED>
-__global__ void __launch_bounds__(kQkvWarps * 32, 3) qkv_kernel(const __grid_constant__ QkvParams p)
+__global__ void __launch_bounds__(kQkvWarps * 32, kQkvBlocks) qkv_kernel(const __grid_constant__ QkvParams p)
 {
     extern __shared__ __align__(1024) uint8_t qkv_smem[];
     QkvShared &sh = *reinterpret_cast<QkvShared *>(qkv_smem);
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 7, oct = lane >> 3, n_rot = p.rope.n_rot;
-    const int tile = blockIdx.x / p.chunks, share = blockIdx.x - tile * p.chunks, t0 = tile * kQkvTokens;
+    // blocks of all heads, then those that take a share
+    const int part = (int)blockIdx.x - p.full, cut = part < 0 ? 0 : part / p.chunks, share = part < 0 ? 0 : part - cut * p.chunks;
+    const int t0 = (part < 0 ? (int)blockIdx.x : p.full + cut) * kQkvTokens, q_heads = part < 0 ? p.n_q_heads : p.q_heads, kv_heads = part < 0 ? p.n_kv_heads : p.kv_heads;
     // slots of the token before the block's, of its own, and of the one behind
     const int at = t0 - 1 + lane;
     const int slot = lane < kQkvTokens + 2 && at >= 0 && at < p.n_tokens ? (p.slots ? p.slots[at] : 0) : -1;
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__(kQkvWarps * 32, 3) qkv_kernel(const __grid_con
     }
     const float *norm = threadIdx.x < kD ? p.q_norm : p.k_norm;
     const float weight = norm ? norm[threadIdx.x % kD] : 0.f;
-    const int q1 = min(p.n_q_heads, (share + 1) * p.q_heads), k1 = min(p.n_kv_heads, (share + 1) * p.kv_heads);
+    const int q1 = min(p.n_q_heads, (share + 1) * q_heads), k1 = min(p.n_kv_heads, (share + 1) * kv_heads);
     auto piece = [](int h0, int h1, int parts, int part, int &first) {   // heads of one of the warps that share tokens
         const int each = (max(0, h1 - h0) + parts - 1) / parts;
         first = h0 + part * each;
@@ -362,12 +366,12 @@ __global__ void __launch_bounds__(kQkvWarps * 32, 3) qkv_kernel(const __grid_con
     Stream w;
     const int qi = 4 * (warp & 1) + oct;
     int q_first, k_first, ki = qi, sl = 0;
-    const int nq = piece(share * p.q_heads, q1, kQkvWarps / 2, warp >> 1, q_first);
+    const int nq = piece(share * q_heads, q1, kQkvWarps / 2, warp >> 1, q_first);
     w.q_mine = __shfl_sync(0xffffffffu, slot, 1 + qi) >= 0;
     int nk;
     bool pair = false, beyond = false;
     if (!PAGED) {
-        nk = piece(share * p.kv_heads, k1, kQkvWarps / 2, warp >> 1, k_first);
+        nk = piece(share * kv_heads, k1, kQkvWarps / 2, warp >> 1, k_first);
         w.k_mine = w.q_mine;
     } else {
         // pages: two octets to a token that begins a pair and its partner; without pairs an octet to each token
@@ -375,14 +379,14 @@ __global__ void __launch_bounds__(kQkvWarps * 32, 3) qkv_kernel(const __grid_con
         slot_list(q, sh.list[warp]);
         const bool pairs = (q.pair & q.lead) != 0;
         beyond = q.pair & q.lead & 1u << kQkvTokens;   // with the first token of the block behind
-        const int per = pairs ? 2 : 4, groups = max(1, (q.leads + per - 1) / per), parts = kQkvWarps / groups, part = warp / groups;   // (at most four groups)
-        const int n = (warp - part * groups) * per + (pairs ? oct >> 1 : oct), e = pairs ? oct & 1 : 0;
+        const int per = pairs ? 2 : 4, groups = max(1, (q.leads + per - 1) / per), parts = kQkvWarps / groups, which = warp / groups;   // (at most four groups)
+        const int n = (warp - which * groups) * per + (pairs ? oct >> 1 : oct), e = pairs ? oct & 1 : 0;
         const int lead = n < q.leads ? sh.list[warp][n] : 1;
         pair = n < q.leads && (q.pair >> lead & 1);
         w.k_mine = n < q.leads && (e == 0 || pair);
         ki = lead - 1 + (pair ? e : 0);
         sl = __shfl_sync(0xffffffffu, slot, 1 + ki);
-        nk = q.leads > 0 ? piece(share * p.kv_heads, k1, parts, part, k_first) : 0;
+        nk = q.leads > 0 ? piece(share * kv_heads, k1, parts, which, k_first) : 0;
     }
     w.q = p.q + (t0 + qi) * p.q_stride + q_first * kD + 8 * c;
     w.k = p.k + (t0 + ki) * p.k_stride + k_first * kD + 8 * c;
@@ -495,16 +499,22 @@ cudaError_t launch_qkv(const QkvParams &in, int v_type, int k_type, int n_sms, c
     QkvParams p = in;
     const int tiles = (int)(((long long)p.n_tokens + kQkvTokens - 1) / kQkvTokens);
     const int most = (p.n_q_heads > p.n_kv_heads ? p.n_q_heads : p.n_kv_heads) / 2;
-    // Shares of the heads until there are two blocks for every SM: what a block does before its first row costs about
-    // ten rows of a warp (777 tokens, 64 + 8 heads: 9.4 us at one block for every SM, 8.6 at two, 11.7 at four; 64
-    // tokens, 32 + 8 heads: 3.7, a share for every two heads).
-    const long long want = 2ll * n_sms;
-    long long chunks = (want + tiles - 1) / tiles;
+    // Few tokens: shares of the heads until there are two blocks for every SM, or three where that is no more than the
+    // GPU holds; what a block does before its first row costs about ten rows of a warp (777 tokens, 64 + 8 heads: 9.4 us
+    // at one block for every SM, 8.6 at two, 11.7 at four; 500 tokens, 40 + 8: 6.4 at two, 5.9 at three; 64 tokens, 32 +
+    // 8: 3.7, a share for every two heads).  Many: whole tokens in full waves, and the last wave's shared by all SMs
+    // (40 + 8 heads, 8192 tokens, two and a quarter waves: 36.1 us, 38.0 uncut, 36.8 at two blocks for every SM; 4096
+    // tokens: 21.0, 23.6, 21.3; 16384: 67.5, all alike).
+    const int room = kQkvBlocks * n_sms, rest = tiles % room;
+    long long chunks = 1;
+    if (rest && tiles < room) chunks = room / rest > (2 * n_sms + rest - 1) / rest ? room / rest : (2 * n_sms + rest - 1) / rest;
+    else if (rest) chunks = (n_sms + rest - 1) / rest;
     chunks = chunks > most ? most : chunks;
     p.chunks = chunks < 1 ? 1 : (int)chunks;
+    p.full = tiles - rest;
     p.q_heads = (p.n_q_heads + p.chunks - 1) / p.chunks;
     p.kv_heads = (p.n_kv_heads + p.chunks - 1) / p.chunks;
-    return launch_pdl(qkv_fn(p, v_type, k_type), p, tiles * p.chunks, kQkvWarps * 32, (int)sizeof(QkvShared), s, pdl);
+    return launch_pdl(qkv_fn(p, v_type, k_type), p, p.full + rest * p.chunks, kQkvWarps * 32, (int)sizeof(QkvShared), s, pdl);
 }
 
 }  // namespace kvq

@@ -43,7 +43,8 @@ struct QkvParams {
     float eps;
     int n_tokens, n_q_heads, n_kv_heads;
     int paged;
-    int chunks, q_heads, kv_heads;   // shares of the heads, and the heads of a share
+    int full;                        // blocks that take all heads of their tokens; the others
+    int chunks, q_heads, kv_heads;   // a share of so many, of so many heads
 };
 
 struct ForkParams {

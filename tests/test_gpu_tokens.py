@@ -248,6 +248,28 @@ def test_a_large_step():
     assert (np.abs(k - y) <= fp16_bound(y, size) + 0.5 * step * (1 + 2.0 ** -20)).all()
 
 
+@pytest.mark.parametrize("T,Hq,H", [(3650, 9, 3), (3900, 12, 2), (7301, 3, 5), (11000, 4, 1)])
+def test_a_large_step_is_its_parts(T, Hq, H):
+    """The bits do not depend on how the launch deals out tokens and heads: one call, and calls of some tokens each."""
+    r = np.random.default_rng(T)
+    page, part = 32, 611
+    n_pages = -(-T // page) + 3
+    t = to_dev(_tokens(r, T, Hq, H))
+    order = np.concatenate([np.arange(1, T // 2), r.permutation(np.arange(T // 2, n_pages * page))])[:T]   # neighbours, and none
+    slots = np.where(r.random(T) < 0.1, np.where(r.random(T) < 0.5, -1, n_pages * page + 5), order)
+    pos, w = i32(r.integers(0, 131072, T)), to_dev(r.standard_normal(128).astype(np.float32))
+    rope, slots = kvq.Rope(128, device=dev()), i32(slots)
+    got = []
+    for step in (T, part):
+        q, pool = torch.full((T, Hq, 128), 3.0, dtype=torch.float16, device=dev()), kvq.PagePool(n_pages, page, H, Q8)
+        pool.data.fill_(0)
+        for a in range(0, T, step):
+            b = slice(a, a + step)
+            kvq.kvq_qkv(t[b, :Hq], t[b, Hq:Hq + H], t[b, Hq + H:], pos[b], rope, q[b], pool=pool, slots=slots[b], q_norm=w, k_norm=w)
+        got.append((q, pool.data))
+    assert torch.equal(got[0][0].view(torch.int16), got[1][0].view(torch.int16)) and torch.equal(got[0][1], got[1][1])
+
+
 # ------------------------------------------------------------------ fork --
 def _fork_state(r, B, page, most, extra, hi, group=1, hidden=0.0):
     """Old tables of groups whose members share whole pages of a prefix."""
