@@ -739,12 +739,13 @@ cudaError_t launch_gather_many(const PagedRowsParams &rows, int v_type, int k_ty
 // Where tokens move, each slot may be another's source, so rows go through the
 // workspace (one launch out, one in) unless the caller says that none is.  8092 tokens
 // of 8 heads (q8_0 V, keys turned) through the workspace 16.4 us, two launches whose 70
-// MB would take 10.4.  131072 keys turned where they lie 71 us, 4.0 TB/s, 0.59 of a
-// copy's rate: instructions, 63 % of the issue slots (390 for eight rows: codes to
-// numbers, the turn, largest values, new codes).  A head's row is fetched while
-// nothing of the one before waits any more: fetched a head ahead it took 77-99 us, the
-// registers costing more warps than the wait does; held to 72 registers (seven blocks
-// on an SM) 71, to six blocks 72, five 74.5, eight 80.
+// MB would take 10.4.  131072 keys turned where they lie 61 us, 4.7 TB/s, 0.69 of a
+// copy's rate: instructions, some 380 for eight rows (codes to numbers, the turn,
+// largest values, new codes), three quarters of what the SMs can issue.  There the next
+// two heads' int8 keys are on their way in shared memory: loaded into registers when
+// they are needed 71 us, a head ahead 77-99, since that costs more warps than the wait
+// does; three heads ahead 62.  72 registers (seven blocks on an SM) 61, six blocks the
+// same, five 63, eight 68; through the workspace six take 18.6.
 // ---------------------------------------------------------------------------
 constexpr int kMoveWarps = 4;
 constexpr int kMoveTokens = 8;   // of a warp
@@ -897,6 +898,8 @@ __global__ void __launch_bounds__(kMoveWarps * 32, 7) move_kernel(const MovePara
     constexpr int kTile = PageTile<VT, KT>::BYTES, kRow = Staged<VT, KT>::BYTES;
     __shared__ __align__(16) MoveShared shared[kMoveWarps];
     __shared__ __align__(16) float scratch[ROT == kRotPart ? kMoveWarps : 1][8][ROT == kRotPart ? kD + 4 : 1];
+    constexpr bool kRinged = WAY == kMoveDirect && KT == KVQ_K_I8 && ROT != kRotNone;
+    __shared__ uint4 ring[kRinged ? kMoveWarps : 1][2][3][kRinged ? 32 : 1];   // K codes and scales of two heads, for keys that turn where they lie
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, quad = lane >> 2;
@@ -948,7 +951,23 @@ __global__ void __launch_bounds__(kMoveWarps * 32, 7) move_kernel(const MovePara
                 if (values) quad_get_value<VT, KT>(r, src, fu, c);
             }
         };
-        get();   // the first head's row, on its way while the angles are worked out
+        const bool ringed = kRinged && !values;
+        auto fetch = [&](int h, int at) {
+            if (mine && h < h1) {
+                const uint8_t *tile = src + (size_t)(h - h0) * head_bytes;
+                const uint32_t to = smem_u32(&ring[warp][at][0][lane]);
+                copy16(to, tile + quad_k_off(fu, c, 0));
+                copy16(to + 512, tile + quad_k_off(fu, c, 1));
+                copy16(to + 1024, tile + PageTile<VT, KT>::KS_OFF + 16 * (fu / 2));
+            }
+            copy_commit();
+        };
+        if (ringed) {   // the first heads' rows, on their way while the angles are worked out
+            fetch(h0, 0);
+            fetch(h0 + 1, 1);
+        } else {
+            get();
+        }
         int row = 0;
         if (ROT != kRotNone && any) {   // angles of the quads' turns, one row for all where they are the same
             const int one = __shfl_sync(0xffffffffu, turn, __ffs(__ballot_sync(0xffffffffu, turns)) - 1);
@@ -967,6 +986,26 @@ __global__ void __launch_bounds__(kMoveWarps * 32, 7) move_kernel(const MovePara
         }
         const float *cosines = sh.cosines[row], *sines = sh.sines[row];
         float *const mem = scratch[ROT == kRotPart ? warp : 0][ROT == kRotPart ? quad : 0];
+        if (ringed) {
+            for (int h = h0, at = 0; h < h1; ++h, at ^= 1) {
+                copy_wait<1>();
+                if (mine) {
+                    const uint4 a = ring[warp][at][0][lane], b = ring[warp][at][1][lane], s = ring[warp][at][2][lane];
+                    const uint32_t sel = fu & 1 ? 0x7632 : 0x5410;
+                    r.k[0] = a.x, r.k[1] = a.y, r.k[2] = a.z, r.k[3] = a.w;
+                    r.k[4] = b.x, r.k[5] = b.y, r.k[6] = b.z, r.k[7] = b.w;
+                    r.ks[0] = __byte_perm(s.x, s.y, sel);
+                    r.ks[1] = __byte_perm(s.z, s.w, sel);
+                }
+                turn_key<false, VT, KT, ROT>(r, true, cosines, sines, c, p.rope.n_rot, mem);
+                if (turns) quad_put_key<VT, KT>(r, dst, tu, c);
+                dst += head_bytes;
+                __syncwarp();   // the row has been read: its place may be filled again
+                fetch(h + 2, at);
+            }
+            copy_wait<0>();
+            continue;
+        }
         if (WAY == kMoveDirect && !values) {   // keys turn where they lie: only those that do are written
             for (int h = h0;;) {
                 turn_key<false, VT, KT, ROT>(r, true, cosines, sines, c, p.rope.n_rot, mem);

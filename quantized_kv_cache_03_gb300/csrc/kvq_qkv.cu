@@ -20,16 +20,6 @@ struct QkvShared {
     uint8_t list[kQkvWarps][kQkvTokens];
 };
 
-// 16 bytes from global to shared memory; the copies of a thread form groups, of
-// which all but the newest N have arrived.
-__device__ __forceinline__ void copy16(uint32_t to, const void *from)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 // ---- eight lanes (an octet) to a row ----
 // A row's 256 bytes are read and written as whole lines, and what multiplies a
 // token's rows fits into a lane's registers.  Lane c holds values 8 c + i and

@@ -24,6 +24,16 @@ namespace kvq {
 __device__ __forceinline__ __half2 h2_of(uint32_t w) { return *reinterpret_cast<const __half2 *>(&w); }
 __device__ __forceinline__ uint32_t bits_of(const __half2 &h) { return *reinterpret_cast<const uint32_t *>(&h); }
 
+// 16 bytes from global to shared memory; the copies of a thread form groups, of
+// which all but the newest N have arrived.
+__device__ __forceinline__ void copy16(uint32_t to, const void *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // What rotates, and so how a lane's values are paired.
 constexpr int kRotNone = 0, kRotPairs = 1, kRotHalf = 2, kRotPart = 3;   // half: n_rot = 128; part: halves of less
 
@@ -148,7 +158,7 @@ __device__ __forceinline__ uint2 codes8(const uint4 &x, float s)
 // Largest magnitudes of eight fp16 values: of the low halves, of the high ones.
 __device__ __forceinline__ uint32_t top8(const uint4 &w)
 {
-    return bits_of(__hmax2(__hmax2(h2_of(w.x & 0x7fff7fffu), h2_of(w.y & 0x7fff7fffu)), __hmax2(h2_of(w.z & 0x7fff7fffu), h2_of(w.w & 0x7fff7fffu))));
+    return bits_of(__hmax2(__hmax2(__habs2(h2_of(w.x)), __habs2(h2_of(w.y))), __hmax2(__habs2(h2_of(w.z)), __habs2(h2_of(w.w)))));
 }
 // The scales of two blocks from their largest magnitudes.
 template <bool Q4>
