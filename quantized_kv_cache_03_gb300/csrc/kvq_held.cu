@@ -738,7 +738,7 @@ cudaError_t launch_gather_many(const PagedRowsParams &rows, int v_type, int k_ty
 //
 // Where tokens move, each slot may be another's source, so rows go through the
 // workspace (one launch out, one in) unless the caller says that none is.  8092 tokens
-// of 8 heads (q8_0 V, keys turned) through the workspace 16.4 us, two launches whose 70
+// of 8 heads (q8_0 V, keys turned) through the workspace 15.9 us, two launches whose 70
 // MB would take 10.4.  131072 keys turned where they lie 61 us, 4.7 TB/s, 0.69 of a
 // copy's rate: instructions, some 380 for eight rows (codes to numbers, the turn,
 // largest values, new codes), three quarters of what the SMs can issue.  There the next
@@ -937,12 +937,15 @@ __global__ void __launch_bounds__(kMoveWarps * 32, 7) move_kernel(const MovePara
         uint8_t *dst = tile_of(p.pool, to >> p.pool.pshift, h0, (to & P1) >> 4, kTile);
         uint8_t *staged = WAY == kMoveDirect ? nullptr : p.rows + ((size_t)(t0 + i - 1) * p.pool.n_kv_heads + h0) * kRow;
         QuadRow<VT, KT> r;
+        auto clear = [](QuadRow<VT, KT> &r) {
 #pragma unroll
-        for (int k = 0; k < QuadRow<VT, KT>::KW; ++k) r.k[k] = 0;
+            for (int k = 0; k < QuadRow<VT, KT>::KW; ++k) r.k[k] = 0;
 #pragma unroll
-        for (int k = 0; k < QuadRow<VT, KT>::VW; ++k) r.v[k] = 0;
-        r.ks[0] = r.ks[1] = r.vs = 0;
-        auto get = [&]() {
+            for (int k = 0; k < QuadRow<VT, KT>::VW; ++k) r.v[k] = 0;
+            r.ks[0] = r.ks[1] = r.vs = 0;
+        };
+        clear(r);
+        auto get = [&](QuadRow<VT, KT> &r) {
             if (!mine) return;
             if (WAY == kMoveIn) {
                 stage_get<VT, KT>(staged, r, c);
@@ -966,7 +969,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32, 7) move_kernel(const MovePara
             fetch(h0, 0);
             fetch(h0 + 1, 1);
         } else {
-            get();
+            get(r);
         }
         int row = 0;
         if (ROT != kRotNone && any) {   // angles of the quads' turns, one row for all where they are the same
@@ -1019,17 +1022,22 @@ __global__ void __launch_bounds__(kMoveWarps * 32, 7) move_kernel(const MovePara
         }
         for (int h = h0;;) {
             if (ROT != kRotNone && any) turn_key<true, VT, KT, ROT>(r, turns, cosines, sines, c, p.rope.n_rot, mem);
+            src += head_bytes;
+            QuadRow<VT, KT> next;   // (without a turn there are registers for it: 16.3 us through the workspace without)
+            clear(next);
+            uint8_t *const to_staged = staged;
+            staged += kRow;
+            if (ROT == kRotNone && h + 1 < h1) get(next);
             if (WAY == kMoveOut) {
-                if (mine) stage_put<VT, KT>(staged, r, c);
+                if (mine) stage_put<VT, KT>(to_staged, r, c);
             } else {
                 if (mine) quad_put_key<VT, KT>(r, dst, tu, c);
                 quad_put_value<VT, KT>(r, dst, tu, c, pair, mine);
             }
             if (++h >= h1) break;
-            src += head_bytes;
             dst += head_bytes;
-            staged += kRow;
-            get();
+            if (ROT == kRotNone) r = next;
+            else get(r);
         }
     }
 }
