@@ -233,7 +233,8 @@ kvq_status kvq_page_copy(const kvq_pages *pools, int32_t n_pools, const int32_t 
  *             token's `to` and another's `from`; the tokens pass through the
  *             workspace.  Zero: no slot is both, except a token's own (from = to).
  *  workspace  device, 256-byte aligned, kvq_paged_move_workspace_size() bytes; as
- *             kvq_paged_attn's.  Not read where staged is 0.
+ *             kvq_paged_attn's.  Not read where staged is 0.  (Up to 256 tokens stay
+ *             on the chip; it is asked for all the same.)
  * Without a turn (turn NULL or 0) a token's bytes go over as they are, and V's always
  * do.  A turned int8 key is dequantized (code * scale), turned in fp32, rounded to
  * fp16 and quantized again by kvq_append's rule, 32-blocks past n_rot excepted; a turned

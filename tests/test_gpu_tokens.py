@@ -599,6 +599,30 @@ def test_turned_keys(way, layout, n_rot, k_type, v_type):
     assert (np.abs(k1[to] - y) <= allowed)[moved].all()
 
 
+@pytest.mark.parametrize("k_type,v_type", [(I8, Q4), (I8, Q8), (F16, Q4), (F16, Q8)])
+@pytest.mark.parametrize("layout,n_rot", [(HALF, 128), (PAIRS, 64), (HALF, 40), (HALF, 0)])
+@pytest.mark.parametrize("kind", ["down", "mixed", "reversed"])
+def test_staged_moves_of_all_sizes(kind, layout, n_rot, k_type, v_type):
+    """Slots that are one another's source, whatever holds the rows meanwhile: the bits of two moves by way of other pages."""
+    r = np.random.default_rng(n_rot)
+    page, H, half = 64, 3, 13 * 64
+    pool, _ = _filled(r, 2 * half // page, page, H, k_type, v_type)
+    cut = pool.data.numel() // 2
+    start, rope = pool.data.clone(), kvq.Rope(n_rot, layout=layout, device=dev())
+    for n in (2, 31, 32, 33, 64, 65, 128, 129, 255, 256, 257, 700):
+        frm, to = (x.copy() for x in _moves(r, kind, half, n))
+        frm[::9], to[4::11] = -1, 2 ** 30                     # tokens without a slot
+        turn = i32(r.integers(-3, 3, n) * 1000)
+        there = np.where((frm >= 0) & (to < 2 ** 30), half + np.arange(n), -1)
+        pool.data.copy_(start)
+        kvq.kvq_paged_move(pool, i32(frm), i32(there), rope=rope, turn=turn, staged=False)
+        kvq.kvq_paged_move(pool, i32(there), i32(to), staged=False)
+        want = pool.data[:cut].clone()
+        pool.data.copy_(start)
+        kvq.kvq_paged_move(pool, i32(frm), i32(to), rope=rope, turn=turn, staged=True)
+        assert torch.equal(pool.data[:cut], want) and torch.equal(pool.data[cut:], start[cut:]), n
+
+
 def test_a_turn_and_back():
     """Turning keys away and back costs two quantizations, no more."""
     r = np.random.default_rng(9)
