@@ -256,7 +256,7 @@ struct Stream {
     const uint16_t *q, *k, *v;     // the lane's part of the next rows of its octet's tokens
     int nq, nk;                    // rows of each still to come
     uint32_t to;                   // the lane's part of the next batch, in shared memory
-    bool q_mine, k_mine;
+    bool q_there, k_mine;          // q rows are read before their slots are known
 };
 constexpr uint32_t kBatchBytes = kBatch * 4 * kD * 2;
 __device__ __forceinline__ void stream_row(uint32_t to, const uint16_t *from, bool there)
@@ -271,7 +271,7 @@ __device__ __forceinline__ void stream_get(Stream &w)
 {
     if (w.nq > 0) {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) stream_row(w.to + i * 8 * kD, w.q + i * kD, w.q_mine && i < w.nq);
+        for (int i = 0; i < kBatch; ++i) stream_row(w.to + i * 8 * kD, w.q + i * kD, w.q_there && i < w.nq);
         w.q += kBatch * kD;
         w.nq -= kBatch;
     } else if (w.nk > 0) {
@@ -302,7 +302,7 @@ __device__ __forceinline__ void stream_get(Stream &w)
 // its codes are those of an append of the fp16 row.
 //
 // Bound by memory, with the arithmetic close behind: 8192 tokens of 40 + 2 * 8 heads
-// (q4_0 V, norms, halves) 36.1 us for 215 MB, 6.0 TB/s, 0.88 of a copy's rate, at half
+// (q4_0 V, norms, halves) 34.7 us for 215 MB, 6.2 TB/s, 0.91 of a copy's rate, at half
 // of the issue slots and 20 warps on an SM.  What a row costs in instructions decides
 // how much of a copy's rate is left, so
 //  - a block takes eight tokens and a share of the heads: angles are worked out once
@@ -313,11 +313,11 @@ __device__ __forceinline__ void stream_get(Stream &w)
 //  - rows come in through a ring in shared memory, two batches of four rows to an
 //    octet, because loads into registers leave too few registers for the warps (a row
 //    ahead in registers 52; a ring of eight rows with a wait for each 41.4; this 38.6,
-//    38.0 with the rates and positions asked for before the slots are looked at, 36.1
-//    with the last wave cut up);
+//    38.0 with the rates and positions asked for before the slots are looked at, 36.0
+//    with the last wave cut up, 34.7 with the first queries asked for then too);
 //  - queries and then keys and values go through one stream of batches (a loop for
 //    keys and one for values 46; two blocks on an SM with no spill 40.8, three 38.0).
-// 777 tokens (64 + 2 * 8 heads, F16 K) take 8 us, 64 tokens 3.7: a launch, slots, rows
+// 777 tokens (64 + 2 * 8 heads, F16 K) take 8 us, 64 tokens 3.5: a launch, slots, rows
 // and angles each waiting for memory once.
 template <int VT, int KT, int ROT, bool PAGED>
 __global__ void __launch_bounds__(kQkvWarps * 32, kQkvBlocks) qkv_kernel(const __grid_constant__ QkvParams p)
@@ -357,12 +357,18 @@ __global__ void __launch_bounds__(kQkvWarps * 32, kQkvBlocks) qkv_kernel(const _
     const int qi = 4 * (warp & 1) + oct;
     int q_first, k_first, ki = qi, sl = 0;
     const int nq = piece(share * q_heads, q1, kQkvWarps / 2, warp >> 1, q_first);
-    w.q_mine = __shfl_sync(0xffffffffu, slot, 1 + qi) >= 0;
+    w.q_there = t0 + qi < p.n_tokens;
+    w.q = p.q + (t0 + qi) * p.q_stride + q_first * kD + 8 * c;
+    w.nq = nq;
+    w.nk = 0;
+    w.to = smem_u32(sh.ring[warp][0][0][oct]) + 16 * c;
+    stream_get<PAGED>(w);
+    const bool q_mine = __shfl_sync(0xffffffffu, slot, 1 + qi) >= 0;
     int nk;
     bool pair = false, beyond = false;
     if (!PAGED) {
         nk = piece(share * kv_heads, k1, kQkvWarps / 2, warp >> 1, k_first);
-        w.k_mine = w.q_mine;
+        w.k_mine = q_mine;
     } else {
         // pages: two octets to a token that begins a pair and its partner; without pairs an octet to each token
         const SlotPairs q = slot_pairs(slot, slot >= 0 && slot < p.pool.n_slots, kQkvTokens);
@@ -378,13 +384,13 @@ __global__ void __launch_bounds__(kQkvWarps * 32, kQkvBlocks) qkv_kernel(const _
         sl = __shfl_sync(0xffffffffu, slot, 1 + ki);
         nk = q.leads > 0 ? piece(share * kv_heads, k1, parts, which, k_first) : 0;
     }
-    w.q = p.q + (t0 + qi) * p.q_stride + q_first * kD + 8 * c;
     w.k = p.k + (t0 + ki) * p.k_stride + k_first * kD + 8 * c;
     w.v = p.v + (t0 + ki) * p.v_stride + k_first * kD + 8 * c;
-    w.nq = nq;
     w.nk = nk;
-    w.to = smem_u32(sh.ring[warp][0][0][oct]) + 16 * c;
-    stream_get<PAGED>(w);
+    if (nq == 0) {   // (the first batch was empty: the next is the first)
+        w.to ^= kBatchBytes;
+        stream_get<PAGED>(w);
+    }
     stream_get<PAGED>(w);
     if (turns) {
         auto put = [&](int t, int position) {
@@ -420,7 +426,7 @@ __global__ void __launch_bounds__(kQkvWarps * 32, kQkvBlocks) qkv_kernel(const _
     };
     if (nq > 0) {
         k = oct_coef<ROT>(q_norm, sh.cosines[qi], sh.sines[qi], c, n_rot);
-        rows(nq, p.q_out + (t0 + qi) * p.q_out_stride + q_first * kD, w.q_mine, q_norm != nullptr);
+        rows(nq, p.q_out + (t0 + qi) * p.q_out_stride + q_first * kD, q_mine, q_norm != nullptr);
     }
     if (nk == 0) return;
     k = oct_coef<ROT>(k_norm, sh.cosines[ki], sh.sines[ki], c, n_rot);
@@ -490,11 +496,11 @@ cudaError_t launch_qkv(const QkvParams &in, int v_type, int k_type, int n_sms, c
     const int tiles = (int)(((long long)p.n_tokens + kQkvTokens - 1) / kQkvTokens);
     const int most = (p.n_q_heads > p.n_kv_heads ? p.n_q_heads : p.n_kv_heads) / 2;
     // Few tokens: shares of the heads until there are two blocks for every SM, or three where that is no more than the
-    // GPU holds; what a block does before its first row costs about ten rows of a warp (777 tokens, 64 + 8 heads: 9.4 us
-    // at one block for every SM, 8.6 at two, 11.7 at four; 500 tokens, 40 + 8: 6.4 at two, 5.9 at three; 64 tokens, 32 +
-    // 8: 3.7, a share for every two heads).  Many: whole tokens in full waves, and the last wave's shared by all SMs
-    // (40 + 8 heads, 8192 tokens, two and a quarter waves: 36.1 us, 38.0 uncut, 36.8 at two blocks for every SM; 4096
-    // tokens: 21.0, 23.6, 21.3; 16384: 67.5, all alike).
+    // GPU holds; what a block does before its first row costs about ten rows of a warp (40 + 8 heads, 777 tokens: 7.0 us
+    // at one block for every SM, 6.6 at two, 8.9 at four; 500 tokens 6.2 at two, 5.8 at three; 1024 tokens 9.2, 7.7,
+    // 10.1 at one, two, four).  Many: whole tokens in full waves, and the last wave's shared by all SMs (8192 tokens, two
+    // and a quarter waves: 34.7 us, 36.1 uncut, 35.4 at two blocks for every SM; 4096 tokens: 20.1, 21.4, 20.3; 16384:
+    // 65, all alike).
     const int room = kQkvBlocks * n_sms, rest = tiles % room;
     long long chunks = 1;
     if (rest && tiles < room) chunks = room / rest > (2 * n_sms + rest - 1) / rest ? room / rest : (2 * n_sms + rest - 1) / rest;
