@@ -370,12 +370,18 @@ __global__ void __launch_bounds__(kForkWide) fork_clear_kernel(const ForkParams 
 {
     pdl_wait();
     pdl_trigger();
-    if (blockIdx.x == 0) {
-        const ForkSeqs q(p.seqs, p.n_seqs);
+    if (blockIdx.x == 0) {   // lengths in shared memory, where their maxima cost no trips, then to the workspace
+        extern __shared__ int seqs[];
+        const ForkSeqs q(seqs, p.n_seqs), out(p.seqs, p.n_seqs);
         fork_lengths<kForkWide>(p, q);
         for (int b = threadIdx.x; b < p.n_seqs; b += kForkWide) {
             const int tail = fork_tail(p, q, b);
-            q.tail[b] = tail;
+            out.from[b] = q.from[b];
+            out.kept[b] = q.kept[b];
+            out.olds[b] = q.olds[b];
+            out.whole[b] = q.whole[b];
+            out.used[b] = q.used[b];
+            out.tail[b] = tail;
             if (is_page(p, tail)) p.owner[tail] = p.n_seqs;
         }
         if (threadIdx.x == 0) p.totals[0] = min(max(*p.n_free, 0), p.n_pages);
@@ -482,9 +488,11 @@ __global__ void __launch_bounds__(kForkWide) fork_deal_kernel(const ForkParams p
 }
 
 constexpr int fork_cluster_smem(int n_seqs, int n_pages) { return (ForkSeqs::kArrays * n_seqs + 3 * ((n_pages + 31) / 32) + 2 * PageTable::kSlots) * (int)sizeof(int); }
+constexpr int fork_clear_smem(int n_seqs) { return ForkSeqs::kArrays * n_seqs * (int)sizeof(int); }
 cudaError_t prepare_page_fork()
 {
-    return cudaFuncSetAttribute(fork_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, fork_cluster_smem(kForkMaxSeqs, kForkMaxPages));
+    const cudaError_t e = cudaFuncSetAttribute(fork_clear_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, fork_clear_smem(KVQ_MAX_PAGED_SEQS));
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(fork_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, fork_cluster_smem(kForkMaxSeqs, kForkMaxPages));
 }
 
 cudaError_t launch_page_fork(const ForkParams &in, int n_sms, cudaStream_t s, bool pdl)
@@ -496,7 +504,7 @@ cudaError_t launch_page_fork(const ForkParams &in, int n_sms, cudaStream_t s, bo
     if (p.n_seqs <= kForkMaxSeqs && p.n_pages <= kForkMaxPages && entries <= 128 * 1024)
         return launch_pdl(fork_cluster_kernel, p, kForkCtas, kForkThreads, fork_cluster_smem(p.n_seqs, p.n_pages), s, pdl);
     auto grid = [&](long long items, int most) { return (int)(items < 1 ? 1 : items > most ? most : items); };
-    cudaError_t e = launch_pdl(fork_clear_kernel, p, 1 + grid(((long long)p.n_pages * 3 / 16 + kForkWide - 1) / kForkWide, 2 * n_sms), kForkWide, 0, s, pdl);
+    cudaError_t e = launch_pdl(fork_clear_kernel, p, 1 + grid(((long long)p.n_pages * 3 / 16 + kForkWide - 1) / kForkWide, 2 * n_sms), kForkWide, fork_clear_smem(p.n_seqs), s, pdl);
     if (e == cudaSuccess) e = launch_pdl(fork_mark_kernel, p, grid((long long)p.n_seqs * ((p.max_blocks + 127) / 128) / (kForkMark / 32) + 1, 8 * n_sms), kForkMark, 0, s, pdl);
     if (e == cudaSuccess) e = launch_pdl(fork_count_kernel, p, p.blocks + 1, kForkWide, 0, s, pdl);
     if (e == cudaSuccess) e = launch_pdl(fork_deal_kernel, p, p.blocks, kForkWide, 0, s, pdl);
