@@ -748,7 +748,7 @@ cudaError_t launch_gather_many(const PagedRowsParams &rows, int v_type, int k_ty
 // through the workspace (one launch out, one in) unless the caller says that none is.  8092 tokens
 // of 8 heads (q8_0 V, keys turned) through the workspace 15.9 us, two launches whose 70
 // MB would take 10.4.  131072 keys turned where they lie 61 us, 4.7 TB/s, 0.69 of a
-// copy's rate: instructions, some 380 for eight rows (codes to numbers, the turn,
+// copy's rate: instructions, some 400 for eight rows (codes to numbers, the turn,
 // largest values, new codes), three quarters of what the SMs can issue.  There the next
 // two heads' int8 keys are on their way in shared memory: loaded into registers when
 // they are needed 71 us, a head ahead 77-99, since that costs more warps than the wait
