@@ -225,7 +225,8 @@ kvq_status kvq_page_copy(const kvq_pages *pools, int32_t n_pools, const int32_t 
  * tokens of a verified tree close ranks, a context drops a stretch and the rest
  * moves up, or (from = to) keys turn where they lie when whole pages were dropped.
  *  from, to   device int32 [n_tokens]; tokens with a slot that is negative or past
- *             the pool are skipped.  Two tokens must not share a `to`.
+ *             the pool are skipped.  Two tokens must not share a `to`.  A page that
+ *             several places list changes for all of them.
  *  rope, turn the rotation the keys were written with (host; its amplitude is not
  *             applied: the held keys carry it) and device int32 [n_tokens], the positions
  *             to turn each token by (negative: back); both or neither NULL.

@@ -623,6 +623,28 @@ def test_staged_moves_of_all_sizes(kind, layout, n_rot, k_type, v_type):
         assert torch.equal(pool.data[:cut], want) and torch.equal(pool.data[cut:], start[cut:]), n
 
 
+def test_moved_past_32_bits():
+    H, page = 8, 256
+    n_pages = (5 << 30) // (H * 16 * 4352)
+    pool, rope = kvq.PagePool(n_pages, page, H, Q8), kvq.Rope(128, device=dev())
+    r = np.random.default_rng(10)
+    n = 300
+    x = to_dev(_tokens(r, n, 1, H))
+    far, near = (n_pages - 3) * page + 7 + np.arange(n), 5 + np.arange(n)
+    one, turn = kvq.PagePool(6, page, H, Q8), i32(r.integers(-9, 9, n))
+    kvq.kvq_paged_append(one, x[:, 1:1 + H].contiguous(), x[:, 1 + H:].contiguous(), i32(near))
+    kvq.kvq_paged_move(one, i32(near), i32(near), rope=rope, turn=turn, staged=False)
+    want = [torch.zeros((n, H, 128), device=dev()) for _ in range(2)]
+    kvq.kvq_paged_gather(one, i32(near), *want)
+    for m, staged in ((n, True), (200, True), (n, False)):
+        kvq.kvq_paged_append(pool, x[:, 1:1 + H].contiguous(), x[:, 1 + H:].contiguous(), i32(far))
+        got = [torch.zeros((n, H, 128), device=dev()) for _ in range(2)]
+        kvq.kvq_paged_move(pool, i32(far[:m]), i32(near[:m]), rope=rope, turn=turn[:m], staged=staged)
+        kvq.kvq_paged_move(pool, i32(near[:m]), i32(far[:m]), staged=staged)
+        kvq.kvq_paged_gather(pool, i32(far), *got)
+        assert torch.equal(got[0][:m], want[0][:m]) and torch.equal(got[1][:m], want[1][:m]) and want[0].any()
+
+
 def test_a_turn_and_back():
     """Turning keys away and back costs two quantizations, no more."""
     r = np.random.default_rng(9)
