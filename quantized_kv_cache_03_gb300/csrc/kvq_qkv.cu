@@ -495,16 +495,23 @@ cudaError_t launch_qkv(const QkvParams &in, int v_type, int k_type, int n_sms, c
     QkvParams p = in;
     const int tiles = (int)(((long long)p.n_tokens + kQkvTokens - 1) / kQkvTokens);
     const int most = (p.n_q_heads > p.n_kv_heads ? p.n_q_heads : p.n_kv_heads) / 2;
-    // Few tokens: shares of the heads until there are two blocks for every SM, or three where that is no more than the
-    // GPU holds; what a block does before its first row costs about ten rows of a warp (40 + 8 heads, 777 tokens: 7.0 us
-    // at one block for every SM, 6.6 at two, 8.9 at four; 500 tokens 6.2 at two, 5.8 at three; 1024 tokens 9.2, 7.7,
-    // 10.1 at one, two, four).  Many: whole tokens in full waves, and the last wave's shared by all SMs (8192 tokens, two
-    // and a quarter waves: 34.7 us, 36.1 uncut, 35.4 at two blocks for every SM; 4096 tokens: 20.1, 21.4, 20.3; 16384:
-    // 65, all alike).
-    const int room = kQkvBlocks * n_sms, rest = tiles % room;
+    // Few tokens: shares of the heads.  With one block to an SM the next launch finds room beside this one's and starts
+    // early; more blocks cost about 2.5 us of that, and eight tokens' rows of a query head 0.13 us in a block (of a kv
+    // head about five times that).  So one block to an SM, unless that leaves each 38 rows more than three would (32 + 8
+    // heads, single tokens, blocks for every SM at one / three: 128 tokens 3.9 / 5.3 us, 256 4.9 / 6.1, 400 6.0 / 6.5;
+    // 700 tokens 10.6 / 9.0; 16 + 2 heads 5.3 / 6.0).  Where every SM has one anyway, two at least (32 + 8 heads, 1600
+    // tokens: 10.3 us at two, 11.5 at one), but for few heads (16 + 2 heads, 2400 tokens: 9.2 / 7.5).
+    // Many tokens: whole ones in full waves, and the last wave's shared by all SMs (40 + 8 heads, 8192 tokens, two and a
+    // quarter waves: 34.7 us, 36.1 uncut, 35.4 at two blocks for every SM; 4096 tokens: 20.1, 21.4, 20.3; 16384: 65, all
+    // alike).
+    const int room = kQkvBlocks * n_sms, rest = tiles % room, rows = p.n_q_heads + 5 * p.n_kv_heads;
     long long chunks = 1;
-    if (rest && tiles < room) chunks = room / rest > (2 * n_sms + rest - 1) / rest ? room / rest : (2 * n_sms + rest - 1) / rest;
-    else if (rest) chunks = (n_sms + rest - 1) / rest;
+    if (rest && tiles < room) {
+        const long long one = rest < n_sms ? n_sms / rest : 1, two = (2 * n_sms + rest - 1) / rest, full = room / rest > two ? room / rest : two;
+        chunks = rows * (full - one) < (rest < n_sms ? 38 : 19) * one * full ? one : full;
+    } else if (rest) {
+        chunks = (n_sms + rest - 1) / rest;
+    }
     chunks = chunks > most ? most : chunks;
     p.chunks = chunks < 1 ? 1 : (int)chunks;
     p.full = tiles - rest;
