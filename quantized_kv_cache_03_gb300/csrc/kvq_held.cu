@@ -5,10 +5,12 @@
 namespace kvq {
 
 // ---------------------------------------------------------------------------
-// Positions: a row's sequence by a search over q_start in shared memory, four
-// rows a thread, so that a search serves its neighbours (one row of a sequence
-// stands at its length less the rows from it to the sequence's end).  Latency alone:
-// 64 rows of 64 sequences 2.4 us, 777 rows of 9 1.8 us: q_start, then the length.
+// Positions: a row's sequence by a search over q_start in shared memory; it stands
+// at the sequence's length less the rows from it to the sequence's end.  Latency
+// alone: one round of loads and a search, a row to each thread: 64 rows of 64
+// sequences 1.0 us, 8192 of 20 1.4 us, 40000 of 1024 1.8 us (four rows to a thread,
+// which share a search where they can: 2.4, 1.7, 3.2; lengths from global memory after
+// it 0.1 us more).
 // ---------------------------------------------------------------------------
 constexpr int kPosThreads = 256;
 
@@ -16,39 +18,34 @@ __global__ void __launch_bounds__(kPosThreads) positions_kernel(const PositionsP
 {
     extern __shared__ int qs[];
     const int n = p.n_seqs;
+    int *const lens = qs + n + 1;
     pdl_wait();
     pdl_trigger();
-    for (int i = threadIdx.x; i <= n; i += kPosThreads) qs[i] = min(max(p.q_start[i], 0), p.n_tokens);
-    __syncthreads();
-    const long long t0 = 4 * ((long long)blockIdx.x * kPosThreads + threadIdx.x);
-    int lo = 0, end = 0, base = 0;   // the sequence of the row before, its end and the position of row 0 in it
-    bool known = false;
-    for (int k = 0; k < 4 && t0 + k < p.n_tokens; ++k) {
-        const int t = (int)t0 + k;
-        int pos = -1;
-        if (t >= qs[0] && t < qs[n]) {
-            if (!known || t >= end) {
-                int a = known ? lo : 0, b = n;   // last sequence that begins at t or before
-                while (b - a > 1) {
-                    const int mid = (a + b) >> 1;
-                    if (qs[mid] <= t) a = mid;
-                    else b = mid;
-                }
-                lo = a;
-                end = qs[a + 1];
-                base = (int)((unsigned)p.lens[a] - (unsigned)end);
-                known = true;
-            }
-            pos = (int)((unsigned)base + (unsigned)t);
-        }
-        p.positions[t] = pos;
+#pragma unroll 4
+    for (int i = threadIdx.x; i <= n; i += kPosThreads) {
+        const int q = p.q_start[i];
+        if (i < n) lens[i] = p.lens[i];
+        qs[i] = min(max(q, 0), p.n_tokens);
     }
+    __syncthreads();
+    const long long t = (long long)blockIdx.x * kPosThreads + threadIdx.x;
+    if (t >= p.n_tokens) return;
+    int pos = -1;
+    if (t >= qs[0] && t < qs[n]) {
+        int a = 0, b = n;   // last sequence that begins at t or before
+        while (b - a > 1) {
+            const int mid = (a + b) >> 1;
+            if (qs[mid] <= t) a = mid;
+            else b = mid;
+        }
+        pos = (int)((unsigned)lens[a] - (unsigned)qs[a + 1] + (unsigned)t);
+    }
+    p.positions[t] = pos;
 }
 
 cudaError_t launch_positions(const PositionsParams &p, cudaStream_t s, bool pdl)
 {
-    const int per = 4 * kPosThreads;
-    return launch_pdl(positions_kernel, p, (int)(((long long)p.n_tokens + per - 1) / per), kPosThreads, (p.n_seqs + 1) * (int)sizeof(int), s, pdl);
+    return launch_pdl(positions_kernel, p, (int)(((long long)p.n_tokens + kPosThreads - 1) / kPosThreads), kPosThreads, (2 * p.n_seqs + 1) * (int)sizeof(int), s, pdl);
 }
 
 // ---------------------------------------------------------------------------
