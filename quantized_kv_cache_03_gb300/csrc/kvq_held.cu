@@ -743,7 +743,7 @@ cudaError_t launch_gather_many(const PagedRowsParams &rows, int v_type, int k_ty
 //
 // Where tokens move, each slot may be another's source, so more than a few rows go
 // through the workspace (one launch out, one in) unless the caller says that none is.  8092 tokens
-// of 8 heads (q8_0 V, keys turned) through the workspace 15.9 us, two launches whose 70
+// of 8 heads (q8_0 V, keys turned) through the workspace 15.7 us, two launches whose 70
 // MB would take 10.4.  131072 keys turned where they lie 61 us, 4.7 TB/s, 0.69 of a
 // copy's rate: instructions, some 400 for eight rows (codes to numbers, the turn,
 // largest values, new codes), three quarters of what the SMs can issue.  There the next
@@ -897,9 +897,22 @@ __device__ __forceinline__ void stage_get(const uint8_t *row, QuadRow<VT, KT> &r
     }
 }
 
+// A lane's rates: of pairs lane and lane + 32; loaded once for all tokens (64 tokens of
+// move_once_kernel 3.5 us, 4.9 with a load for each token's angles).
+struct MoveRates {
+    unsigned long long r[2];
+    __device__ __forceinline__ explicit MoveRates(const RopeDesc &rope)
+    {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int j = (int)(threadIdx.x & 31) + 32 * i;
+            r[i] = j < rope.n_rot / 2 ? rope.turns[j] : 0;
+        }
+    }
+};
 // Angles of the quads' turns, one row for all where they are the same; the lane's
 // row.  Called by the whole warp, some of whose quads turn.
-__device__ __forceinline__ int move_angles(MoveShared &sh, const RopeDesc &rope, int turn, bool turns)
+__device__ __forceinline__ int move_angles(MoveShared &sh, const MoveRates &rates, int turn, bool turns)
 {
     const int lane = threadIdx.x & 31;
     const int one = __shfl_sync(0xffffffffu, turn, __ffs(__ballot_sync(0xffffffffu, turns)) - 1);
@@ -907,10 +920,11 @@ __device__ __forceinline__ int move_angles(MoveShared &sh, const RopeDesc &rope,
     __syncwarp();   // the rows before may still be read
     for (int k = 0; k < (same ? 1 : kMoveTokens); ++k) {
         const int t = same ? one : __shfl_sync(0xffffffffu, turn, 4 * k);
-        for (int j = lane; j < rope.n_rot / 2; j += 32) {
-            const float2 a = angle_of(rope.turns[j], t, 1.f);
-            sh.cosines[k][j] = a.x;
-            sh.sines[k][j] = a.y;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {   // (behind n_rot / 2 nobody reads)
+            const float2 a = angle_of(rates.r[i], t, 1.f);
+            sh.cosines[k][lane + 32 * i] = a.x;
+            sh.sines[k][lane + 32 * i] = a.y;
         }
     }
     __syncwarp();
@@ -996,7 +1010,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32, 7) move_kernel(const MovePara
         } else {
             get(r);
         }
-        const int row = ROT != kRotNone && any ? move_angles(sh, p.rope, turn, turns) : 0;
+        const int row = ROT != kRotNone && any ? move_angles(sh, MoveRates(p.rope), turn, turns) : 0;
         const float *cosines = sh.cosines[row], *sines = sh.sines[row];
         float *const mem = scratch[ROT == kRotPart ? warp : 0][ROT == kRotPart ? quad : 0];
         if (ringed) {
@@ -1054,9 +1068,11 @@ __global__ void __launch_bounds__(kMoveWarps * 32, 7) move_kernel(const MovePara
 
 // Few tokens that may be one another's source: a cluster takes all of them, of one
 // head, in registers, and writes none before every one has been read.  A launch less
-// than by way of the workspace: 64 tokens of 8 heads (q4_0 V) 3.0 us against 5.0, 256
-// 3.4 against 5.2, with keys turned 5.0 against 6.7; 256 of 32 heads 5.4 against 7.1.
-// Clusters of more than eight CTAs are not portable.
+// than by way of the workspace: 64 tokens of 8 heads (q4_0 V) 2.4 us against 5.0, with
+// keys turned, each otherwise, 3.5 against 5.6; F16 K and q8_0 V, no two slots neighbours, 3.6 against
+// 9.6, 256 tokens 9.1 against 10.2 (bytes stored one by one: an SM's store unit; so the
+// tokens go to as many CTAs as there are: 64 in two 7.2).  Clusters of more than eight
+// CTAs are not portable, and with 512 tokens the way through the workspace is as fast.
 template <int VT, int KT, int ROT>
 __global__ void __launch_bounds__(kMoveWarps * 32) move_once_kernel(const MoveParams p)
 {
@@ -1067,11 +1083,12 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_once_kernel(const MovePa
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, quad = lane >> 2;
     MoveShared &sh = shared[warp];
-    const int h = (int)blockIdx.x / p.chunks, t0 = (((int)blockIdx.x - h * p.chunks) * kMoveWarps + warp) * kMoveTokens;
+    const int h = (int)blockIdx.x / p.chunks, t0 = (((int)blockIdx.x - h * p.chunks) * (int)(blockDim.x / 32) + warp) * kMoveTokens;
     const int at = t0 - 1 + lane;
     const bool there = lane < kMoveTokens + 2 && at >= 0 && at < p.n_tokens;
     const int from_all = there ? p.from[at] : -1, to_all = there ? p.to[at] : -1;
     const int turn_all = ROT != kRotNone && there ? p.turn[at] : 0;
+    const MoveRates rates(p.rope);   // (n_rot is 0 without a turn)
     auto inside = [&](int slot) { return slot >= 0 && slot < p.pool.n_slots; };
     const SlotPairs q = slot_pairs(to_all, t0 < p.n_tokens && inside(from_all) && inside(to_all), kMoveTokens);
     slot_list(q, sh.list);
@@ -1107,7 +1124,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_once_kernel(const MovePa
 #pragma unroll
         for (int g = 0; g < kGroups; ++g)
             if (__any_sync(0xffffffffu, turns[g])) {
-                const int row = move_angles(sh, p.rope, turn[g], turns[g]);
+                const int row = move_angles(sh, rates, turn[g], turns[g]);
                 turn_key<true, VT, KT, ROT>(r[g], turns[g], sh.cosines[row], sh.sines[row], c, p.rope.n_rot, scratch[ROT == kRotPart ? warp : 0][ROT == kRotPart ? quad : 0]);
             }
     }
@@ -1120,18 +1137,20 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_once_kernel(const MovePa
         quad_put_value<VT, KT>(r[g], dst, to[g] & 15, c, pair[g], mine[g]);
     }
 }
-constexpr int kMoveOnceCtas = 8, kMoveOnce = kMoveOnceCtas * kMoveWarps * kMoveTokens;   // of a cluster, tokens
+constexpr int kOnceCtas = 8;   // of a cluster
 
 template <int VT, int KT, int ROT>
 static cudaError_t move_once(const MoveParams &in, cudaStream_t s, bool pdl)
 {
     MoveParams p = in;
     p.heads = 1;
+    const int windows = (p.n_tokens + kMoveTokens - 1) / kMoveTokens;
     p.chunks = 1;   // CTAs of a cluster
-    while (p.chunks * kMoveWarps * kMoveTokens < p.n_tokens) p.chunks *= 2;
+    while (p.chunks < kOnceCtas && p.chunks < windows) p.chunks *= 2;
+    const int warps = (windows + p.chunks - 1) / p.chunks;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.chunks * p.pool.n_kv_heads);
-    cfg.blockDim = dim3(kMoveWarps * 32);
+    cfg.blockDim = dim3(warps * 32);
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1147,7 +1166,7 @@ static cudaError_t move_once(const MoveParams &in, cudaStream_t s, bool pdl)
 template <int VT, int KT, int ROT>
 static cudaError_t move_t(const MoveParams &p, int blocks, cudaStream_t s, bool pdl)
 {
-    if (p.rows && p.n_tokens <= kMoveOnce) return move_once<VT, KT, ROT>(p, s, pdl);
+    if (p.rows && p.n_tokens <= kOnceCtas * kMoveWarps * kMoveTokens) return move_once<VT, KT, ROT>(p, s, pdl);
     if (!p.rows) return launch_pdl(move_kernel<VT, KT, ROT, kMoveDirect>, p, blocks, kMoveWarps * 32, 0, s, pdl);
     const cudaError_t e = launch_pdl(move_kernel<VT, KT, ROT, kMoveOut>, p, blocks, kMoveWarps * 32, 0, s, pdl);
     return e != cudaSuccess ? e : launch_pdl(move_kernel<VT, KT, kRotNone, kMoveIn>, p, blocks, kMoveWarps * 32, 0, s, pdl);
