@@ -20,7 +20,6 @@ __global__ void __launch_bounds__(kPosThreads) positions_kernel(const PositionsP
     const int n = p.n_seqs;
     int *const lens = qs + n + 1;
     pdl_wait();
-    pdl_trigger();
 #pragma unroll 4
     for (int i = threadIdx.x; i <= n; i += kPosThreads) {
         const int q = p.q_start[i];
@@ -366,7 +365,6 @@ __global__ void __cluster_dims__(kForkCtas, 1, 1) __launch_bounds__(kForkThreads
 __global__ void __launch_bounds__(kForkWide) fork_clear_kernel(const ForkParams p)
 {
     pdl_wait();
-    pdl_trigger();
     if (blockIdx.x == 0) {   // lengths in shared memory, where their maxima cost no trips, then to the workspace
         extern __shared__ int seqs[];
         const ForkSeqs q(seqs, p.n_seqs), out(p.seqs, p.n_seqs);
@@ -390,7 +388,6 @@ __global__ void __launch_bounds__(kForkWide) fork_clear_kernel(const ForkParams 
 __global__ void __launch_bounds__(kForkMark) fork_mark_kernel(const ForkParams p)
 {
     pdl_wait();
-    pdl_trigger();
     const int at = blockIdx.x * kForkMark + threadIdx.x, all = gridDim.x * kForkMark, runs = fork_runs(p);
     const ForkSeqs q(p.seqs, p.n_seqs);
     for (long long item = at >> 5; item < (long long)p.n_seqs * runs; item += all >> 5) {
@@ -431,7 +428,6 @@ __global__ void __launch_bounds__(kForkWide) fork_count_kernel(const ForkParams 
 {
     __shared__ int2 tmp[kForkWide / 32];
     pdl_wait();
-    pdl_trigger();
     int2 total;
     if ((int)blockIdx.x < p.blocks) {
         fork_scan<kForkWide>(make_int2(ForkShare(p).n, 0), total, tmp);
@@ -464,7 +460,6 @@ __global__ void __launch_bounds__(kForkWide) fork_deal_kernel(const ForkParams p
 {
     __shared__ int2 tmp[kForkWide / 32];
     pdl_wait();
-    pdl_trigger();
     const ForkSeqs q(p.seqs, p.n_seqs);
     const ForkShare share(p);
     int2 blocks = make_int2(0, 0), total;   // pages of the blocks before this one, of all
@@ -525,7 +520,6 @@ template <int POOLS>
 __global__ void __launch_bounds__(kCopyWarps * 32) page_copy_kernel(const __grid_constant__ CopyParams<POOLS> p)
 {
     pdl_wait();
-    pdl_trigger();
     const unsigned pool = blockIdx.y, i = blockIdx.x / (unsigned)p.blocks, unit = (blockIdx.x - i * p.blocks) * kCopyWarps + (threadIdx.x >> 5);
     const int from = p.from[i], to = p.to[i], lane = threadIdx.x & 31;
     if (from < 0 || to < 0 || from >= p.n_pages || to >= p.n_pages || from == to) return;
@@ -642,7 +636,6 @@ __global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(const GatherP
 {
     using T = PageTile<VT, KT>;
     pdl_wait();
-    pdl_trigger();
     const int lane = threadIdx.x & 31, c = lane & 3, quad = lane >> 2;
     const long long job = (long long)blockIdx.x * kGatherWarps + (threadIdx.x >> 5);
     const int window = (int)(job / p.chunks), h0 = (int)(job - (long long)window * p.chunks) * p.heads, h1 = min(p.pool.n_kv_heads, h0 + p.heads);
@@ -711,17 +704,15 @@ __global__ void __launch_bounds__(kGatherWarps * 32) gather_kernel(const GatherP
 }
 
 template <bool O16>
-static cudaError_t gather_t(const GatherParams &p, int v_type, int k_type, int blocks, cudaStream_t s)
+static cudaError_t gather_t(const GatherParams &p, int v_type, int k_type, int blocks, cudaStream_t s, bool pdl)
 {
     void (*fn)(GatherParams) =
         k_type == KVQ_K_F16 ? (v_type == KVQ_V_Q4_0 ? gather_kernel<KVQ_V_Q4_0, KVQ_K_F16, O16> : gather_kernel<KVQ_V_Q8_0, KVQ_K_F16, O16>)
                             : (v_type == KVQ_V_Q4_0 ? gather_kernel<KVQ_V_Q4_0, KVQ_K_I8, O16> : gather_kernel<KVQ_V_Q8_0, KVQ_K_I8, O16>);
-    // Never beside the last blocks of the launch in front: blocks that are placed while those still hold registers
-    // crowd on the few SMs with room for them (777 tokens after kvq_qkv: 16.5 us for the two, 11.7 so).
-    return launch_pdl(fn, p, blocks, kGatherWarps * 32, 0, s, false);
+    return launch_pdl(fn, p, blocks, kGatherWarps * 32, 0, s, pdl);
 }
 
-cudaError_t launch_gather_many(const PagedRowsParams &rows, int v_type, int k_type, int out_type, int n_sms, cudaStream_t s)
+cudaError_t launch_gather_many(const PagedRowsParams &rows, int v_type, int k_type, int out_type, int n_sms, cudaStream_t s, bool pdl)
 {
     GatherParams p = {rows.pool, rows.slots, rows.n_tokens, rows.k_out, rows.v_out, 1, 1};
     const long long windows = ((long long)p.n_tokens + 7) / 8;
@@ -730,7 +721,7 @@ cudaError_t launch_gather_many(const PagedRowsParams &rows, int v_type, int k_ty
     p.heads = want < 1 ? 1 : want > p.pool.n_kv_heads ? p.pool.n_kv_heads : (int)want;
     p.chunks = (p.pool.n_kv_heads + p.heads - 1) / p.heads;
     const int blocks = (int)((windows * p.chunks + kGatherWarps - 1) / kGatherWarps);
-    return out_type == KVQ_OUT_F16 ? gather_t<true>(p, v_type, k_type, blocks, s) : gather_t<false>(p, v_type, k_type, blocks, s);
+    return out_type == KVQ_OUT_F16 ? gather_t<true>(p, v_type, k_type, blocks, s, pdl) : gather_t<false>(p, v_type, k_type, blocks, s, pdl);
 }
 
 // ---------------------------------------------------------------------------
@@ -940,7 +931,6 @@ __global__ void __launch_bounds__(kMoveWarps * 32, 7) move_kernel(const MovePara
     constexpr bool kRinged = WAY == kMoveDirect && KT == KVQ_K_I8 && ROT != kRotNone;
     __shared__ uint4 ring[kRinged ? kMoveWarps : 1][2][3][kRinged ? 32 : 1];   // K codes and scales of two heads, for keys that turn where they lie
     pdl_wait();
-    pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, quad = lane >> 2;
     MoveShared &sh = shared[warp];
     const long long job = (long long)blockIdx.x * kMoveWarps + warp;
@@ -1080,7 +1070,6 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_once_kernel(const MovePa
     __shared__ __align__(16) MoveShared shared[kMoveWarps];
     __shared__ __align__(16) float scratch[ROT == kRotPart ? kMoveWarps : 1][8][ROT == kRotPart ? kD + 4 : 1];
     pdl_wait();
-    pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 3, quad = lane >> 2;
     MoveShared &sh = shared[warp];
     const int h = (int)blockIdx.x / p.chunks, t0 = (((int)blockIdx.x - h * p.chunks) * (int)(blockDim.x / 32) + warp) * kMoveTokens;

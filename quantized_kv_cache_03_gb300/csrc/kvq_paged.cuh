@@ -263,7 +263,7 @@ cudaError_t launch_paged_append(const PagedRowsParams &p, int v_type, int k_type
 cudaError_t launch_paged_gather(const PagedRowsParams &p, int v_type, int k_type, int out_type, int n_sms, cudaStream_t s,
                                 bool pdl);
 // The same for many rows (kvq_held.cu).
-cudaError_t launch_gather_many(const PagedRowsParams &p, int v_type, int k_type, int out_type, int n_sms, cudaStream_t s);
+cudaError_t launch_gather_many(const PagedRowsParams &p, int v_type, int k_type, int out_type, int n_sms, cudaStream_t s, bool pdl);
 cudaError_t launch_paged_combine(const PagedAttnParams &p, const PagedCuts &cuts, int out_type, cudaStream_t s, bool pdl);
 // Row-tile attention (kvq_paged_attn_q4.cu / _q8.cu): nt = 8-row tiles per CTA (1 or 2).
 cudaError_t prepare_paged_q4(int nt, int k_type, int out_type, int *ctas_per_sm);

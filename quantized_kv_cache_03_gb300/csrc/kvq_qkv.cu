@@ -1,6 +1,8 @@
 // kvq_qkv.cu -- new tokens on their way into the paged cache: heads normalized
 // and rotated, queries (and keys, without pages) written as fp16, keys and values
 // quantized into their slots.
+#include <cfloat>
+
 #include "kvq_quad.cuh"
 
 namespace kvq {
@@ -325,7 +327,6 @@ __global__ void __launch_bounds__(kQkvWarps * 32, kQkvBlocks) qkv_kernel(const _
     extern __shared__ __align__(1024) uint8_t qkv_smem[];
     QkvShared &sh = *reinterpret_cast<QkvShared *>(qkv_smem);
     pdl_wait();
-    pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 7, oct = lane >> 3, n_rot = p.rope.n_rot;
     // blocks of all heads, then those that take a share
     const int part = (int)blockIdx.x - p.full, cut = part < 0 ? 0 : part / p.chunks, share = part < 0 ? 0 : part - cut * p.chunks;
@@ -495,25 +496,28 @@ cudaError_t launch_qkv(const QkvParams &in, int v_type, int k_type, int n_sms, c
     QkvParams p = in;
     const int tiles = (int)(((long long)p.n_tokens + kQkvTokens - 1) / kQkvTokens);
     const int most = (p.n_q_heads > p.n_kv_heads ? p.n_q_heads : p.n_kv_heads) / 2;
-    // Few tokens: shares of the heads.  With one block to an SM the next launch finds room beside this one's and starts
-    // early; more blocks cost about 2.5 us of that, and eight tokens' rows of a query head 0.13 us in a block (of a kv
-    // head about five times that).  So one block to an SM, unless that leaves each 38 rows more than three would (32 + 8
-    // heads, single tokens, blocks for every SM at one / three: 128 tokens 3.9 / 5.3 us, 256 4.9 / 6.1, 400 6.0 / 6.5;
-    // 700 tokens 10.6 / 9.0; 16 + 2 heads 5.3 / 6.0).  Where every SM has one anyway, two at least (32 + 8 heads, 1600
-    // tokens: 10.3 us at two, 11.5 at one), but for few heads (16 + 2 heads, 2400 tokens: 9.2 / 7.5).
+    // Few tokens: shares of the heads, as many as leave so many blocks to each SM.  Another block to an SM costs what
+    // about 17 rows of a query head do (what it works out before its first row; a kv head counts as five), so one block
+    // until shares get large (32 + 8 heads, single tokens, one / two / three: 256 tokens 4.8 / 5.1 / 6.1 us, 500 tokens
+    // 6.9 / 6.8 / 8.5, 700 tokens 10.8 / 8.5 / 9.0; prompts of 1100 tokens 8.3 / 6.5 / 7.1).
     // Many tokens: whole ones in full waves, and the last wave's shared by all SMs (40 + 8 heads, 8192 tokens, two and a
     // quarter waves: 34.7 us, 36.1 uncut, 35.4 at two blocks for every SM; 4096 tokens: 20.1, 21.4, 20.3; 16384: 65, all
     // alike).
     const int room = kQkvBlocks * n_sms, rest = tiles % room, rows = p.n_q_heads + 5 * p.n_kv_heads;
-    long long chunks = 1;
-    if (rest && tiles < room) {
-        const long long one = rest < n_sms ? n_sms / rest : 1, two = (2 * n_sms + rest - 1) / rest, full = room / rest > two ? room / rest : two;
-        chunks = rows * (full - one) < (rest < n_sms ? 38 : 19) * one * full ? one : full;
-    } else if (rest) {
-        chunks = (n_sms + rest - 1) / rest;
+    int chunks = rest ? (n_sms + rest - 1) / rest : 1;
+    if (tiles < room) {
+        float least = FLT_MAX;
+        for (int blocks = 1; blocks <= kQkvBlocks; ++blocks) {
+            const int shares = blocks * n_sms / rest;
+            const float cost = shares ? (float)rows / shares + 17.f * (blocks - 1) : FLT_MAX;
+            if (cost < least) {
+                least = cost;
+                chunks = shares;
+            }
+        }
     }
     chunks = chunks > most ? most : chunks;
-    p.chunks = chunks < 1 ? 1 : (int)chunks;
+    p.chunks = chunks < 1 ? 1 : chunks;
     p.full = tiles - rest;
     p.q_heads = (p.n_q_heads + p.chunks - 1) / p.chunks;
     p.kv_heads = (p.n_kv_heads + p.chunks - 1) / p.chunks;
