@@ -491,8 +491,9 @@ cudaError_t launch_page_fork(const ForkParams &in, int n_sms, cudaStream_t s, bo
 {
     ForkParams p = in;
     const long long entries = (long long)p.n_seqs * p.max_blocks;
-    // Eight SMs against all of them and four launches: 256 places of 129 entries 7.1 us against 10.8, 512 of 257 11.0
-    // against 12.9, 1024 of 129 15.2 against 14.6.
+    // Eight SMs against all of them and four launches: 256 places of 129 entries 7.1 us against 9.8, 1024 of 126 10.8
+    // against 12.7, 256 of 501 9.4 against 10.7; beyond, 256 of 1001 (75000 pages) 12.5 against 11.9, 512 of 501 (77000)
+    // 13.2 against 12.3, 1024 of 501 21.6 against 15.7.
     if (p.n_seqs <= kForkMaxSeqs && p.n_pages <= kForkMaxPages && entries <= 128 * 1024)
         return launch_pdl(fork_cluster_kernel, p, kForkCtas, kForkThreads, fork_cluster_smem(p.n_seqs, p.n_pages), s, pdl);
     auto grid = [&](long long items, int most) { return (int)(items < 1 ? 1 : items > most ? most : items); };
