@@ -509,7 +509,8 @@ cudaError_t launch_page_fork(const ForkParams &in, int n_sms, cudaStream_t s, bo
 // one run of bytes; all of it is on its way before the first is written.  Bound by
 // memory: 2048 pages of 64 tokens, 8 heads, 570 MB both ways in 84.2 us, a plain
 // copy's rate (1.00); 256 pages of 16 tokens, two in five of them copied, in each
-// of 32 pools 182 MB in 29.5 us (0.91: blocks with nothing to do come and go).
+// of 32 pools 182 MB in 29.4 us (0.91: a short launch's ramps; blocks with nothing to do
+// cost nothing: two pools to a block 29.8, four 30.3).
 // Streaming loads and stores, since neither side is read again soon.  A page of one
 // head 1.6 us.
 // ---------------------------------------------------------------------------
