@@ -159,6 +159,36 @@ def test_rows_left_out():
     assert torch.equal(pool.data, want.data)
 
 
+@pytest.mark.parametrize("T", [1, 40, 700, 3700])
+def test_in_place_into_pages(T):
+    """A fused projection's output whose queries turn where they lie, captured and replayed; keys, values and the rows of
+    tokens that are left out stay as they are."""
+    Hq, H, page = 5, 2, 32
+    r = np.random.default_rng(T)
+    x = to_dev(_tokens(r, T, Hq, H))
+    n_pages = -(-T // page) + 1
+    slots = np.where(r.random(T) < 0.3, -1, np.arange(T) + 7)
+    slots[-(T // 3):] = -1 if T > 2 else slots[0]
+    slots, pos, rope = i32(slots), i32(r.integers(0, 99999, T)), kvq.Rope(128, device=dev())
+    w = to_dev(r.standard_normal(128).astype(np.float32))
+    pools = [kvq.PagePool(n_pages, page, H, Q4) for _ in range(2)]
+    want = x[:, :Hq].clone()
+    for p in pools:
+        p.data.fill_(POISON)
+    kvq.kvq_qkv(x[:, :Hq], x[:, Hq:Hq + H], x[:, Hq + H:], pos, rope, want, pool=pools[0], slots=slots, q_norm=w)
+    y = x.clone()
+    call = kvq.QkvCall(y[:, :Hq], y[:, Hq:Hq + H], y[:, Hq + H:], pos, rope, y[:, :Hq], pool=pools[1], slots=slots, q_norm=w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(2):
+        y.copy_(x)
+        pools[1].data.fill_(POISON)
+        graph.replay()
+        assert torch.equal(y[:, :Hq], want) and torch.equal(y[:, Hq:], x[:, Hq:]) and torch.equal(pools[0].data, pools[1].data)
+    assert torch.equal(want[slots < 0], x[:, :Hq][slots < 0])
+
+
 def test_values_that_are_not_finite_and_large_ones():
     """A head that holds an infinity or NaN is its own affair; values that do not rotate are not touched by it."""
     r = np.random.default_rng(5)
