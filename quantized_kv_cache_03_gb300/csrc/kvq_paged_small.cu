@@ -437,8 +437,8 @@ static cudaError_t gather_t(const PagedRowsParams &p, int v_type, int k_type, cu
 
 cudaError_t launch_paged_gather(const PagedRowsParams &p, int v_type, int k_type, int out_type, int n_sms, cudaStream_t s, bool pdl)
 {
-    // Eight rows to a warp from 4096 rows on (8 heads, q8_0 V, fp16 / fp32 output: 512 tokens 2.2 / 2.5 us here and 1.8 /
-    // 2.2 there, 256 tokens 1.6 / 1.7 and 1.8 / 2.1).
+    // Eight rows to a warp from 4096 rows on (8 heads, q8_0 V, fp16 / fp32 output: 512 tokens 2.2 / 2.4 us here and 1.7 /
+    // 2.0 there, 256 tokens 1.5 / 1.7 and 1.7 / 2.0).
     if ((long long)p.n_tokens * p.pool.n_kv_heads >= 4096) return launch_gather_many(p, v_type, k_type, out_type, n_sms, s, pdl);
     return out_type == KVQ_OUT_F16 ? gather_t<true>(p, v_type, k_type, s, pdl) : gather_t<false>(p, v_type, k_type, s, pdl);
 }
