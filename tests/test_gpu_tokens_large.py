@@ -1,0 +1,131 @@
+"""Launches of the calls around the paged cache that are large enough for their
+long loops: a warp that goes over several heads, blocks of all heads in more than
+one wave, a thread that pushes more than one word of marks.  Against the same
+work in small calls, bit for bit, or plain Python."""
+import numpy as np
+import pytest
+import torch
+
+from quantized_kv_cache_03_gb300 import kvq
+
+from kvq_cases import dev
+from paged_cases import i32
+
+pytestmark = pytest.mark.gpu
+
+I8, F16 = kvq.K_I8, kvq.K_F16
+Q4, Q8 = kvq.V_Q4_0, kvq.V_Q8_0
+HALF, PAIRS = kvq.ROPE_HALF, kvq.ROPE_PAIRS
+FORMATS = [(I8, Q4), (I8, Q8), (F16, Q4), (F16, Q8)]
+# kv heads, and how many of them a warp takes: all in shares of four, a short last share, three shares, one
+HEADS = [(8, 4), (7, 4), (5, 2), (3, 3)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def tokens_for(H, heads, warps):
+    """Tokens from which a warp takes so many of H heads: windows of eight tokens, `warps` of them to be left for every SM."""
+    sms = torch.cuda.get_device_properties(dev()).multi_processor_count
+    n = 8 * -(-heads * warps * sms // H) + 3
+    assert -(-n // 8) * H // (warps * sms) == heads
+    return n
+
+
+def held(T, page, H, k_type, v_type):
+    """A pool that holds T tokens at least, of magnitudes from 2^-6 to 2^6."""
+    g = torch.Generator(device=dev()).manual_seed(T)
+    pool = kvq.PagePool(-(-T // page), page, H, v_type, k_type=k_type)
+    T = pool.n_pages * page
+    kv = torch.randn((2, T, H, 128), generator=g, device=dev()) * torch.exp2(12 * torch.rand((2, T, H, 1), generator=g, device=dev()) - 6)
+    kv[0, 3, 0, 32:64] = 0
+    kvq.kvq_paged_append(pool, kv[0].half(), kv[1].half(), torch.arange(T, dtype=torch.int32, device=dev()))
+    return pool
+
+
+def in_parts(pool, frm, to, rope=None, turn=None, part=601):
+    """Moved directly by calls so small that a warp takes one head."""
+    for a in range(0, len(frm), part):
+        b = slice(a, a + part)
+        kvq.kvq_paged_move(pool, frm[b], to[b], rope=rope, turn=None if turn is None else turn[b], staged=False)
+
+
+def turns(r, n):
+    """Stretches of one turn, tokens each with its own, and some that stay."""
+    t = r.integers(-5000, 5000, n)
+    t[n // 3:n // 2] = -517
+    t[::11] = 0
+    return i32(t)
+
+
+# ------------------------------------------------------------------ move --
+@pytest.mark.parametrize("k_type,v_type", FORMATS)
+@pytest.mark.parametrize("layout,n_rot", [(HALF, 128), (PAIRS, 128), (HALF, 40), (PAIRS, 64)])
+@pytest.mark.parametrize("H,heads", HEADS)
+def test_keys_turned_in_place(H, heads, layout, n_rot, k_type, v_type):
+    r = np.random.default_rng(H)
+    n = tokens_for(H, heads, 24)
+    pool = held(n + 40, 64, H, k_type, v_type)
+    slots, turn, rope = i32(np.arange(n) + 5), turns(r, n), kvq.Rope(n_rot, layout=layout, device=dev())
+    start = pool.data.clone()
+    in_parts(pool, slots, slots, rope, turn)
+    want = pool.data.clone()
+    assert not torch.equal(want, start)
+    pool.data.copy_(start)
+    kvq.kvq_paged_move(pool, slots, slots, rope=rope, turn=turn, staged=False)
+    assert torch.equal(pool.data, want)
+
+
+@pytest.mark.parametrize("k_type,v_type", FORMATS)
+@pytest.mark.parametrize("layout,n_rot", [(HALF, 0), (HALF, 128), (PAIRS, 40), (HALF, 64)])
+@pytest.mark.parametrize("H,heads", HEADS)
+def test_tokens_moved(H, heads, layout, n_rot, k_type, v_type):
+    """To other pages directly; and down over themselves and in any order, staged, against two direct moves by way of other pages."""
+    r = np.random.default_rng(n_rot)
+    n, page = tokens_for(H, heads, 24), 32
+    half = -(-(n + 9) // page) * page
+    pool = held(2 * half, page, H, k_type, v_type)
+    cut = pool.data.numel() // 2
+    start, turn = pool.data.clone(), turns(r, n) if n_rot else None
+    rope = kvq.Rope(n_rot, layout=layout, device=dev()) if n_rot else None
+    there = i32(half + np.arange(n))
+    mixed = r.permutation(half)[:n], r.permutation(half)[:n]
+    for frm, to in ((np.arange(n) + 9, np.arange(n)), mixed):
+        frm[::97], to[5::101] = -1, 2 ** 30          # tokens without a slot
+        ok = i32(np.where((frm >= 0) & (to < 2 ** 30), half + np.arange(n), -1))
+        frm, to = i32(frm), i32(to)
+        pool.data.copy_(start)
+        in_parts(pool, frm, there, rope, turn)
+        away = pool.data.clone()
+        in_parts(pool, ok, to)
+        want = pool.data[:cut].clone()
+        pool.data.copy_(start)
+        kvq.kvq_paged_move(pool, frm, there, rope=rope, turn=turn, staged=False)
+        assert torch.equal(pool.data, away)
+        pool.data.copy_(start)
+        kvq.kvq_paged_move(pool, frm, to, rope=rope, turn=turn, staged=True)
+        assert torch.equal(pool.data[:cut], want) and torch.equal(pool.data[cut:], start[cut:])
+
+
+# ---------------------------------------------------------------- gather --
+@pytest.mark.parametrize("k_type,v_type", FORMATS)
+@pytest.mark.parametrize("H,heads", HEADS)
+def test_gathered(H, heads, k_type, v_type):
+    """Against calls of fewer rows than the kernel for many takes."""
+    r = np.random.default_rng(heads)
+    n, part = tokens_for(H, heads, 48), 4095 // H
+    pool = held(5000, 128, H, k_type, v_type)
+    slots = r.integers(0, pool.n_pages * 128, n)
+    slots[:3000] = np.arange(3000) + 1
+    slots[::89], slots[7::97] = -1, 2 ** 30
+    slots = i32(slots)
+    for dt in (torch.float32, torch.float16):
+        one, two = (torch.full((2, n, H, 128), 777.0, dtype=dt, device=dev()) for _ in range(2))
+        kvq.kvq_paged_gather(pool, slots, one[0], one[1])
+        for a in range(0, n, part):
+            b = slice(a, a + part)
+            kvq.kvq_paged_gather(pool, slots[b], two[0, b], two[1, b])
+        assert torch.equal(one, two)
