@@ -9,7 +9,8 @@ import torch
 from quantized_kv_cache_03_gb300 import kvq
 
 from kvq_cases import dev
-from paged_cases import i32
+from paged_cases import i32, to_dev
+from tokens_cases import fork_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -129,3 +130,35 @@ def test_gathered(H, heads, k_type, v_type):
             b = slice(a, a + part)
             kvq.kvq_paged_gather(pool, slots[b], two[0, b], two[1, b])
         assert torch.equal(one, two)
+
+
+# ------------------------------------------------------------------ fork --
+def test_fork_over_nine_million_pages():
+    """Several words of four pages' marks to a thread: pages given back that fill a thread's share, cross from one share and one
+    block to the next, lie in its later words alone, and the last word, of one page."""
+    r = np.random.default_rng(3)
+    B, page, most, n_pages = 40, 16, 2000, 9_000_001
+    words = -(-n_pages // 4)
+    of_block = -(-words // 1024)                                  # a block's, and a thread's
+    per = -(-of_block // 1024)
+    assert per > 2 and words % of_block and n_pages % 4 == 1
+    runs = [np.arange(5 * 4 * per), 4 * of_block * 7 - 50 + np.arange(100), 4 * (of_block * 500 + per * 3 + 1) + np.arange(4 * (per - 1)), n_pages - 1 - np.arange(77)]
+    listed = np.unique(np.concatenate(runs + [r.integers(0, n_pages, 60000)]))
+    listed = r.permutation(listed)[:B * most]
+    others = np.setdiff1d(r.integers(0, n_pages, 4000), listed)[:1000]
+    table = np.full((B, most), -9, np.int32)
+    lens = np.zeros(B, np.int64)
+    for b in range(B):
+        row = listed[b::B]
+        table[b, :len(row)], lens[b] = row, len(row) * page - r.integers(0, page)
+    free = np.full(n_pages, -5, np.int32)
+    free[:len(others)] = others
+    for parent, keep in ((np.where(r.random(B) < 0.3, np.arange(B), -1), None), (np.full(B, B), None), (r.integers(0, 4, B), r.integers(0, 300 * page, B))):
+        ref = fork_ref(page, n_pages, lens, table, free, len(others), np.full((B, most), -8, np.int32), most, parent, keep)
+        o = dict(table_out=torch.full((B, most), -8, dtype=torch.int32, device=dev()), lens=i32(np.zeros(B)), n_free=i32([0]), free=to_dev(free),
+                 **{k: i32(np.full(B, 99)) for k in ("copy_from", "copy_to", "copy_held", "status")})
+        kvq.kvq_page_fork(page, n_pages, i32(lens), to_dev(table), o["free"], i32([len(others)]), o["table_out"], o["lens"], o["n_free"], o["copy_from"], o["copy_to"],
+                          o["copy_held"], o["status"], parent=i32(parent), keep=None if keep is None else i32(keep))
+        assert ref["n_free"][0] > len(others)
+        for k, v in ref.items():
+            assert np.array_equal(o[k].cpu().numpy(), v), k
