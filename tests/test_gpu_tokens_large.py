@@ -10,7 +10,7 @@ from quantized_kv_cache_03_gb300 import kvq
 
 from kvq_cases import dev
 from paged_cases import i32, to_dev
-from tokens_cases import fork_ref
+from tokens_cases import fork_ref, fp16_bound, normalized, rates, rotated
 
 pytestmark = pytest.mark.gpu
 
@@ -130,6 +130,53 @@ def test_gathered(H, heads, k_type, v_type):
             b = slice(a, a + part)
             kvq.kvq_paged_gather(pool, slots[b], two[0, b], two[1, b])
         assert torch.equal(one, two)
+
+
+# ------------------------------------------------------------------- qkv --
+def qkv_tokens(waves, extra):
+    """Tokens of so many full waves of blocks (three to an SM, eight tokens each), and some that are shared out."""
+    return 24 * waves * torch.cuda.get_device_properties(dev()).multi_processor_count + extra
+
+
+@pytest.mark.parametrize("layout,n_rot,norm", [(HALF, 128, False), (PAIRS, 128, True), (HALF, 40, True), (HALF, 64, False), (PAIRS, 24, False), (HALF, 0, True)])
+@pytest.mark.parametrize("to", ["rows", "in place"] + FORMATS)
+@pytest.mark.parametrize("waves,extra,Hq,H", [(1, 2, 9, 3), (1, 409, 12, 2), (2, 1207, 3, 5), (1, 3001, 0, 2)])
+def test_new_tokens_in_more_than_a_wave(waves, extra, Hq, H, to, layout, n_rot, norm):
+    """One call, and calls of less than a wave."""
+    r = np.random.default_rng(extra)
+    T, page, part = qkv_tokens(waves, extra), 32, 611
+    g = torch.Generator(device=dev()).manual_seed(T)
+    x = torch.randn((T, Hq + 2 * H, 128), generator=g, device=dev()).half()
+    n_pages = -(-T // page) + 3
+    order = np.concatenate([np.arange(1, T // 2), r.permutation(np.arange(T // 2, n_pages * page))])[:T]      # neighbours, and none
+    slots = i32(np.where(r.random(T) < 0.1, np.where(r.random(T) < 0.5, -1, n_pages * page + 5), order))
+    pos, rope = i32(r.integers(0, 131072, T)), kvq.Rope(n_rot, layout=layout, device=dev())
+    w = torch.randn((2, 128), generator=g, device=dev()) if norm else [None, None]
+    got = []
+    for step in (T, part):
+        t = x.clone()
+        qo = t[:, :Hq] if to == "in place" else torch.full((T, Hq, 128), 3.0, dtype=torch.float16, device=dev())
+        if to in FORMATS:
+            pool = kvq.PagePool(n_pages, page, H, to[1], k_type=to[0])
+            pool.data.fill_(0)
+            res = pool.data
+        else:
+            res = ko = t[:, Hq:Hq + H] if to == "in place" else torch.full((T, H, 128), 3.0, dtype=torch.float16, device=dev())
+        for a in range(0, T, step):
+            b = slice(a, a + step)
+            keys = dict(v16=t[b, Hq + H:], pool=pool) if to in FORMATS else dict(v16=None, k_out=ko[b])
+            kvq.kvq_qkv(t[b, :Hq] if Hq else None, t[b, Hq:Hq + H], positions=pos[b], rope=rope, q_out=qo[b] if Hq else None, slots=slots[b], q_norm=w[0], k_norm=w[1], **keys)
+        got.append((qo.contiguous().view(torch.int16), res.contiguous().view(torch.int16), t[:, Hq + H:]))
+    for one, two in zip(*got):
+        assert torch.equal(one, two)
+    assert torch.equal(got[0][2], x[:, Hq + H:])
+    if to == "rows":       # and the first and last of them by the formula
+        f, pick = rates(n_rot)[0], np.r_[0:40, T - 40:T]
+        out = slots.cpu().numpy()[pick] < 0
+        for a, b, o, wt in ((0, Hq, qo, w[0]), (Hq, Hq + H, ko, w[1])):
+            y, size = rotated(normalized(x[pick, a:b].cpu().numpy(), None if wt is None else wt.cpu().numpy(), 1e-6), pos.cpu().numpy()[pick], f, 1.0, layout)
+            o = o[pick].cpu().numpy().astype(np.float64)
+            assert (np.abs(o - y) <= fp16_bound(y, size))[~out].all() and (o[out] == 3).all()
 
 
 # ------------------------------------------------------------------ fork --
