@@ -2,6 +2,7 @@
 // and rotated, queries (and keys, without pages) written as fp16, keys and values
 // quantized into their slots.
 #include <cfloat>
+#include <cstddef>
 
 #include "kvq_quad.cuh"
 
@@ -15,12 +16,16 @@ constexpr int kBatch = 4;       // rows that an octet takes at a time
 static_assert(kQkvWarps * 32 == 2 * kD, "a thread to each weight of the two norms");
 static_assert(kQkvTokens == 8 && kQkvWarps % 4 == 0, "four tokens to a warp, and four groups of them in a block at most");
 
-struct QkvShared {
-    uint16_t ring[kQkvWarps][2][kBatch][4][kD];
+constexpr int kSharedAlign = 1024;
+struct alignas(16) QkvShared {
+    uint16_t ring[kQkvWarps][kBatch][4][2][kD];   // the places of a row in the two batches side by side: kRowBytes apart in any aligned memory
     float cosines[kQkvTokens + 1][kAngleRow], sines[kQkvTokens + 1][kAngleRow];
     float norm[2][kD];          // of queries, of keys
     uint8_t list[kQkvWarps][kQkvTokens];
 };
+constexpr uint32_t kRowBytes = kD * 2;
+static_assert((kRowBytes & (kRowBytes - 1)) == 0 && kSharedAlign % (2 * kRowBytes) == 0 && offsetof(QkvShared, ring) % (2 * kRowBytes) == 0,
+              "one bit of an address tells the two places of a row apart");
 
 // ---- eight lanes (an octet) to a row ----
 // A row's 256 bytes are read and written as whole lines, and what multiplies a
@@ -257,10 +262,10 @@ __device__ __forceinline__ void oct_put_value(const Oct16 &x, uint8_t *tile, con
 struct Stream {
     const uint16_t *q, *k, *v;     // the lane's part of the next rows of its octet's tokens
     int nq, nk;                    // rows of each still to come
-    uint32_t to;                   // the lane's part of the next batch, in shared memory
+    uint32_t to;                   // the lane's part of the next batch's first row, in shared memory
     bool q_there, k_mine;          // q rows are read before their slots are known
 };
-constexpr uint32_t kBatchBytes = kBatch * 4 * kD * 2;
+constexpr uint32_t kStep = 4 * 2 * kRowBytes;   // from row to row of an octet's batch
 __device__ __forceinline__ void stream_row(uint32_t to, const uint16_t *from, bool there)
 {
     if (there) {
@@ -273,27 +278,27 @@ __device__ __forceinline__ void stream_get(Stream &w)
 {
     if (w.nq > 0) {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) stream_row(w.to + i * 8 * kD, w.q + i * kD, w.q_there && i < w.nq);
+        for (int i = 0; i < kBatch; ++i) stream_row(w.to + i * kStep, w.q + i * kD, w.q_there && i < w.nq);
         w.q += kBatch * kD;
         w.nq -= kBatch;
     } else if (w.nk > 0) {
         if (PAGED) {
 #pragma unroll
             for (int i = 0; i < kBatch / 2; ++i) {
-                stream_row(w.to + 2 * i * 8 * kD, w.k + i * kD, w.k_mine && i < w.nk);
-                stream_row(w.to + (2 * i + 1) * 8 * kD, w.v + i * kD, w.k_mine && i < w.nk);
+                stream_row(w.to + 2 * i * kStep, w.k + i * kD, w.k_mine && i < w.nk);
+                stream_row(w.to + (2 * i + 1) * kStep, w.v + i * kD, w.k_mine && i < w.nk);
             }
             w.k += kBatch / 2 * kD;
             w.v += kBatch / 2 * kD;
             w.nk -= kBatch / 2;
         } else {
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) stream_row(w.to + i * 8 * kD, w.k + i * kD, w.k_mine && i < w.nk);
+            for (int i = 0; i < kBatch; ++i) stream_row(w.to + i * kStep, w.k + i * kD, w.k_mine && i < w.nk);
             w.k += kBatch * kD;
             w.nk -= kBatch;
         }
     }
-    w.to ^= kBatchBytes;
+    w.to ^= kRowBytes;
     copy_commit();
 }
 
@@ -324,7 +329,7 @@ __device__ __forceinline__ void stream_get(Stream &w)
 template <int VT, int KT, int ROT, bool PAGED>
 __global__ void __launch_bounds__(kQkvWarps * 32, kQkvBlocks) qkv_kernel(const __grid_constant__ QkvParams p)
 {
-    extern __shared__ __align__(1024) uint8_t qkv_smem[];
+    extern __shared__ __align__(kSharedAlign) uint8_t qkv_smem[];
     QkvShared &sh = *reinterpret_cast<QkvShared *>(qkv_smem);
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 7, oct = lane >> 3, n_rot = p.rope.n_rot;
@@ -362,7 +367,7 @@ __global__ void __launch_bounds__(kQkvWarps * 32, kQkvBlocks) qkv_kernel(const _
     w.q = p.q + (t0 + qi) * p.q_stride + q_first * kD + 8 * c;
     w.nq = nq;
     w.nk = 0;
-    w.to = smem_u32(sh.ring[warp][0][0][oct]) + 16 * c;
+    w.to = smem_u32(sh.ring[warp][0][oct][0]) + 16 * c;
     stream_get<PAGED>(w);
     const bool q_mine = __shfl_sync(0xffffffffu, slot, 1 + qi) >= 0;
     int nk;
@@ -389,7 +394,7 @@ __global__ void __launch_bounds__(kQkvWarps * 32, kQkvBlocks) qkv_kernel(const _
     w.v = p.v + (t0 + ki) * p.v_stride + k_first * kD + 8 * c;
     w.nk = nk;
     if (nq == 0) {   // (the first batch was empty: the next is the first)
-        w.to ^= kBatchBytes;
+        w.to ^= kRowBytes;
         stream_get<PAGED>(w);
     }
     stream_get<PAGED>(w);
@@ -416,7 +421,7 @@ __global__ void __launch_bounds__(kQkvWarps * 32, kQkvBlocks) qkv_kernel(const _
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 if (i >= n) break;
-                const Oct16 o = oct_turn<ROT>(oct_load<ROT>(sh.ring[warp][at_batch][i][oct], c, n_rot), k, norm, p.eps);
+                const Oct16 o = oct_turn<ROT>(oct_load<ROT>(sh.ring[warp][i][oct][at_batch], c, n_rot), k, norm, p.eps);
                 if (mine) oct_store<ROT>(dst + i * kD, c, n_rot, o);
             }
             dst += kBatch * kD;
@@ -444,7 +449,7 @@ __global__ void __launch_bounds__(kQkvWarps * 32, kQkvBlocks) qkv_kernel(const _
 #pragma unroll
         for (int i = 0; i < kBatch / 2; ++i) {
             if (i >= n) break;
-            uint16_t *krow = sh.ring[warp][at_batch][2 * i][oct];
+            uint16_t *krow = sh.ring[warp][2 * i][oct][at_batch];
             Oct16 o = oct_turn<ROT>(oct_load<ROT>(krow, c, n_rot), k, k_norm != nullptr, p.eps);
             if (ROT == kRotPart) {   // back to neighbours
                 __syncwarp();
@@ -453,7 +458,7 @@ __global__ void __launch_bounds__(kQkvWarps * 32, kQkvBlocks) qkv_kernel(const _
                 o = oct_load<kRotNone>(krow, c, 0);
             }
             oct_put_key<VT, KT>(o, tile16, place, c, w.k_mine);
-            oct_put_value<VT, KT>(oct_load<kRotNone>(sh.ring[warp][at_batch][2 * i + 1][oct], c, 0), tile16, place, c, w.k_mine);
+            oct_put_value<VT, KT>(oct_load<kRotNone>(sh.ring[warp][2 * i + 1][oct][at_batch], c, 0), tile16, place, c, w.k_mine);
             tile16 += head_bytes;
         }
         at_batch ^= 1;
