@@ -41,7 +41,11 @@ extern "C" {
  * known to 0.004 there).  A rate is therefore kept as the part of a full turn
  * that one position makes, in units of 2^-64: position times rate in 64-bit
  * integers drops the full turns and nothing else, and its top 32 bits give the
- * angle to 2^-32 of a turn for every int32 position, also a negative one.
+ * angle to 2^-32 of a turn for every int32 position, also a negative one: the
+ * angle of the rate as it is kept.  A rate of kvq_rope_turns comes from arithmetic
+ * in double and is off by up to 2^-54 of a turn per position (scaled ones 2^-52, and
+ * 1/factor times that where factor is below 1), which is 2^-32 of a turn at
+ * position 2^22 and 2^-23 at the ends of int32.
  */
 typedef enum kvq_rope_layout {
     KVQ_ROPE_HALF = 0,

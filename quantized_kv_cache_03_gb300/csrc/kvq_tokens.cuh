@@ -17,7 +17,8 @@ struct RopeDesc {
 // cos and sin of position * rate, both times amplitude.  The product of the
 // position and the rate (parts of a turn, 2^-64) wraps at full turns; its top
 // 32 bits as a signed number are the angle in (-1, 1) half turns, exact to
-// 2^-32 of a turn and rounded to 24 bits: 1.9e-7 rad at most.
+// 2^-32 of a turn for the rate as it is kept and rounded to 24 bits: 1.9e-7 rad at
+// most.
 __device__ __forceinline__ float2 angle_of(unsigned long long rate, int pos, float amplitude)
 {
     const unsigned long long t = rate * (unsigned long long)(long long)pos;

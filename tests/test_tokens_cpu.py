@@ -71,6 +71,34 @@ def test_far_positions_keep_their_angle(lib):
             assert min(off, 1 - off) <= abs(pos) * rate * Decimal(2) ** -48 + Decimal(2) ** -52, (i, pos)
 
 
+@pytest.mark.parametrize("kw,off", [(dict(), -54), (dict(scaling=1, factor=3.0), -52), (dict(scaling=1, factor=0.25), -50), (dict(scaling=2, factor=8.0), -52),
+                                    (dict(scaling=3, factor=40.0, original=300.0, fast=32.0, slow=1.0), -52), (dict(scaling=4, factor=8.0, original=8192.0, fast=4.0, slow=1.0), -52)])
+def test_rates_to_what_the_header_says(lib, kw, off):
+    """Against 40-digit arithmetic: 2^off of a turn per position, and 2^-65 for the unit in which a rate is kept.  With u = 2^-53, a
+    plain rate r = base^-e (up to 1) is off by 0.37 u for its exponent's rounding (r e ln base is 1 / 2.718 at most) and 1.05 u of the
+    power, by 0.35 u for 2 pi as a double and by u for the division: 2.77 u / (2 pi) < u / 2.  A blend adds its share, two products
+    and a sum, less than 5 u / (2 pi); a factor below 1 multiplies all."""
+    from decimal import Decimal as D, getcontext
+    getcontext().prec = 40
+    two_pi, zero = D("6.28318530717958647692528676655900576839433879875021164194989"), D(0)
+    scaling, factor, original, fast, slow = kw.get("scaling", 0), *(D(kw.get(k, 1.0)) for k in ("factor", "original", "fast", "slow"))
+    for n_rot, base in ((8, 500000.0), (40, 10000.0), (104, 500000.0), (128, 10000.0), (128, 2.0)):
+        _, t, _ = _turns(lib, n_rot, base, **kw)
+        b = D(base) * factor ** (D(n_rot) / (n_rot - 2)) if scaling == 2 else D(base)
+        if scaling == 3:
+            lo, hi = (n_rot * (original / (two_pi * k)).ln() / (2 * b.ln()) for k in (fast, slow))
+            lo, hi = max(lo.to_integral_value(rounding="ROUND_FLOOR"), zero), min(hi.to_integral_value(rounding="ROUND_CEILING"), D(n_rot - 1))
+        for i in range(n_rot // 2):
+            r = b ** (D(-2 * i) / n_rot)
+            share = [zero, D(1), zero, (i - lo) / max(hi - lo, D("0.001")) if scaling == 3 else zero, (fast - original * r / two_pi) / (fast - slow) if scaling == 4 else zero][scaling]
+            share = min(max(share, zero), D(1))
+            want = (r / factor * share + r * (1 - share)) / two_pi
+            for pos in (1, 4096, 2 ** 22, 2 ** 31 - 1, -2 ** 31):
+                d = (D(int(t[i]) * pos % 2 ** 64) / 2 ** 64 - want * pos) % 1
+                d = abs(d)
+                assert min(d, 1 - d) <= abs(pos) * (D(2) ** off + D(2) ** -65), (n_rot, base, i, pos)
+
+
 @pytest.mark.parametrize("kw", [dict(n_rot=-8), dict(n_rot=4), dict(n_rot=136), dict(base=1.0), dict(base=float("nan")), dict(base=float("inf")),
                                 dict(scaling=-1), dict(scaling=5), dict(scaling=1, factor=0.0), dict(scaling=2, factor=float("inf")),
                                 dict(scaling=3, factor=2.0, original=0.0, fast=32.0, slow=1.0), dict(scaling=4, factor=2.0, original=10.0, fast=1.0, slow=1.0),
