@@ -830,7 +830,7 @@ __device__ __forceinline__ void turn_key(QuadRow<VT, KT> &r, bool turns, const f
             }
         return;
     }
-    const QuadCodes q = quad_quantize<false>(h);
+    const QuadCodes q = quad_quantize(h);
 #pragma unroll
     for (int b = 0; b < 4; ++b)
         if ((!SOME || turns) && (ROT == kRotHalf || 32 * b < n_rot)) {   // the block holds a value that rotates

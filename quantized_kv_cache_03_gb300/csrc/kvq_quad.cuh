@@ -1,6 +1,8 @@
-// kvq_quad.cuh -- a cache row (one token of one head) held by four lanes, a quad,
-// so that a warp works on eight rows: rotated, quantized, taken out of a page's
-// tile and put into one.
+// kvq_quad.cuh -- a held cache row (one token of one head) in four lanes, a quad, so
+// that a warp works on eight rows: taken out of a page's tile, its key turned and
+// quantized anew, put into a tile (kvq_paged_move, the gather of many rows).  What
+// rotation and quantization need of eight neighbouring values also serves kvq_qkv,
+// which has eight lanes to a row.
 //
 // Lane c of a quad holds values 32 b + 8 c + i of the row (b < 4, i < 8): eight
 // neighbours of every 32-block.  The two values of a pair are then one lane's, side
@@ -37,10 +39,11 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 // What rotates, and so how a lane's values are paired.
 constexpr int kRotNone = 0, kRotPairs = 1, kRotHalf = 2, kRotPart = 3;   // half: n_rot = 128; part: halves of less
 
-// A lane's fp16 values: eight neighbours of each 32-block, or (part) two groups of four for each b.
+// A lane's fp16 values: eight neighbours of each 32-block.
 struct Quad16 {
     uint4 b[4];
 };
+// Group pair m of a row (part).
 struct PartGroups {
     int a, b;        // first dims of the groups
     bool rotates;
@@ -52,34 +55,6 @@ struct PartGroups {
         b = rotates ? a + 4 * h4 : a + 4;
     }
 };
-template <int ROT>
-__device__ __forceinline__ Quad16 quad_load(const uint16_t *row, int c, int n_rot)
-{
-    Quad16 r;
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-        if (ROT == kRotPart) {
-            const PartGroups g(c + 4 * b, n_rot);
-            const uint2 x = *reinterpret_cast<const uint2 *>(row + g.a), y = *reinterpret_cast<const uint2 *>(row + g.b);
-            r.b[b] = make_uint4(x.x, x.y, y.x, y.y);
-        } else {
-            r.b[b] = *reinterpret_cast<const uint4 *>(row + 32 * b + 8 * c);
-        }
-    return r;
-}
-template <int ROT>
-__device__ __forceinline__ void quad_store(uint16_t *row, int c, int n_rot, const Quad16 &r)
-{
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-        if (ROT == kRotPart) {
-            const PartGroups g(c + 4 * b, n_rot);
-            *reinterpret_cast<uint2 *>(row + g.a) = make_uint2(r.b[b].x, r.b[b].y);
-            *reinterpret_cast<uint2 *>(row + g.b) = make_uint2(r.b[b].z, r.b[b].w);
-        } else {
-            *reinterpret_cast<uint4 *>(row + 32 * b + 8 * c) = r.b[b];
-        }
-}
 
 // The same values in fp32, as pairs for packed arithmetic: of neighbours
 // (x0 x1), (x2 x3), ..., or, where pairs side by side rotate, of their first
@@ -168,13 +143,12 @@ __device__ __forceinline__ __half2 scales_of(uint32_t top)
     return __floats2half2_rn(a.x * (Q4 ? 0.125f : 1.f / 127.f), a.y * (Q4 ? 0.125f : 1.f / 127.f));
 }
 
-// The row's codes and scales: word 2 b + g of a block's lane holds codes 8 c + 4 g
+// The row's int8 codes and scales: word 2 b + g of a block's lane holds codes 8 c + 4 g
 // and on.
 struct QuadCodes {
     uint32_t w[8];
     uint32_t s[2];   // scales of blocks 0, 1 and 2, 3 (fp16 bits)
 };
-template <bool Q4>
 __device__ __forceinline__ QuadCodes quad_quantize(const Quad16 &x)
 {
     uint32_t top[2];
@@ -190,12 +164,12 @@ __device__ __forceinline__ QuadCodes quad_quantize(const Quad16 &x)
     QuadCodes r;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const __half2 s = scales_of<Q4>(top[h]);
+        const __half2 s = scales_of<false>(top[h]);
         r.s[h] = bits_of(s);
         const float2 f = __half22float2(s);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const uint2 w = codes8<Q4>(x.b[2 * h + k], k ? f.y : f.x);
+            const uint2 w = codes8<false>(x.b[2 * h + k], k ? f.y : f.x);
             r.w[4 * h + 2 * k] = w.x;
             r.w[4 * h + 2 * k + 1] = w.y;
         }
@@ -205,17 +179,8 @@ __device__ __forceinline__ QuadCodes quad_quantize(const Quad16 &x)
 // The scale of block c, for its lane.
 __device__ __forceinline__ uint32_t own_scale(const uint32_t (&s)[2], int c) { return (c & 2 ? s[1] : s[0]) >> (c & 1 ? 16 : 0) & 0xffff; }
 
-// Four words of q4_0 code bytes, one of each block: bytes 4 quart .. + 3, where
-// lane c has quart[c] = 0, 2, 1, 3 (its low nibbles are its own or lane c - 2's).
+// Of a block's q4_0 code bytes lane c has 4 quart .. + 3, quart = 0, 2, 1, 3.
 __device__ __forceinline__ int quart_of(int c) { return (c & 1) << 1 | c >> 1; }
-__device__ __forceinline__ void quad_nibbles(const QuadCodes &q, int c, uint32_t (&w)[4])
-{
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        const uint32_t keep = c & 2 ? q.w[2 * b + 1] : q.w[2 * b], got = __shfl_xor_sync(0xffffffffu, c & 2 ? q.w[2 * b] : q.w[2 * b + 1], 2);
-        w[b] = c & 2 ? got | keep << 4 : keep | got << 4;
-    }
-}
 
 // ---- in and out of tiles ----
 // A lane's part of K: eight words of codes, or sixteen of fp16 values, and the
@@ -226,22 +191,6 @@ struct QuadRow {
     static constexpr int KW = KT == KVQ_K_F16 ? 16 : 8, VW = VT == KVQ_V_Q8_0 ? 8 : 4;
     uint32_t k[KW], ks[2], v[VW], vs;
 };
-
-// V of a row just quantized.
-template <int VT, int KT>
-__device__ __forceinline__ void quad_values(QuadRow<VT, KT> &r, const QuadCodes &codes, int c)
-{
-    if (VT == KVQ_V_Q8_0) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) r.v[k] = codes.w[k];
-    } else {
-        uint32_t w[4];
-        quad_nibbles(codes, c, w);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) r.v[k] = w[k];
-    }
-    r.vs = own_scale(codes.s, c);
-}
 
 __device__ __forceinline__ int quad_k_off(int u, int c, int jh) { return ((2 * (u / 8) + jh) * 32 + 4 * (u % 8) + c) * 16; }
 __device__ __forceinline__ int quad_v8_off(int u, int c, int gi, int jh) { return ((2 * (u / 8) + jh) * 32 + 4 * (2 * c + gi) + (u % 8) / 2) * 16; }
