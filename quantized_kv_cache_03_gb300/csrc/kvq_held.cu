@@ -736,8 +736,11 @@ cudaError_t launch_gather_many(const PagedRowsParams &rows, int v_type, int k_ty
 //
 // Where tokens move, each slot may be another's source, so more than a few rows go
 // through the workspace (one launch out, one in) unless the caller says that none is.  8092 tokens
-// of 8 heads (q8_0 V, keys turned) through the workspace 15.7 us, two launches whose 70
-// MB would take 10.4.  131072 keys turned where they lie 61 us, 4.7 TB/s, 0.69 of a
+// of 8 heads (q8_0 V, keys turned): 35 MB in and out, 5.2 us at a copy's rate; directly
+// 11.7 us, through the workspace, which doubles the bytes, 15.7.  Both wait for rows: a
+// quad whose keys turn has one in flight at a time.  Pairs half of part of a head apart
+// pass through shared memory and back (16.4 and 22.8 us).  F16 K goes word by word, 18.0
+// and 31.4 us for 7.5.  131072 keys turned where they lie 61 us, 4.7 TB/s, 0.69 of a
 // copy's rate: instructions, some 400 for eight rows (codes to numbers, the turn,
 // largest values, new codes), three quarters of what the SMs can issue.  There the next
 // two heads' int8 keys are on their way in shared memory: loaded into registers when

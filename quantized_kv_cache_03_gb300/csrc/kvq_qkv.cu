@@ -326,6 +326,9 @@ __device__ __forceinline__ void stream_get(Stream &w)
 //    keys and one for values 46; two blocks on an SM with no spill 40.8, three 38.0).
 // 777 tokens (64 + 2 * 8 heads, F16 K) take 8 us, 64 tokens 3.5: a launch, slots, rows
 // and angles each waiting for memory once.
+// Pairs side by side take 42.6 us for the 8192 tokens (q8_0 V 36.9), halves of part of
+// a head, whose keys pass through shared memory and back to neighbours, 47.5 (rows that
+// stay fp16 40.7).
 template <int VT, int KT, int ROT, bool PAGED>
 __global__ void __launch_bounds__(kQkvWarps * 32, kQkvBlocks) qkv_kernel(const __grid_constant__ QkvParams p)
 {

@@ -89,7 +89,7 @@ struct MoveParams {
 
 // With programmatic dependent launch the next launch is prepared while one runs, but its blocks are placed only as this
 // one's end: these kernels do not call pdl_trigger.  Blocks that are placed early wait on the few SMs with room for them
-// and crowd there (kvq_qkv of 777 tokens and their gather, in a stream: 16.8 us, 13.2 so; 8192 tokens 45.2, 42.6; a page
+// and crowd there (kvq_qkv of 777 tokens and their gather, in a stream: 16.8 us, 13.4 so; 8192 tokens 45.2, 42.7; a page
 // copied 1.76, 1.53).  The fork's one cluster, which leaves most SMs free, does call it (7.1 us, 7.2 without).
 cudaError_t launch_positions(const PositionsParams &p, cudaStream_t s, bool pdl);
 cudaError_t prepare_qkv();
