@@ -1,7 +1,7 @@
 """Launches of the calls around the paged cache that are large enough for their
 long loops: a warp that goes over several heads, blocks of all heads in more than
 one wave, a thread that pushes more than one word of marks.  Against the same
-work in small calls, bit for bit, or plain Python."""
+work in small calls, bit for bit, or plain Python.  And two calls side by side."""
 import numpy as np
 import pytest
 import torch
@@ -209,3 +209,60 @@ def test_fork_over_nine_million_pages():
         assert ref["n_free"][0] > len(others)
         for k, v in ref.items():
             assert np.array_equal(o[k].cpu().numpy(), v), k
+
+
+# ---------------------------------------------------------- two at a time --
+@pytest.mark.parametrize("n", [200, 9000])
+def test_two_moves_at_once(n):
+    """Captured on two streams with a workspace each, replayed side by side."""
+    H, rope = 8, kvq.Rope(128, device=dev())
+    pools = [held(n + 40 + i, 64, H, I8, Q8) for i in range(2)]
+    start = [p.data.clone() for p in pools]
+    frm, to, turn = i32(np.arange(n) + 31), i32(np.arange(n)), i32(np.full(n, -31))
+    want = []
+    for p, s in zip(pools, start):
+        kvq.kvq_paged_move(p, frm, to, rope=rope, turn=turn)
+        want.append(p.data.clone())
+        p.data.copy_(s)
+    calls = [kvq.PagedMoveCall(p, frm, to, rope, turn) for p in pools]
+    streams, graphs = [torch.cuda.Stream() for _ in range(2)], [torch.cuda.CUDAGraph() for _ in range(2)]
+    for c, g in zip(calls, graphs):
+        with torch.cuda.graph(g):
+            c()
+    for _ in range(5):
+        for p, s in zip(pools, start):
+            p.data.copy_(s)
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p.data, w) for p, w in zip(pools, want))
+
+
+@pytest.mark.parametrize("B,most,n_pages", [(300, 40, 5000), (1500, 100, 200000)])
+def test_two_forks_at_once(B, most, n_pages):
+    """Of each size (one cluster, the whole GPU), with a workspace each."""
+    page, places = 16, []
+    for seed in range(2):
+        r = np.random.default_rng(seed)
+        table = r.permutation(n_pages)[np.arange(B * most) % (n_pages - 50)].reshape(B, most).astype(np.int32)
+        lens, parent, keep = r.integers(0, most * page + 1, B), r.integers(-1, B, B), r.integers(0, most * page, B)
+        free = np.full(n_pages, -5, np.int32)
+        free[:50] = np.arange(50)
+        ref = fork_ref(page, n_pages, lens, table, free, 50, np.full((B, most), -8, np.int32), most, parent, keep)
+        o = dict(table_out=torch.full((B, most), -8, dtype=torch.int32, device=dev()), lens=i32(np.zeros(B)), n_free=i32([0]), free=to_dev(free),
+                 **{k: i32(np.full(B, 99)) for k in ("copy_from", "copy_to", "copy_held", "status")})
+        call = kvq.PageForkCall(page, n_pages, i32(lens), to_dev(table), o["free"], i32([50]), o["table_out"], o["lens"], o["n_free"], o["copy_from"], o["copy_to"],
+                                o["copy_held"], o["status"], parent=i32(parent), keep=i32(keep))
+        places.append((call, o, ref, torch.cuda.Stream(), free))
+    for _ in range(5):
+        for _, o, _, _, free in places:
+            o["free"].copy_(to_dev(free))
+        torch.cuda.synchronize()
+        for call, _, _, s, _ in places:
+            call(s)
+        torch.cuda.synchronize()
+        for _, o, ref, _, _ in places:
+            for k, v in ref.items():
+                assert np.array_equal(o[k].cpu().numpy(), v), k
